@@ -317,7 +317,7 @@ def _plain_attn(s):
     top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
     p1, p2 = torch.exp(s1 - top), torch.exp(s2 - top)
     total = p1.sum(-1, keepdim=True) + p2.sum(-1, keepdim=True)
-    o1 = (p1.transpose(0, 1).reshape(Hkv, -1, P) @ vp).view(Hkv, B, Hq // Hkv, d).transpose(0, 1)
+    o1 = (p1.transpose(0, 1).reshape(Hkv, B * (Hq // Hkv), P) @ vp).view(Hkv, B, Hq // Hkv, d).transpose(0, 1)
     share = torch.where(total > 0, 1.0 / total, torch.zeros_like(total))
     a = (o1 + p2 @ vo) * share
     wt = None

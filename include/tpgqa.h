@@ -73,10 +73,14 @@ typedef enum tp_status {
   TP_ERR_CUDA = 9,             /* a CUDA runtime call failed; see tp_last_cuda_error */
   TP_ERR_WORKSPACE = 10,       /* workspace missing or too small                     */
   TP_ERR_UNSUPPORTED = 11,     /* valid request the library does not implement       */
-  TP_ERR_BAD_TOKEN = 12        /* an embedding lookup met a token id outside [0, V)  */
+  TP_ERR_BAD_TOKEN = 12,       /* an embedding lookup met a token id outside [0, V)  */
+  TP_ERR_BAD_LENGTH = 13       /* a cache call met a length outside [0, capacity]    */
 } tp_status;
 
-typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1 } tp_dtype;
+/* TP_E4M3 (8-bit floats: 4 exponent bits, 3 mantissa bits, no infinities) is
+ * taken by the calls that name it: tp_add_rmsnorm's output and the operands of
+ * tp_linear_epilogue. */
+typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1, TP_E4M3 = 2 } tp_dtype;
 
 /* A 2-D row-major view: element (i, j) lives at ptr + (i * ld + j) * size(dtype).
  * ld >= cols. rows or cols may be 0 (empty); each is below 2^31 (their product,
@@ -524,6 +528,67 @@ tp_status tp_attn_proj(const tp_plan *plan, const tp_tensor *x, const tp_tensor 
                        int32_t combine, tp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Between the projections: residual addition with root-mean-square norm, the
+ * epilogue work of a plain projection, attention over a cache behind a shared
+ * prefix, and eviction from that cache.
+ * ------------------------------------------------------------------------- */
+
+/* Residual addition and root-mean-square norm, per token (row):
+ *   z = x[0] + x[1] + ... + x[n_x-1] + residual     (f32, in this order)
+ *   residual_out = z rounded to its type
+ *   v = z * rsqrt(mean(z^2) + eps) * weight          (from the unrounded z)
+ *   y = v rounded to bf16, or to e4m3 codes of v / y_scale[row] with
+ *   y_scale[row] = max(max_i |v_i|, 2^-96) / 448.
+ *  n_x          : 1..64; x[r] are [T x D], all f32 or all bf16: one activation,
+ *                 or the per-rank partials that TP_COMBINE_NONE leaves (their
+ *                 all-reduce is then this call's first addition).
+ *  residual     : [T x D] f32 or bf16, or NULL (no residual is added).
+ *  weight       : [1 x D] f32 or bf16.
+ *  eps          : finite, > 0.
+ *  residual_out : [T x D] in residual's type, or NULL; it may be residual itself
+ *                 (same base and pitch), and overlaps nothing else. Needs a residual.
+ *  y            : [T x D] bf16 or e4m3; overlaps no input.
+ *  y_scale      : f32 [T] device array with an e4m3 y, else NULL.
+ * A row with a NaN gives a row of NaN. Bases are aligned to their element; bases
+ * and pitches on 16 bytes take the vector path.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_RANK_FAILED,
+ * TP_ERR_CUDA. */
+tp_status tp_add_rmsnorm(int32_t n_x, const tp_tensor *x, const tp_tensor *residual,
+                         const tp_tensor *weight, float eps, tp_tensor *residual_out, tp_tensor *y,
+                         float *y_scale, tp_stream_t stream);
+
+/* Eviction from the sequences' caches by accumulated attention weight. A cache
+ * [B*C x heads*d] holds sequence b's keys (or values) in rows b*C .. b*C+len_b-1,
+ * C = rows / batch. For every sequence and kv head with len_b > budget the first
+ * n_first and the last n_recent positions are kept, and of those between the
+ * budget - n_first - n_recent with the largest weight (of equal weights the lower
+ * position; NaN counts as the lowest weight, -0 as 0). With len_b <= budget
+ * everything is kept. Kept rows move to the front of the sequence's rows in
+ * their order; heads keep different positions, so each head's columns move by
+ * themselves.
+ *  plan        : its kv heads; d = head_dim, a multiple of 8.
+ *  lengths     : device int32 [batch]. One outside [0, C] is taken as the nearer
+ *                bound and reported by tp_device_status (TP_ERR_BAD_LENGTH).
+ *  k, v        : per kv source (one per rank, or one when the plan replicates
+ *                K/V) bf16 [B*C x heads*d].
+ *  weight      : per kv source f32 [B*heads x C], row b*heads + h.
+ *  k_out, v_out: per kv source bf16 [B*C2 x heads*d], C2 >= min(budget, C); rows past
+ *                a sequence's new length are left as they were. k_out and v_out
+ *                may be k and v themselves (same bases and pitches: the move is
+ *                in place), else they overlap no input.
+ *  weight_out  : per kv source f32 [B*heads x C3], C3 >= min(budget, C), the kept
+ *                weights, 0 past the new length; may be weight itself.
+ *  lengths_out : device int32 [batch], min(len_b, budget); may be lengths.
+ *  kept        : device int32 [sources][B*heads][budget]: the kept positions in
+ *                rising order, -1 past the new length. Always written: the move reads it.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_UNSUPPORTED,
+ * TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_cache_evict(const tp_plan *plan, int64_t batch, const int32_t *lengths, const tp_tensor *k,
+                         const tp_tensor *v, const tp_tensor *weight, int32_t budget, int32_t n_first,
+                         int32_t n_recent, tp_tensor *k_out, tp_tensor *v_out, tp_tensor *weight_out,
+                         int32_t *lengths_out, int32_t *kept, tp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status, health and diagnostics.
  * ------------------------------------------------------------------------- */
 
@@ -541,9 +606,9 @@ int32_t tp_last_cuda_error(void);
 tp_status tp_set_rank_health(int32_t rank, int32_t healthy);
 
 /* Synchronises `stream`, then reads and clears the device status word that
- * kernels set when a bounded wait runs out or an embedding lookup meets a bad
- * token id (the first such event is kept). Returns TP_OK, TP_ERR_TIMEOUT,
- * TP_ERR_BAD_TOKEN or TP_ERR_CUDA. *detail (optional) receives the raw word
+ * kernels set when a bounded wait runs out, an embedding lookup meets a bad
+ * token id or a cache call a bad length (the first such event is kept). Returns
+ * TP_OK, TP_ERR_TIMEOUT, TP_ERR_BAD_TOKEN, TP_ERR_BAD_LENGTH or TP_ERR_CUDA. *detail (optional) receives the raw word
  * (0 = none).
  * The library looks up the device addresses of its own device variables (this
  * status word, the scratch array of tp_mlp_block_static) once per device and

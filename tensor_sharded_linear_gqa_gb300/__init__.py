@@ -7,7 +7,8 @@ the library's CUDA kernels. There is no CPU fallback: the first call loads
 ``python -m tensor_sharded_linear_gqa_gb300.build``).
 
 Tensors are passed either as ``TpTensor`` or as 2-D CUDA ``torch.Tensor`` views
-with unit column stride (float32 or bfloat16). Per-rank arguments are Python
+with unit column stride (float32 or bfloat16; float8_e4m3fn where a call takes
+it). Per-rank arguments are Python
 sequences. ``stream`` is a ``torch.cuda.Stream``, a raw ``cudaStream_t`` int, or
 None for the current torch stream.
 """
@@ -25,10 +26,10 @@ TP_OK = 0
 STATUS_NAMES = ["TP_OK", "TP_ERR_INVALID_ARG", "TP_ERR_TP_SIZE_NOT_POW2", "TP_ERR_NOT_DIVISIBLE",
                 "TP_ERR_GQA_SHAPE", "TP_ERR_DTYPE", "TP_ERR_ALIGNMENT", "TP_ERR_RANK_FAILED",
                 "TP_ERR_TIMEOUT", "TP_ERR_CUDA", "TP_ERR_WORKSPACE", "TP_ERR_UNSUPPORTED",
-                "TP_ERR_BAD_TOKEN"]
+                "TP_ERR_BAD_TOKEN", "TP_ERR_BAD_LENGTH"]
 for _i, _n in enumerate(STATUS_NAMES):
     globals()[_n] = _i
-TP_F32, TP_BF16 = 0, 1
+TP_F32, TP_BF16, TP_E4M3 = 0, 1, 2
 TP_SHARD_COLUMN, TP_SHARD_ROW, TP_SHARD_VOCAB, TP_SHARD_REPLICATED = 0, 1, 2, 3
 TP_COMM_NONE, TP_COMM_ALL_REDUCE, TP_COMM_ALL_GATHER, TP_COMM_REDUCE_SCATTER = 0, 1, 2, 3
 TP_W_Q, TP_W_K, TP_W_V, TP_W_O, TP_W_GATE, TP_W_UP, TP_W_DOWN, TP_W_COUNT = range(8)
@@ -110,6 +111,9 @@ _SIGS = {
     "tp_qkv_proj": ([ctypes.c_void_p, _T, _T, _T, _T, _T, _T, _T, _S], ctypes.c_int),
     "tp_attn_proj": ([ctypes.c_void_p, _T, _T, _T, _T, _T, _T, _T, _T, _T, _T, ctypes.c_int32,
                       _S], ctypes.c_int),
+    "tp_add_rmsnorm": ([ctypes.c_int32, _T, _T, _T, ctypes.c_float, _T, _T, ctypes.c_void_p, _S], ctypes.c_int),
+    "tp_cache_evict": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _T, _T, _T, ctypes.c_int32, ctypes.c_int32,
+                        ctypes.c_int32, _T, _T, _T, ctypes.c_void_p, ctypes.c_void_p, _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "tp_last_cuda_error": ([], ctypes.c_int32),
     "tp_set_rank_health": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_int),
@@ -171,6 +175,8 @@ def tensor(t) -> TpTensor:
         dt = TP_F32
     elif t.dtype == torch.bfloat16:
         dt = TP_BF16
+    elif t.dtype == torch.float8_e4m3fn:
+        dt = TP_E4M3
     else:
         raise TypeError(f"unsupported dtype {t.dtype}")
     if t.numel() > 0 and not t.is_cuda:
@@ -180,6 +186,8 @@ def tensor(t) -> TpTensor:
 
 
 def _arr(seq):
+    if isinstance(seq, ctypes.Array):  # an arr() the caller keeps
+        return seq
     seq = list(seq)
     a = (TpTensor * max(len(seq), 1))()
     for i, t in enumerate(seq):
@@ -401,6 +409,53 @@ def tp_attn_proj(plan: Plan, x, w_q, w_k, w_v, q, k, v, a, w_o, y, combine: int,
     _check(_lib.tp_attn_proj(plan.handle, ctypes.byref(xs), _arr(w_q), _arr(w_k), _arr(w_v),
                              _arr(q), _arr(k), _arr(v), _arr(a), _arr(w_o), _arr(y), combine,
                              _stream(stream)), "tp_attn_proj")
+
+
+# ---- between the projections ----------------------------------------------------
+def _opt(t):
+    """Pointer to a TpTensor, or None."""
+    return None if t is None else ctypes.byref(tensor(t))
+
+
+def _row(t):
+    """A 1-D tensor as the [1 x n] view the library takes."""
+    return t if isinstance(t, TpTensor) or t.dim() == 2 else t.unsqueeze(0)
+
+
+def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=None, stream=None) -> None:
+    """z = sum of x (one tensor or a list of per-rank partials) + residual, to residual_out;
+    y = z * rsqrt(mean(z^2) + eps) * weight, in bf16, or as e4m3 codes with y_scale [T]."""
+    xs = _arr(x if isinstance(x, (list, tuple, ctypes.Array)) else [x])
+    n = len(x) if isinstance(x, (list, tuple)) else len(xs)
+    _check(_lib.tp_add_rmsnorm(n, xs, _opt(residual), _opt(_row(weight)), eps, _opt(residual_out), _opt(y),
+                               None if y_scale is None else _dev_ptr(y_scale, "torch.float32"), _stream(stream)),
+           "tp_add_rmsnorm")
+
+
+def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int, n_recent: int, k_out, v_out, weight_out,
+                   lengths_out, kept, stream=None) -> None:
+    """Keeps `budget` positions of every sequence and kv head: the first n_first, the last
+    n_recent and the heaviest between. k, v, weight and their outputs: one entry per kv source."""
+    batch = lengths.numel()
+    sources = 1 if plan.dims.num_kv_heads < plan.tp_size else plan.tp_size
+    rows = kept.numel() // max(budget, 1)
+    if rows * budget != kept.numel() or rows != batch * (plan.dims.num_kv_heads if sources == 1 else
+                                                         sources * (plan.dims.num_kv_heads // sources)):
+        raise ValueError("kept must hold sources * batch * heads * budget entries")
+    if lengths_out.numel() != batch:
+        raise ValueError("lengths_out must have one entry per sequence")
+    arrays = [_sources(a, sources) for a in (k, v, weight, k_out, v_out, weight_out)]
+    _check(_lib.tp_cache_evict(plan.handle, batch, _dev_ptr(lengths, "torch.int32"), arrays[0], arrays[1], arrays[2], budget,
+                               n_first, n_recent, arrays[3], arrays[4], arrays[5], _dev_ptr(lengths_out, "torch.int32"),
+                               _dev_ptr(kept, "torch.int32"), _stream(stream)), "tp_cache_evict")
+
+
+def _sources(seq, n: int):
+    """_arr of a per-rank argument, with at least n entries."""
+    a = _arr(seq)
+    if len(a) < n or (not isinstance(seq, ctypes.Array) and len(seq) < n):
+        raise ValueError(f"expected {n} tensors, one per rank or kv source")
+    return a
 
 
 # ---- status and diagnostics ---------------------------------------------------

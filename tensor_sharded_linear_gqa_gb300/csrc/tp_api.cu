@@ -579,6 +579,8 @@ cudaError_t get_dev_ctx(DevCtx *out) {
   return cudaSuccess;
 }
 
+tp_status check_rank_health(int32_t n) { return check_health(n); }
+
 int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
@@ -1473,6 +1475,7 @@ extern "C" const char *tp_status_str(tp_status s) {
     case TP_ERR_WORKSPACE: return "TP_ERR_WORKSPACE";
     case TP_ERR_UNSUPPORTED: return "TP_ERR_UNSUPPORTED";
     case TP_ERR_BAD_TOKEN: return "TP_ERR_BAD_TOKEN";
+    case TP_ERR_BAD_LENGTH: return "TP_ERR_BAD_LENGTH";
   }
   return "TP_ERR_UNKNOWN";
 }
@@ -1502,7 +1505,8 @@ extern "C" tp_status tp_device_status(tp_stream_t stream, int32_t *detail) {
     if (e != cudaSuccess) return cuda_fail(e);
   }
   if (detail) *detail = word;
-  return word == 0 ? TP_OK : (word == kDevBadToken ? TP_ERR_BAD_TOKEN : TP_ERR_TIMEOUT);
+  if (word == 0) return TP_OK;
+  return word == kDevBadToken ? TP_ERR_BAD_TOKEN : (word == kDevBadLength ? TP_ERR_BAD_LENGTH : TP_ERR_TIMEOUT);
 }
 
 extern "C" tp_status tp_set_wait_budget(int64_t nanoseconds) {

@@ -26,6 +26,7 @@ enum : int {
   kDevTimeoutDrain = 0x104,     // teardown gave up waiting for in-flight copies
   kDevTimeoutDebug = 0x1FF,     // tp_debug_wait_timeout's wait
   kDevBadToken = 0x201,         // an embedding lookup met a token id outside [0, V)
+  kDevBadLength = 0x202,        // a cache call met a length outside [0, capacity]
 };
 
 struct DevCtx {
@@ -38,6 +39,9 @@ struct DevCtx {
 cudaError_t get_dev_ctx(DevCtx *out);
 
 int num_sms();
+
+// TP_ERR_RANK_FAILED when one of ranks [0, n) is marked failed, else TP_OK.
+tp_status check_rank_health(int32_t n);
 
 // Records a failed CUDA call for tp_last_cuda_error() and returns TP_ERR_CUDA.
 tp_status cuda_fail(cudaError_t e);

@@ -1,0 +1,107 @@
+"""Refusals of the operators between the projections: every case below returns its status
+before any CUDA call, so it runs without a GPU."""
+import ctypes
+
+import pytest
+
+import tensor_sharded_linear_gqa_gb300 as tp
+
+FAKE = 1 << 40  # never dereferenced: every case fails validation first
+BF, F32, E4 = tp.TP_BF16, tp.TP_F32, tp.TP_E4M3
+
+
+def T(dtype, rows, cols, ld=None, ptr=FAKE):
+    return tp.TpTensor(ptr, dtype, 0, rows, cols, ld if ld is not None else max(cols, 1))
+
+
+def arr(*ts):
+    a = (tp.TpTensor * len(ts))()
+    for i, t in enumerate(ts):
+        a[i] = t
+    return a
+
+
+def ref(t):
+    return None if t is None else ctypes.byref(t)
+
+
+# ---- tp_add_rmsnorm --------------------------------------------------------------
+def norm_status(n=1, x=None, res=None, w=T(F32, 1, 64), eps=1e-5, res_out=None, y=T(BF, 4, 64), scale=None):
+    x = x if x is not None else [T(F32, 4, 64)] * n
+    return tp.raw_status("tp_add_rmsnorm", n, arr(*x), ref(res), ref(w), eps, ref(res_out), ref(y), scale, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=0, x=[T(F32, 4, 64)]), "INVALID_ARG"),
+    (dict(n=65, x=[T(F32, 4, 64)]), "INVALID_ARG"),
+    (dict(eps=0.0), "INVALID_ARG"), (dict(eps=float("nan")), "INVALID_ARG"), (dict(eps=float("inf")), "INVALID_ARG"),
+    (dict(w=None), "INVALID_ARG"), (dict(y=None), "INVALID_ARG"),
+    (dict(w=T(F32, 1, 63)), "INVALID_ARG"), (dict(w=T(F32, 2, 64)), "INVALID_ARG"), (dict(w=T(E4, 1, 64)), "DTYPE"),
+    (dict(y=T(BF, 5, 64)), "INVALID_ARG"), (dict(y=T(F32, 4, 64)), "DTYPE"), (dict(y=T(BF, 4, 64, ptr=None)), "INVALID_ARG"),
+    (dict(y=T(E4, 4, 64)), "INVALID_ARG"),                     # 8-bit output without scales
+    (dict(scale=FAKE), "INVALID_ARG"),                         # scales without an 8-bit output
+    (dict(y=T(E4, 4, 64), scale=FAKE + 2), "ALIGNMENT"),
+    (dict(res_out=T(F32, 4, 64)), "INVALID_ARG"),              # nothing to write it from
+    (dict(res=T(F32, 4, 64), res_out=T(BF, 4, 64)), "DTYPE"),
+    (dict(res=T(E4, 4, 64)), "DTYPE"), (dict(res=T(F32, 3, 64)), "INVALID_ARG"),
+    (dict(n=2, x=[T(F32, 4, 64), T(BF, 4, 64)]), "DTYPE"),
+    (dict(n=2, x=[T(F32, 4, 64), T(F32, 4, 65)]), "INVALID_ARG"),
+    (dict(x=[T(E4, 4, 64)]), "DTYPE"), (dict(x=[T(F32, 4, 64, ld=63)]), "INVALID_ARG"),
+    (dict(x=[T(F32, 4, 64, ptr=FAKE + 2)]), "ALIGNMENT"), (dict(x=[T(7, 4, 64)]), "INVALID_ARG"),
+    (dict(x=[T(F32, -1, 64)]), "INVALID_ARG"),
+])
+def test_norm_refusals(kw, status):
+    assert norm_status(**kw) == getattr(tp, "TP_ERR_" + status)
+
+
+def test_norm_empty_and_failed_rank():
+    assert norm_status(x=[T(F32, 0, 64, ptr=None)], y=T(BF, 0, 64, ptr=None)) == tp.TP_OK
+    tp.tp_set_rank_health(1, False)
+    try:
+        assert norm_status(n=2) == tp.TP_ERR_RANK_FAILED
+    finally:
+        tp.tp_set_rank_health(1, True)
+
+
+def test_other_calls_do_not_take_8_bit_operands():
+    a = arr(T(E4, 4, 64))
+    assert tp.raw_status("tp_column_linear", 1, a, arr(T(E4, 8, 64)), arr(T(BF, 4, 8)), 0, None) == tp.TP_ERR_INVALID_ARG
+    assert tp.raw_status("tp_row_linear", 1, a, arr(T(E4, 8, 64)), arr(T(F32, 4, 8)), 0, None) == tp.TP_ERR_INVALID_ARG
+
+
+# ---- tp_cache_evict ----------------------------------------------------------------
+PLAN = tp.tp_plan_create(2, 512, 4, 2, 128, 64)  # two ranks, one kv head of 128 each
+
+
+def evict_status(plan=PLAN, batch=2, lengths=FAKE, rows=40, rows_out=20, cols=128, kd=BF, wd=F32, w_cols=20, wo_cols=10,
+                 budget=10, first=1, recent=2, lengths_out=FAKE, kept=FAKE, ld=None, k_out_ptr=2 * FAKE, v_out_ptr=3 * FAKE,
+                 k_ptr=FAKE, v_ptr=FAKE, w_rows=2):
+    k, v = [T(kd, rows, cols, ld, k_ptr)] * 2, [T(kd, rows, cols, ld, v_ptr)] * 2
+    ko, vo = [T(kd, rows_out, cols, ld, k_out_ptr)] * 2, [T(kd, rows_out, cols, ld, v_out_ptr)] * 2
+    w, wo = [T(wd, w_rows, w_cols)] * 2, [T(wd, w_rows, wo_cols, None, 4 * FAKE)] * 2
+    return tp.raw_status("tp_cache_evict", plan.handle if plan else None, batch, lengths, arr(*k), arr(*v), arr(*w), budget,
+                         first, recent, arr(*ko), arr(*vo), arr(*wo), lengths_out, kept, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(plan=None), "INVALID_ARG"), (dict(batch=-1), "INVALID_ARG"), (dict(lengths=None), "INVALID_ARG"),
+    (dict(lengths_out=None), "INVALID_ARG"), (dict(kept=None), "INVALID_ARG"), (dict(kept=FAKE + 2), "ALIGNMENT"),
+    (dict(lengths=FAKE + 1), "ALIGNMENT"), (dict(budget=0), "INVALID_ARG"), (dict(first=-1), "INVALID_ARG"),
+    (dict(recent=-1), "INVALID_ARG"), (dict(first=9, recent=2), "INVALID_ARG"), (dict(rows=41), "INVALID_ARG"),
+    (dict(rows_out=18), "INVALID_ARG"),                   # nine rows a sequence for a budget of ten
+    (dict(cols=64), "INVALID_ARG"), (dict(kd=F32), "DTYPE"), (dict(wd=BF), "DTYPE"), (dict(w_cols=19), "INVALID_ARG"),
+    (dict(wo_cols=9), "INVALID_ARG"), (dict(ld=132), "ALIGNMENT"), (dict(w_rows=3), "INVALID_ARG"),
+    (dict(k_out_ptr=FAKE), "INVALID_ARG"),                # K onto itself with another capacity
+    (dict(k_out_ptr=FAKE, rows_out=40), "INVALID_ARG"),   # K in place, V not
+    (dict(k_ptr=FAKE + 8), "ALIGNMENT"),
+])
+def test_evict_refusals(kw, status):
+    assert evict_status(**kw) == getattr(tp, "TP_ERR_" + status)
+
+
+def test_evict_unsupported_and_empty():
+    odd = tp.tp_plan_create(1, 60, 1, 1, 60, 4)  # a head of 120 bytes
+    assert evict_status(plan=odd, cols=60) == tp.TP_ERR_UNSUPPORTED
+    assert evict_status(batch=0, rows=0, rows_out=0, w_rows=0, w_cols=0, wo_cols=0) == tp.TP_OK
+    with pytest.raises(ValueError):
+        tp._sources([], 2)

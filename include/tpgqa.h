@@ -557,6 +557,41 @@ tp_status tp_add_rmsnorm(int32_t n_x, const tp_tensor *x, const tp_tensor *resid
                          const tp_tensor *weight, float eps, tp_tensor *residual_out, tp_tensor *y,
                          float *y_scale, tp_stream_t stream);
 
+typedef enum tp_activation {
+  TP_ACT_NONE = 0,
+  TP_ACT_RELU = 1,
+  TP_ACT_GELU = 2, /* v Phi(v) = v/2 (1 + erf(v / sqrt 2)) */
+  TP_ACT_SILU = 3  /* v / (1 + e^-v)                       */
+} tp_activation;
+
+/* Matrix product with dequantisation, bias, activation and residual in its
+ * epilogue, rounded once:
+ *   y[t, f] = act(x_scale[t] * w_scale[f] * sum_k X[t, k] W[f, k] + bias[f]) + residual[t, f]
+ * with f32 accumulation and epilogue arithmetic.
+ *  shard   : TP_SHARD_COLUMN: x[0] is the one X [T x K], w[r] is rank r's [n_r x K],
+ *            its features the output columns after the lower ranks' (the all-gather
+ *            as concatenation). TP_SHARD_ROW: x[r] is rank r's [T x k_r], w[r] its
+ *            [n x k_r]; the ranks' products are summed in one accumulator
+ *            (TP_COMBINE_FUSED's sum).
+ *  x, w    : all bf16 or all e4m3. A rank with an empty slice is skipped.
+ *  x_scale : f32 [T] device array with e4m3 operands, else NULL: one scale per token
+ *            over the whole row (all ranks' slices of it), as tp_add_rmsnorm writes.
+ *  w_scale : f32 [features] device array with e4m3 operands, else NULL: one scale per
+ *            output feature, in output column order.
+ *  bias    : [1 x features] f32 or bf16, or NULL.
+ *  residual: [T x features] f32 or bf16, or NULL; it may be y itself in y's type.
+ *  y       : [T x features] f32 or bf16; overlaps no other input.
+ * X, W, y and residual have 16-byte aligned bases and pitches; in column mode
+ * every rank's first output column is 16-byte aligned in y and residual too.
+ * Weights are read early (see Overlap above). At most 16 ranks whose slices are
+ * not neighbours in one tensor, else TP_ERR_UNSUPPORTED; so are rows of no input
+ * features at all.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_TP_SIZE_NOT_POW2, TP_ERR_DTYPE, TP_ERR_ALIGNMENT,
+ * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_linear_epilogue(int32_t tp_size, int32_t shard, const tp_tensor *x, const float *x_scale,
+                             const tp_tensor *w, const float *w_scale, const tp_tensor *bias, int32_t activation,
+                             const tp_tensor *residual, tp_tensor *y, tp_stream_t stream);
+
 /* Eviction from the sequences' caches by accumulated attention weight. A cache
  * [B*C x heads*d] holds sequence b's keys (or values) in rows b*C .. b*C+len_b-1,
  * C = rows / batch. For every sequence and kv head with len_b > budget the first

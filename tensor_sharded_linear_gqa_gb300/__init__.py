@@ -36,6 +36,8 @@ TP_W_Q, TP_W_K, TP_W_V, TP_W_O, TP_W_GATE, TP_W_UP, TP_W_DOWN, TP_W_COUNT = rang
 WEIGHT_NAMES = ["q_proj", "k_proj", "v_proj", "o_proj", "gate_proj", "up_proj", "down_proj"]
 TP_COMBINE_NONE, TP_COMBINE_FUSED, TP_COMBINE_RING, TP_COMBINE_RING_FUSED, TP_COMBINE_RING_SHARED = 0, 1, 2, 3, 4
 TP_RING_STEPS, TP_RING_FUSED, TP_RING_FUSED_SHARED = 0, 1, 2
+TP_ACT_NONE, TP_ACT_RELU, TP_ACT_GELU, TP_ACT_SILU = 0, 1, 2, 3
+ACTIVATIONS = {"none": TP_ACT_NONE, "relu": TP_ACT_RELU, "gelu": TP_ACT_GELU, "silu": TP_ACT_SILU}
 TP_MOE_EXPERT_PARALLEL, TP_MOE_WITHIN_EXPERT = 0, 1
 
 
@@ -112,6 +114,8 @@ _SIGS = {
     "tp_attn_proj": ([ctypes.c_void_p, _T, _T, _T, _T, _T, _T, _T, _T, _T, _T, ctypes.c_int32,
                       _S], ctypes.c_int),
     "tp_add_rmsnorm": ([ctypes.c_int32, _T, _T, _T, ctypes.c_float, _T, _T, ctypes.c_void_p, _S], ctypes.c_int),
+    "tp_linear_epilogue": ([ctypes.c_int32, ctypes.c_int32, _T, ctypes.c_void_p, _T, ctypes.c_void_p, _T, ctypes.c_int32,
+                            _T, _T, _S], ctypes.c_int),
     "tp_cache_evict": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _T, _T, _T, ctypes.c_int32, ctypes.c_int32,
                         ctypes.c_int32, _T, _T, _T, ctypes.c_void_p, ctypes.c_void_p, _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -430,6 +434,17 @@ def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=Non
     _check(_lib.tp_add_rmsnorm(n, xs, _opt(residual), _opt(_row(weight)), eps, _opt(residual_out), _opt(y),
                                None if y_scale is None else _dev_ptr(y_scale, "torch.float32"), _stream(stream)),
            "tp_add_rmsnorm")
+
+
+def tp_linear_epilogue(tp_size: int, shard: int, x, w, y, bias=None, activation: int = TP_ACT_NONE, residual=None,
+                       x_scale=None, w_scale=None, stream=None) -> None:
+    """y = activation(x w^T * x_scale * w_scale + bias) + residual. shard: TP_SHARD_COLUMN (x: [X],
+    w: the ranks' weight rows) or TP_SHARD_ROW (x, w: the ranks' slices of the input features)."""
+    _check(_lib.tp_linear_epilogue(tp_size, shard, _sources(x, tp_size if shard == TP_SHARD_ROW else 1),
+                                   None if x_scale is None else _dev_ptr(x_scale, "torch.float32"), _sources(w, tp_size),
+                                   None if w_scale is None else _dev_ptr(w_scale, "torch.float32"),
+                                   None if bias is None else _opt(_row(bias)), activation, _opt(residual), _opt(y),
+                                   _stream(stream)), "tp_linear_epilogue")
 
 
 def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int, n_recent: int, k_out, v_out, weight_out,

@@ -2002,6 +2002,19 @@ bool encode_bf16_map_2d(CUtensorMap *map, const void *base, long long rows, long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows_map(CUtensorMap *map, const tp_tensor &t, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const bool f8 = t.dtype == TP_E4M3;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(t.cols), static_cast<cuuint64_t>(t.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(t.ld) * (f8 ? 1 : 2)};
+  const cuuint32_t box[2] = {f8 ? 128u : 64u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, t.ptr, dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 GemmBuilder::GemmBuilder() { std::memset(&p, 0, sizeof(p)); }
 
 int GemmBuilder::add_map(const void *base, long long rows, long long k, long long ld, int box_rows,

@@ -26,9 +26,9 @@ inline bool view_ok(const tp_tensor &t) {
 }
 inline bool ptr_aligned(const void *p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 inline bool elem_aligned(const tp_tensor &t) { return ptr_aligned(t.ptr, elem_size(t.dtype)); }
-// Base and row pitch on 16-byte boundaries.
+// Base and row pitch (of more than one row) on 16-byte boundaries.
 inline bool vec_aligned(const tp_tensor &t) {
-  return ptr_aligned(t.ptr, 16) && (t.ld * elem_size(t.dtype)) % 16 == 0;
+  return ptr_aligned(t.ptr, 16) && (t.rows <= 1 || (t.ld * elem_size(t.dtype)) % 16 == 0);
 }
 
 inline tp_status launched(cudaError_t e) {

@@ -331,6 +331,9 @@ tp_status launch_vocab_embed(const EmbedArgs &a, bool vec16, cudaStream_t s);
 bool encode_bf16_map_2d(CUtensorMap *map, const void *base, long long rows, long long cols, long long ld,
                         int box_rows);
 
+// The same for a bf16 or e4m3 view: boxes 128 bytes wide (64 bf16, 128 e4m3) x box_rows rows.
+bool encode_rows_map(CUtensorMap *map, const tp_tensor &t, int box_rows);
+
 // ---------------------------------------------------------------------------
 // Attention core (attention.cu): one CTA per (128-query tile, q head).
 // ---------------------------------------------------------------------------

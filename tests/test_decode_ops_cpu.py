@@ -105,3 +105,38 @@ def test_evict_unsupported_and_empty():
     assert evict_status(batch=0, rows=0, rows_out=0, w_rows=0, w_cols=0, wo_cols=0) == tp.TP_OK
     with pytest.raises(ValueError):
         tp._sources([], 2)
+
+
+# ---- tp_linear_epilogue ------------------------------------------------------------
+def linear_status(n=1, shard=tp.TP_SHARD_COLUMN, x=None, xs=None, w=None, ws=None, bias=None, act=0, res=None, y=T(BF, 4, 96)):
+    x = x or [T(BF, 4, 64)]
+    w = w or [T(BF, 96 // n, 64)] * n
+    return tp.raw_status("tp_linear_epilogue", n, shard, arr(*x), xs, arr(*w), ws, ref(bias), act, ref(res), ref(y), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=3), "TP_SIZE_NOT_POW2"), (dict(n=0, w=[T(BF, 96, 64)]), "INVALID_ARG"), (dict(shard=tp.TP_SHARD_VOCAB), "INVALID_ARG"),
+    (dict(act=4), "INVALID_ARG"), (dict(act=-1), "INVALID_ARG"), (dict(y=None), "INVALID_ARG"),
+    (dict(y=T(BF, 4, 95)), "INVALID_ARG"), (dict(y=T(BF, 5, 96)), "INVALID_ARG"), (dict(y=T(E4, 4, 96)), "DTYPE"),
+    (dict(x=[T(F32, 4, 64)], w=[T(F32, 96, 64)]), "DTYPE"), (dict(x=[T(E4, 4, 64)], xs=FAKE, ws=FAKE), "DTYPE"),
+    (dict(w=[T(BF, 96, 63)]), "INVALID_ARG"), (dict(x=[T(BF, 4, 64, ptr=FAKE + 2)]), "ALIGNMENT"),
+    (dict(x=[T(BF, 4, 60)], w=[T(BF, 96, 60, 64)]), "ALIGNMENT"), (dict(y=T(BF, 4, 96, 97)), "ALIGNMENT"),
+    (dict(x=[T(E4, 4, 64)], w=[T(E4, 96, 64)]), "INVALID_ARG"),                    # 8 bits without scales
+    (dict(x=[T(E4, 4, 64)], w=[T(E4, 96, 64)], xs=FAKE), "INVALID_ARG"),
+    (dict(xs=FAKE), "INVALID_ARG"), (dict(ws=FAKE), "INVALID_ARG"),                # scales without 8 bits
+    (dict(x=[T(E4, 4, 64)], w=[T(E4, 96, 64)], xs=FAKE + 2, ws=FAKE), "ALIGNMENT"),
+    (dict(bias=T(F32, 1, 95)), "INVALID_ARG"), (dict(bias=T(E4, 1, 96)), "DTYPE"), (dict(bias=T(F32, 1, 96, ptr=FAKE + 1)), "ALIGNMENT"),
+    (dict(res=T(F32, 4, 95)), "INVALID_ARG"), (dict(res=T(E4, 4, 96)), "DTYPE"), (dict(res=T(F32, 4, 96, ptr=FAKE + 4)), "ALIGNMENT"),
+    (dict(n=2, w=[T(BF, 44, 64), T(BF, 52, 64)]), "ALIGNMENT"),                    # the second shard's columns at 88 bytes
+    (dict(n=2, shard=tp.TP_SHARD_ROW, x=[T(BF, 4, 64), T(BF, 4, 64)], w=[T(BF, 96, 64), T(BF, 95, 64)]), "INVALID_ARG"),
+    (dict(n=2, shard=tp.TP_SHARD_ROW, x=[T(BF, 4, 64), T(BF, 3, 64)], w=[T(BF, 96, 64)] * 2), "INVALID_ARG"),
+    (dict(x=[T(BF, 4, 0)], w=[T(BF, 96, 0)]), "UNSUPPORTED"),                      # no input features
+    (dict(n=32, x=[T(BF, 4, 64)], w=[T(BF, 8, 64)] * 32, y=T(BF, 4, 256)), "UNSUPPORTED"),  # 32 weights lying apart
+])
+def test_linear_refusals(kw, status):
+    assert linear_status(**kw) == getattr(tp, "TP_ERR_" + status)
+
+
+def test_linear_empty():
+    assert linear_status(x=[T(BF, 0, 64, ptr=None)], y=T(BF, 0, 96, ptr=None)) == tp.TP_OK
+    assert linear_status(w=[T(BF, 0, 64, ptr=None)], y=T(BF, 4, 0, ptr=None)) == tp.TP_OK

@@ -592,6 +592,40 @@ tp_status tp_linear_epilogue(int32_t tp_size, int32_t shard, const tp_tensor *x,
                              const tp_tensor *w, const float *w_scale, const tp_tensor *bias, int32_t activation,
                              const tp_tensor *residual, tp_tensor *y, tp_stream_t stream);
 
+/* Workspace bytes tp_prefix_attn needs for these sizes: the splits' f32 partial
+ * results and, with weights != 0, the own keys' scores. 0 for a null plan,
+ * negative or unsupported sizes, and where none is needed. */
+size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t prefix, int64_t capacity,
+                                     int32_t weights);
+
+/* Attention of one new token per sequence over a prefix shared by the whole batch
+ * and the sequence's own cache: for q head h of sequence b, with g its kv head,
+ *   a[b, h] = softmax(q[b, h] [Kp_g ; Ko_b,g]^T / sqrt(d)) [Vp_g ; Vo_b,g]
+ * over all P prefix keys and the own keys in rows 0 .. lengths[b]-1 of the
+ * sequence's C cache rows (the new token's own key among them, if it is to see
+ * itself). No position encoding is applied. A row without any key is zero.
+ *  q[r], a[r] : [batch x Hq_r*d] bf16, rank r's q heads and output columns.
+ *  k_prefix, v_prefix : per kv source (one per rank, or one when the plan
+ *               replicates K/V) bf16 [P x heads*d]; P may be 0.
+ *  k_own, v_own : per kv source bf16 [batch*C x heads*d]; C may be 0. Rows past a
+ *               length are not read.
+ *  lengths    : device int32 [batch]. One outside [0, C] is taken as the nearer bound
+ *               and reported by tp_device_status (TP_ERR_BAD_LENGTH).
+ *  weight_out : per kv source f32 [batch*heads x C] (row b*heads + g), or NULL:
+ *               weight_out[j] = weight_in[j] + sum over the kv head's q heads of own key
+ *               j's softmax weight; 0 for j >= lengths[b]. May be weight_in.
+ *  weight_in  : as weight_out, or NULL (nothing is accumulated yet).
+ *  workspace  : at least tp_prefix_attn_workspace_size bytes, 16-byte aligned.
+ * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16.
+ * d must be 64 or 128, tp_size at most 32, a kv head's group at most 256 q heads,
+ * else TP_ERR_UNSUPPORTED. Outputs overlap no input except weight_out = weight_in.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
+ * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_prefix,
+                         const tp_tensor *v_prefix, const tp_tensor *k_own, const tp_tensor *v_own,
+                         const int32_t *lengths, const tp_tensor *weight_in, tp_tensor *weight_out, tp_tensor *a,
+                         void *workspace, size_t workspace_bytes, tp_stream_t stream);
+
 /* Eviction from the sequences' caches by accumulated attention weight. A cache
  * [B*C x heads*d] holds sequence b's keys (or values) in rows b*C .. b*C+len_b-1,
  * C = rows / batch. For every sequence and kv head with len_b > budget the first

@@ -116,6 +116,10 @@ _SIGS = {
     "tp_add_rmsnorm": ([ctypes.c_int32, _T, _T, _T, ctypes.c_float, _T, _T, ctypes.c_void_p, _S], ctypes.c_int),
     "tp_linear_epilogue": ([ctypes.c_int32, ctypes.c_int32, _T, ctypes.c_void_p, _T, ctypes.c_void_p, _T, ctypes.c_int32,
                             _T, _T, _S], ctypes.c_int),
+    "tp_prefix_attn_workspace_size": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32],
+                                      ctypes.c_size_t),
+    "tp_prefix_attn": ([ctypes.c_void_p, ctypes.c_int64, _T, _T, _T, _T, _T, ctypes.c_void_p, _T, _T, _T, ctypes.c_void_p,
+                        ctypes.c_size_t, _S], ctypes.c_int),
     "tp_cache_evict": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _T, _T, _T, ctypes.c_int32, ctypes.c_int32,
                         ctypes.c_int32, _T, _T, _T, ctypes.c_void_p, ctypes.c_void_p, _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -445,6 +449,22 @@ def tp_linear_epilogue(tp_size: int, shard: int, x, w, y, bias=None, activation:
                                    None if w_scale is None else _dev_ptr(w_scale, "torch.float32"),
                                    None if bias is None else _opt(_row(bias)), activation, _opt(residual), _opt(y),
                                    _stream(stream)), "tp_linear_epilogue")
+
+
+def tp_prefix_attn_workspace_size(plan: Plan, batch: int, prefix: int, capacity: int, weights: bool) -> int:
+    return int(_lib.tp_prefix_attn_workspace_size(plan.handle, batch, prefix, capacity, int(weights)))
+
+
+def tp_prefix_attn(plan: Plan, q, k_prefix, v_prefix, k_own, v_own, lengths, a, workspace, weight_in=None, weight_out=None,
+                   stream=None) -> None:
+    """One new token per sequence over the shared prefix and the sequence's own cache. q, a: one
+    entry per rank; caches and weights: one per kv source; workspace: a CUDA byte tensor."""
+    n, sources = plan.tp_size, 1 if plan.dims.num_kv_heads < plan.tp_size else plan.tp_size
+    _check(_lib.tp_prefix_attn(plan.handle, lengths.numel(), _sources(q, n), _sources(k_prefix, sources),
+                               _sources(v_prefix, sources), _sources(k_own, sources), _sources(v_own, sources),
+                               _dev_ptr(lengths, "torch.int32"), None if weight_in is None else _sources(weight_in, sources),
+                               None if weight_out is None else _sources(weight_out, sources), _sources(a, n),
+                               workspace.data_ptr(), workspace.numel(), _stream(stream)), "tp_prefix_attn")
 
 
 def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int, n_recent: int, k_out, v_out, weight_out,

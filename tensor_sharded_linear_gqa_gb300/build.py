@@ -28,7 +28,7 @@ LIB = os.path.join(PKG, "libtpgqa.so")
 STAMP = os.path.join(BUILD, "stamp.json")
 
 SOURCES = ["plan.cpp", "tp_api.cu", "gemm_tcgen05.cu", "gemm_f32.cu", "combine.cu", "mlp_static.cu", "vocab.cu", "moe.cu", "attention.cu",
-           "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu"]
+           "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu", "prefix_attention.cu"]
 HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

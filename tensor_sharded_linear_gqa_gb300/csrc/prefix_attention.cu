@@ -1,0 +1,972 @@
+// Attention of one new token per sequence over a prefix that the whole batch
+// shares and each sequence's own cache, with GQA:
+//   A[b, h] = softmax([q K_prefix^T, q K_own(b)^T] / sqrt(d)) [V_prefix ; V_own(b)]
+// and, on request, every own key's softmax weight summed over its q heads and
+// added to its accumulated weight.
+//
+// Every query row of a kv head (B sequences x G heads of its group) sees the same
+// prefix, so the prefix part is one dense product of B*G rows against P keys and
+// K/V are read once, not B times: k_prefix_part runs it on the tensor cores
+// (tcgen05) in tiles of 128 rows, split over the keys where there are too few
+// rows to fill the SMs. The own part differs per sequence and is bound by reading
+// the cache: k_own_part streams it through shared memory (cp.async) into
+// m16n8k16 products whose 16 rows are the group's heads; P stays in registers.
+// Both leave unnormalised f32 sums with their reference maximum m and sum l per
+// (split, row); k_combine joins them: sum of 2^(m_s - M) O_s over sum of
+// 2^(m_s - M) l_s, which is the softmax over all keys, whatever the split.
+//
+// k_own_part does not wait for k_prefix_part, which it shares nothing with: it
+// starts as that kernel's CTAs leave and waits for it only before it ends, so
+// that what follows it on the stream follows both.
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "op_util.h"
+#include "sm100_ptx.cuh"
+
+namespace tpgqa {
+namespace {
+
+using namespace op;
+
+constexpr int kMaxRanks32 = 32;
+constexpr int kSms = 152;  // a GB300's; splits and workspace sizes follow it, not the device at hand
+
+struct PrefixAttnParams {
+  CUtensorMap k_map[kMaxRanks32], v_map[kMaxRanks32];  // prefix K and V of each kv source
+  const void *q[kMaxRanks32];
+  void *a[kMaxRanks32];
+  long long q_ld[kMaxRanks32], a_ld[kMaxRanks32];
+  const void *k_own[kMaxRanks32], *v_own[kMaxRanks32];
+  long long ko_ld[kMaxRanks32], vo_ld[kMaxRanks32];
+  const float *w_in[kMaxRanks32];
+  float *w_out[kMaxRanks32];
+  long long wi_ld[kMaxRanks32], wo_ld[kMaxRanks32];
+  const int *lengths;
+  float *part_o;    // [split][row][d]
+  float2 *part_ml;  // [split][row] (m in log2 units, l)
+  float *scores;    // [row][capacity], s * log2(e) / sqrt(d) of the own keys; null: not wanted
+  int batch, heads_q, heads_kv, group, heads_per_rank, heads_per_source, d;
+  int prefix, blocks, split_p, pairs;  // 128-key blocks; key splits; 256-row tile pairs per kv head
+  int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
+  int has_prev;                        // k_own_part runs behind k_prefix_part
+  float scale_log2;
+  int *status;
+  long long wait_ns;
+};
+
+__device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// q row (or output row) of sequence b, global q head h.
+__device__ __forceinline__ const __nv_bfloat16 *q_row(const PrefixAttnParams &p, int b, int h) {
+  const int r = h / p.heads_per_rank;
+  return static_cast<const __nv_bfloat16 *>(p.q[r]) + b * p.q_ld[r] + static_cast<long long>(h - r * p.heads_per_rank) * p.d;
+}
+// Row of the partial results: the rows of a kv head are neighbours.
+__device__ __forceinline__ long long part_row(const PrefixAttnParams &p, int kv, int b, int g) {
+  return (static_cast<long long>(kv) * p.batch + b) * p.group + g;
+}
+__device__ __forceinline__ int own_length(const PrefixAttnParams &p, int b) {
+  return min(max(__ldg(p.lengths + b), 0), p.cap);
+}
+
+// ---------------------------------------------------------------------------
+// The shared prefix. A work item is (kv head, pair of adjacent 128-row tiles, key
+// split); both tiles use every K and V tile that is loaded. Warp roles:
+//   warp 0     TMA: lane 0 the K ring, lane 1 the V ring (two 128-key stages each);
+//   warp 1     MMA issuer: S_A, S_B, P_A V, S_A of the next block, P_B V, ...;
+//   warps 2-5  softmax of tile A, 6-9 of tile B, one thread per row; each thread
+//              also gathers its own q row into the swizzled Q tile (a group's
+//              heads may lie on several ranks, so no one tensor map covers them).
+// TMEM: S of A at columns 0, of B at 128 (P overwrites its first half as bf16 and
+// is read from there), O at 256 and 384. V is used as it lies, [keys x d], as an
+// MN-major operand, so no transposed copy is made. The running reference maximum
+// m moves only on a split's first block or when a block's sum of p passes 2^64.
+// ---------------------------------------------------------------------------
+constexpr int kPrefThreads = 320;
+constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
+constexpr float kSumLimit = 0x1p64f;
+
+// Shared-memory descriptor of an MN-major bf16 tile: rows of 64 MN values (128
+// bytes, swizzled) per k index, 8-row groups 1024 bytes apart (stride offset), the
+// next 64 MN values `mn_stride` bytes on (leading offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // B operand MN-major
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+template <int D>
+struct PrefCfg {
+  static constexpr int kCh = D / 64;                      // 64-column sub-tiles of a head
+  static constexpr uint32_t kTile = kCh * kSubTile;       // a [128 x D] tile
+  static constexpr uint32_t kK = 2 * kTile, kV = 4 * kTile, kBar = 6 * kTile;
+  static constexpr size_t kSmem = kBar + 256 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_constant__ PrefixAttnParams p) {
+  using C = PrefCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t sQ = ptx::smem_addr(smem), sK0 = sQ + C::kK, sV0 = sQ + C::kV;
+  uint8_t *bar_area = smem + C::kBar;
+  const uint32_t bar0 = ptx::smem_addr(bar_area);
+  const uint32_t q_full0 = bar0, k_full0 = bar0 + 16, k_empty0 = bar0 + 32, v_full0 = bar0 + 48, v_empty0 = bar0 + 64,
+                 s_full0 = bar0 + 80, p_full0 = bar0 + 96, o_full0 = bar0 + 112, o_free0 = bar0 + 128, drain = bar0 + 144;
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 152);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 156);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = p.batch * p.group;
+  const int items = p.heads_kv * p.pairs * p.split_p;
+  // item -> (kv head, tile pair, split, its blocks); splits of one head are neighbours
+  auto item = [&](int it, int &kv, int &pair, int &split, int &b0, int &b1) {
+    split = it % p.split_p;
+    const int r = it / p.split_p;
+    pair = r % p.pairs;
+    kv = r / p.pairs;
+    b0 = static_cast<int>(static_cast<long long>(p.blocks) * split / p.split_p);
+    b1 = static_cast<int>(static_cast<long long>(p.blocks) * (split + 1) / p.split_p);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(q_full0 + 8 * s, 128);
+      ptx::mbar_init(k_full0 + 8 * s, 1);
+      ptx::mbar_init(k_empty0 + 8 * s, 1);
+      ptx::mbar_init(v_full0 + 8 * s, 1);
+      ptx::mbar_init(v_empty0 + 8 * s, 1);
+      ptx::mbar_init(s_full0 + 8 * s, 1);
+      ptx::mbar_init(p_full0 + 8 * s, 128);
+      ptx::mbar_init(o_full0 + 8 * s, 1);
+      ptx::mbar_init(o_free0 + 8 * s, 128);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t *>(tmem_slot)), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  int issued[2] = {0, 0};
+  if (warp == 0) {
+    if (lane < 2) {
+      const uint32_t full0 = lane == 0 ? k_full0 : v_full0, empty0 = lane == 0 ? k_empty0 : v_empty0;
+      const uint32_t dst0 = lane == 0 ? sK0 : sV0;
+      bool run = true;
+      int g = 0;
+      for (int it = blockIdx.x; run && it < items; it += gridDim.x) {
+        int kv, pair, split, b0, b1;
+        item(it, kv, pair, split, b0, b1);
+        const int src = kv / p.heads_per_source;
+        const int col = (kv - src * p.heads_per_source) * D;
+        const CUtensorMap *map = lane == 0 ? &p.k_map[src] : &p.v_map[src];
+        for (int j = b0; j < b1; ++j, ++g) {
+          const int s = g & 1;
+          if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * s, ((g >> 1) & 1) ^ 1, p.wait_ns)) {
+            if (!*abort_flag) record(p.status, kDevTimeoutProducer);
+            *abort_flag = 1;
+            run = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(full0 + 8 * s, C::kTile);
+          for (int c = 0; c < C::kCh; ++c)
+            ptx::tma_load_2d(dst0 + s * C::kTile + c * kSubTile, map, col + c * 64, j * 128, full0 + 8 * s);
+          ++issued[s];
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (*abort_flag || !ptx::mbar_wait(bar, parity, p.wait_ns)) {
+          if (!*abort_flag) record(p.status, kDevTimeoutMma);
+          ok = false;
+          return false;
+        }
+        return true;
+      };
+      auto issue_s = [&](int x, int g) {  // S_X = Q_X K^T
+        const uint32_t qa = sQ + static_cast<uint32_t>(x) * C::kTile, ka = sK0 + static_cast<uint32_t>(g & 1) * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ptx::mma_bf16(tmem + static_cast<uint32_t>(x * 128), ptx::smem_desc_sw128(qa + (kk >> 2) * kSubTile) + 2 * (kk & 3),
+                        ptx::smem_desc_sw128(ka + (kk >> 2) * kSubTile) + 2 * (kk & 3), idesc_s, kk > 0 ? 1u : 0u);
+        ptx::mma_commit(s_full0 + 8 * x);
+      };
+      auto issue_pv = [&](int x, int g, bool first) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
+        const uint32_t va = sV0 + static_cast<uint32_t>(g & 1) * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_bf16_ts(tmem + 256u + static_cast<uint32_t>(x * 128), tmem + static_cast<uint32_t>(x * 128) + 8u * kk,
+                           desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, (!first || kk > 0) ? 1u : 0u);
+      };
+      int g = 0;
+      uint32_t np[2] = {0, 0}, nact[2] = {0, 0};
+      for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        int kv, pair, split, b0, b1;
+        item(it, kv, pair, split, b0, b1);
+        const int nb = b1 - b0;
+        const int tiles = (2 * pair + 1) * 128 < rows ? 2 : 1;
+        if (!wait(k_full0 + 8 * (g & 1), (g >> 1) & 1)) break;
+        for (int x = 0; ok && x < tiles; ++x) {
+          if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
+          ptx::tc_fence_after();
+          issue_s(x, g);
+        }
+        if (!ok) break;
+        ptx::mma_commit(k_empty0 + 8 * (g & 1));
+        for (int j = 0; ok && j < nb; ++j) {
+          const int gj = g + j;
+          if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
+          bool next_k = false;
+          for (int x = 0; ok && x < tiles; ++x) {
+            if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
+            ++np[x];
+            if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
+            ptx::tc_fence_after();
+            issue_pv(x, gj, j == 0);
+            if (j + 1 == nb) {
+              ptx::mma_commit(o_full0 + 8 * x);
+            } else {
+              if (!next_k) {
+                if (!wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
+                ptx::tc_fence_after();
+                next_k = true;
+              }
+              issue_s(x, gj + 1);
+            }
+          }
+          if (!ok) break;
+          ptx::mma_commit(v_empty0 + 8 * (gj & 1));
+          if (next_k) ptx::mma_commit(k_empty0 + 8 * ((gj + 1) & 1));
+        }
+        for (int x = 0; x < tiles; ++x) ++nact[x];
+        g += nb;
+      }
+      if (!ok) *abort_flag = 1;
+      ptx::mma_commit(drain);
+      if (!ptx::mbar_wait(drain, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+    }
+  } else {
+    const int x = (warp - 2) >> 2;
+    const int qw = warp & 3;
+    const int row = qw * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(qw * 32) << 16;
+    const uint32_t sb = tmem + lane_off + static_cast<uint32_t>(x * 128);
+    const uint32_t ob = tmem + lane_off + 256u + static_cast<uint32_t>(x * 128);
+    const uint32_t s_full = s_full0 + 8 * x, p_full = p_full0 + 8 * x;
+    bool ok = true;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+      const bool ready = ptx::mbar_wait(bar, parity, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ready && *abort_flag == 0)) {
+        if (lane == 0) {
+          if (!ready) record(p.status, kDevTimeoutEpilogue);
+          *abort_flag = 1;
+        }
+        return false;
+      }
+      return true;
+    };
+    uint32_t gs = 0, nact = 0;
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      int kv, pair, split, b0, b1;
+      item(it, kv, pair, split, b0, b1);
+      const int nb = b1 - b0;
+      const int m_row = (2 * pair + x) * 128 + row;  // row of the kv head: sequence * group + head
+      if ((2 * pair + x) * 128 >= rows) continue;
+      // this thread's q row into the Q tile; the previous item's products have read
+      // it (its o_full was waited for)
+      {
+        const uint32_t dst = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(row) * 128u;
+        const bool there = m_row < rows;
+        const int b = there ? m_row / p.group : 0, gq = there ? m_row - b * p.group : 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(q_row(p, b, kv * p.group + gq));
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = there ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t at = dst + (c >> 3) * kSubTile + static_cast<uint32_t>(((c & 7) ^ (row & 7)) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(q_full0 + 8 * x);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nb; ++j, ++gs) {
+        if (!wait_all(s_full, gs & 1)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const int lim = p.prefix - (b0 + j) * 128;  // keys of the block that exist
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&vc)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]);
+          ptx::tmem_ld_32cols(sb + 32 * c, vc);
+        }
+        ptx::tmem_ld_wait();
+        ptx::tmem_regs_ready(v);
+        if (lim < 128) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim) v[i] = __float_as_uint(-INFINITY);
+        }
+        const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
+        bool find_max = j == 0, move = false;
+        float m_new = m, s0, s1;
+#pragma unroll 1
+        for (;;) {
+          if (find_max) {
+            float mq[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mq[q] = __uint_as_float(v[32 * q + 31]);
+#pragma unroll
+              for (int i = 0; i < 30; i += 2)
+                mq[q] = max3(mq[q], __uint_as_float(v[32 * q + i]), __uint_as_float(v[32 * q + i + 1]));
+              mq[q] = fmaxf(mq[q], __uint_as_float(v[32 * q + 30]));
+            }
+            const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * p.scale_log2;
+            move = m_blk > m + 8.f;
+            m_new = move ? m_blk : m;
+          }
+          const uint64_t nm2 = pack2(-m_new, -m_new);
+          uint64_t sumh[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint64_t &sum2 = sumh[h];
+            sum2 = pack2(0.f, 0.f);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float y0, y1;
+              unpack2(fma2(pack2(__uint_as_float(v[32 * h + i]), __uint_as_float(v[32 * h + i + 1])), c2, nm2), y0, y1);
+              const float a0 = ex2(y0), a1 = ex2(y1);
+              sum2 = add2(sum2, pack2(a0, a1));
+              pk[i >> 1] = pack_bf16(a0, a1);
+            }
+            ptx::tmem_st_16cols(sb + 16 * h, pk);
+          }
+          unpack2(add2(add2(sumh[0], sumh[1]), add2(sumh[2], sumh[3])), s0, s1);
+          if (find_max || !__any_sync(0xffffffffu, !(s0 + s1 <= kSumLimit))) break;
+          find_max = true;
+          ptx::tmem_st_wait();
+        }
+        const float alpha = move ? exp2f(m - m_new) : 1.f;
+        l = l * alpha + (s0 + s1);
+        m = m_new;
+        if (j > 0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            ptx::tmem_ld_32cols(ob + c * 32, o);
+            ptx::tmem_ld_wait();
+            ptx::tmem_regs_ready(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            ptx::tmem_st_32cols(ob + c * 32, o);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      if (!wait_all(o_full0 + 8 * x, nact & 1)) {
+        ok = false;
+        break;
+      }
+      ++nact;
+      ptx::tc_fence_after();
+      const long long at = static_cast<long long>(split) * p.batch * p.heads_q + static_cast<long long>(kv) * rows + m_row;
+      if (m_row < rows) p.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        ptx::tmem_ld_32cols(ob + c * 32, v);
+        ptx::tmem_ld_wait();
+        ptx::tmem_regs_ready(v);
+        if (m_row < rows) {
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                 __uint_as_float(v[4 * i + 3]));
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(o_free0 + 8 * x);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 0 && lane < 2) {
+    const uint32_t full0 = lane == 0 ? k_full0 : v_full0;
+    for (int s = 0; s < 2; ++s)
+      if (issued[s] > 0 && !ptx::mbar_wait(full0 + 8 * s, (issued[s] - 1) & 1, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The own caches. CTA (sequence and kv head, key split, 16-head tile); 64-key
+// stages, the four warps take 16 keys each and keep their own m, l and O, which
+// are joined at the end. Keys past the length are zero-filled in shared memory,
+// never read from the cache (stale values there may be anything), and masked.
+// ---------------------------------------------------------------------------
+constexpr int kOwnThreads = 128;
+constexpr int kOwnKeys = 64;
+constexpr int kOwnStages = 3;
+
+template <int D>
+struct OwnCfg {
+  static constexpr int kMat = kOwnKeys * D * 2;  // bytes of a stage's K (or V)
+  static constexpr int kSmem = kOwnStages * 2 * kMat;
+  static_assert(kSmem >= 4 * 16 * D * 4, "the warps' outputs fit over the stages");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kOwnThreads) k_own_part(const __grid_constant__ PrefixAttnParams p) {
+  using C = OwnCfg<D>;
+  extern __shared__ __align__(128) uint8_t own_smem[];
+  __shared__ float2 s_ml[4][16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
+  const int split = blockIdx.y, g0 = blockIdx.z * 16;
+  if (!p.has_prev) grid_dep_wait();
+  grid_dep_launch();
+  const int len = own_length(p, b);
+  if (kv == 0 && split == 0 && g0 == 0 && tid == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  const int j0 = split * p.chunk, j1 = min(len, j0 + p.chunk);
+  if (j0 < j1) {
+    const int src = kv / p.heads_per_source;
+    const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
+    const __nv_bfloat16 *k0 = static_cast<const __nv_bfloat16 *>(p.k_own[src]) + static_cast<long long>(b) * p.cap * p.ko_ld[src] + col;
+    const __nv_bfloat16 *v0 = static_cast<const __nv_bfloat16 *>(p.v_own[src]) + static_cast<long long>(b) * p.cap * p.vo_ld[src] + col;
+    const long long k_ld = p.ko_ld[src], v_ld = p.vo_ld[src];
+    const uint32_t sbase = ptx::smem_addr(own_smem);
+    const int steps = (j1 - j0 + kOwnKeys - 1) / kOwnKeys;
+    constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+    auto load = [&](int step) {
+      if (step < steps) {
+        const uint32_t ks = sbase + static_cast<uint32_t>(step % kOwnStages) * 2 * C::kMat, vs = ks + C::kMat;
+#pragma unroll
+        for (int i = 0; i < kOwnKeys * kPieces / kOwnThreads; ++i) {
+          const int idx = tid + i * kOwnThreads;
+          const int r = idx / kPieces, c = idx % kPieces;
+          const int j = j0 + step * kOwnKeys + r;
+          const bool valid = j < j1;
+          const uint32_t at = static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16);
+          const long long jj = valid ? j : j0;
+          cp_async16(ks + at, k0 + jj * k_ld + c * 8, valid);
+          cp_async16(vs + at, v0 + jj * v_ld + c * 8, valid);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kOwnStages - 1; ++s) load(s);
+    // q as the A operand: rows lane/4 and lane/4 + 8 are heads g0 + ...
+    const int r_lo = g0 + (lane >> 2), r_hi = r_lo + 8;
+    uint32_t qa[D / 16][4];
+    {
+      const uint32_t *q_lo = r_lo < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_lo)) : nullptr;
+      const uint32_t *q_hi = r_hi < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_hi)) : nullptr;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int at = kk * 8 + (lane & 3);
+        qa[kk][0] = q_lo ? __ldg(q_lo + at) : 0u;
+        qa[kk][1] = q_hi ? __ldg(q_hi + at) : 0u;
+        qa[kk][2] = q_lo ? __ldg(q_lo + at + 4) : 0u;
+        qa[kk][3] = q_hi ? __ldg(q_hi + at + 4) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int step = 0; step < steps; ++step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
+      __syncthreads();  // the stage is there for every thread, and the one loaded next is free
+      load(step + kOwnStages - 1);
+      const int key0 = j0 + step * kOwnKeys + warp * 16;
+      if (key0 >= j1) continue;
+      const uint32_t ks = sbase + static_cast<uint32_t>(step % kOwnStages) * 2 * C::kMat, vs = ks + C::kMat;
+      float s[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int r = warp * 16 + ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
+        uint32_t kb[4];
+        ldsm4(ks + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), kb);
+        mma16816(s[0], qa[kk], kb[0], kb[1]);
+        mma16816(s[1], qa[kk], kb[2], kb[3]);
+      }
+      // s[n][0,1]: row r_lo, keys key0 + 8n + 2 (lane%4) + {0, 1}; s[n][2,3]: row r_hi
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + 8 * n + 2 * (lane & 3) + (i & 1);
+          s[n][i] = key < j1 ? s[n][i] * p.scale_log2 : -INFINITY;
+          mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
+        }
+      if (p.scores) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int g = h ? r_hi : r_lo;
+          if (g < p.group) {
+            float *dst = p.scores + part_row(p, kv, b, g) * p.cap;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int key = key0 + 8 * n + 2 * (lane & 3) + i;
+                if (key < j1) dst[key] = s[n][2 * h + i];
+              }
+          }
+        }
+      }
+      float m_new[2], alpha[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        m_new[h] = fmaxf(m[h], mx[h]);
+        // the step holds at least one key, so m_new is above -inf unless a score is not a number
+        alpha[h] = m[h] == m_new[h] ? 1.f : ex2(m[h] - m_new[h]);
+        l[h] *= alpha[h];
+        m[h] = m_new[h];
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[n][i] = ex2(s[n][i] - m[i >> 1]);
+          l[i >> 1] += s[n][i];
+        }
+      // P rounded to bf16 for the product, as every GEMM operand here; l sums the unrounded p
+      const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                              pack_bf16(s[1][2], s[1][3])};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int r = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * i + (lane >> 4);
+        uint32_t vb[4];
+        ldsm4_t(vs + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), vb);
+        mma16816(o[2 * i], pa, vb[0], vb[1]);
+        mma16816(o[2 * i + 1], pa, vb[2], vb[3]);
+      }
+    }
+    // join the four warps
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // every stage has been read
+    float *so = reinterpret_cast<float *>(own_smem);  // [warp][16 rows][D]
+    if ((lane & 3) == 0) {
+      s_ml[warp][lane >> 2] = make_float2(m[0], l[0]);
+      s_ml[warp][(lane >> 2) + 8] = make_float2(m[1], l[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const int c = i * 8 + 2 * (lane & 3);
+      *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2)) * D + c) = make_float2(o[i][0], o[i][1]);
+      *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2) + 8) * D + c) = make_float2(o[i][2], o[i][3]);
+    }
+    __syncthreads();
+    const int n_rows = min(16, p.group - g0);
+    for (int i = tid; i < n_rows * (D / 4); i += kOwnThreads) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mt = fmaxf(mt, s_ml[w][r].x);
+      float lt = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 ml = s_ml[w][r];
+        if (ml.y == 0.f && ml.x == -INFINITY) continue;  // a warp without keys
+        const float f = ex2(ml.x - mt);
+        const float4 ov = *reinterpret_cast<const float4 *>(so + (w * 16 + r) * D + c);
+        lt += f * ml.y;
+        acc.x += f * ov.x;
+        acc.y += f * ov.y;
+        acc.z += f * ov.z;
+        acc.w += f * ov.w;
+      }
+      const long long at = static_cast<long long>(p.split_p + split) * p.batch * p.heads_q + part_row(p, kv, b, g0 + r);
+      *reinterpret_cast<float4 *>(p.part_o + at * D + c) = acc;
+      if (c == 0) p.part_ml[at] = make_float2(mt, lt);
+    }
+  }
+  // what follows this kernel on the stream follows the prefix kernel too
+  if (p.has_prev) grid_dep_wait();
+}
+
+// ---------------------------------------------------------------------------
+// Joins the splits of a (sequence, kv head): one warp per head of the group, then
+// the own keys' weights.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant__ PrefixAttnParams p) {
+  constexpr int kPer = D / 32;  // output columns of a lane
+  __shared__ float s_lse[kJoinThreads];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = own_length(p, b);
+  if (p.split_o == 0 && kv == 0 && threadIdx.x == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  const int own = len > 0 ? (len + p.chunk - 1) / p.chunk : 0;
+  const int n = p.split_p + own;
+  const long long stride = static_cast<long long>(p.batch) * p.heads_q;
+  for (int g = warp; g < p.group; g += kJoinThreads / 32) {
+    const long long row = part_row(p, kv, b, g);
+    float mt = -INFINITY;
+    for (int s = lane; s < n; s += 32) mt = fmaxf(mt, p.part_ml[s * stride + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    float lt = 0.f, acc[kPer] = {};
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float2 ml = p.part_ml[s * stride + row];
+      const float f = ex2(ml.x - mt);
+      lt += f * ml.y;
+      const float *src = p.part_o + (s * stride + row) * D + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(src + i);
+        acc[i] += f * v.x;
+        acc[i + 1] += f * v.y;
+      }
+    }
+    // no key at all: the row is zero, and no key has a weight
+    const float inv = n > 0 ? 1.f / lt : 0.f;
+    const int h = kv * p.group + g;
+    const int r = h / p.heads_per_rank;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[r]) + b * p.a_ld[r] +
+                         static_cast<long long>(h - r * p.heads_per_rank) * D + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0) s_lse[g] = mt + log2f(lt);
+  }
+  if (!p.w_out[0]) return;
+  __syncthreads();
+  const int src = kv / p.heads_per_source;
+  const long long wrow = static_cast<long long>(b) * p.heads_per_source + (kv - src * p.heads_per_source);
+  const float *wi = p.w_in[src] ? p.w_in[src] + wrow * p.wi_ld[src] : nullptr;
+  float *wo = p.w_out[src] + wrow * p.wo_ld[src];
+  const float *sc = p.scores + part_row(p, kv, b, 0) * p.cap;
+  for (int j = threadIdx.x; j < p.cap; j += kJoinThreads) {
+    float w = 0.f;
+    if (j < len) {
+#pragma unroll 4
+      for (int g = 0; g < p.group; ++g) w += ex2(sc[static_cast<long long>(g) * p.cap + j] - s_lse[g]);
+      if (wi) w += wi[j];
+    }
+    wo[j] = w;
+  }
+}
+
+// The launch shape: pure functions of the sizes, shared by the workspace's size.
+struct Shape {
+  int pairs, blocks, split_p, chunk, split_o;
+};
+Shape shape_of(long long batch, long long group, long long heads_kv, long long prefix, long long cap) {
+  Shape s = {};
+  const long long rows = batch * group;
+  s.pairs = static_cast<int>((rows + 255) / 256);
+  s.blocks = static_cast<int>((prefix + 127) / 128);
+  if (prefix > 0) {
+    // key splits: the fewest block steps of the busiest SM, counting about two
+    // blocks' time for an item's start and its partial results
+    const long long bases = heads_kv * s.pairs;
+    long long best = -1;
+    for (int c = 1; c <= s.blocks && c <= 2 * kSms; ++c) {
+      const long long waves = (bases * c + kSms - 1) / kSms;
+      const long long cost = waves * ((s.blocks + c - 1) / c + 2);
+      if (best < 0 || cost < best) {
+        best = cost;
+        s.split_p = c;
+      }
+      if (bases * c >= 2 * kSms) break;
+    }
+  }
+  if (cap > 0) {
+    // own keys per split: 512, halved while the grid leaves SMs idle
+    s.chunk = 512;
+    const long long units = batch * heads_kv * ((group + 15) / 16);
+    while (s.chunk > kOwnKeys && units * ((cap + s.chunk - 1) / s.chunk) < 2 * kSms) s.chunk /= 2;
+    s.split_o = static_cast<int>((cap + s.chunk - 1) / s.chunk);
+  } else {
+    s.chunk = 1;
+  }
+  return s;
+}
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+struct Regions {
+  size_t o, ml, scores, total;
+};
+Regions regions_of(const Shape &s, long long batch, long long heads_q, long long d, long long cap, bool weights) {
+  Regions r;
+  const size_t rows = static_cast<size_t>(s.split_p + s.split_o) * batch * heads_q;
+  r.o = 0;
+  r.ml = round256(rows * d * 4);
+  r.scores = r.ml + round256(rows * 8);
+  r.total = r.scores + (weights ? round256(static_cast<size_t>(batch) * heads_q * cap * 4) : 0);
+  return r;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> g(mu);
+  if (dev < 32 && (mask & (1u << dev))) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 32) mask |= 1u << dev;
+  return e;
+}
+
+template <int D>
+tp_status launch_all(const PrefixAttnParams &p, cudaStream_t s) {
+  static unsigned mask_p = 0, mask_o = 0;
+  static std::mutex mu;
+  cudaError_t e = allow_smem(k_prefix_part<D>, static_cast<int>(PrefCfg<D>::kSmem), mask_p, mu);
+  if (e == cudaSuccess) e = allow_smem(k_own_part<D>, OwnCfg<D>::kSmem, mask_o, mu);
+  if (e != cudaSuccess) return cuda_fail(e);
+  tp_status st = TP_OK;
+  if (p.split_p > 0) {
+    const int items = p.heads_kv * p.pairs * p.split_p, sms = num_sms();
+    st = launched(launch_kernel(k_prefix_part<D>, dim3(static_cast<unsigned>(items < sms ? items : sms)),
+                                dim3(kPrefThreads), PrefCfg<D>::kSmem, s, 1, p));
+    if (st != TP_OK) return st;
+  }
+  if (p.split_o > 0) {
+    const dim3 grid(static_cast<unsigned>(p.batch * p.heads_kv), static_cast<unsigned>(p.split_o),
+                    static_cast<unsigned>((p.group + 15) / 16));
+    st = launched(launch_kernel(k_own_part<D>, grid, dim3(kOwnThreads), OwnCfg<D>::kSmem, s, 1, p));
+    if (st != TP_OK) return st;
+  }
+  return launched(launch_kernel(k_combine<D>, dim3(static_cast<unsigned>(p.batch * p.heads_kv)), dim3(kJoinThreads), 0, s,
+                                1, p));
+}
+
+// Sizes that the launch shape's 32-bit arithmetic and the kernels take.
+bool sizes_ok(const tp_dims &d, long long batch, long long prefix, long long cap) {
+  const long long group = d.num_q_heads / d.num_kv_heads;
+  return batch <= 0x7fffffffLL / 256 / d.num_q_heads && prefix <= 0x7fffffffLL - 256 && cap <= 0x7fffffffLL - 1024 &&
+         group <= kJoinThreads && (cap + kOwnKeys - 1) / kOwnKeys <= 65535;
+}
+
+}  // namespace
+}  // namespace tpgqa
+
+using namespace tpgqa;
+using namespace tpgqa::op;
+
+extern "C" size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t prefix, int64_t capacity,
+                                                int32_t weights) {
+  tp_dims d;
+  if (!plan || batch < 0 || prefix < 0 || capacity < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
+  if (batch == 0 || !sizes_ok(d, batch, prefix, capacity)) return 0;
+  const Shape s = shape_of(batch, d.num_q_heads / d.num_kv_heads, d.num_kv_heads, prefix, capacity);
+  return regions_of(s, batch, d.num_q_heads, d.head_dim, capacity, weights != 0).total;
+}
+
+extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_prefix,
+                                    const tp_tensor *v_prefix, const tp_tensor *k_own, const tp_tensor *v_own,
+                                    const int32_t *lengths, const tp_tensor *weight_in, tp_tensor *weight_out,
+                                    tp_tensor *a, void *workspace, size_t workspace_bytes, tp_stream_t stream) {
+  tp_dims dims;
+  tp_rank_shard sh;
+  if (!plan || tp_plan_dims(plan, &dims) != TP_OK || tp_plan_query_rank(plan, 0, &sh) != TP_OK) return TP_ERR_INVALID_ARG;
+  if (!q || !k_prefix || !v_prefix || !k_own || !v_own || !a || batch < 0) return TP_ERR_INVALID_ARG;
+  if (weight_in && !weight_out) return TP_ERR_INVALID_ARG;
+  const int n = dims.tp_size;
+  const long long hd = dims.head_dim;
+  if ((hd != 64 && hd != 128) || n > kMaxRanks32) return TP_ERR_UNSUPPORTED;
+  const int sources = sh.kv_replicated ? 1 : n;
+  const long long kvc = (sh.kv_head_end - sh.kv_head_begin) * hd, qc = dims.num_q_heads / n * hd;
+  const long long P = k_prefix[0].rows, cap = batch ? k_own[0].rows / batch : 0;
+  auto check = [&](const tp_tensor &t, long long rows, long long cols) -> tp_status {
+    if (!view_ok(t)) return TP_ERR_INVALID_ARG;
+    if (t.dtype != TP_BF16) return TP_ERR_DTYPE;
+    if (t.rows != rows || t.cols != cols) return TP_ERR_INVALID_ARG;
+    return rows > 0 && !vec_aligned(t) ? TP_ERR_ALIGNMENT : TP_OK;
+  };
+  tp_status st;
+  for (int r = 0; r < n; ++r) {
+    if ((st = check(q[r], batch, qc)) != TP_OK) return st;
+    if ((st = check(a[r], batch, qc)) != TP_OK) return st;
+  }
+  for (int r = 0; r < sources; ++r) {
+    if ((st = check(k_prefix[r], P, kvc)) != TP_OK || (st = check(v_prefix[r], P, kvc)) != TP_OK) return st;
+    if ((st = check(k_own[r], batch * cap, kvc)) != TP_OK || (st = check(v_own[r], batch * cap, kvc)) != TP_OK) return st;
+    for (const tp_tensor *w : {weight_in, static_cast<const tp_tensor *>(weight_out)}) {
+      if (!w) continue;
+      if (!view_ok(w[r]) || w[r].rows != batch * (kvc / hd) || w[r].cols != cap) return TP_ERR_INVALID_ARG;
+      if (w[r].dtype != TP_F32) return TP_ERR_DTYPE;
+      if (!ptr_aligned(w[r].ptr, 4)) return TP_ERR_ALIGNMENT;
+    }
+  }
+  if (batch > 0 && !lengths) return TP_ERR_INVALID_ARG;
+  if (!ptr_aligned(lengths, 4)) return TP_ERR_ALIGNMENT;
+  if (!sizes_ok(dims, batch, P, cap)) return TP_ERR_UNSUPPORTED;
+  const bool weights = weight_out && cap > 0;
+  const long long group = dims.num_q_heads / dims.num_kv_heads;
+  const Shape shape = shape_of(batch, group, dims.num_kv_heads, P, cap);
+  const Regions reg = regions_of(shape, batch, dims.num_q_heads, hd, cap, weights);
+  if (batch > 0 && reg.total > 0) {
+    if (!workspace || workspace_bytes < reg.total) return TP_ERR_WORKSPACE;
+    if (!ptr_aligned(workspace, 16)) return TP_ERR_ALIGNMENT;
+  }
+  if ((st = check_rank_health(n)) != TP_OK) return st;
+  if (batch == 0) return TP_OK;
+  DevCtx ctx;
+  const cudaError_t e = get_dev_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e);
+  static thread_local PrefixAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int r = 0; r < n; ++r) {
+    p.q[r] = q[r].ptr;
+    p.q_ld[r] = q[r].ld;
+    p.a[r] = a[r].ptr;
+    p.a_ld[r] = a[r].ld;
+  }
+  for (int r = 0; r < sources; ++r) {
+    if (P > 0) {
+      tp_tensor k = k_prefix[r], v = v_prefix[r];
+      if (P == 1) k.ld = v.ld = (kvc + 7) / 8 * 8;  // the pitch of a single row is free
+      if (!encode_rows_map(&p.k_map[r], k, 128) || !encode_rows_map(&p.v_map[r], v, 128)) return TP_ERR_INVALID_ARG;
+    }
+    p.k_own[r] = k_own[r].ptr;
+    p.v_own[r] = v_own[r].ptr;
+    p.ko_ld[r] = k_own[r].ld;
+    p.vo_ld[r] = v_own[r].ld;
+    if (weights) {
+      p.w_out[r] = static_cast<float *>(weight_out[r].ptr);
+      p.wo_ld[r] = weight_out[r].ld;
+      if (weight_in) {
+        p.w_in[r] = static_cast<const float *>(weight_in[r].ptr);
+        p.wi_ld[r] = weight_in[r].ld;
+      }
+    }
+  }
+  char *ws = static_cast<char *>(workspace);
+  p.lengths = lengths;
+  p.part_o = reinterpret_cast<float *>(ws + reg.o);
+  p.part_ml = reinterpret_cast<float2 *>(ws + reg.ml);
+  p.scores = weights ? reinterpret_cast<float *>(ws + reg.scores) : nullptr;
+  p.batch = static_cast<int>(batch);
+  p.heads_q = dims.num_q_heads;
+  p.heads_kv = dims.num_kv_heads;
+  p.group = static_cast<int>(group);
+  p.heads_per_rank = dims.num_q_heads / n;
+  p.heads_per_source = dims.num_kv_heads / sources;
+  p.d = static_cast<int>(hd);
+  p.prefix = static_cast<int>(P);
+  p.blocks = shape.blocks;
+  p.split_p = shape.split_p;
+  p.pairs = shape.pairs;
+  p.cap = static_cast<int>(cap);
+  p.chunk = shape.chunk;
+  p.split_o = shape.split_o;
+  p.has_prev = p.split_p > 0 && pdl_enabled();
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
+  p.status = ctx.status;
+  p.wait_ns = ctx.wait_ns;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return hd == 128 ? launch_all<128>(p, s) : launch_all<64>(p, s);
+}

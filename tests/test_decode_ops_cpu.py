@@ -140,3 +140,42 @@ def test_linear_refusals(kw, status):
 def test_linear_empty():
     assert linear_status(x=[T(BF, 0, 64, ptr=None)], y=T(BF, 0, 96, ptr=None)) == tp.TP_OK
     assert linear_status(w=[T(BF, 0, 64, ptr=None)], y=T(BF, 4, 0, ptr=None)) == tp.TP_OK
+
+
+# ---- tp_prefix_attn ------------------------------------------------------------------
+def attn_status(plan=PLAN, batch=3, q=None, kp=None, ko=None, vp=None, vo=None, lengths=FAKE, wi=None, wo=None, a=None, ws=FAKE,
+                ws_bytes=1 << 40):
+    q, a = q or T(BF, 3, 256), a or T(BF, 3, 256)
+    kp, ko = kp or T(BF, 50, 128), ko or T(BF, 30, 128)
+    vp, vo = vp or kp, vo or ko
+    two = lambda t: None if t is None else arr(t, t)  # noqa: E731
+    return tp.raw_status("tp_prefix_attn", plan.handle if plan else None, batch, two(q), two(kp), two(vp), two(ko), two(vo),
+                         lengths, two(wi), two(wo), two(a), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(plan=None), "INVALID_ARG"), (dict(batch=-1), "INVALID_ARG"), (dict(lengths=None), "INVALID_ARG"),
+    (dict(lengths=FAKE + 1), "ALIGNMENT"), (dict(q=T(BF, 4, 256)), "INVALID_ARG"), (dict(q=T(BF, 3, 128)), "INVALID_ARG"),
+    (dict(q=T(F32, 3, 256)), "DTYPE"), (dict(a=T(F32, 3, 256)), "DTYPE"), (dict(a=T(BF, 3, 256, 257)), "ALIGNMENT"),
+    (dict(q=T(BF, 3, 256, ptr=FAKE + 2)), "ALIGNMENT"), (dict(kp=T(BF, 50, 64)), "INVALID_ARG"),
+    (dict(vp=T(BF, 49, 128)), "INVALID_ARG"), (dict(ko=T(BF, 31, 128)), "INVALID_ARG"), (dict(vo=T(BF, 33, 128)), "INVALID_ARG"),
+    (dict(kp=T(E4, 50, 128)), "DTYPE"), (dict(ko=T(BF, 30, 128, 130)), "ALIGNMENT"),
+    (dict(wo=T(F32, 3, 9)), "INVALID_ARG"), (dict(wo=T(F32, 4, 10)), "INVALID_ARG"), (dict(wo=T(BF, 3, 10)), "DTYPE"),
+    (dict(wi=T(F32, 3, 10)), "INVALID_ARG"),                       # weights in, none out
+    (dict(wi=T(F32, 3, 10, ptr=FAKE + 2), wo=T(F32, 3, 10)), "ALIGNMENT"),
+    (dict(ws=None), "WORKSPACE"), (dict(ws_bytes=1000), "WORKSPACE"), (dict(ws=FAKE + 8), "ALIGNMENT"),
+])
+def test_attn_refusals(kw, status):
+    assert attn_status(**kw) == getattr(tp, "TP_ERR_" + status)
+
+
+def test_attn_unsupported_empty_and_workspace():
+    odd = tp.tp_plan_create(2, 512, 4, 2, 96, 64)
+    assert attn_status(plan=odd, q=T(BF, 3, 192), a=T(BF, 3, 192), kp=T(BF, 50, 96), ko=T(BF, 30, 96)) == tp.TP_ERR_UNSUPPORTED
+    assert attn_status(batch=0, q=T(BF, 0, 256), a=T(BF, 0, 256), ko=T(BF, 0, 128)) == tp.TP_OK
+    size = tp.tp_prefix_attn_workspace_size
+    assert size(PLAN, 0, 100, 100, True) == 0 and size(PLAN, 4, -1, 0, False) == 0 and size(PLAN, 4, 0, 0, True) == 0
+    assert size(PLAN, 4, 0, 100, True) - size(PLAN, 4, 0, 100, False) == 4 * 4 * 100 * 4  # four q heads' scores, a multiple of 256
+    assert attn_status(ws_bytes=size(PLAN, 3, 50, 10, False) - 1) == tp.TP_ERR_WORKSPACE
+    assert size(PLAN, 1 << 40, 1, 1, False) == 0
+    assert attn_status(batch=1 << 40, q=T(BF, 1 << 30, 256)) == tp.TP_ERR_INVALID_ARG

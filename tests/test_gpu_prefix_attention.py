@@ -1,0 +1,205 @@
+"""tp_prefix_attn against the softmax over prefix and own keys in float64.
+
+Tolerances, from the roundings the call makes (u = 2^-24): a score is a sum of d exact products
+in f32, off by at most (d / 16 + 16) * 2u of the sum of the products' sizes, and its scaling adds
+4u of it; so a softmax weight is off by at most twice the largest score error (its own and the
+normaliser's), plus 2^-18 for the exponentials and the joins of the splits. P is rounded to bf16
+for P V (2^-8 of each p) and the output is rounded once (2^-8). An accumulated weight adds its
+group's weights in f32."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import tensor_sharded_linear_gqa_gb300 as tp
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16 = torch.bfloat16
+
+
+class Case:
+    def __init__(self, tp_size, hq, hkv, d, B, P, C, lens, seed=0, q_std=1.0, views=False):
+        g = torch.Generator(device="cuda").manual_seed(seed * 7919 + B * 31 + P + C)
+        draw = lambda r, c, std=1.0: (torch.randn(r, c, generator=g, device="cuda") * std).to(BF16)  # noqa: E731
+        self.plan = tp.tp_plan_create(tp_size, hq * d, hq, hkv, d, tp_size)
+        self.n, self.s = tp_size, tp_size if hkv >= tp_size else 1
+        self.hq, self.hkv, self.d, self.B, self.P, self.C = hq, hkv, d, B, P, C
+        self.q = draw(B, hq * d, q_std)
+        self.kp, self.vp, self.ko, self.vo = draw(P, hkv * d), draw(P, hkv * d), draw(B * C, hkv * d), draw(B * C, hkv * d)
+        self.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.w = torch.rand(self.s, B * (hkv // self.s), C, generator=g, device="cuda")
+        self.views = views
+
+    def parts(self, t, n):
+        out = list(t.split(t.shape[1] // n, dim=1))
+        return out if self.views else [x.contiguous() for x in out]
+
+    def run(self, weights=True, alias=False, stream=None, first=False):
+        q = self.parts(self.q, self.n)
+        kv = [self.parts(t, self.s) for t in (self.kp, self.vp, self.ko, self.vo)]
+        whole = torch.full_like(self.q, float("nan"))
+        a = list(whole.split(whole.shape[1] // self.n, dim=1)) if self.views else [torch.full_like(x, float("nan")) for x in q]
+        ws = torch.empty(tp.tp_prefix_attn_workspace_size(self.plan, self.B, self.P, self.C, weights), dtype=torch.uint8,
+                         device="cuda")
+        wi = list(self.w.clone())
+        wo = (wi if alias else [torch.full_like(x, float("nan")) for x in wi]) if weights else None
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        tp.tp_prefix_attn(self.plan, q, *kv, self.lens, a, ws, weight_in=wi if weights and not first else None, weight_out=wo,
+                          stream=stream)
+        torch.cuda.synchronize()
+        return torch.cat(a, 1), None if wo is None else torch.stack(wo)
+
+    def check(self, a, w, first=False, skip=()):
+        d, G, hr = self.d, self.hq // self.hkv, self.hkv // self.s
+        for b in range(self.B):
+            n = min(max(int(self.lens[b]), 0), self.C)
+            for h in range(self.hkv):
+                if (b, h) in skip:
+                    continue
+                cols = slice(h * d, (h + 1) * d)
+                own = slice(b * self.C, b * self.C + n)
+                k = torch.cat([self.kp[:, cols], self.ko[own, cols]]).double()
+                v = torch.cat([self.vp[:, cols], self.vo[own, cols]]).double()
+                q = self.q[b].view(self.hq, d)[h * G:(h + 1) * G].double()
+                got = a[b].view(self.hq, d)[h * G:(h + 1) * G].double()
+                if self.P + n == 0:
+                    assert (got == 0).all()
+                    p = torch.zeros(G, 0, dtype=torch.float64, device="cuda")
+                    rel = torch.zeros(G, 1, device="cuda")
+                else:
+                    s = q @ k.t() / d ** 0.5
+                    ds = ((d / 16 + 16) * 2 * U * (q.abs() @ k.abs().t()) / d ** 0.5 + 4 * U * s.abs()).amax(1, keepdim=True)
+                    p = torch.softmax(s, dim=1)
+                    out = p @ v
+                    rel = 2 * ds + 2.0 ** -18
+                    tol = (2.0 ** -8 + rel) * (p @ v.abs()) + 2.0 ** -8 * out.abs()
+                    assert ((got - out).abs() <= 1.02 * tol + 1e-30).all(), (b, h, float(((got - out).abs() - tol).max()))
+                if w is not None:
+                    row = w[h // hr, b * hr + h % hr].double()
+                    ref = p[:, self.P:].sum(0)
+                    tol = (p[:, self.P:] * rel).sum(0) + (G + 2) * U * ref
+                    if not first:
+                        ref = ref + self.w[h // hr, b * hr + h % hr, :n].double()
+                        tol = tol + U * ref
+                    assert ((row[:n] - ref).abs() <= 1.02 * tol + 1e-30).all()
+                    assert (row[n:] == 0).all()
+
+
+SHAPES = [  # tp, Hq, Hkv, d, B, P, C, lengths
+    (1, 1, 1, 128, 1, 1, 1, [0]), (1, 1, 1, 128, 1, 0, 1, [1]), (1, 2, 1, 64, 2, 0, 3, [0, 3]),
+    (1, 4, 4, 128, 3, 127, 0, [0, 0, 0]), (1, 16, 4, 128, 1, 100, 64, [33]), (2, 8, 2, 64, 5, 300, 70, [0, 1, 69, 70, 16]),
+    (4, 8, 4, 128, 3, 129, 200, [200, 63, 65]), (8, 64, 8, 128, 9, 515, 130, [0, 5, 64, 128, 129, 130, 17, 16, 15]),
+    (8, 32, 4, 128, 6, 1024, 40, [1, 2, 3, 38, 39, 40]),   # K/V replicated, a group on two ranks
+    (4, 12, 2, 64, 4, 250, 33, [33, 0, 7, 32]),            # six heads a group, replicated
+    (2, 6, 2, 128, 50, 384, 65, [i % 66 for i in range(50)]),  # three heads a group, two row tiles
+    (1, 40, 2, 128, 2, 130, 600, [600, 513]),              # twenty heads a group: two 16-head tiles
+    (1, 7, 1, 128, 40, 1000, 20, [20 - i % 21 for i in range(40)]),
+    (1, 2, 2, 128, 2, 20000, 1100, [1100, 1023]),          # many splits of both parts
+    (1, 8, 1, 64, 100, 2050, 5, [i % 6 for i in range(100)]),  # 800 rows: four tile pairs
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s[:7])))
+@pytest.mark.parametrize("views", [False, True])
+def test_against_softmax(shape, views):
+    need_gpu()
+    c = Case(*shape, views=views)
+    a, w = c.run()
+    c.check(a, w)
+    assert tp.tp_device_status()[0] == tp.TP_OK
+    a2, w2 = c.run(alias=True)  # weights accumulated in place; the same bits
+    assert torch.equal(a, a2) and torch.equal(w, w2)
+    a3, _ = c.run(weights=False)
+    assert torch.equal(a, a3)
+    a4, w4 = c.run(first=True)
+    assert torch.equal(a, a4)
+    c.check(a4, w4, first=True)
+
+
+@pytest.mark.parametrize("q_std", [4.0, 30.0])
+def test_sharp_scores(q_std):
+    need_gpu()
+    c = Case(2, 16, 2, 128, 4, 700, 150, [150, 0, 77, 64], seed=2, q_std=q_std)
+    c.check(*c.run())
+
+
+def test_block_maxima_that_jump():
+    """Rows whose block maxima rise by tens of log2 units, so the reference maximum lags and then moves."""
+    need_gpu()
+    c = Case(1, 4, 1, 128, 70, 128 * 12, 300, [300 - i for i in range(70)], seed=5)
+    ramp = torch.arange(12, device="cuda").repeat_interleave(128)[:, None] * 1.3
+    c.kp += (ramp * torch.sign(c.q[0, :128].float())).to(BF16)
+    c.ko += (torch.linspace(0, 8, c.B * c.C, device="cuda")[:, None] * torch.sign(c.q[1, :128].float())).to(BF16)
+    c.check(*c.run())
+
+
+def test_stale_rows_past_the_length_do_not_matter():
+    need_gpu()
+    c = Case(1, 8, 2, 128, 4, 60, 90, [0, 13, 64, 90], seed=6)
+    want = c.run()
+    for b, n in enumerate(c.lens.tolist()):
+        c.ko[b * 90 + n:(b + 1) * 90] = float("nan")
+        c.vo[b * 90 + n:(b + 1) * 90] = float("inf")
+        c.w[:, b * 2:(b + 1) * 2, n:] = float("nan")
+    got = c.run()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_a_sequence_with_nan_spoils_only_itself():
+    need_gpu()
+    c = Case(1, 8, 2, 128, 3, 200, 50, [50, 50, 20], seed=7)
+    c.vo[50 + 3, 5] = float("nan")          # sequence 1, kv head 0
+    a, w = c.run()
+    assert torch.isnan(a[1].view(8, 128)[:4, 5].float()).all()
+    c.check(a, w, skip={(1, 0)})
+
+
+def test_bad_lengths_are_clamped_and_reported():
+    need_gpu()
+    for C, lens in ((20, [21, -1]), (0, [0, 4])):
+        c = Case(1, 4, 2, 64, 2, 40, C, lens)
+        a, w = c.run()
+        c.check(a, w)
+        assert tp.tp_device_status()[0] == tp.TP_ERR_BAD_LENGTH
+        assert tp.tp_device_status()[0] == tp.TP_OK
+
+
+def test_other_stream_and_captured_graph():
+    need_gpu()
+    c = Case(2, 8, 2, 128, 6, 300, 40, [0, 3, 40, 20, 17, 16], seed=9)
+    want = c.run()
+    side = torch.cuda.Stream()
+    got = c.run(stream=side)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    q = c.parts(c.q, 2)
+    kv = [c.parts(t, 2) for t in (c.kp, c.vp, c.ko, c.vo)]
+    a = [torch.zeros_like(x) for x in q]
+    ws = torch.empty(tp.tp_prefix_attn_workspace_size(c.plan, c.B, c.P, c.C, False), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tp.tp_prefix_attn(c.plan, q, *kv, c.lens, a, ws)
+    for _ in range(3):
+        for x in a:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(torch.cat(a, 1), want[0])
+
+
+def test_eviction_reads_the_accumulated_weights():
+    need_gpu()
+    c = Case(2, 8, 2, 128, 3, 100, 64, [64, 50, 10], seed=11)
+    a, w = c.run()
+    kv = [c.parts(t, 2) for t in (c.ko, c.vo)]
+    kept = torch.empty(2, 3, 32, dtype=torch.int32, device="cuda")
+    lens = c.lens.clone()
+    before = [t.clone() for t in kv[0]]
+    wl = list(w)
+    tp.tp_cache_evict(c.plan, lens, kv[0], kv[1], wl, 32, 2, 8, kv[0], kv[1], wl, lens, kept)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [32, 32, 10]
+    for s in range(2):
+        at = kept[s, 1].long()
+        assert torch.equal(kv[0][s][64:96], before[s][64 + at])

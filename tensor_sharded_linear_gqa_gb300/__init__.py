@@ -16,6 +16,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtpgqa.so")
@@ -80,6 +82,7 @@ class TPError(RuntimeError):
 _P = ctypes.POINTER
 _T = _P(TpTensor)
 _S = ctypes.c_void_p  # cudaStream_t
+_A = ctypes.c_void_p
 _SIGS = {
     "tp_plan_create": ([_P(TpDims), _P(ctypes.c_void_p)], ctypes.c_int),
     "tp_plan_destroy": ([ctypes.c_void_p], ctypes.c_int),
@@ -113,15 +116,14 @@ _SIGS = {
     "tp_qkv_proj": ([ctypes.c_void_p, _T, _T, _T, _T, _T, _T, _T, _S], ctypes.c_int),
     "tp_attn_proj": ([ctypes.c_void_p, _T, _T, _T, _T, _T, _T, _T, _T, _T, _T, ctypes.c_int32,
                       _S], ctypes.c_int),
-    "tp_add_rmsnorm": ([ctypes.c_int32, _T, _T, _T, ctypes.c_float, _T, _T, ctypes.c_void_p, _S], ctypes.c_int),
-    "tp_linear_epilogue": ([ctypes.c_int32, ctypes.c_int32, _T, ctypes.c_void_p, _T, ctypes.c_void_p, _T, ctypes.c_int32,
-                            _T, _T, _S], ctypes.c_int),
-    "tp_prefix_attn_workspace_size": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32],
+    # descriptors by address: an arr(), byref() or the address of packed ones
+    "tp_add_rmsnorm": ([ctypes.c_int32, _A, _A, _A, ctypes.c_float, _A, _A, _A, _S], ctypes.c_int),
+    "tp_linear_epilogue": ([ctypes.c_int32, ctypes.c_int32, _A, _A, _A, _A, _A, ctypes.c_int32, _A, _A, _S], ctypes.c_int),
+    "tp_prefix_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32],
                                       ctypes.c_size_t),
-    "tp_prefix_attn": ([ctypes.c_void_p, ctypes.c_int64, _T, _T, _T, _T, _T, ctypes.c_void_p, _T, _T, _T, ctypes.c_void_p,
-                        ctypes.c_size_t, _S], ctypes.c_int),
-    "tp_cache_evict": ([ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, _T, _T, _T, ctypes.c_int32, ctypes.c_int32,
-                        ctypes.c_int32, _T, _T, _T, ctypes.c_void_p, ctypes.c_void_p, _S], ctypes.c_int),
+    "tp_prefix_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _A, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
+    "tp_cache_evict": ([_A, ctypes.c_int64, _A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _A, _A, _A, _A,
+                        _A, _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "tp_last_cuda_error": ([], ctypes.c_int32),
     "tp_set_rank_health": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_int),
@@ -151,6 +153,7 @@ class _Lib:
                 f = getattr(cdll, n)
                 f.argtypes = args
                 f.restype = res
+                setattr(self, n, f)  # found directly from now on
             self._cdll = cdll
         return getattr(self._cdll, name)
 
@@ -170,46 +173,89 @@ def _check(status: int, where: str) -> None:
 
 
 # ---- marshalling ------------------------------------------------------------
+# A descriptor is packed straight into the argument's buffer: building it field by
+# field through ctypes costs about as long as the rest of a small call.
+_DESC = struct.Struct("=Qiiqqq")
+_DTYPES: dict = {}
+
+
+def _dtypes() -> dict:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3})
+    return _DTYPES
+
+
+def _fields(t) -> tuple:
+    """(ptr, dtype, reserved, rows, cols, ld) of a TpTensor or a 2-D CUDA torch tensor."""
+    if isinstance(t, TpTensor):
+        return t.ptr or 0, t.dtype, t.reserved, t.rows, t.cols, t.ld
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("expected a 2-D tensor")
+    rows, cols = shape
+    ld, step = t.stride()
+    dt = (_DTYPES or _dtypes()).get(t.dtype)
+    if rows and cols:
+        if step != 1:
+            raise ValueError("expected unit stride along columns")
+        if dt is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        return t.data_ptr(), dt, 0, rows, cols, ld if rows > 1 else max(ld, cols)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return 0, dt, 0, rows, cols, ld if rows > 1 else max(ld, cols, 1)
+
+
 def tensor(t) -> TpTensor:
     """TpTensor view of a 2-D CUDA torch tensor with unit column stride (or a TpTensor)."""
     if isinstance(t, TpTensor):
         return t
-    import torch
-    if t.dim() != 2:
-        raise ValueError("expected a 2-D tensor")
-    if t.numel() > 0 and t.stride(1) != 1:
-        raise ValueError("expected unit stride along columns")
-    if t.dtype == torch.float32:
-        dt = TP_F32
-    elif t.dtype == torch.bfloat16:
-        dt = TP_BF16
-    elif t.dtype == torch.float8_e4m3fn:
-        dt = TP_E4M3
-    else:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.numel() > 0 and not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1], 1)
-    return TpTensor(t.data_ptr() if t.numel() > 0 else None, dt, 0, t.shape[0], t.shape[1], ld)
+    return TpTensor(*_fields(t))
+
+
+_ARRAYS: dict = {}  # array type by length
 
 
 def _arr(seq):
     if isinstance(seq, ctypes.Array):  # an arr() the caller keeps
         return seq
-    seq = list(seq)
-    a = (TpTensor * max(len(seq), 1))()
-    for i, t in enumerate(seq):
-        a[i] = tensor(t)
-    return a
+    if not isinstance(seq, (list, tuple)):
+        seq = list(seq)
+    n = len(seq)
+    kind = _ARRAYS.get(n)
+    if kind is None:
+        kind = _ARRAYS[n] = TpTensor * max(n, 1)
+    buf = bytearray(_DESC.size * max(n, 1))
+    at = 0
+    for t in seq:
+        _DESC.pack_into(buf, at, *_fields(t))
+        at += _DESC.size
+    return kind.from_buffer(buf)
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """The current torch stream's handle, by the binding's own accessor where torch has it
+    (torch.cuda.current_stream() builds a Stream object for it first)."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.current_stream()  # initialises CUDA
+    if raw is not None and device is not None:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
 
 
 # ---- plan -----------------------------------------------------------------------
@@ -350,8 +396,14 @@ def tp_moe_workspace_size(dims: TpMoeDims, tokens: int) -> int:
     return int(_lib.tp_moe_workspace_size(ctypes.byref(dims), tokens))
 
 
+_DTYPE_NAMES: dict = {}  # str(dtype) by dtype: formatting it costs more than the rest of the check
+
+
 def _dev_ptr(t, dtype: str) -> int:
-    if str(t.dtype) != dtype or not t.is_contiguous():
+    name = _DTYPE_NAMES.get(t.dtype)
+    if name is None:
+        name = _DTYPE_NAMES[t.dtype] = str(t.dtype)
+    if name != dtype or not t.is_contiguous():
         raise TypeError(f"expected a contiguous {dtype} tensor")
     return t.data_ptr() if t.numel() else 0
 
@@ -420,77 +472,132 @@ def tp_attn_proj(plan: Plan, x, w_q, w_k, w_v, q, k, v, a, w_o, y, combine: int,
 
 
 # ---- between the projections ----------------------------------------------------
-def _opt(t):
-    """Pointer to a TpTensor, or None."""
-    return None if t is None else ctypes.byref(tensor(t))
+class _Scratch(threading.local):
+    """Descriptors of the call being made, one buffer per thread (the library reads them during the
+    call only): a small call spends less time on its kernels than on building ctypes objects."""
+
+    def __init__(self):
+        self.room = 0
+        self.grow(256)
+
+    def grow(self, room: int) -> None:
+        self.buf = bytearray(_DESC.size * room)
+        self.base = ctypes.addressof((ctypes.c_char * len(self.buf)).from_buffer(self.buf))
+        self.room, self.used = room, 0
 
 
-def _row(t):
-    """A 1-D tensor as the [1 x n] view the library takes."""
-    return t if isinstance(t, TpTensor) or t.dim() == 2 else t.unsqueeze(0)
+_scratch = _Scratch()
+
+
+class _Args:
+    """Packs one call's tensors: each method returns the address of what it packed."""
+
+    __slots__ = ("s",)
+
+    def __init__(self, most: int):
+        self.s = s = _scratch
+        s.used = 0
+        if most > s.room:
+            s.grow(most)
+
+    def many(self, seq, n: int):
+        """A per-rank argument with at least n entries; an arr() the caller keeps goes as it is."""
+        if isinstance(seq, ctypes.Array):
+            if len(seq) < n:
+                raise ValueError(f"expected {n} tensors, one per rank or kv source")
+            return seq
+        if len(seq) < n:
+            raise ValueError(f"expected {n} tensors, one per rank or kv source")
+        s = self.s
+        first = at = s.used * _DESC.size
+        for i in range(n):
+            _DESC.pack_into(s.buf, at, *_fields(seq[i]))
+            at += _DESC.size
+        s.used += n
+        return s.base + first
+
+    def one(self, t):
+        """A single descriptor; None for None."""
+        if t is None:
+            return None
+        s = self.s
+        at = s.used * _DESC.size
+        _DESC.pack_into(s.buf, at, *_fields(t))
+        s.used += 1
+        return s.base + at
+
+    def row(self, t):
+        """A vector: its 1-D tensor is the [1 x n] view that the library takes."""
+        return self.one(t if t is None or isinstance(t, TpTensor) or t.dim() == 2 else t.unsqueeze(0))
+
+
+def _opt_ptr(t, dtype: str):
+    return None if t is None else _dev_ptr(t, dtype)
 
 
 def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=None, stream=None) -> None:
     """z = sum of x (one tensor or a list of per-rank partials) + residual, to residual_out;
     y = z * rsqrt(mean(z^2) + eps) * weight, in bf16, or as e4m3 codes with y_scale [T]."""
-    xs = _arr(x if isinstance(x, (list, tuple, ctypes.Array)) else [x])
-    n = len(x) if isinstance(x, (list, tuple)) else len(xs)
-    _check(_lib.tp_add_rmsnorm(n, xs, _opt(residual), _opt(_row(weight)), eps, _opt(residual_out), _opt(y),
-                               None if y_scale is None else _dev_ptr(y_scale, "torch.float32"), _stream(stream)),
-           "tp_add_rmsnorm")
+    many = isinstance(x, (list, tuple, ctypes.Array))
+    n = len(x) if many else 1
+    a = _Args(n + 4)
+    st = _lib.tp_add_rmsnorm(n, a.many(x, n) if many else a.one(x), a.one(residual), a.row(weight), eps,
+                             a.one(residual_out), a.one(y), _opt_ptr(y_scale, "torch.float32"), _stream(stream))
+    if st:
+        raise TPError(st, "tp_add_rmsnorm")
 
 
 def tp_linear_epilogue(tp_size: int, shard: int, x, w, y, bias=None, activation: int = TP_ACT_NONE, residual=None,
                        x_scale=None, w_scale=None, stream=None) -> None:
     """y = activation(x w^T * x_scale * w_scale + bias) + residual. shard: TP_SHARD_COLUMN (x: [X],
     w: the ranks' weight rows) or TP_SHARD_ROW (x, w: the ranks' slices of the input features)."""
-    _check(_lib.tp_linear_epilogue(tp_size, shard, _sources(x, tp_size if shard == TP_SHARD_ROW else 1),
-                                   None if x_scale is None else _dev_ptr(x_scale, "torch.float32"), _sources(w, tp_size),
-                                   None if w_scale is None else _dev_ptr(w_scale, "torch.float32"),
-                                   None if bias is None else _opt(_row(bias)), activation, _opt(residual), _opt(y),
-                                   _stream(stream)), "tp_linear_epilogue")
+    a = _Args(2 * tp_size + 3 if tp_size > 0 else 3)
+    st = _lib.tp_linear_epilogue(tp_size, shard, a.many(x, tp_size if shard == TP_SHARD_ROW else 1),
+                                 _opt_ptr(x_scale, "torch.float32"), a.many(w, tp_size), _opt_ptr(w_scale, "torch.float32"),
+                                 a.row(bias), activation, a.one(residual), a.one(y), _stream(stream))
+    if st:
+        raise TPError(st, "tp_linear_epilogue")
 
 
 def tp_prefix_attn_workspace_size(plan: Plan, batch: int, prefix: int, capacity: int, weights: bool) -> int:
     return int(_lib.tp_prefix_attn_workspace_size(plan.handle, batch, prefix, capacity, int(weights)))
 
 
+def _kv_sources(plan: Plan) -> int:
+    return 1 if plan.dims.num_kv_heads < plan.dims.tp_size else plan.dims.tp_size
+
+
 def tp_prefix_attn(plan: Plan, q, k_prefix, v_prefix, k_own, v_own, lengths, a, workspace, weight_in=None, weight_out=None,
                    stream=None) -> None:
     """One new token per sequence over the shared prefix and the sequence's own cache. q, a: one
     entry per rank; caches and weights: one per kv source; workspace: a CUDA byte tensor."""
-    n, sources = plan.tp_size, 1 if plan.dims.num_kv_heads < plan.tp_size else plan.tp_size
-    _check(_lib.tp_prefix_attn(plan.handle, lengths.numel(), _sources(q, n), _sources(k_prefix, sources),
-                               _sources(v_prefix, sources), _sources(k_own, sources), _sources(v_own, sources),
-                               _dev_ptr(lengths, "torch.int32"), None if weight_in is None else _sources(weight_in, sources),
-                               None if weight_out is None else _sources(weight_out, sources), _sources(a, n),
-                               workspace.data_ptr(), workspace.numel(), _stream(stream)), "tp_prefix_attn")
+    n, src = plan.dims.tp_size, _kv_sources(plan)
+    g = _Args(2 * n + 6 * src)
+    st = _lib.tp_prefix_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_prefix, src), g.many(v_prefix, src),
+                             g.many(k_own, src), g.many(v_own, src), _dev_ptr(lengths, "torch.int32"),
+                             None if weight_in is None else g.many(weight_in, src),
+                             None if weight_out is None else g.many(weight_out, src), g.many(a, n), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(stream))
+    if st:
+        raise TPError(st, "tp_prefix_attn")
 
 
 def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int, n_recent: int, k_out, v_out, weight_out,
                    lengths_out, kept, stream=None) -> None:
     """Keeps `budget` positions of every sequence and kv head: the first n_first, the last
     n_recent and the heaviest between. k, v, weight and their outputs: one entry per kv source."""
-    batch = lengths.numel()
-    sources = 1 if plan.dims.num_kv_heads < plan.tp_size else plan.tp_size
-    rows = kept.numel() // max(budget, 1)
-    if rows * budget != kept.numel() or rows != batch * (plan.dims.num_kv_heads if sources == 1 else
-                                                         sources * (plan.dims.num_kv_heads // sources)):
+    batch, src = lengths.numel(), _kv_sources(plan)
+    if kept.numel() != batch * plan.dims.num_kv_heads * budget:
         raise ValueError("kept must hold sources * batch * heads * budget entries")
     if lengths_out.numel() != batch:
         raise ValueError("lengths_out must have one entry per sequence")
-    arrays = [_sources(a, sources) for a in (k, v, weight, k_out, v_out, weight_out)]
-    _check(_lib.tp_cache_evict(plan.handle, batch, _dev_ptr(lengths, "torch.int32"), arrays[0], arrays[1], arrays[2], budget,
-                               n_first, n_recent, arrays[3], arrays[4], arrays[5], _dev_ptr(lengths_out, "torch.int32"),
-                               _dev_ptr(kept, "torch.int32"), _stream(stream)), "tp_cache_evict")
-
-
-def _sources(seq, n: int):
-    """_arr of a per-rank argument, with at least n entries."""
-    a = _arr(seq)
-    if len(a) < n or (not isinstance(seq, ctypes.Array) and len(seq) < n):
-        raise ValueError(f"expected {n} tensors, one per rank or kv source")
-    return a
+    a = _Args(6 * src)
+    st = _lib.tp_cache_evict(plan.handle, batch, _dev_ptr(lengths, "torch.int32"), a.many(k, src), a.many(v, src),
+                             a.many(weight, src), budget, n_first, n_recent, a.many(k_out, src), a.many(v_out, src),
+                             a.many(weight_out, src), _dev_ptr(lengths_out, "torch.int32"), _dev_ptr(kept, "torch.int32"),
+                             _stream(stream))
+    if st:
+        raise TPError(st, "tp_cache_evict")
 
 
 # ---- status and diagnostics ---------------------------------------------------

@@ -103,8 +103,18 @@ def test_evict_unsupported_and_empty():
     odd = tp.tp_plan_create(1, 60, 1, 1, 60, 4)  # a head of 120 bytes
     assert evict_status(plan=odd, cols=60) == tp.TP_ERR_UNSUPPORTED
     assert evict_status(batch=0, rows=0, rows_out=0, w_rows=0, w_cols=0, wo_cols=0) == tp.TP_OK
+
+
+def test_binding_counts_its_per_rank_arguments():
     with pytest.raises(ValueError):
-        tp._sources([], 2)
+        tp.tp_linear_epilogue(2, tp.TP_SHARD_COLUMN, [T(BF, 4, 64)], [T(BF, 8, 64)], T(BF, 4, 16))
+    with pytest.raises(ValueError):
+        tp.tp_linear_epilogue(2, tp.TP_SHARD_ROW, arr(T(BF, 4, 64)), arr(*[T(BF, 8, 64)] * 2), T(BF, 4, 8), stream=1)
+    with pytest.raises(tp.TPError):  # enough of them, and the library refuses the shapes
+        tp.tp_linear_epilogue(2, tp.TP_SHARD_COLUMN, [T(BF, 4, 64)], [T(BF, 8, 64)] * 2, T(BF, 4, 17), stream=1)
+    many = [T(BF, 4, 64)] * 400  # more than the scratch holds at first
+    with pytest.raises(tp.TPError):
+        tp.tp_add_rmsnorm(many, None, T(BF, 1, 64), 1e-5, None, T(BF, 4, 64), stream=1)
 
 
 # ---- tp_linear_epilogue ------------------------------------------------------------

@@ -16,9 +16,18 @@
 //                   SMs split K over a cluster; the f32 partials are summed through
 //                   distributed shared memory in rank order, so results repeat.
 //   k_linear_pair   many tokens. Bound by the tensor cores: persistent SM pairs on
-//                   256 x 256 tiles (cta_group::2), two accumulators in TMEM, so
-//                   the epilogue of a tile runs under the products of the next.
-// Warp roles in both: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-5 are
+//                   tiles of 256 tokens x BN features (cta_group::2). The tile's sum
+//                   lives in the epilogue warps' registers, so both accumulators
+//                   in TMEM stay with the MMAs, under which the whole epilogue runs.
+//
+// The tensor core truncates where it adds a step's products into the f32
+// accumulator: an error of one sign that grows with the steps. So no accumulator
+// runs for more than kChunkSteps steps (1024 bf16 or 2048 e4m3 values of K) where
+// TMEM has room: k_linear_pair's epilogue adds each chunk to the sum in registers,
+// k_linear_split gives each chunk its own columns and adds them at the end, both
+// rounding to nearest. Over K = 8192 in bf16 this takes the error of an f32
+// output, relative to its size, from 8e-6 to about 1e-6.
+// Warp roles in both: warp 0 loads (TMA), warp 1 issues the MMAs, the others are
 // the epilogue. Every wait is bounded, as in the grouped GEMM.
 #include <cstdlib>
 #include <cstring>
@@ -32,27 +41,34 @@ namespace {
 
 using namespace op;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;       // k_linear_split
+constexpr int kChunkSteps = 64;     // MMA steps (32 bytes of K each) of one accumulator
 constexpr int kMaxParts = 16;  // weight shards (column) or K slices (row)
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kWTile = 128 * 128;  // bytes of one 128-row, 128-byte-wide box
 
+// The scalars come first and lie together: a kernel's first read of each 64-byte
+// line of its parameters is a miss of a few hundred nanoseconds.
 struct LinearParams {
-  CUtensorMap x[kMaxParts];  // one per K slice
-  CUtensorMap w[kMaxParts];  // one per K slice, or one per weight shard
-  int k_tiles[kMaxParts];    // 128-byte-wide k-tiles of each slice
-  int n[kMaxParts];          // output features of each shard
-  int n_tile0[kMaxParts];    // its first feature tile
-  long long col0[kMaxParts];  // its first output column
+  int tok_tile, stages, sub, split;  // k_linear_split: token tile, stages, k-tiles a stage, CTAs sharing K
+  int regions, region_cols;          // its accumulators in TMEM and their stride
+  int early_w;                       // W loads before the dependency wait
   int n_slices, n_shards, kt_total, n_tiles, rows, m_tiles;
   int act, y_f32, res_f32, bias_f32;
   const float *x_scale, *w_scale;  // null: no scales
   const void *bias, *res;          // null: none
   void *y;
   long long y_ld, res_ld;
-  int tok_tile, stages, split, early_w;
   int *status;
   long long wait_ns;
+  struct {
+    int n;       // output features of a shard
+    int tile0;   // its first feature tile
+    long long col0;  // its first output column
+  } shard[kMaxParts];
+  int k_tiles[kMaxParts];    // 128-byte-wide k-tiles of each K slice
+  CUtensorMap w[kMaxParts];  // one per K slice, or one per weight shard
+  CUtensorMap x[kMaxParts];  // one per K slice
 };
 
 __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
@@ -60,7 +76,7 @@ __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status
 // Shard of a feature tile (shards are laid out in tile order).
 __device__ __forceinline__ int shard_of(const LinearParams &p, int nt) {
   int s = 0;
-  while (s + 1 < p.n_shards && nt >= p.n_tile0[s + 1]) ++s;
+  while (s + 1 < p.n_shards && nt >= p.shard[s + 1].tile0) ++s;
   return s;
 }
 
@@ -80,97 +96,162 @@ __device__ __forceinline__ void activate(float (&f)[N], int act) {
   }
 }
 
-// Four neighbouring features of one token: acc -> y. col: output column (bias, scales, y, residual).
-__device__ __forceinline__ void finish4(const LinearParams &p, long long tok, long long col, int left, float (&f)[4]) {
-  if (p.w_scale) {
-    const float sx = __ldg(p.x_scale + tok);
+// N neighbouring values of a row of f32 or bf16 as f32; `left` of them exist, the
+// rest read as 0. Whole groups are aligned for vector loads.
+template <int N>
+__device__ __forceinline__ void load_row(const void *base, bool f32, long long at, int left, float (&v)[N]) {
+  if (f32) {
+    const float *r = static_cast<const float *>(base) + at;
+    if (left >= N) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) f[i] *= sx * __ldg(p.w_scale + col + i);
-  }
-  if (p.bias) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left)
-        f[i] += p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + col + i)
-                           : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[col + i]);
-  }
-  activate(f, p.act);
-  if (p.res) {
-    const long long at = tok * p.res_ld + col;
-    if (p.res_f32) {
-      const float *r = static_cast<const float *>(p.res) + at;
-      if (left >= 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(r);
-        f[0] += v.x; f[1] += v.y; f[2] += v.z; f[3] += v.w;
-      } else {
-        for (int i = 0; i < left; ++i) f[i] += r[i];
+      for (int i = 0; i < N; i += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(r + i);
+        v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
       }
     } else {
-      const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(p.res) + at;
-      if (left >= 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(r);
-        f[0] += bf16_lo(v.x); f[1] += bf16_hi(v.x); f[2] += bf16_lo(v.y); f[3] += bf16_hi(v.y);
-      } else {
-        for (int i = 0; i < left; ++i) f[i] += __bfloat162float(r[i]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = i < left ? r[i] : 0.f;
+    }
+  } else {
+    const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(base) + at;
+    if (left >= N) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(r + i);
+        v[i] = bf16_lo(w.x); v[i + 1] = bf16_hi(w.x); v[i + 2] = bf16_lo(w.y); v[i + 3] = bf16_hi(w.y);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = i < left ? __bfloat162float(r[i]) : 0.f;
     }
   }
-  const long long at = tok * p.y_ld + col;
-  if (p.y_f32) {
-    float *y = static_cast<float *>(p.y) + at;
-    if (left >= 4) *reinterpret_cast<float4 *>(y) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      for (int i = 0; i < left; ++i) y[i] = f[i];
+}
+template <int N>
+__device__ __forceinline__ void store_row(void *base, bool f32, long long at, int left, const float (&v)[N]) {
+  if (f32) {
+    float *r = static_cast<float *>(base) + at;
+    if (left >= N) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(r + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) r[i] = v[i];
+    }
   } else {
-    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + at;
-    if (left >= 4) *reinterpret_cast<uint2 *>(y) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-    else
-      for (int i = 0; i < left; ++i) y[i] = __float2bfloat16_rn(f[i]);
+    __nv_bfloat16 *r = static_cast<__nv_bfloat16 *>(base) + at;
+    if (left >= N) {
+      if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+          *reinterpret_cast<uint4 *>(r + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                                                         pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<uint2 *>(r + i) = make_uint2(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) r[i] = __float2bfloat16_rn(v[i]);
+    }
   }
+}
+
+// Scale of the weight's feature and bias at output column c; 1 and 0 where there is none.
+__device__ __forceinline__ float2 column_terms(const LinearParams &p, long long c, bool there) {
+  float2 t = make_float2(1.f, 0.f);
+  if (there) {
+    if (p.w_scale) t.x = __ldg(p.w_scale + c);
+    if (p.bias)
+      t.y = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + c)
+                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[c]);
+  }
+  return t;
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens: features on the MMA's M, tokens on its N, K split over a cluster.
 // ---------------------------------------------------------------------------
 template <bool F8>
-__global__ void __launch_bounds__(kThreads, 1) k_linear_split(const __grid_constant__ LinearParams p) {
+__global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_constant__ LinearParams p) {
   constexpr int kElems = F8 ? 128 : 64;  // values of a 128-byte box row
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const int S = p.stages, NT = p.tok_tile;
-  const uint32_t stage_bytes = kWTile + static_cast<uint32_t>(NT) * 128u;
+  const int S = p.stages, NT = p.tok_tile, U = p.sub;
+  const uint32_t tile_bytes = kWTile + static_cast<uint32_t>(NT) * 128u;
+  const uint32_t stage_bytes = static_cast<uint32_t>(U) * tile_bytes;
   const uint32_t sbase = ptx::smem_addr(smem);
-  auto w_slot = [&](int st) { return sbase + static_cast<uint32_t>(st) * stage_bytes; };
-  auto x_slot = [&](int st) { return w_slot(st) + kWTile; };
-  uint8_t *bar_area = smem + static_cast<uint32_t>(S) * stage_bytes;
+  auto w_slot = [&](int st, int j) { return sbase + static_cast<uint32_t>(st) * stage_bytes + static_cast<uint32_t>(j) * tile_bytes; };
+  auto x_slot = [&](int st, int j) { return w_slot(st, j) + kWTile; };
+  uint8_t *bar_area = smem + max(static_cast<uint32_t>(S) * stage_bytes, static_cast<uint32_t>(NT) * 512u);
   const uint32_t bar0 = ptx::smem_addr(bar_area);
   auto full_bar = [&](int i) { return bar0 + 8u * i; };
   auto empty_bar = [&](int i) { return bar0 + 8u * (S + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * S);
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 8 * (2 * S + 1));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 8 * (2 * S + 1) + 4);
+  float *s_scale = reinterpret_cast<float *>(bar_area + 8 * (2 * S + 2));  // [token]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
   const int tile = blockIdx.x / p.split;
   const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;  // token tiles of one feature tile are neighbours
   const int shard = shard_of(p, nt);
-  const int feat0 = (nt - p.n_tile0[shard]) * 128;  // within the shard
+  const int feat0 = (nt - p.shard[shard].tile0) * 128;  // within the shard
   const int kb0 = static_cast<int>(static_cast<long long>(p.kt_total) * part / p.split);
   const int kb1 = static_cast<int>(static_cast<long long>(p.kt_total) * (part + 1) / p.split);
-  uint32_t tmem_cols = 32;
-  while (tmem_cols < static_cast<uint32_t>(NT)) tmem_cols *= 2;
+  const uint32_t tmem_cols = static_cast<uint32_t>(p.regions * p.region_cols);
+  const int nkb = kb1 - kb0, n_stages = (nkb + U - 1) / U;
+  const int per_region = (n_stages + p.regions - 1) / p.regions;  // stages of an accumulator
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(full_bar(i), 1);
-      ptx::mbar_init(empty_bar(i), 1);
+  // The loading thread's cursors over the k-tiles, (slice, k-tile in it), of W and of X.
+  struct Cursor {
+    int sl, kt;
+  };
+  auto next = [&](Cursor &c) {
+    if (++c.kt == p.k_tiles[c.sl]) {
+      c.kt = 0;
+      ++c.sl;
     }
-    ptx::mbar_init(done_bar, 1);
-    *abort_flag = 0;
-    ptx::fence_barrier_init();
+  };
+  Cursor wc = {0, kb0};
+  while (wc.kt >= p.k_tiles[wc.sl]) wc.kt -= p.k_tiles[wc.sl++];
+  Cursor xc = wc;
+  int pre = 0;
+  // the W (or X) boxes of one stage; neighbouring k-tiles of a row are one 128 * U byte run in memory
+  // One thread issues every load and one every MMA, so their loops hold no division:
+  // a remainder by the run-time stage count costs as much as the rest of a step.
+  auto load_w = [&](int st, int n, bool issue) {
+    if (issue) ptx::mbar_arrive_expect_tx(full_bar(st), static_cast<uint32_t>(n) * kWTile);
+    uint32_t dst = w_slot(st, 0);
+    for (int j = 0; j < n; ++j, next(wc), dst += tile_bytes)
+      if (issue) ptx::tma_load_2d(dst, &p.w[p.n_shards > 1 ? shard : wc.sl], wc.kt * kElems, feat0, full_bar(st));
+  };
+  auto load_x = [&](int st, int n, bool issue) {
+    if (issue) ptx::mbar_arrive_expect_tx(full_bar(st), static_cast<uint32_t>(n) * (tile_bytes - kWTile));
+    uint32_t dst = x_slot(st, 0);
+    for (int j = 0; j < n; ++j, next(xc), dst += tile_bytes)
+      if (issue) ptx::tma_load_2d(dst, &p.x[xc.sl], xc.kt * kElems, mt * NT, full_bar(st));
+  };
+  if (warp == 0) {
+    const bool leader = ptx::elect_one();
+    if (leader) {
+      for (int i = 0; i < S; ++i) {
+        ptx::mbar_init(full_bar(i), 2);  // W's and X's loading warps
+        ptx::mbar_init(empty_bar(i), 1);
+      }
+      ptx::mbar_init(done_bar, 1);
+      *abort_flag = 0;
+      ptx::fence_barrier_init();
+      ptx::fence_proxy_async_smem();
+    }
+    // W does not come from the previous kernel: its first stages start before the
+    // grid-dependency wait and before anything else of this CTA.
+    if (p.early_w)
+      for (; pre < S && pre < n_stages; ++pre) load_w(pre, min(U, nkb - pre * U), leader);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t *>(tmem_slot)), tmem_cols);
@@ -180,80 +261,81 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_split(const __grid_const
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
-    // k-tile kb of the whole K range -> (slice, k-tile in it)
-    auto seek = [&](int kb, int &sl, int &kt) {
-      sl = 0;
-      kt = kb;
-      while (kt >= p.k_tiles[sl]) kt -= p.k_tiles[sl++];
-    };
-    auto load_w = [&](int st, int sl, int kt) {
-      ptx::tma_load_2d(w_slot(st), &p.w[p.n_shards > 1 ? shard : sl], kt * kElems, feat0, full_bar(st));
-    };
-    // W does not come from the previous kernel: its first stages start before
-    // the grid-dependency wait, each barrier already expecting the X bytes.
-    int pre = 0;
-    if (p.early_w) {
-      int sl, kt;
-      seek(kb0, sl, kt);
-      for (; pre < S && kb0 + pre < kb1; ++pre) {
-        ptx::mbar_arrive_expect_tx(full_bar(pre), stage_bytes);
-        load_w(pre, sl, kt);
-        if (++kt == p.k_tiles[sl]) {
-          kt = 0;
-          ++sl;
-        }
+  // Warp 0 loads W, warp 2 loads X; the other warps fetch the tokens' scales. A warp
+  // walks its stages converged and one lane issues: with a branch on the lane index
+  // around the whole walk an issue took about 300 ns, which set the kernel's pace.
+  if (warp == 0 || warp == 2) {
+    const bool leader = ptx::elect_one();
+    int st = 0;
+    uint32_t parity = 1;  // of the stage's empty barrier
+    for (int i = 0, left_k = nkb; i < n_stages; ++i, left_k -= U) {
+      const int n = min(U, left_k);
+      if (i >= S && !__all_sync(0xffffffffu, ptx::mbar_wait(empty_bar(st), parity, p.wait_ns))) {
+        record(p.status, kDevTimeoutProducer);
+        *abort_flag = 1;
+        break;
+      }
+      if (warp == 2) load_x(st, n, leader);
+      else if (i >= pre) load_w(st, n, leader);
+      if (++st == S) {
+        st = 0;
+        parity ^= 1;
       }
     }
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    int sl, kt;
-    seek(kb0, sl, kt);
-    for (int i = 0; kb0 + i < kb1; ++i) {
-      const int st = i % S;
-      if (i >= pre) {
-        if (*abort_flag) break;
-        if (!ptx::mbar_wait(empty_bar(st), ((i / S) & 1) ^ 1, p.wait_ns)) {
-          record(p.status, kDevTimeoutProducer);
-          *abort_flag = 1;
-          break;
-        }
-        ptx::mbar_arrive_expect_tx(full_bar(st), stage_bytes);
-        load_w(st, sl, kt);
-      }
-      ptx::tma_load_2d(x_slot(st), &p.x[sl], kt * kElems, mt * NT, full_bar(st));
-      if (++kt == p.k_tiles[sl]) {
-        kt = 0;
-        ++sl;
-      }
+  } else if (warp >= 3) {
+    for (int t = threadIdx.x - 96; t < NT; t += kThreads - 96) {
+      const long long tok = static_cast<long long>(mt) * NT + t;
+      s_scale[t] = p.x_scale && tok < p.rows ? __ldg(p.x_scale + tok) : 1.f;
     }
-  } else {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
   }
-  if (warp == 1 && lane == 0) {
+  if (warp == 1) {  // the whole warp walks the stages, one lane issues
     const uint32_t idesc = F8 ? ptx::idesc_e4m3_f32(128, NT) : ptx::idesc_bf16_f32(128, NT);
-    for (int i = 0; kb0 + i < kb1; ++i) {
-      const int st = i % S;
-      if (*abort_flag) break;
-      if (!ptx::mbar_wait(full_bar(st), (i / S) & 1, p.wait_ns)) {
+    const bool leader = ptx::elect_one();
+    int st = 0, in_region = 0;
+    uint32_t parity = 0, d = tmem;
+    for (int i = 0, left_k = nkb; i < n_stages; ++i, left_k -= U) {
+      const int n = min(U, left_k);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(full_bar(st), parity, p.wait_ns))) {
         record(p.status, kDevTimeoutMma);
         *abort_flag = 1;
         break;
       }
       ptx::tc_fence_after();
-      const uint64_t wd = ptx::smem_desc_sw128(w_slot(st)), xd = ptx::smem_desc_sw128(x_slot(st));
+      uint32_t at = w_slot(st, 0);
+      for (int j = 0; j < n; ++j, at += tile_bytes) {
+        const uint64_t wd = ptx::smem_desc_sw128(at), xd = ptx::smem_desc_sw128(at + kWTile);
+        const uint32_t more = (in_region | j) != 0 ? 1u : 0u;
+        if (leader) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (F8) ptx::mma_f8(tmem, wd + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
-        else ptx::mma_bf16(tmem, wd + 2 * k, xd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            if (F8) ptx::mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+            else ptx::mma_bf16(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+          }
+        }
       }
-      ptx::mma_commit(empty_bar(st));
+      if (leader) ptx::mma_commit(empty_bar(st));
+      __syncwarp();
+      if (++st == S) {
+        st = 0;
+        parity ^= 1;
+      }
+      if (++in_region == per_region) {  // the next accumulator
+        in_region = 0;
+        d += static_cast<uint32_t>(p.region_cols);
+      }
     }
-    ptx::mma_commit(done_bar);
+    if (leader) ptx::mma_commit(done_bar);
   }
   __syncwarp();
+  // this lane's four features: their terms load under the products
+  const int left = p.shard[shard].n - feat0 - lane * 4;
+  const long long col = p.shard[shard].col0 + feat0 + lane * 4;
+  float2 terms[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) terms[i] = column_terms(p, col + i, i < left);
   // Every warp waits for the last product; the stage buffers are free from then on.
   const bool ready = __all_sync(0xffffffffu, ptx::mbar_wait(done_bar, 0, p.wait_ns));
   if (!ready && lane == 0) {
@@ -262,15 +344,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_split(const __grid_const
   }
   ptx::tc_fence_after();
   float *red = reinterpret_cast<float *>(smem);  // [token][128 features] f32
-  if (warp >= 2 && ready) {
+  if (ready) {  // two warps per quarter of the TMEM lanes, every other 16 tokens each
     const int q = warp & 3;
-    for (int c = 0; c < NT; c += 16) {
-      uint32_t v[16];
-      ptx::tmem_ld_16cols(tmem + c + (static_cast<uint32_t>(q * 32) << 16), v);
-      ptx::tmem_ld_wait();
-      ptx::tmem_regs_ready(v);
+    const int used = (n_stages + per_region - 1) / per_region;
+    for (int c = 16 * (warp >> 2); c < NT; c += 32) {
+      float f[16];
+      for (int r = 0; r < used; r += 2) {  // two accumulators' loads in flight
+        uint32_t v[16], w[16];
+        const uint32_t at = tmem + r * p.region_cols + c + (static_cast<uint32_t>(q * 32) << 16);
+        const bool two = r + 1 < used;
+        ptx::tmem_ld_16cols(at, v);
+        ptx::tmem_ld_16cols(two ? at + p.region_cols : at, w);
+        ptx::tmem_ld_wait();
+        ptx::tmem_regs_ready(v);
+        ptx::tmem_regs_ready(w);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) red[(c + j) * 128 + q * 32 + lane] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) {
+          f[j] = r == 0 ? __uint_as_float(v[j]) : f[j] + __uint_as_float(v[j]);
+          if (two) f[j] += __uint_as_float(w[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) red[(c + j) * 128 + q * 32 + lane] = f[j];
     }
   }
   ptx::tc_fence_before();
@@ -287,47 +382,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_split(const __grid_const
   }
   if (p.split > 1) ptx::cluster_sync();
   else __syncthreads();
-  // The cluster's CTAs share the tile's tokens; a warp finishes one token at a
-  // time, four features a lane, the partials added in cluster order.
+  // The cluster's CTAs share the tile's tokens. A warp finishes two tokens at a
+  // time, four features a lane; the partials are added in cluster order.
   if (*abort_flag == 0) {
-    const int t1 = NT * (part + 1) / p.split;
-    const int left = p.n[shard] - feat0 - lane * 4;
-    const uint32_t red_addr = ptx::smem_addr(red);
-    for (int t = NT * part / p.split + warp; t < t1; t += kThreads / 32) {
-      const long long tok = static_cast<long long>(mt) * NT + t;
-      if (tok >= p.rows) break;
-      float f[4];
+    constexpr int kWarps = kThreads / 32, kTok = 2;
+    const int t1 = min(NT * (part + 1) / p.split, static_cast<int>(p.rows - static_cast<long long>(mt) * NT));
+    const uint32_t red_addr = ptx::smem_addr(red) + static_cast<uint32_t>(lane * 16);
+#pragma unroll 1
+    for (int t0 = NT * part / p.split + warp; t0 < t1; t0 += kTok * kWarps) {
+      float f[kTok][4], res[kTok][4], sx[kTok];
+      const long long tok0 = static_cast<long long>(mt) * NT + t0;
+#pragma unroll
+      for (int u = 0; u < kTok; ++u) {
+        const bool on = t0 + u * kWarps < t1 && left > 0;
+        sx[u] = on ? s_scale[t0 + u * kWarps] : 1.f;
+        if (p.res && on) load_row(p.res, p.res_f32, (tok0 + u * kWarps) * p.res_ld + col, left, res[u]);
+      }
       if (p.split == 1) {
-        const float4 v = *reinterpret_cast<const float4 *>(red + t * 128 + lane * 4);
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+          const float4 v = ptx::ld_shared_f4(red_addr + static_cast<uint32_t>(min(t0 + u * kWarps, t1 - 1)) * 512u);
+          f[u][0] = v.x; f[u][1] = v.y; f[u][2] = v.z; f[u][3] = v.w;
+        }
       } else {
-        float4 v[8];
+        float4 v[8][kTok];  // every partial's load is in flight before the first is added
 #pragma unroll
         for (int r = 0; r < 8; ++r)
           if (r < p.split)
-            v[r] = ptx::ld_shared_cluster_f4(ptx::mapa_shared(red_addr + static_cast<uint32_t>(t * 128 + lane * 4) * 4u, r));
-        f[0] = v[0].x; f[1] = v[0].y; f[2] = v[0].z; f[3] = v[0].w;
+#pragma unroll
+            for (int u = 0; u < kTok; ++u)
+              v[r][u] = ptx::ld_shared_cluster_f4(
+                  ptx::mapa_shared(red_addr + static_cast<uint32_t>(min(t0 + u * kWarps, t1 - 1)) * 512u, r));
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+          f[u][0] = v[0][u].x; f[u][1] = v[0][u].y; f[u][2] = v[0][u].z; f[u][3] = v[0][u].w;
+        }
 #pragma unroll
         for (int r = 1; r < 8; ++r)
-          if (r < p.split) {
-            f[0] += v[r].x; f[1] += v[r].y; f[2] += v[r].z; f[3] += v[r].w;
-          }
+          if (r < p.split)
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) {
+              f[u][0] += v[r][u].x; f[u][1] += v[r][u].y; f[u][2] += v[r][u].z; f[u][3] += v[r][u].w;
+            }
       }
-      if (left > 0) finish4(p, tok, p.col0[shard] + feat0 + lane * 4, left, f);
+#pragma unroll
+      for (int u = 0; u < kTok; ++u) {
+        if (t0 + u * kWarps >= t1 || left <= 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[u][i] = f[u][i] * (sx[u] * terms[i].x) + terms[i].y;
+        activate(f[u], p.act);
+        if (p.res) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[u][i] += res[u][i];
+        }
+        store_row(p.y, p.y_f32, (tok0 + u * kWarps) * p.y_ld + col, left, f[u]);
+      }
     }
   }
   __syncwarp();
-  if (p.split > 1) ptx::cluster_sync();  // peers have read this CTA's partials
+  if (p.split > 1) ptx::cluster_sync_relaxed();  // peers have read this CTA's partials
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: persistent SM pairs, 256 tokens x 256 features per tile.
+// Many tokens: persistent SM pairs, 256 tokens x BN features per tile. Each CTA
+// holds its 128 tokens' accumulator rows and loads its half of the W rows. Eight
+// epilogue warps: two per quarter of the TMEM lanes, each with half of the columns.
 // ---------------------------------------------------------------------------
-constexpr int kSub = 2;                                   // k-tiles per stage
-constexpr int kPairStage = kSub * 2 * kWTile;              // 64 KB per CTA
-constexpr int kPairStages = 3;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256;
+constexpr int kSub = 2;           // k-tiles per stage
+constexpr int kPairThreads = 320;
+constexpr int kChunkStages = kChunkSteps / 4 / kSub;
 constexpr int kGroup = 16;  // token tiles walked for one feature tile before the next (keeps both in L2)
+
+template <int BN>
+struct PairCfg {
+  static constexpr int kWBytes = BN / 2 * 128;  // this CTA's rows of one k-tile of W
+  static constexpr int kStage = kSub * (kWTile + kWBytes);
+  static constexpr int kTerms = 8 * (BN / 2) * 8;  // scale and bias of each epilogue warp's columns
+  static constexpr int kFit = (kSmemLimit - 1024 - 256 - kTerms) / kStage;
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kSmem = 1024 + kStages * kStage + kTerms + 256;
+  static_assert(kWBytes % 1024 == 0, "k-tiles keep the swizzle's alignment");
+};
 
 // Tile -> (token tile, feature tile): groups of kGroup token tiles, token tile fastest.
 __device__ __forceinline__ void pair_tile(const LinearParams &p, int tile, int &mt, int &nt) {
@@ -338,16 +473,19 @@ __device__ __forceinline__ void pair_tile(const LinearParams &p, int tile, int &
   nt = r / rows;
 }
 
-template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool F8, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ LinearParams p) {
+  using C = PairCfg<BN>;
   constexpr int kElems = F8 ? 128 : 64;
-  constexpr int S = kPairStages;
+  constexpr int S = C::kStages;
+  constexpr int kHalf = BN / 2;  // columns of an epilogue warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   const uint32_t sX = ptx::smem_addr(smem), sW = sX + S * kSub * kWTile;
-  uint8_t *bar_area = smem + S * kPairStage;
+  float2 *terms_area = reinterpret_cast<float2 *>(smem + S * C::kStage);
+  uint8_t *bar_area = smem + S * C::kStage + C::kTerms;
   const uint32_t bar0 = ptx::smem_addr(bar_area);
   auto full_bar = [&](int i) { return bar0 + 8u * i; };
   auto empty_bar = [&](int i) { return bar0 + 8u * (S + i); };
@@ -363,6 +501,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int tiles = p.m_tiles * p.n_tiles;
   auto slice_stages = [&](int sl) { return (p.k_tiles[sl] + kSub - 1) / kSub; };
+  int nk = 0;  // stages of a tile, and the chunks they make
+  for (int sl = 0; sl < p.n_slices; ++sl) nk += slice_stages(sl);
+  const int chunks = (nk + kChunkStages - 1) / kChunkStages;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -371,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(tfull_bar(a), 1);
-      ptx::mbar_init(tempty_bar(a), 8);  // 4 epilogue warps in each CTA
+      ptx::mbar_init(tempty_bar(a), 16);  // 8 epilogue warps in each CTA
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -388,117 +529,162 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      int kb = 0;
-      bool go = true;
-      for (int tile = pair; go && tile < tiles; tile += npairs) {
-        int mt, nt;
-        pair_tile(p, tile, mt, nt);
-        const int shard = shard_of(p, nt);
-        const int x_row = mt * 256 + static_cast<int>(rank) * 128;
-        const int w_row = (nt - p.n_tile0[shard]) * 256 + static_cast<int>(rank) * 128;
-        for (int sl = 0; go && sl < p.n_slices; ++sl) {
-          const CUtensorMap *wm = &p.w[p.n_shards > 1 ? shard : sl];
-          for (int ks = 0; ks < slice_stages(sl); ++ks, ++kb) {
-            const int st = kb % S;
-            if (*abort_flag || !ptx::mbar_wait(empty_bar(st), ((kb / S) & 1) ^ 1, p.wait_ns)) {
-              if (!*abort_flag) record(p.status, kDevTimeoutProducer);
-              *abort_flag = 1;
-              go = false;
-              break;
-            }
-            const uint32_t lead_full = ptx::mapa_shared(full_bar(st), 0);
-            if (leader) ptx::mbar_arrive_expect_tx(full_bar(st), 2 * kPairStage);
+  if (warp == 0) {  // converged, one lane issues
+    const bool issue = ptx::elect_one();
+    int st = 0;
+    uint32_t parity = 1;
+    bool go = true;
+    for (int tile = pair; go && tile < tiles; tile += npairs) {
+      int mt, nt;
+      pair_tile(p, tile, mt, nt);
+      const int shard = shard_of(p, nt);
+      const int x_row = mt * 256 + static_cast<int>(rank) * 128;
+      const int w_row = (nt - p.shard[shard].tile0) * BN + static_cast<int>(rank) * kHalf;
+      for (int sl = 0; go && sl < p.n_slices; ++sl) {
+        const CUtensorMap *wm = &p.w[p.n_shards > 1 ? shard : sl], *xm = &p.x[sl];
+        const int stages = slice_stages(sl);
+        for (int ks = 0; ks < stages; ++ks) {
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(empty_bar(st), parity, p.wait_ns) && *abort_flag == 0)) {
+            if (*abort_flag == 0) record(p.status, kDevTimeoutProducer);
+            *abort_flag = 1;
+            go = false;
+            break;
+          }
+          const uint32_t lead_full = ptx::mapa_shared(full_bar(st), 0);
+          if (issue) {
+            if (leader) ptx::mbar_arrive_expect_tx(full_bar(st), 2 * C::kStage);
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {  // a k-tile past the slice's end reads zeros
-              ptx::tma_load_2d_pair(sX + (st * kSub + j) * kWTile, &p.x[sl], (ks * kSub + j) * kElems, x_row, lead_full);
-              ptx::tma_load_2d_pair(sW + (st * kSub + j) * kWTile, wm, (ks * kSub + j) * kElems, w_row, lead_full);
+              ptx::tma_load_2d_pair(sX + (st * kSub + j) * kWTile, xm, (ks * kSub + j) * kElems, x_row, lead_full);
+              ptx::tma_load_2d_pair(sW + (st * kSub + j) * C::kWBytes, wm, (ks * kSub + j) * kElems, w_row, lead_full);
             }
+          }
+          if (++st == S) {
+            st = 0;
+            parity ^= 1;
           }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      constexpr uint32_t idesc = F8 ? ptx::idesc_e4m3_f32(256, 256) : ptx::idesc_bf16_f32(256, 256);
-      int nk = 0;
-      for (int sl = 0; sl < p.n_slices; ++sl) nk += slice_stages(sl);
-      int kb = 0;
+    if (leader) {
+      const bool issue = ptx::elect_one();
+      constexpr uint32_t idesc = F8 ? ptx::idesc_e4m3_f32(256, BN) : ptx::idesc_bf16_f32(256, BN);
+      int st = 0, g = 0;  // stage; chunks over all tiles
+      uint32_t parity = 0;
       bool ok = true;
-      for (int tile = pair, j = 0; ok && tile < tiles; tile += npairs, ++j) {
-        const int a = j & 1;
-        if (*abort_flag || !ptx::mbar_wait(tempty_bar(a), ((j >> 1) & 1) ^ 1, p.wait_ns)) {
-          if (!*abort_flag) record(p.status, kDevTimeoutMma);
-          *abort_flag = 1;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(a * 256);
-        for (int k0 = 0; k0 < nk; ++k0, ++kb) {
-          const int st = kb % S;
-          if (*abort_flag || !ptx::mbar_wait(full_bar(st), (kb / S) & 1, p.wait_ns)) {
-            if (!*abort_flag) record(p.status, kDevTimeoutMma);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, par, p.wait_ns) && *abort_flag == 0)) return true;
+        if (*abort_flag == 0) record(p.status, kDevTimeoutMma);
+        *abort_flag = 1;
+        ok = false;
+        return false;
+      };
+      for (int tile = pair; ok && tile < tiles; tile += npairs) {
+        for (int k0 = 0; ok && k0 < nk; k0 += kChunkStages, ++g) {
+          const int a = g & 1;
+          if (!wait(tempty_bar(a), ((g >> 1) & 1) ^ 1)) break;
           ptx::tc_fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(a * 256);
+          const int n = min(kChunkStages, nk - k0);
+          for (int i = 0; i < n; ++i) {
+            if (!wait(full_bar(st), parity)) break;
+            ptx::tc_fence_after();
+            if (issue) {
 #pragma unroll
-          for (int i = 0; i < kSub; ++i) {
-            const uint64_t xd = ptx::smem_desc_sw128(sX + (st * kSub + i) * kWTile);
-            const uint64_t wd = ptx::smem_desc_sw128(sW + (st * kSub + i) * kWTile);
+              for (int j = 0; j < kSub; ++j) {
+                const uint64_t xd = ptx::smem_desc_sw128(sX + (st * kSub + j) * kWTile);
+                const uint64_t wd = ptx::smem_desc_sw128(sW + (st * kSub + j) * C::kWBytes);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (F8) ptx::mma_f8_pair(d, xd + 2 * k, wd + 2 * k, idesc, (k0 | i | k) != 0 ? 1u : 0u);
-              else ptx::mma_bf16_pair(d, xd + 2 * k, wd + 2 * k, idesc, (k0 | i | k) != 0 ? 1u : 0u);
+                for (int k = 0; k < 4; ++k) {
+                  if (F8) ptx::mma_f8_pair(d, xd + 2 * k, wd + 2 * k, idesc, (i | j | k) != 0 ? 1u : 0u);
+                  else ptx::mma_bf16_pair(d, xd + 2 * k, wd + 2 * k, idesc, (i | j | k) != 0 ? 1u : 0u);
+                }
+              }
+              ptx::mma_commit_pair_multicast(empty_bar(st), 0x3);
+            }
+            __syncwarp();
+            if (++st == S) {
+              st = 0;
+              parity ^= 1;
             }
           }
-          ptx::mma_commit_pair_multicast(empty_bar(st), 0x3);
+          if (ok && issue) ptx::mma_commit_pair_multicast(tfull_bar(a), 0x3);
         }
-        if (!ok) break;
-        ptx::mma_commit_pair_multicast(tfull_bar(a), 0x3);
       }
-      ptx::mma_commit_pair_multicast(drain_bar, 0x1);
-      if (!ptx::mbar_wait(drain_bar, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      if (issue) {
+        ptx::mma_commit_pair_multicast(drain_bar, 0x1);
+        if (!ptx::mbar_wait(drain_bar, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      }
     }
   } else {
-    const int q = warp & 3;
-    for (int tile = pair, j = 0; tile < tiles; tile += npairs, ++j) {
-      const int a = j & 1;
-      const bool ready = ptx::mbar_wait(tfull_bar(a), (j >> 1) & 1, p.wait_ns);
-      if (!ready && lane == 0) record(p.status, kDevTimeoutEpilogue);
-      ptx::tc_fence_after();
-      if (!__all_sync(0xffffffffu, ready && (*abort_flag == 0))) {
-        if (lane == 0) *abort_flag = 1;
-        break;
-      }
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    float2 *terms = terms_area + (warp - 2) * kHalf;  // this warp's own: no barrier beyond the warp
+    const uint32_t lane_off = (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+    int g = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < tiles; tile += npairs) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
       const int shard = shard_of(p, nt);
       const long long tok = static_cast<long long>(mt) * 256 + rank * 128 + q * 32 + lane;
-      const int feat0 = (nt - p.n_tile0[shard]) * 256;
-      const uint32_t tb = tmem + static_cast<uint32_t>(a * 256) + (static_cast<uint32_t>(q * 32) << 16);
-      const uint32_t lead_tempty = ptx::mapa_shared(tempty_bar(a), 0);
-#pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t v[32];
-        ptx::tmem_ld_32cols(tb + c, v);
-        ptx::tmem_ld_wait();
-        ptx::tmem_regs_ready(v);
-        if (c + 32 == 256) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_remote(lead_tempty);
+      const int feat0 = (nt - p.shard[shard].tile0) * BN + half * kHalf;
+      const long long col = p.shard[shard].col0 + feat0;
+      const int n_left = p.shard[shard].n - feat0;  // columns of this warp's half that exist
+      const bool row_on = tok < p.rows;
+      __syncwarp();
+      for (int c = lane; c < kHalf; c += 32) terms[c] = column_terms(p, col + c, c < n_left);
+      __syncwarp();
+      const float sx = p.x_scale && row_on ? __ldg(p.x_scale + tok) : 1.f;
+      if (p.res && row_on) {  // the residual comes into L2 under the products
+        const int es = p.res_f32 ? 4 : 2;
+        const char *r = static_cast<const char *>(p.res) + (tok * p.res_ld + col) * es;
+        for (int c = 0; c < min(kHalf, n_left) * es; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + c));
+      }
+      float sum[kHalf];
+      for (int ch = 0; ch < chunks; ++ch, ++g) {
+        const int a = g & 1;
+        const bool ready = ptx::mbar_wait(tfull_bar(a), (g >> 1) & 1, p.wait_ns);
+        if (!ready && lane == 0) record(p.status, kDevTimeoutEpilogue);
+        ptx::tc_fence_after();
+        if (!__all_sync(0xffffffffu, ready && (*abort_flag == 0))) {
+          if (lane == 0) *abort_flag = 1;
+          ok = false;
+          break;
         }
-        const int left = p.n[shard] - feat0 - c;
-        if (tok < p.rows && left > 0) {
+        const uint32_t tb = tmem + static_cast<uint32_t>(a * 256) + lane_off;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float f[4] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
-                          __uint_as_float(v[i + 3])};
-            if (left - i > 0) finish4(p, tok, p.col0[shard] + feat0 + c + i, left - i, f);
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t v[16];
+          ptx::tmem_ld_16cols(tb + c, v);
+          ptx::tmem_ld_wait();
+          ptx::tmem_regs_ready(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[c + i] = ch == 0 ? __uint_as_float(v[i]) : sum[c + i] + __uint_as_float(v[i]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(tempty_bar(a), 0));
+      }
+      if (!ok) break;
+      if (row_on) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 8) {
+          if (c >= n_left) break;
+          float res[8], f[8];
+          if (p.res) load_row(p.res, p.res_f32, tok * p.res_ld + col + c, n_left - c, res);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float4 t = *reinterpret_cast<const float4 *>(terms + c + i);
+            f[i] = sum[c + i] * (sx * t.x) + t.y;
+            f[i + 1] = sum[c + i + 1] * (sx * t.z) + t.w;
           }
+          activate(f, p.act);
+          if (p.res) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += res[i];
+          }
+          store_row(p.y, p.y_f32, tok * p.y_ld + col + c, n_left - c, f);
         }
       }
     }
@@ -540,15 +726,24 @@ tp_status launch_split(const LinearParams &p, size_t smem, cudaStream_t s) {
   return launched(launch_kernel(k_linear_split<F8>, dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split)),
                                 dim3(kThreads), smem, s, static_cast<unsigned>(p.split), p));
 }
-template <bool F8>
+template <bool F8, int BN>
 tp_status launch_pair(const LinearParams &p, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_linear_pair<F8>, mask, mu);
+  const cudaError_t e = allow_smem(k_linear_pair<F8, BN>, mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
   const int tiles = p.m_tiles * p.n_tiles, most = num_sms() / 2;
-  return launched(launch_kernel(k_linear_pair<F8>, dim3(2u * static_cast<unsigned>(tiles < most ? tiles : most)),
-                                dim3(kThreads), kPairSmem, s, 1, p));
+  return launched(launch_kernel(k_linear_pair<F8, BN>, dim3(2u * static_cast<unsigned>(tiles < most ? tiles : most)),
+                                dim3(kPairThreads), PairCfg<BN>::kSmem, s, 1, p));
+}
+template <bool F8>
+tp_status launch_pair_bn(const LinearParams &p, int bn, cudaStream_t s) {
+  switch (bn) {
+    case 128: return launch_pair<F8, 128>(p, s);
+    case 160: return launch_pair<F8, 160>(p, s);
+    case 192: return launch_pair<F8, 192>(p, s);
+    default: return launch_pair<F8, 224>(p, s);
+  }
 }
 
 // Whether view b continues view a to the right (same rows, next columns) or below.
@@ -658,9 +853,9 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     p.n_tiles = 0;
     col = 0;
     for (int i = 0; i < p.n_shards; ++i) {
-      p.n[i] = static_cast<int>(ws[i].rows);
-      p.n_tile0[i] = p.n_tiles;
-      p.col0[i] = col;
+      p.shard[i].n = static_cast<int>(ws[i].rows);
+      p.shard[i].tile0 = p.n_tiles;
+      p.shard[i].col0 = col;
       p.n_tiles += static_cast<int>((ws[i].rows + tile_n - 1) / tile_n);
       col += ws[i].rows;
     }
@@ -683,14 +878,27 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
   p.early_w = !(env && env[0] == '0');
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-  // The pair kernel from half a wave of its tiles on; below that the split kernel's
+  // The pair kernel from a quarter wave of its tiles on; below that the split kernel's
   // smaller tiles and its split of K put more SMs to work.
-  lay_out(256);
   const long long m256 = (T + 255) / 256;
+  lay_out(256);
   const bool pair = T > 128 && m256 * p.n_tiles >= num_sms() / 4;
-  int x_box, w_box = 128;
+  int x_box = 128, w_box = 128, bn = 224;
   if (pair) {
-    x_box = 128;
+    // The tile width whose last wave wastes least: the busiest pair's columns,
+    // the wider tile (fewer bytes loaded per product) where two are equal.
+    long long best = -1;
+    for (int w = 224; w >= 128; w -= 32) {
+      lay_out(w);
+      const long long tiles = m256 * p.n_tiles, pairs = num_sms() / 2;
+      const long long cost = (tiles + pairs - 1) / pairs * w;
+      if (best < 0 || cost < best) {
+        best = cost;
+        bn = w;
+      }
+    }
+    lay_out(bn);
+    w_box = bn / 2;
     p.m_tiles = static_cast<int>(m256);
     if (m256 * p.n_tiles > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
   } else {
@@ -699,21 +907,34 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     const long long per = (T + p.m_tiles - 1) / p.m_tiles;
     p.tok_tile = static_cast<int>((per + 15) / 16 * 16);
     x_box = p.tok_tile;
-    const int stage = kWTile + p.tok_tile * 128;
-    p.stages = (kSmemLimit - 1024 - 512) / stage;
+    const int tile_bytes = kWTile + p.tok_tile * 128;
+    static const int e_sub = [] { const char *f = getenv("TPGQA_LIN_SUB"); return f ? atoi(f) : 2; }();
+    static const int e_kb = [] { const char *f = getenv("TPGQA_LIN_KB"); return f ? atoi(f) : 110; }();
+    static const int e_per = [] { const char *f = getenv("TPGQA_LIN_PER"); return f ? atoi(f) : 1; }();
+    p.sub = e_sub;
+    p.stages = ((p.tok_tile > 128 ? 222 : e_kb) * 1024 - 2048) / (tile_bytes * p.sub);
+    if (p.stages < 2) { p.sub = 1; p.stages = ((p.tok_tile > 128 ? 222 : e_kb) * 1024 - 2048) / tile_bytes; }
     if (p.stages > 12) p.stages = 12;
     // the largest cluster that one wave holds, with at least two k-tiles a CTA
     const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
     p.split = 1;
     for (int c = 2; c <= 8; ++c)
-      if (tiles * c <= num_sms() && tiles <= max_active_clusters(c) && p.kt_total >= 2 * c) p.split = c;
+      if (tiles * c <= num_sms() * e_per && tiles <= max_active_clusters(c) * e_per && p.kt_total >= 2 * c) p.split = c;
     if (tiles * p.split > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
+    // accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation
+    p.region_cols = 32;
+    while (p.region_cols < p.tok_tile) p.region_cols *= 2;
+    const int steps = (p.kt_total + p.split - 1) / p.split * 4;
+    p.regions = 1;
+    while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= 256) p.regions *= 2;
   }
   for (int i = 0; i < p.n_slices; ++i)
     if (!encode_rows_map(&p.x[i], xs[i], x_box)) return TP_ERR_INVALID_ARG;
   for (int i = 0; i < parts; ++i)
     if (!encode_rows_map(&p.w[i], ws[i], w_box)) return TP_ERR_INVALID_ARG;
-  if (pair) return dt == TP_E4M3 ? launch_pair<true>(p, s) : launch_pair<false>(p, s);
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * (kWTile + p.tok_tile * 128) + 8 * (2 * p.stages + 2) + 64;
+  if (pair) return dt == TP_E4M3 ? launch_pair_bn<true>(p, bn, s) : launch_pair_bn<false>(p, bn, s);
+  size_t smem = 1024 + static_cast<size_t>(p.stages) * p.sub * (kWTile + p.tok_tile * 128);
+  const size_t out = 1024 + static_cast<size_t>(p.tok_tile) * 512;  // the partials lie over the stages
+  smem = (smem > out ? smem : out) + 8 * (2 * p.stages + 2) + p.tok_tile * 4 + 64;
   return dt == TP_E4M3 ? launch_split<true>(p, smem, s) : launch_split<false>(p, smem, s);
 }

@@ -141,6 +141,12 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// The same without ordering memory: for CTAs that only have to be past a point (a
+// release would wait for every earlier global store of the thread).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Arrive on an mbarrier of another CTA of the cluster (shared::cluster address).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
@@ -241,6 +247,19 @@ __device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap *map, int x
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y), "r"(z)
                : "memory");
+}
+
+// True in one lane of a converged warp. A branch on it (rather than on the lane index)
+// keeps what the warp computes around it in uniform registers, which is where
+// tcgen05.mma and the bulk copies take their operands from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // ---- tcgen05 ----------------------------------------------------------------------

@@ -11,10 +11,10 @@
 //   k_linear_split  few tokens. Bound by streaming W, so the 128 rows of the MMA's
 //                   M are output features and the tokens are its N (16..256): no
 //                   accumulator row is padding, and a stage is 16 KB of W and 128
-//                   bytes a token of X, which leaves eight and more stages (about
-//                   190 KB) in flight per SM. Too few feature tiles to fill the
-//                   SMs split K over a cluster; the f32 partials are summed through
-//                   distributed shared memory in rank order, so results repeat.
+//                   bytes a token of X, about 200 KB in flight per SM. Too few
+//                   feature tiles to fill the SMs split K over a cluster; the f32
+//                   partials are summed through distributed shared memory in rank
+//                   order, so results repeat.
 //   k_linear_pair   many tokens. Bound by the tensor cores: persistent SM pairs on
 //                   tiles of 256 tokens x BN features (cta_group::2). The tile's sum
 //                   lives in the epilogue warps' registers, so both accumulators
@@ -50,7 +50,7 @@ constexpr int kWTile = 128 * 128;  // bytes of one 128-row, 128-byte-wide box
 // The scalars come first and lie together: a kernel's first read of each 64-byte
 // line of its parameters is a miss of a few hundred nanoseconds.
 struct LinearParams {
-  int tok_tile, stages, sub, split;  // k_linear_split: token tile, stages, k-tiles a stage, CTAs sharing K
+  int tok_tile, stages, split;       // k_linear_split: token tile, stages (one k-tile each), CTAs sharing K
   int regions, region_cols;          // its accumulators in TMEM and their stride
   int early_w;                       // W loads before the dependency wait
   int n_slices, n_shards, kt_total, n_tiles, rows, m_tiles;
@@ -180,12 +180,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const int S = p.stages, NT = p.tok_tile, U = p.sub;
-  const uint32_t tile_bytes = kWTile + static_cast<uint32_t>(NT) * 128u;
-  const uint32_t stage_bytes = static_cast<uint32_t>(U) * tile_bytes;
+  const int S = p.stages, NT = p.tok_tile;
+  const uint32_t stage_bytes = kWTile + static_cast<uint32_t>(NT) * 128u;
   const uint32_t sbase = ptx::smem_addr(smem);
-  auto w_slot = [&](int st, int j) { return sbase + static_cast<uint32_t>(st) * stage_bytes + static_cast<uint32_t>(j) * tile_bytes; };
-  auto x_slot = [&](int st, int j) { return w_slot(st, j) + kWTile; };
+  auto w_slot = [&](int st) { return sbase + static_cast<uint32_t>(st) * stage_bytes; };
   uint8_t *bar_area = smem + max(static_cast<uint32_t>(S) * stage_bytes, static_cast<uint32_t>(NT) * 512u);
   const uint32_t bar0 = ptx::smem_addr(bar_area);
   auto full_bar = [&](int i) { return bar0 + 8u * i; };
@@ -204,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   const int kb0 = static_cast<int>(static_cast<long long>(p.kt_total) * part / p.split);
   const int kb1 = static_cast<int>(static_cast<long long>(p.kt_total) * (part + 1) / p.split);
   const uint32_t tmem_cols = static_cast<uint32_t>(p.regions * p.region_cols);
-  const int nkb = kb1 - kb0, n_stages = (nkb + U - 1) / U;
-  const int per_region = (n_stages + p.regions - 1) / p.regions;  // stages of an accumulator
+  const int nkb = kb1 - kb0;
+  const int per_region = (nkb + p.regions - 1) / p.regions;  // k-tiles of an accumulator
 
   // The loading thread's cursors over the k-tiles, (slice, k-tile in it), of W and of X.
   struct Cursor {
@@ -221,20 +219,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   while (wc.kt >= p.k_tiles[wc.sl]) wc.kt -= p.k_tiles[wc.sl++];
   Cursor xc = wc;
   int pre = 0;
-  // the W (or X) boxes of one stage; neighbouring k-tiles of a row are one 128 * U byte run in memory
-  // One thread issues every load and one every MMA, so their loops hold no division:
-  // a remainder by the run-time stage count costs as much as the rest of a step.
-  auto load_w = [&](int st, int n, bool issue) {
-    if (issue) ptx::mbar_arrive_expect_tx(full_bar(st), static_cast<uint32_t>(n) * kWTile);
-    uint32_t dst = w_slot(st, 0);
-    for (int j = 0; j < n; ++j, next(wc), dst += tile_bytes)
-      if (issue) ptx::tma_load_2d(dst, &p.w[p.n_shards > 1 ? shard : wc.sl], wc.kt * kElems, feat0, full_bar(st));
+  // The loops of the issuing warps hold no division: a remainder by the run-time
+  // stage count costs as much as the rest of a step.
+  auto load_w = [&](int st, bool issue) {
+    if (issue) {
+      ptx::mbar_arrive_expect_tx(full_bar(st), kWTile);
+      ptx::tma_load_2d(w_slot(st), &p.w[p.n_shards > 1 ? shard : wc.sl], wc.kt * kElems, feat0, full_bar(st));
+    }
+    next(wc);
   };
-  auto load_x = [&](int st, int n, bool issue) {
-    if (issue) ptx::mbar_arrive_expect_tx(full_bar(st), static_cast<uint32_t>(n) * (tile_bytes - kWTile));
-    uint32_t dst = x_slot(st, 0);
-    for (int j = 0; j < n; ++j, next(xc), dst += tile_bytes)
-      if (issue) ptx::tma_load_2d(dst, &p.x[xc.sl], xc.kt * kElems, mt * NT, full_bar(st));
+  auto load_x = [&](int st, bool issue) {
+    if (issue) {
+      ptx::mbar_arrive_expect_tx(full_bar(st), stage_bytes - kWTile);
+      ptx::tma_load_2d(w_slot(st) + kWTile, &p.x[xc.sl], xc.kt * kElems, mt * NT, full_bar(st));
+    }
+    next(xc);
   };
   if (warp == 0) {
     const bool leader = ptx::elect_one();
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
     // W does not come from the previous kernel: its first stages start before the
     // grid-dependency wait and before anything else of this CTA.
     if (p.early_w)
-      for (; pre < S && pre < n_stages; ++pre) load_w(pre, min(U, nkb - pre * U), leader);
+      for (; pre < S && pre < nkb; ++pre) load_w(pre, leader);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t *>(tmem_slot)), tmem_cols);
@@ -271,15 +270,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
     const bool leader = ptx::elect_one();
     int st = 0;
     uint32_t parity = 1;  // of the stage's empty barrier
-    for (int i = 0, left_k = nkb; i < n_stages; ++i, left_k -= U) {
-      const int n = min(U, left_k);
+    for (int i = 0; i < nkb; ++i) {
       if (i >= S && !__all_sync(0xffffffffu, ptx::mbar_wait(empty_bar(st), parity, p.wait_ns))) {
         record(p.status, kDevTimeoutProducer);
         *abort_flag = 1;
         break;
       }
-      if (warp == 2) load_x(st, n, leader);
-      else if (i >= pre) load_w(st, n, leader);
+      if (warp == 2) load_x(st, leader);
+      else if (i >= pre) load_w(st, leader);
       if (++st == S) {
         st = 0;
         parity ^= 1;
@@ -296,24 +294,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
     const bool leader = ptx::elect_one();
     int st = 0, in_region = 0;
     uint32_t parity = 0, d = tmem;
-    for (int i = 0, left_k = nkb; i < n_stages; ++i, left_k -= U) {
-      const int n = min(U, left_k);
+    for (int i = 0; i < nkb; ++i) {
       if (!__all_sync(0xffffffffu, ptx::mbar_wait(full_bar(st), parity, p.wait_ns))) {
         record(p.status, kDevTimeoutMma);
         *abort_flag = 1;
         break;
       }
       ptx::tc_fence_after();
-      uint32_t at = w_slot(st, 0);
-      for (int j = 0; j < n; ++j, at += tile_bytes) {
-        const uint64_t wd = ptx::smem_desc_sw128(at), xd = ptx::smem_desc_sw128(at + kWTile);
-        const uint32_t more = (in_region | j) != 0 ? 1u : 0u;
-        if (leader) {
+      const uint64_t wd = ptx::smem_desc_sw128(w_slot(st)), xd = ptx::smem_desc_sw128(w_slot(st) + kWTile);
+      const uint32_t more = in_region != 0 ? 1u : 0u;
+      if (leader) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (F8) ptx::mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
-            else ptx::mma_bf16(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
-          }
+        for (int k = 0; k < 4; ++k) {
+          if (F8) ptx::mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+          else ptx::mma_bf16(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
         }
       }
       if (leader) ptx::mma_commit(empty_bar(st));
@@ -346,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   float *red = reinterpret_cast<float *>(smem);  // [token][128 features] f32
   if (ready) {  // two warps per quarter of the TMEM lanes, every other 16 tokens each
     const int q = warp & 3;
-    const int used = (n_stages + per_region - 1) / per_region;
+    const int used = (nkb + per_region - 1) / per_region;
     for (int c = 16 * (warp >> 2); c < NT; c += 32) {
       float f[16];
       for (int r = 0; r < used; r += 2) {  // two accumulators' loads in flight
@@ -907,19 +901,18 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     const long long per = (T + p.m_tiles - 1) / p.m_tiles;
     p.tok_tile = static_cast<int>((per + 15) / 16 * 16);
     x_box = p.tok_tile;
-    const int tile_bytes = kWTile + p.tok_tile * 128;
-    static const int e_sub = [] { const char *f = getenv("TPGQA_LIN_SUB"); return f ? atoi(f) : 2; }();
-    static const int e_kb = [] { const char *f = getenv("TPGQA_LIN_KB"); return f ? atoi(f) : 110; }();
-    static const int e_per = [] { const char *f = getenv("TPGQA_LIN_PER"); return f ? atoi(f) : 1; }();
-    p.sub = e_sub;
-    p.stages = ((p.tok_tile > 128 ? 222 : e_kb) * 1024 - 2048) / (tile_bytes * p.sub);
-    if (p.stages < 2) { p.sub = 1; p.stages = ((p.tok_tile > 128 ? 222 : e_kb) * 1024 - 2048) / tile_bytes; }
-    if (p.stages > 12) p.stages = 12;
-    // the largest cluster that one wave holds, with at least two k-tiles a CTA
-    const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
+    // Half of an SM's shared memory, so that two CTAs share it (the next kernel's first
+    // weights load beside this one's end), while that leaves four stages and more;
+    // beyond 128 tokens all of it. At 61 tokens, 4096 -> 14336 in e4m3: 15.9 us with two
+    // CTAs an SM of 110 KB, 16.5 with one of 222 KB, 18.7 with three of 72 KB.
+    const int stage = kWTile + p.tok_tile * 128;
+    const bool two = p.tok_tile <= 128;
+    p.stages = ((two ? 110 : 222) * 1024 - 2048) / stage;
+    // the largest cluster that leaves every CTA its place, with at least two k-tiles a CTA
+    const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles, per_sm = two ? 2 : 1;
     p.split = 1;
     for (int c = 2; c <= 8; ++c)
-      if (tiles * c <= num_sms() * e_per && tiles <= max_active_clusters(c) * e_per && p.kt_total >= 2 * c) p.split = c;
+      if (tiles * c <= num_sms() * per_sm && tiles <= max_active_clusters(c) * per_sm && p.kt_total >= 2 * c) p.split = c;
     if (tiles * p.split > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
     // accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation
     p.region_cols = 32;
@@ -933,7 +926,7 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
   for (int i = 0; i < parts; ++i)
     if (!encode_rows_map(&p.w[i], ws[i], w_box)) return TP_ERR_INVALID_ARG;
   if (pair) return dt == TP_E4M3 ? launch_pair_bn<true>(p, bn, s) : launch_pair_bn<false>(p, bn, s);
-  size_t smem = 1024 + static_cast<size_t>(p.stages) * p.sub * (kWTile + p.tok_tile * 128);
+  size_t smem = 1024 + static_cast<size_t>(p.stages) * (kWTile + p.tok_tile * 128);
   const size_t out = 1024 + static_cast<size_t>(p.tok_tile) * 512;  // the partials lie over the stages
   smem = (smem > out ? smem : out) + 8 * (2 * p.stages + 2) + p.tok_tile * 4 + 64;
   return dt == TP_E4M3 ? launch_split<true>(p, smem, s) : launch_split<false>(p, smem, s);

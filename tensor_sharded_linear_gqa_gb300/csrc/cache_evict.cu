@@ -220,20 +220,27 @@ __device__ __forceinline__ void write_length(const EvictParams &p, int b) {
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;    // rows in flight per thread, gather
+constexpr int kMoveUnroll = 4;    // rows in flight per thread, gather
 constexpr int kPlaceUnroll = 4;   // the same, in place
 
-// Gather into another buffer. CTA: x = (sequence, chunk of kept places), y =
-// (source, head, K or V); a thread keeps one 16-byte piece of the head's row and
-// steps over the places, eight loads in flight.
-__global__ void __launch_bounds__(kMoveThreads) k_evict_gather(const __grid_constant__ EvictParams p) {
+// Gather into another buffer. CTA: (sequence, chunk of kept places) with (source,
+// head, K or V) fastest, so that the heads of a row, which lie side by side in
+// memory, are read and written at about the same time; a thread keeps one 16-byte
+// piece of the head's row and steps over the places, four loads in flight. Each
+// CTA waits twice (for kept, then for the rows), so full occupancy, 32 registers a
+// thread, carries it: 64 caches of up to 2048 keys to 1024 take 93 us in all,
+// against 104 with eight loads a thread and 126 with sixteen at the occupancy that
+// those leave. Rows are read and written once: streaming accesses.
+__global__ void __launch_bounds__(kMoveThreads, 8) k_evict_gather(const __grid_constant__ EvictParams p) {
   grid_dep_wait();
   grid_dep_launch();
   const int lanes = p.d / 8;  // 16-byte pieces of a head's row
-  const bool is_v = blockIdx.y & 1;
-  const int h = (blockIdx.y >> 1) % p.heads, src = (blockIdx.y >> 1) / p.heads;
-  const int b = blockIdx.x / p.chunks, chunk = blockIdx.x - b * p.chunks;
-  if (blockIdx.y == 0 && chunk == 0 && threadIdx.x == 0) write_length(p, b);
+  const int columns = 2 * p.sources * p.heads;
+  const int group = blockIdx.x / columns, column = blockIdx.x - group * columns;
+  const int b = group / p.chunks, chunk = group - b * p.chunks;
+  const int src = (column >> 1) % p.sources, h = (column >> 1) / p.sources;
+  const bool is_v = column & 1;
+  if (column == 0 && chunk == 0 && threadIdx.x == 0) write_length(p, b);
   const int rows = kMoveThreads / lanes;
   const int piece = threadIdx.x % lanes, row0 = threadIdx.x / lanes;
   if (row0 >= rows) return;
@@ -253,10 +260,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_gather(const __grid_cons
   }
 #pragma unroll
   for (int i = 0; i < kMoveUnroll; ++i)
-    if (from[i] >= 0) x[i] = *reinterpret_cast<const uint4 *>(in + from[i] * in_ld);
+    if (from[i] >= 0) x[i] = __ldcs(reinterpret_cast<const uint4 *>(in + from[i] * in_ld));
 #pragma unroll
   for (int i = 0; i < kMoveUnroll; ++i)
-    if (from[i] >= 0) *reinterpret_cast<uint4 *>(out + (c0 + i * rows + row0) * out_ld) = x[i];
+    if (from[i] >= 0) __stcs(reinterpret_cast<uint4 *>(out + (c0 + i * rows + row0) * out_ld), x[i]);
 }
 
 // In place: CTA x = (sequence, source, head, K or V), y = one 64-byte column slice
@@ -345,7 +352,7 @@ extern "C" tp_status tp_cache_evict(const tp_plan *plan, int64_t batch, const in
   if (cap_out < need) return TP_ERR_INVALID_ARG;
   const long long rows_per_cta = kMoveThreads / (d / 8) * kMoveUnroll;
   const long long chunks = need > 0 ? (need + rows_per_cta - 1) / rows_per_cta : 1;
-  if (batch > 0 && chunks > 0x7fffffff / batch) return TP_ERR_UNSUPPORTED;
+  if (batch > 0 && chunks > 0x7fffffff / (batch * 2 * heads * sources)) return TP_ERR_UNSUPPORTED;
   tp_status st = check_rank_health(dims.tp_size);
   if (st != TP_OK) return st;
   if (batch == 0) return TP_OK;
@@ -396,7 +403,6 @@ extern "C" tp_status tp_cache_evict(const tp_plan *plan, int64_t batch, const in
   if (same && cap > 0)
     return launched(launch_kernel(k_evict_in_place, dim3(units * 2, static_cast<unsigned>((lanes + 3) / 4)),
                                   dim3(kMoveThreads), 0, s, 1, p));
-  const unsigned gy = static_cast<unsigned>(2 * sources * heads);
-  return launched(launch_kernel(k_evict_gather, dim3(static_cast<unsigned>(batch * p.chunks), gy), dim3(kMoveThreads), 0,
-                                s, 1, p));
+  return launched(launch_kernel(k_evict_gather, dim3(static_cast<unsigned>(batch * p.chunks * 2 * sources * heads)),
+                                dim3(kMoveThreads), 0, s, 1, p));
 }

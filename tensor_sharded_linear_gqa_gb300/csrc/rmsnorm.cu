@@ -138,8 +138,13 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx) {
 // The row in registers: thread t holds the 8-element groups t, t + blockDim, ...
 // (ITEMS of them). Bases and pitches are 16-byte aligned; a row's last group may
 // be partial and is moved by elements.
-template <typename XT, typename RT, typename YT, int ITEMS>
-__global__ void __launch_bounds__(512) k_add_rmsnorm(const __grid_constant__ NormParams p) {
+// ONE: a single x, whose few registers let three CTAs share an SM: with rows that
+// load, reduce and store at different times memory stays busy (4096 x 8192, f32 x and
+// bf16 residual: 58 us, against 69 us with two CTAs of up to 64 registers). The loads
+// of several partials need those registers (64 x 4096, eight partials: 5.4 us, 8.3
+// with three CTAs).
+template <typename XT, typename RT, typename YT, int ITEMS, bool ONE>
+__global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_constant__ NormParams p) {
   constexpr bool kRes = !std::is_same<RT, NoRes>::value;
   grid_dep_wait();
   grid_dep_launch();
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(512) k_add_rmsnorm(const __grid_constant__ Nor
       for (int i = 0; i < 8; ++i) z[j][i] = 0.0f;
   }
   // four partials' loads in flight at a time; added in rank order
-  for (int r0 = 1; r0 < p.n_x; r0 += 4) {
+  for (int r0 = 1; !ONE && r0 < p.n_x; r0 += 4) {
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
       const int c = (threadIdx.x + j * blockDim.x) * 8;
@@ -262,19 +267,24 @@ __global__ void __launch_bounds__(512) k_add_rmsnorm_elems(const __grid_constant
   }
 }
 
-template <typename XT, typename RT, typename YT>
-tp_status launch_typed(const NormParams &p, bool vec, cudaStream_t s) {
-  const int groups = (p.cols + 7) / 8;
+template <typename XT, typename RT, typename YT, bool ONE>
+tp_status launch_vec(const NormParams &p, int groups, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.rows));
   auto threads_for = [](int per) { return dim3(static_cast<unsigned>(per <= 32 ? 32 : (per + 31) / 32 * 32)); };
   // The fewest groups per thread that keep the CTA within 512 threads.
-  if (vec && groups <= 512)
-    return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 1>, grid, threads_for(groups), 0, s, 1, p));
-  if (vec && groups <= 1024)
-    return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 2>, grid, threads_for((groups + 1) / 2), 0, s, 1, p));
+  if (groups <= 512)
+    return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 1, ONE>, grid, threads_for(groups), 0, s, 1, p));
+  if (groups <= 1024)
+    return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 2, ONE>, grid, threads_for((groups + 1) / 2), 0, s, 1, p));
+  return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 4, ONE>, grid, threads_for((groups + 3) / 4), 0, s, 1, p));
+}
+
+template <typename XT, typename RT, typename YT>
+tp_status launch_typed(const NormParams &p, bool vec, cudaStream_t s) {
+  const int groups = (p.cols + 7) / 8;
   if (vec && groups <= 2048)
-    return launched(launch_kernel(k_add_rmsnorm<XT, RT, YT, 4>, grid, threads_for((groups + 3) / 4), 0, s, 1, p));
-  return launched(launch_kernel(k_add_rmsnorm_elems<XT, RT, YT>, grid, dim3(512), 0, s, 1, p));
+    return p.n_x == 1 ? launch_vec<XT, RT, YT, true>(p, groups, s) : launch_vec<XT, RT, YT, false>(p, groups, s);
+  return launched(launch_kernel(k_add_rmsnorm_elems<XT, RT, YT>, dim3(static_cast<unsigned>(p.rows)), dim3(512), 0, s, 1, p));
 }
 
 template <typename XT, typename RT>

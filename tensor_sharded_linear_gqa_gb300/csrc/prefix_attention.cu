@@ -33,27 +33,32 @@ using namespace op;
 constexpr int kMaxRanks32 = 32;
 constexpr int kSms = 152;  // a GB300's; splits and workspace sizes follow it, not the device at hand
 
+// The scalars come first and lie together: a kernel's first read of each 64-byte
+// line of its parameters is a miss of a few hundred nanoseconds.
 struct PrefixAttnParams {
-  CUtensorMap k_map[kMaxRanks32], v_map[kMaxRanks32];  // prefix K and V of each kv source
-  const void *q[kMaxRanks32];
-  void *a[kMaxRanks32];
-  long long q_ld[kMaxRanks32], a_ld[kMaxRanks32];
-  const void *k_own[kMaxRanks32], *v_own[kMaxRanks32];
-  long long ko_ld[kMaxRanks32], vo_ld[kMaxRanks32];
-  const float *w_in[kMaxRanks32];
-  float *w_out[kMaxRanks32];
-  long long wi_ld[kMaxRanks32], wo_ld[kMaxRanks32];
-  const int *lengths;
-  float *part_o;    // [split][row][d]
-  float2 *part_ml;  // [split][row] (m in log2 units, l)
-  float *scores;    // [row][capacity], s * log2(e) / sqrt(d) of the own keys; null: not wanted
   int batch, heads_q, heads_kv, group, heads_per_rank, heads_per_source, d;
   int prefix, blocks, split_p, pairs;  // 128-key blocks; key splits; 256-row tile pairs per kv head
   int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
   int has_prev;                        // k_own_part runs behind k_prefix_part
   float scale_log2;
+  const int *lengths;
+  float *part_o;    // [split][row][d]
+  float2 *part_ml;  // [split][row] (m in log2 units, l)
+  float *scores;    // [row][capacity], s * log2(e) / sqrt(d) of the own keys; null: not wanted
   int *status;
   long long wait_ns;
+  const void *q[kMaxRanks32];
+  long long q_ld[kMaxRanks32];
+  const void *k_own[kMaxRanks32], *v_own[kMaxRanks32];
+  long long ko_ld[kMaxRanks32], vo_ld[kMaxRanks32];
+  void *a[kMaxRanks32];
+  long long a_ld[kMaxRanks32];
+  const float *w_in[kMaxRanks32];
+  float *w_out[kMaxRanks32];
+  long long wi_ld[kMaxRanks32], wo_ld[kMaxRanks32];
+};
+struct PrefixMaps {
+  CUtensorMap k[kMaxRanks32], v[kMaxRanks32];  // prefix K and V of each kv source
 };
 
 __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
@@ -139,7 +144,7 @@ struct PrefCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_constant__ PrefixAttnParams p) {
+__global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_constant__ PrefixAttnParams p, const __grid_constant__ PrefixMaps maps) {
   using C = PrefCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
         item(it, kv, pair, split, b0, b1);
         const int src = kv / p.heads_per_source;
         const int col = (kv - src * p.heads_per_source) * D;
-        const CUtensorMap *map = lane == 0 ? &p.k_map[src] : &p.v_map[src];
+        const CUtensorMap *map = lane == 0 ? &maps.k[src] : &maps.v[src];
         for (int j = b0; j < b1; ++j, ++g) {
           const int s = g & 1;
           if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * s, ((g >> 1) & 1) ^ 1, p.wait_ns)) {
@@ -712,22 +717,34 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
   const long long stride = static_cast<long long>(p.batch) * p.heads_q;
   for (int g = warp; g < p.group; g += kJoinThreads / 32) {
     const long long row = part_row(p, kv, b, g);
-    float mt = -INFINITY;
-    for (int s = lane; s < n; s += 32) mt = fmaxf(mt, p.part_ml[s * stride + row].x);
+    float mt = -INFINITY, lt = 0.f, acc[kPer] = {};
+    for (int s0 = 0; s0 < n; s0 += 32) {  // a lane per split, then every lane its columns of all of them
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (s0 + lane < n) ml = p.part_ml[(s0 + lane) * stride + row];
+      float mx = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    float lt = 0.f, acc[kPer] = {};
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float2 ml = p.part_ml[s * stride + row];
-      const float f = ex2(ml.x - mt);
-      lt += f * ml.y;
-      const float *src = p.part_o + (s * stride + row) * D + lane * kPer;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float m_new = fmaxf(mt, mx);
+      const float back = mt == m_new ? 1.f : ex2(mt - m_new);
+      const float f = s0 + lane < n ? ex2(ml.x - m_new) : 0.f;
+      float sum = f * ml.y;
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(src + i);
-        acc[i] += f * v.x;
-        acc[i + 1] += f * v.y;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      lt = lt * back + sum;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) acc[c] *= back;
+      mt = m_new;
+      const int here = min(32, n - s0);
+      const float *src = p.part_o + (s0 * stride + row) * D + lane * kPer;
+#pragma unroll 8
+      for (int j = 0; j < here; ++j) {
+        const float w = __shfl_sync(0xffffffffu, f, j);
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2) {
+          const float2 v = *reinterpret_cast<const float2 *>(src + j * stride * D + c);
+          acc[c] += w * v.x;
+          acc[c + 1] += w * v.y;
+        }
       }
     }
     // no key at all: the row is zero, and no key has a weight
@@ -750,9 +767,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
   for (int j = threadIdx.x; j < p.cap; j += kJoinThreads) {
     float w = 0.f;
     if (j < len) {
-#pragma unroll 4
+      const float old = wi ? wi[j] : 0.f;
+#pragma unroll 8
       for (int g = 0; g < p.group; ++g) w += ex2(sc[static_cast<long long>(g) * p.cap + j] - s_lse[g]);
-      if (wi) w += wi[j];
+      w += old;
     }
     wo[j] = w;
   }
@@ -820,7 +838,7 @@ cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
 }
 
 template <int D>
-tp_status launch_all(const PrefixAttnParams &p, cudaStream_t s) {
+tp_status launch_all(const PrefixAttnParams &p, const PrefixMaps &maps, cudaStream_t s) {
   static unsigned mask_p = 0, mask_o = 0;
   static std::mutex mu;
   cudaError_t e = allow_smem(k_prefix_part<D>, static_cast<int>(PrefCfg<D>::kSmem), mask_p, mu);
@@ -830,7 +848,7 @@ tp_status launch_all(const PrefixAttnParams &p, cudaStream_t s) {
   if (p.split_p > 0) {
     const int items = p.heads_kv * p.pairs * p.split_p, sms = num_sms();
     st = launched(launch_kernel(k_prefix_part<D>, dim3(static_cast<unsigned>(items < sms ? items : sms)),
-                                dim3(kPrefThreads), PrefCfg<D>::kSmem, s, 1, p));
+                                dim3(kPrefThreads), PrefCfg<D>::kSmem, s, 1, p, maps));
     if (st != TP_OK) return st;
   }
   if (p.split_o > 0) {
@@ -918,6 +936,7 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
   const cudaError_t e = get_dev_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e);
   static thread_local PrefixAttnParams p;
+  static thread_local PrefixMaps maps;  // 8 KB: kept off the stack
   std::memset(&p, 0, sizeof(p));
   for (int r = 0; r < n; ++r) {
     p.q[r] = q[r].ptr;
@@ -929,7 +948,7 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
     if (P > 0) {
       tp_tensor k = k_prefix[r], v = v_prefix[r];
       if (P == 1) k.ld = v.ld = (kvc + 7) / 8 * 8;  // the pitch of a single row is free
-      if (!encode_rows_map(&p.k_map[r], k, 128) || !encode_rows_map(&p.v_map[r], v, 128)) return TP_ERR_INVALID_ARG;
+      if (!encode_rows_map(&maps.k[r], k, 128) || !encode_rows_map(&maps.v[r], v, 128)) return TP_ERR_INVALID_ARG;
     }
     p.k_own[r] = k_own[r].ptr;
     p.v_own[r] = v_own[r].ptr;
@@ -968,5 +987,5 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
   p.status = ctx.status;
   p.wait_ns = ctx.wait_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return hd == 128 ? launch_all<128>(p, s) : launch_all<64>(p, s);
+  return hd == 128 ? launch_all<128>(p, maps, s) : launch_all<64>(p, maps, s);
 }

@@ -15,9 +15,10 @@
 // (split, row); k_combine joins them: sum of 2^(m_s - M) O_s over sum of
 // 2^(m_s - M) l_s, which is the softmax over all keys, whatever the split.
 //
-// k_own_part does not wait for k_prefix_part, which it shares nothing with: it
-// starts as that kernel's CTAs leave and waits for it only before it ends, so
-// that what follows it on the stream follows both.
+// The two parts bound different things, so they run at the same time: k_prefix_part
+// leaves some SMs free, and k_own_part, which shares nothing with it, does not wait
+// for it: it starts on those SMs, goes on where that kernel's CTAs leave, and waits
+// for it only in its last CTA, so that what follows it on the stream follows both.
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -37,7 +38,7 @@ constexpr int kSms = 152;  // a GB300's; splits and workspace sizes follow it, n
 // line of its parameters is a miss of a few hundred nanoseconds.
 struct PrefixAttnParams {
   int batch, heads_q, heads_kv, group, heads_per_rank, heads_per_source, d;
-  int prefix, blocks, split_p, pairs;  // 128-key blocks; key splits; 256-row tile pairs per kv head
+  int prefix, blocks, split_p, pairs, ctas_p;  // 128-key blocks; key splits; 256-row tile pairs per kv head; CTAs
   int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
   int has_prev;                        // k_own_part runs behind k_prefix_part
   float scale_log2;
@@ -507,7 +508,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kOwnThreads) k_own_part(const __grid_constant__ PrefixAttnParams p) {
+__global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_constant__ PrefixAttnParams p) {
   using C = OwnCfg<D>;
   extern __shared__ __align__(128) uint8_t own_smem[];
   __shared__ float2 s_ml[4][16];
@@ -527,20 +528,28 @@ __global__ void __launch_bounds__(kOwnThreads) k_own_part(const __grid_constant_
     const long long k_ld = p.ko_ld[src], v_ld = p.vo_ld[src];
     const uint32_t sbase = ptx::smem_addr(own_smem);
     const int steps = (j1 - j0 + kOwnKeys - 1) / kOwnKeys;
-    constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+    constexpr int kPieces = D / 8;                // 16-byte pieces of a row
+    constexpr int kRows = kOwnThreads / kPieces;  // rows that the CTA loads at a time
+    const int c0 = tid % kPieces, r0 = tid / kPieces;
+    // this thread's piece of rows r0, r0 + kRows, ...: pointers walk, nothing is multiplied
+    const char *kp = reinterpret_cast<const char *>(k0 + (j0 + r0) * k_ld + c0 * 8);
+    const char *vp = reinterpret_cast<const char *>(v0 + (j0 + r0) * v_ld + c0 * 8);
+    const long long k_step = kRows * k_ld * 2, v_step = kRows * v_ld * 2;
+    // rows r0 + i kRows share r & 7 where kRows is a multiple of 8 (always: 8 or 16)
+    const uint32_t to0 = static_cast<uint32_t>(r0 * D * 2 + (c0 ^ (r0 & 7)) * 16);
+    int load_stage = 0, load_key = j0 + r0;
     auto load = [&](int step) {
       if (step < steps) {
-        const uint32_t ks = sbase + static_cast<uint32_t>(step % kOwnStages) * 2 * C::kMat, vs = ks + C::kMat;
+        const uint32_t ks = sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat + to0;
+        if (++load_stage == kOwnStages) load_stage = 0;
 #pragma unroll
-        for (int i = 0; i < kOwnKeys * kPieces / kOwnThreads; ++i) {
-          const int idx = tid + i * kOwnThreads;
-          const int r = idx / kPieces, c = idx % kPieces;
-          const int j = j0 + step * kOwnKeys + r;
-          const bool valid = j < j1;
-          const uint32_t at = static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16);
-          const long long jj = valid ? j : j0;
-          cp_async16(ks + at, k0 + jj * k_ld + c * 8, valid);
-          cp_async16(vs + at, v0 + jj * v_ld + c * 8, valid);
+        for (int i = 0; i < kOwnKeys / kRows; ++i) {
+          const bool valid = load_key < j1;
+          cp_async16(ks + i * kRows * D * 2, valid ? kp : reinterpret_cast<const char *>(k0), valid);
+          cp_async16(ks + C::kMat + i * kRows * D * 2, valid ? vp : reinterpret_cast<const char *>(v0), valid);
+          kp += k_step;
+          vp += v_step;
+          load_key += kRows;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -566,13 +575,15 @@ __global__ void __launch_bounds__(kOwnThreads) k_own_part(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int stage = 0;
     for (int step = 0; step < steps; ++step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
       __syncthreads();  // the stage is there for every thread, and the one loaded next is free
       load(step + kOwnStages - 1);
       const int key0 = j0 + step * kOwnKeys + warp * 16;
+      const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
+      if (++stage == kOwnStages) stage = 0;
       if (key0 >= j1) continue;
-      const uint32_t ks = sbase + static_cast<uint32_t>(step % kOwnStages) * 2 * C::kMat, vs = ks + C::kMat;
       float s[2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -692,8 +703,9 @@ __global__ void __launch_bounds__(kOwnThreads) k_own_part(const __grid_constant_
       if (c == 0) p.part_ml[at] = make_float2(mt, lt);
     }
   }
-  // what follows this kernel on the stream follows the prefix kernel too
-  if (p.has_prev) grid_dep_wait();
+  // What follows this kernel on the stream follows the prefix kernel too: the grid
+  // ends with its last CTA, which waits for it (the others leave their SMs).
+  if (p.has_prev && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z) grid_dep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -706,11 +718,14 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant__ PrefixAttnParams p) {
   constexpr int kPer = D / 32;  // output columns of a lane
   __shared__ float s_lse[kJoinThreads];
-  grid_dep_wait();
-  grid_dep_launch();
+  // The lengths were written before the kernels whose results this one joins, and those
+  // began after them: they can be read while the last of them still runs.
+  if (p.split_p + p.split_o == 0) grid_dep_wait();
   const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = own_length(p, b);
+  grid_dep_wait();
+  grid_dep_launch();
   if (p.split_o == 0 && kv == 0 && threadIdx.x == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
   const int own = len > 0 ? (len + p.chunk - 1) / p.chunk : 0;
   const int n = p.split_p + own;
@@ -778,31 +793,43 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
 
 // The launch shape: pure functions of the sizes, shared by the workspace's size.
 struct Shape {
-  int pairs, blocks, split_p, chunk, split_o;
+  int pairs, blocks, split_p, ctas_p, chunk, split_o;
 };
-Shape shape_of(long long batch, long long group, long long heads_kv, long long prefix, long long cap) {
+Shape shape_of(long long batch, long long group, long long heads_kv, long long prefix, long long cap, long long d) {
   Shape s = {};
   const long long rows = batch * group;
   s.pairs = static_cast<int>((rows + 255) / 256);
   s.blocks = static_cast<int>((prefix + 127) / 128);
+  s.ctas_p = kSms;
   if (prefix > 0) {
-    // key splits: the fewest block steps of the busiest SM, counting about two
-    // blocks' time for an item's start and its partial results
     const long long bases = heads_kv * s.pairs;
+    if (cap > 0) {
+      // The prefix part leaves SMs to the own part, which runs beside it: its share of
+      // the two parts' SM time, 2.4 us for a block step (1.2 with one tile of rows) and
+      // 0.55 us for 64 own keys, if the caches are half full (the lengths are the
+      // device's). Fuller caches go on after the prefix, on all SMs. 128 sequences,
+      // 32768 + 1025 keys on average: 94 us on 96 SMs, 98 on 112, 108 on 128, 111 on all.
+      const double t_p = bases * s.blocks * (rows > 128 ? 2.4 : 1.2);
+      const double t_o = 0.5 * batch * heads_kv * ((group + 15) / 16) * cap / 64 * 0.55 * d / 128;
+      s.ctas_p = static_cast<int>(kSms * t_p / (t_p + t_o) + 0.5);
+      if (s.ctas_p < kSms / 4) s.ctas_p = kSms / 4;
+    }
+    // key splits: the fewest block steps of the busiest CTA, counting about four
+    // blocks' time for an item's start and its partial results
     long long best = -1;
     for (int c = 1; c <= s.blocks && c <= 2 * kSms; ++c) {
-      const long long waves = (bases * c + kSms - 1) / kSms;
-      const long long cost = waves * ((s.blocks + c - 1) / c + 2);
+      const long long waves = (bases * c + s.ctas_p - 1) / s.ctas_p;
+      const long long cost = waves * ((s.blocks + c - 1) / c + 4);
       if (best < 0 || cost < best) {
         best = cost;
         s.split_p = c;
       }
-      if (bases * c >= 2 * kSms) break;
+      if (bases * c >= 2 * s.ctas_p) break;
     }
   }
   if (cap > 0) {
-    // own keys per split: 512, halved while the grid leaves SMs idle
-    s.chunk = 512;
+    // own keys per split: 1024, halved while the grid leaves SMs idle
+    s.chunk = 1024;
     const long long units = batch * heads_kv * ((group + 15) / 16);
     while (s.chunk > kOwnKeys && units * ((cap + s.chunk - 1) / s.chunk) < 2 * kSms) s.chunk /= 2;
     s.split_o = static_cast<int>((cap + s.chunk - 1) / s.chunk);
@@ -846,8 +873,8 @@ tp_status launch_all(const PrefixAttnParams &p, const PrefixMaps &maps, cudaStre
   if (e != cudaSuccess) return cuda_fail(e);
   tp_status st = TP_OK;
   if (p.split_p > 0) {
-    const int items = p.heads_kv * p.pairs * p.split_p, sms = num_sms();
-    st = launched(launch_kernel(k_prefix_part<D>, dim3(static_cast<unsigned>(items < sms ? items : sms)),
+    const int items = p.heads_kv * p.pairs * p.split_p;
+    st = launched(launch_kernel(k_prefix_part<D>, dim3(static_cast<unsigned>(items < p.ctas_p ? items : p.ctas_p)),
                                 dim3(kPrefThreads), PrefCfg<D>::kSmem, s, 1, p, maps));
     if (st != TP_OK) return st;
   }
@@ -879,7 +906,7 @@ extern "C" size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t bat
   tp_dims d;
   if (!plan || batch < 0 || prefix < 0 || capacity < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
   if (batch == 0 || !sizes_ok(d, batch, prefix, capacity)) return 0;
-  const Shape s = shape_of(batch, d.num_q_heads / d.num_kv_heads, d.num_kv_heads, prefix, capacity);
+  const Shape s = shape_of(batch, d.num_q_heads / d.num_kv_heads, d.num_kv_heads, prefix, capacity, d.head_dim);
   return regions_of(s, batch, d.num_q_heads, d.head_dim, capacity, weights != 0).total;
 }
 
@@ -924,7 +951,7 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
   if (!sizes_ok(dims, batch, P, cap)) return TP_ERR_UNSUPPORTED;
   const bool weights = weight_out && cap > 0;
   const long long group = dims.num_q_heads / dims.num_kv_heads;
-  const Shape shape = shape_of(batch, group, dims.num_kv_heads, P, cap);
+  const Shape shape = shape_of(batch, group, dims.num_kv_heads, P, cap, hd);
   const Regions reg = regions_of(shape, batch, dims.num_q_heads, hd, cap, weights);
   if (batch > 0 && reg.total > 0) {
     if (!workspace || workspace_bytes < reg.total) return TP_ERR_WORKSPACE;
@@ -979,6 +1006,7 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
   p.blocks = shape.blocks;
   p.split_p = shape.split_p;
   p.pairs = shape.pairs;
+  p.ctas_p = shape.ctas_p;
   p.cap = static_cast<int>(cap);
   p.chunk = shape.chunk;
   p.split_o = shape.split_o;

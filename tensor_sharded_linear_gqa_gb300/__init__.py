@@ -472,63 +472,64 @@ def tp_attn_proj(plan: Plan, x, w_q, w_k, w_v, q, k, v, a, w_o, y, combine: int,
 
 
 # ---- between the projections ----------------------------------------------------
-class _Scratch(threading.local):
+class _Scratch:
     """Descriptors of the call being made, one buffer per thread (the library reads them during the
-    call only): a small call spends less time on its kernels than on building ctypes objects."""
+    call only). Each method packs tensors and returns the address: a small call spends less time
+    on its kernels than building ctypes objects for its arguments would take."""
 
-    def __init__(self):
-        self.room = 0
-        self.grow(256)
+    __slots__ = ("buf", "base", "room", "used")
 
-    def grow(self, room: int) -> None:
+    def __init__(self, room: int):
         self.buf = bytearray(_DESC.size * room)
         self.base = ctypes.addressof((ctypes.c_char * len(self.buf)).from_buffer(self.buf))
-        self.room, self.used = room, 0
-
-
-_scratch = _Scratch()
-
-
-class _Args:
-    """Packs one call's tensors: each method returns the address of what it packed."""
-
-    __slots__ = ("s",)
-
-    def __init__(self, most: int):
-        self.s = s = _scratch
-        s.used = 0
-        if most > s.room:
-            s.grow(most)
-
-    def many(self, seq, n: int):
-        """A per-rank argument with at least n entries; an arr() the caller keeps goes as it is."""
-        if isinstance(seq, ctypes.Array):
-            if len(seq) < n:
-                raise ValueError(f"expected {n} tensors, one per rank or kv source")
-            return seq
-        if len(seq) < n:
-            raise ValueError(f"expected {n} tensors, one per rank or kv source")
-        s = self.s
-        first = at = s.used * _DESC.size
-        for i in range(n):
-            _DESC.pack_into(s.buf, at, *_fields(seq[i]))
-            at += _DESC.size
-        s.used += n
-        return s.base + first
+        self.room, self.used = room, 0  # tensors; bytes
 
     def one(self, t):
         """A single descriptor; None for None."""
         if t is None:
             return None
-        s = self.s
-        at = s.used * _DESC.size
-        _DESC.pack_into(s.buf, at, *_fields(t))
-        s.used += 1
-        return s.base + at
+        at = self.used
+        self.used = at + _DESC_SIZE
+        if type(t) is TpTensor:
+            _PACK(self.buf, at, *_fields(t))
+            return self.base + at
+        rows, cols = t.shape
+        ld, step = t.stride()
+        dt = _DTYPES.get(t.dtype)
+        if step != 1 or dt is None or not rows or not cols or not t.is_cuda:
+            _PACK(self.buf, at, *_fields(t))  # an empty tensor, the first of all, or an error's words
+        else:
+            _PACK(self.buf, at, t.data_ptr(), dt, 0, rows, cols, ld if rows > 1 or ld > cols else cols)
+        return self.base + at
+
+    def many(self, seq, n: int):
+        """A per-rank argument with at least n entries; an arr() the caller keeps goes as it is."""
+        if len(seq) < n:
+            raise ValueError(f"expected {n} tensors, one per rank or kv source")
+        if isinstance(seq, ctypes.Array):
+            return seq
+        first = self.base + self.used
+        one = self.one
+        for i in range(n):
+            one(seq[i])
+        return first
 
     def row(self, t):
         """A vector: its 1-D tensor is the [1 x n] view that the library takes."""
-        return self.one(t if t is None or isinstance(t, TpTensor) or t.dim() == 2 else t.unsqueeze(0))
+        return self.one(t if t is None or type(t) is TpTensor or t.dim() == 2 else t.unsqueeze(0))
+
+
+_DESC_SIZE, _PACK = _DESC.size, _DESC.pack_into
+_local = threading.local()
+
+
+def _args(most: int) -> _Scratch:
+    """The thread's scratch, emptied, with room for `most` tensors."""
+    s = getattr(_local, "scratch", None)
+    if s is None or s.room < most:
+        s = _local.scratch = _Scratch(max(most, 256))
+    s.used = 0
+    return s
 
 
 def _opt_ptr(t, dtype: str):
@@ -540,7 +541,7 @@ def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=Non
     y = z * rsqrt(mean(z^2) + eps) * weight, in bf16, or as e4m3 codes with y_scale [T]."""
     many = isinstance(x, (list, tuple, ctypes.Array))
     n = len(x) if many else 1
-    a = _Args(n + 4)
+    a = _args(n + 4)
     st = _lib.tp_add_rmsnorm(n, a.many(x, n) if many else a.one(x), a.one(residual), a.row(weight), eps,
                              a.one(residual_out), a.one(y), _opt_ptr(y_scale, "torch.float32"), _stream(stream))
     if st:
@@ -551,7 +552,7 @@ def tp_linear_epilogue(tp_size: int, shard: int, x, w, y, bias=None, activation:
                        x_scale=None, w_scale=None, stream=None) -> None:
     """y = activation(x w^T * x_scale * w_scale + bias) + residual. shard: TP_SHARD_COLUMN (x: [X],
     w: the ranks' weight rows) or TP_SHARD_ROW (x, w: the ranks' slices of the input features)."""
-    a = _Args(2 * tp_size + 3 if tp_size > 0 else 3)
+    a = _args(2 * tp_size + 3 if tp_size > 0 else 3)
     st = _lib.tp_linear_epilogue(tp_size, shard, a.many(x, tp_size if shard == TP_SHARD_ROW else 1),
                                  _opt_ptr(x_scale, "torch.float32"), a.many(w, tp_size), _opt_ptr(w_scale, "torch.float32"),
                                  a.row(bias), activation, a.one(residual), a.one(y), _stream(stream))
@@ -572,7 +573,7 @@ def tp_prefix_attn(plan: Plan, q, k_prefix, v_prefix, k_own, v_own, lengths, a, 
     """One new token per sequence over the shared prefix and the sequence's own cache. q, a: one
     entry per rank; caches and weights: one per kv source; workspace: a CUDA byte tensor."""
     n, src = plan.dims.tp_size, _kv_sources(plan)
-    g = _Args(2 * n + 6 * src)
+    g = _args(2 * n + 6 * src)
     st = _lib.tp_prefix_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_prefix, src), g.many(v_prefix, src),
                              g.many(k_own, src), g.many(v_own, src), _dev_ptr(lengths, "torch.int32"),
                              None if weight_in is None else g.many(weight_in, src),
@@ -591,7 +592,7 @@ def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int,
         raise ValueError("kept must hold sources * batch * heads * budget entries")
     if lengths_out.numel() != batch:
         raise ValueError("lengths_out must have one entry per sequence")
-    a = _Args(6 * src)
+    a = _args(6 * src)
     st = _lib.tp_cache_evict(plan.handle, batch, _dev_ptr(lengths, "torch.int32"), a.many(k, src), a.many(v, src),
                              a.many(weight, src), budget, n_first, n_recent, a.many(k_out, src), a.many(v_out, src),
                              a.many(weight_out, src), _dev_ptr(lengths_out, "torch.int32"), _dev_ptr(kept, "torch.int32"),

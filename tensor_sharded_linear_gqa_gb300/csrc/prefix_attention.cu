@@ -41,6 +41,7 @@ struct PrefixAttnParams {
   int prefix, blocks, split_p, pairs, ctas_p;  // 128-key blocks; key splits; 256-row tile pairs per kv head; CTAs
   int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
   int has_prev;                        // k_own_part runs behind k_prefix_part
+  int one_prefix;                      // every source's prefix lies in one tensor, in head order: one map of each
   float scale_log2;
   const int *lengths;
   float *part_o;    // [split][row][d]
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       for (int it = blockIdx.x; run && it < items; it += gridDim.x) {
         int kv, pair, split, b0, b1;
         item(it, kv, pair, split, b0, b1);
-        const int src = kv / p.heads_per_source;
+        const int src = p.one_prefix ? 0 : kv / p.heads_per_source;
         const int col = (kv - src * p.heads_per_source) * D;
         const CUtensorMap *map = lane == 0 ? &maps.k[src] : &maps.v[src];
         for (int j = b0; j < b1; ++j, ++g) {
@@ -971,10 +972,16 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
     p.a[r] = a[r].ptr;
     p.a_ld[r] = a[r].ld;
   }
+  // Sources whose prefixes are neighbouring columns of one tensor need one map together.
+  p.one_prefix = 1;
+  for (int r = 1; r < sources; ++r)
+    for (const tp_tensor *t : {k_prefix, v_prefix})
+      if (t[r].ld != t[0].ld || static_cast<const char *>(t[0].ptr) + r * kvc * 2 != t[r].ptr) p.one_prefix = 0;
   for (int r = 0; r < sources; ++r) {
-    if (P > 0) {
+    if (P > 0 && (r == 0 || !p.one_prefix)) {
       tp_tensor k = k_prefix[r], v = v_prefix[r];
-      if (P == 1) k.ld = v.ld = (kvc + 7) / 8 * 8;  // the pitch of a single row is free
+      if (p.one_prefix) k.cols = v.cols = kvc * sources;
+      if (P == 1) k.ld = v.ld = kvc * sources;  // the pitch of a single row is free
       if (!encode_rows_map(&maps.k[r], k, 128) || !encode_rows_map(&maps.v[r], v, 128)) return TP_ERR_INVALID_ARG;
     }
     p.k_own[r] = k_own[r].ptr;

@@ -2015,6 +2015,22 @@ bool encode_rows_map(CUtensorMap *map, const tp_tensor &t, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows_map_3d(CUtensorMap *map, const tp_tensor &t, int box_rows, int box_kt) {
+  EncodeTiledFn enc = encode_fn();
+  const bool f8 = t.dtype == TP_E4M3;
+  const long long elems = f8 ? 128 : 64;
+  if (!enc || t.cols % elems != 0) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(elems), static_cast<cuuint64_t>(t.rows),
+                              static_cast<cuuint64_t>(t.cols / elems)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(t.ld) * (f8 ? 1 : 2), 128};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(elems), static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_kt)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 GemmBuilder::GemmBuilder() { std::memset(&p, 0, sizeof(p)); }
 
 int GemmBuilder::add_map(const void *base, long long rows, long long k, long long ld, int box_rows,

@@ -51,10 +51,11 @@ constexpr int kWTile = 128 * 128;  // bytes of one 128-row, 128-byte-wide box
 // line of its parameters is a miss of a few hundred nanoseconds.
 struct LinearParams {
   int tok_tile, stages, split;       // k_linear_split: token tile, stages (one k-tile each), CTAs sharing K
+  int box3;                          // k_linear_pair: one copy of a 3-D box brings a stage's k-tiles of an operand
   int regions, region_cols;          // its accumulators in TMEM and their stride
   int early_w;                       // W loads before the dependency wait
   int n_slices, n_shards, kt_total, n_tiles, rows, m_tiles;
-  int act, y_f32, res_f32, bias_f32;
+  int act, y_f32, res_f32, bias_f32, wide32;  // wide32: f32 rows of residual and y in 32-byte accesses
   const float *x_scale, *w_scale;  // null: no scales
   const void *bias, *res;          // null: none
   void *y;
@@ -94,6 +95,19 @@ __device__ __forceinline__ void activate(float (&f)[N], int act) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = __fdividef(f[i], 1.0f + __expf(-f[i]));
   }
+}
+
+// 32 bytes in one access.
+__device__ __forceinline__ void load32(const float *p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store32(float *p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // N neighbouring values of a row of f32 or bf16 as f32; `left` of them exist, the
@@ -547,10 +561,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint32_t lead_full = ptx::mapa_shared(full_bar(st), 0);
           if (issue) {
             if (leader) ptx::mbar_arrive_expect_tx(full_bar(st), 2 * C::kStage);
+            // k-tiles past the slice's end read zeros
+            if (p.box3) {
+              ptx::tma_load_3d_pair(sX + st * kSub * kWTile, xm, 0, x_row, ks * kSub, lead_full);
+              ptx::tma_load_3d_pair(sW + st * kSub * C::kWBytes, wm, 0, w_row, ks * kSub, lead_full);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) {  // a k-tile past the slice's end reads zeros
-              ptx::tma_load_2d_pair(sX + (st * kSub + j) * kWTile, xm, (ks * kSub + j) * kElems, x_row, lead_full);
-              ptx::tma_load_2d_pair(sW + (st * kSub + j) * C::kWBytes, wm, (ks * kSub + j) * kElems, w_row, lead_full);
+              for (int j = 0; j < kSub; ++j) {
+                ptx::tma_load_2d_pair(sX + (st * kSub + j) * kWTile, xm, (ks * kSub + j) * kElems, x_row, lead_full);
+                ptx::tma_load_2d_pair(sW + (st * kSub + j) * C::kWBytes, wm, (ks * kSub + j) * kElems, w_row, lead_full);
+              }
             }
           }
           if (++st == S) {
@@ -666,7 +686,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int c = 0; c < kHalf; c += 8) {
           if (c >= n_left) break;
           float res[8], f[8];
-          if (p.res) load_row(p.res, p.res_f32, tok * p.res_ld + col + c, n_left - c, res);
+          const bool wide = p.wide32 && n_left - c >= 8;
+          if (p.res) {
+            if (wide && p.res_f32) load32(static_cast<const float *>(p.res) + tok * p.res_ld + col + c, res);
+            else load_row(p.res, p.res_f32, tok * p.res_ld + col + c, n_left - c, res);
+          }
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 t = *reinterpret_cast<const float4 *>(terms + c + i);
@@ -678,7 +702,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] += res[i];
           }
-          store_row(p.y, p.y_f32, tok * p.y_ld + col + c, n_left - c, f);
+          if (wide && p.y_f32) store32(static_cast<float *>(p.y) + tok * p.y_ld + col + c, f);
+          else store_row(p.y, p.y_f32, tok * p.y_ld + col + c, n_left - c, f);
         }
       }
     }
@@ -859,6 +884,11 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
   p.y_f32 = y->dtype == TP_F32;
   p.res_f32 = residual && residual->dtype == TP_F32;
   p.bias_f32 = bias && bias->dtype == TP_F32;
+  // every f32 row and first column on 32 bytes
+  p.wide32 = 1;
+  for (const tp_tensor *t : {static_cast<const tp_tensor *>(y), residual})
+    if (t && t->dtype == TP_F32) p.wide32 = p.wide32 && ptr_aligned(t->ptr, 32) && t->ld % 8 == 0;
+  for (int i = 0; !row && i + 1 < parts; ++i) p.wide32 = p.wide32 && ws[i].rows % 8 == 0;
   p.x_scale = x_scale;
   p.w_scale = w_scale;
   p.bias = bias ? bias->ptr : nullptr;
@@ -921,10 +951,18 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     p.regions = 1;
     while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= 256) p.regions *= 2;
   }
+  // A copy costs its issue whatever its size, so where every slice is whole k-tiles one
+  // box spans a stage's k-tiles (4096 x 8192 x 28672 in e4m3: 644 us, 656 with one copy
+  // a k-tile; k_linear_split, whose weights come at memory's rate, gains nothing).
+  p.box3 = pair;
+  for (int i = 0; i < p.n_slices; ++i) p.box3 = p.box3 && xs[i].cols % elems == 0;
+  auto encode = [&](CUtensorMap *m, const tp_tensor &t, int rows) {
+    return p.box3 ? encode_rows_map_3d(m, t, rows, kSub) : encode_rows_map(m, t, rows);
+  };
   for (int i = 0; i < p.n_slices; ++i)
-    if (!encode_rows_map(&p.x[i], xs[i], x_box)) return TP_ERR_INVALID_ARG;
+    if (!encode(&p.x[i], xs[i], x_box)) return TP_ERR_INVALID_ARG;
   for (int i = 0; i < parts; ++i)
-    if (!encode_rows_map(&p.w[i], ws[i], w_box)) return TP_ERR_INVALID_ARG;
+    if (!encode(&p.w[i], ws[i], w_box)) return TP_ERR_INVALID_ARG;
   if (pair) return dt == TP_E4M3 ? launch_pair_bn<true>(p, bn, s) : launch_pair_bn<false>(p, bn, s);
   size_t smem = 1024 + static_cast<size_t>(p.stages) * (kWTile + p.tok_tile * 128);
   const size_t out = 1024 + static_cast<size_t>(p.tok_tile) * 512;  // the partials lie over the stages

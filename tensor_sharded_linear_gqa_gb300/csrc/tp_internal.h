@@ -333,6 +333,10 @@ bool encode_bf16_map_2d(CUtensorMap *map, const void *base, long long rows, long
 
 // The same for a bf16 or e4m3 view: boxes 128 bytes wide (64 bf16, 128 e4m3) x box_rows rows.
 bool encode_rows_map(CUtensorMap *map, const tp_tensor &t, int box_rows);
+// The view as [k-tiles][rows][128 bytes] (its columns a whole number of 128-byte
+// k-tiles): one copy of a box brings box_kt neighbouring k-tiles, each laid out as
+// encode_rows_map's box.
+bool encode_rows_map_3d(CUtensorMap *map, const tp_tensor &t, int box_rows, int box_kt);
 
 // ---------------------------------------------------------------------------
 // Attention core (attention.cu): one CTA per (128-query tile, q head).

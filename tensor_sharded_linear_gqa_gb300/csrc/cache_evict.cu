@@ -86,11 +86,31 @@ __device__ __forceinline__ void block_scan2(int a, int b, int &ea, int &eb, int 
   __syncthreads();  // part may be written again
 }
 
-// One CTA per (sequence, source, head): kept positions and weights.
+// Exclusive prefix sum of one counter over the CTA's threads. The next use of `part`
+// comes after another barrier of the caller's.
+__device__ __forceinline__ int block_scan(int a, int *part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int ia = a;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, ia, o);
+    if (lane >= o) ia += u;
+  }
+  if (lane == 31) part[warp] = ia;
+  __syncthreads();
+  int p = lane < warp ? part[lane] : 0;  // the warps before this one
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+  return __shfl_sync(0xffffffffu, p, 0) + ia - a;
+}
+
+// One CTA per (sequence, source, head): kept positions and weights. A cache of one
+// chunk keeps its weights and keys in registers from the first read on; a longer one
+// its keys in shared memory, or, beyond that, reads the weights again.
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int s_hist[kBins];
-  __shared__ int s_bin, s_above;
+  __shared__ __align__(16) int s_hist[kBins];
+  __shared__ int s_bin, s_above, s_part[kSelThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x;
@@ -109,34 +129,54 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   if (len > p.budget) {
     const int lo = p.n_first, hi = len - p.n_recent;  // candidates [lo, hi)
     int want = p.budget - p.n_first - p.n_recent;     // of them stay; hi - lo > want
-    auto key_at = [&](int j) { return p.keys_in_smem ? s_keys[j] : weight_key(w[j]); };
-    if (p.keys_in_smem) {
+    const bool one = len <= kSelChunk;
+    float val[kSelPer];
+    uint32_t key[kSelPer];
+    auto read_chunk = [&](int c0) {
+#pragma unroll
+      for (int i = 0; i < kSelPer; ++i) {
+        const int j = c0 + tid * kSelPer + i;
+        val[i] = j < len ? w[j] : 0.0f;
+        key[i] = weight_key(val[i]);
+      }
+    };
+    if (one) {
+      read_chunk(0);
+    } else if (p.keys_in_smem) {
       for (int j = tid; j < len; j += kSelThreads) s_keys[j] = weight_key(w[j]);
     }
-    uint32_t prefix = 0, mask = 0;
+    uint32_t prefix = 0;
     int equal = 0;  // how many of the keys equal to the threshold stay
     if (want > 0) {
-      const int shifts[3] = {21, 10, 0};
-      const int bins[3] = {2048, 2048, 1024};
 #pragma unroll
       for (int pass = 0; pass < 3; ++pass) {
-        for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+        // digits of 11, 11 and 10 bits; a key counts while its higher digits are the threshold's
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
+        const uint32_t mask = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
+        for (int i = tid * 4; i < kBins; i += kSelThreads * 4) *reinterpret_cast<int4 *>(s_hist + i) = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-          const uint32_t key = key_at(j);
-          if ((key & mask) == prefix) atomicAdd(&s_hist[(key >> shifts[pass]) & (bins[pass] - 1)], 1);
+        auto count = [&](uint32_t k) {
+          if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+        };
+        if (one) {
+#pragma unroll
+          for (int i = 0; i < kSelPer; ++i) {
+            const int j = tid * kSelPer + i;
+            if (j >= lo && j < hi) count(key[i]);
+          }
+        } else {
+          for (int j = lo + tid; j < hi; j += kSelThreads) count(p.keys_in_smem ? s_keys[j] : weight_key(w[j]));
         }
         __syncthreads();
         // thread t owns the four bins below bins - 4t: a prefix sum from the top
-        const int top = bins[pass] - 1 - tid * 4;
-        int c[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[i] = top - i >= 0 ? s_hist[top - i] : 0;
-          sum += c[i];
+        const int top = bins - 1 - tid * 4;
+        int c[4] = {0, 0, 0, 0};
+        if (top >= 0) {
+          const int4 v = *reinterpret_cast<const int4 *>(s_hist + top - 3);
+          c[0] = v.w; c[1] = v.z; c[2] = v.y; c[3] = v.x;
         }
-        int before, unused, total, unused2;
-        block_scan2(sum, 0, before, unused, total, unused2);
+        const int sum = c[0] + c[1] + c[2] + c[3];
+        const int before = block_scan(sum, s_part);
         // the bin in which the want-th largest lies
         if (before < want && before + sum >= want) {
           int above = before;
@@ -151,10 +191,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
           }
         }
         __syncthreads();
-        prefix |= static_cast<uint32_t>(s_bin) << shifts[pass];
-        mask |= static_cast<uint32_t>(bins[pass] - 1) << shifts[pass];
+        prefix |= static_cast<uint32_t>(s_bin) << shift;
         want -= s_above;
-        __syncthreads();
       }
       equal = want;
     }
@@ -163,23 +201,17 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     // read before any of its places (all at or below their positions) is written.
     int kept_before = 0, equal_before = 0;
     for (int c0 = 0; c0 < len; c0 += kSelChunk) {
-      float val[kSelPer];
+      if (!one) read_chunk(c0);
       bool sure[kSelPer], tie[kSelPer];
       int n_sure = 0, n_tie = 0;
 #pragma unroll
       for (int i = 0; i < kSelPer; ++i) {
         const int j = c0 + tid * kSelPer + i;
-        sure[i] = tie[i] = false;
-        val[i] = 0.0f;
-        if (j < len) {
-          val[i] = w[j];
-          const bool forced = j < lo || j >= hi;
-          const uint32_t key = weight_key(val[i]);
-          sure[i] = forced || (!none && key > prefix);
-          tie[i] = !forced && !none && key == prefix;
-          n_sure += sure[i];
-          n_tie += tie[i];
-        }
+        const bool forced = j < lo || j >= hi;
+        sure[i] = j < len && (forced || (!none && key[i] > prefix));
+        tie[i] = j < len && !forced && !none && key[i] == prefix;
+        n_sure += sure[i];
+        n_tie += tie[i];
       }
       int es, et, ts, tt;
       block_scan2(n_sure, n_tie, es, et, ts, tt);  // its barriers also close the chunk's reads
@@ -390,8 +422,8 @@ extern "C" tp_status tp_cache_evict(const tp_plan *plan, int64_t batch, const in
   p.n_first = n_first;
   p.n_recent = n_recent;
   p.d = static_cast<int>(d);
-  // keys in shared memory only where a cache can lose keys and they fit
-  p.keys_in_smem = cap > budget && cap <= kMaxSmemKeys;
+  // keys in shared memory where a cache can lose keys, outgrows the registers and fits
+  p.keys_in_smem = cap > budget && cap > kSelChunk && cap <= kMaxSmemKeys;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const size_t smem = p.keys_in_smem ? static_cast<size_t>(cap) * 4 : 0;
   cudaError_t ce = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemKeys * 4);

@@ -227,81 +227,93 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
-      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
-      bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (*abort_flag || !ptx::mbar_wait(bar, parity, p.wait_ns)) {
-          if (!*abort_flag) record(p.status, kDevTimeoutMma);
-          ok = false;
-          return false;
-        }
-        return true;
-      };
-      auto issue_s = [&](int x, int g) {  // S_X = Q_X K^T
-        const uint32_t qa = sQ + static_cast<uint32_t>(x) * C::kTile, ka = sK0 + static_cast<uint32_t>(g & 1) * C::kTile;
+  } else if (warp == 1) {  // converged; one lane issues (see elect_one)
+    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+    const bool leader = ptx::elect_one();
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, p.wait_ns) && *abort_flag == 0)) return true;
+      if (*abort_flag == 0) record(p.status, kDevTimeoutMma);
+      ok = false;
+      return false;
+    };
+    auto commit = [&](uint32_t bar) {
+      if (leader) ptx::mma_commit(bar);
+      __syncwarp();
+    };
+    auto issue_s = [&](int x, int g) {  // S_X = Q_X K^T
+      const uint32_t qa = sQ + static_cast<uint32_t>(x) * C::kTile, ka = sK0 + static_cast<uint32_t>(g & 1) * C::kTile;
+      const uint32_t d = tmem + static_cast<uint32_t>(x * 128);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_bf16(tmem + static_cast<uint32_t>(x * 128), ptx::smem_desc_sw128(qa + (kk >> 2) * kSubTile) + 2 * (kk & 3),
+          ptx::mma_bf16(d, ptx::smem_desc_sw128(qa + (kk >> 2) * kSubTile) + 2 * (kk & 3),
                         ptx::smem_desc_sw128(ka + (kk >> 2) * kSubTile) + 2 * (kk & 3), idesc_s, kk > 0 ? 1u : 0u);
         ptx::mma_commit(s_full0 + 8 * x);
-      };
-      auto issue_pv = [&](int x, int g, bool first) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
-        const uint32_t va = sV0 + static_cast<uint32_t>(g & 1) * C::kTile;
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int x, int g, bool first) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
+      const uint32_t va = sV0 + static_cast<uint32_t>(g & 1) * C::kTile;
+      const uint32_t d = tmem + 256u + static_cast<uint32_t>(x * 128), a = tmem + static_cast<uint32_t>(x * 128);
+      const uint32_t more = first ? 0u : 1u;
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_bf16_ts(tmem + 256u + static_cast<uint32_t>(x * 128), tmem + static_cast<uint32_t>(x * 128) + 8u * kk,
-                           desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, (!first || kk > 0) ? 1u : 0u);
-      };
-      int g = 0;
-      uint32_t np[2] = {0, 0}, nact[2] = {0, 0};
-      for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-        int kv, pair, split, b0, b1;
-        item(it, kv, pair, split, b0, b1);
-        const int nb = b1 - b0;
-        const int tiles = (2 * pair + 1) * 128 < rows ? 2 : 1;
-        if (!wait(k_full0 + 8 * (g & 1), (g >> 1) & 1)) break;
+          ptx::mma_bf16_ts(d, a + 8u * kk, desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, kk > 0 ? 1u : more);
+      }
+      __syncwarp();
+    };
+    int g = 0;
+    uint32_t np[2] = {0, 0}, nact[2] = {0, 0};
+    for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+      int kv, pair, split, b0, b1;
+      item(it, kv, pair, split, b0, b1);
+      const int nb = b1 - b0;
+      const int tiles = (2 * pair + 1) * 128 < rows ? 2 : 1;
+      if (!wait(k_full0 + 8 * (g & 1), (g >> 1) & 1)) break;
+      for (int x = 0; ok && x < tiles; ++x) {
+        if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
+        ptx::tc_fence_after();
+        issue_s(x, g);
+      }
+      if (!ok) break;
+      commit(k_empty0 + 8 * (g & 1));
+      for (int j = 0; ok && j < nb; ++j) {
+        const int gj = g + j;
+        if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
+        bool next_k = false;
         for (int x = 0; ok && x < tiles; ++x) {
-          if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
+          if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
+          ++np[x];
+          if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
           ptx::tc_fence_after();
-          issue_s(x, g);
+          issue_pv(x, gj, j == 0);
+          if (j + 1 == nb) {
+            commit(o_full0 + 8 * x);
+          } else {
+            if (!next_k) {
+              if (!wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
+              ptx::tc_fence_after();
+              next_k = true;
+            }
+            issue_s(x, gj + 1);
+          }
         }
         if (!ok) break;
-        ptx::mma_commit(k_empty0 + 8 * (g & 1));
-        for (int j = 0; ok && j < nb; ++j) {
-          const int gj = g + j;
-          if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
-          bool next_k = false;
-          for (int x = 0; ok && x < tiles; ++x) {
-            if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
-            ++np[x];
-            if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
-            ptx::tc_fence_after();
-            issue_pv(x, gj, j == 0);
-            if (j + 1 == nb) {
-              ptx::mma_commit(o_full0 + 8 * x);
-            } else {
-              if (!next_k) {
-                if (!wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
-                ptx::tc_fence_after();
-                next_k = true;
-              }
-              issue_s(x, gj + 1);
-            }
-          }
-          if (!ok) break;
-          ptx::mma_commit(v_empty0 + 8 * (gj & 1));
-          if (next_k) ptx::mma_commit(k_empty0 + 8 * ((gj + 1) & 1));
-        }
-        for (int x = 0; x < tiles; ++x) ++nact[x];
-        g += nb;
+        commit(v_empty0 + 8 * (gj & 1));
+        if (next_k) commit(k_empty0 + 8 * ((gj + 1) & 1));
       }
-      if (!ok) *abort_flag = 1;
+      for (int x = 0; x < tiles; ++x) ++nact[x];
+      g += nb;
+    }
+    if (!ok) *abort_flag = 1;
+    if (leader) {
       ptx::mma_commit(drain);
       if (!ptx::mbar_wait(drain, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
     }
+    __syncwarp();
   } else {
     const int x = (warp - 2) >> 2;
     const int qw = warp & 3;

@@ -841,8 +841,8 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
     }
   }
   if (cap > 0) {
-    // own keys per split: 1024, halved while the grid leaves SMs idle
-    s.chunk = 1024;
+    // own keys per split: 2048, halved while the grid leaves SMs idle
+    s.chunk = 2048;
     const long long units = batch * heads_kv * ((group + 15) / 16);
     while (s.chunk > kOwnKeys && units * ((cap + s.chunk - 1) / s.chunk) < 2 * kSms) s.chunk /= 2;
     s.split_o = static_cast<int>((cap + s.chunk - 1) / s.chunk);

@@ -106,7 +106,10 @@ __device__ __forceinline__ int block_scan(int a, int *part) {
 
 // One CTA per (sequence, source, head): kept positions and weights. A cache of one
 // chunk keeps its weights and keys in registers from the first read on; a longer one
-// its keys in shared memory, or, beyond that, reads the weights again.
+// its keys in shared memory, or, beyond that, reads the weights again. Bound by
+// latency: about ten barriers and three dependent reads, some 7 us before the gather
+// whatever the number of caches that one wave holds (256 threads with eight positions
+// each issue half the instructions and take as long).
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) int s_hist[kBins];
@@ -260,9 +263,11 @@ constexpr int kPlaceUnroll = 4;   // the same, in place
 // memory, are read and written at about the same time; a thread keeps one 16-byte
 // piece of the head's row and steps over the places, four loads in flight. Each
 // CTA waits twice (for kept, then for the rows), so full occupancy, 32 registers a
-// thread, carries it: 64 caches of up to 2048 keys to 1024 take 93 us in all,
-// against 104 with eight loads a thread and 126 with sixteen at the occupancy that
-// those leave. Rows are read and written once: streaming accesses.
+// thread, carries it: when that was set, 64 caches of up to 2048 keys (8 kv heads of
+// 128) went to 1024 in 93 us in all, against 104 with eight loads a thread and 126
+// with sixteen at the occupancy that those leave. It is 91 us now, 5.7 TB/s; the
+// gather alone takes 81 at 72% of DRAM's peak. Rows are read and written once:
+// streaming accesses.
 __global__ void __launch_bounds__(kMoveThreads, 8) k_evict_gather(const __grid_constant__ EvictParams p) {
   grid_dep_wait();
   grid_dep_launch();

@@ -94,6 +94,9 @@ __device__ __forceinline__ int own_length(const PrefixAttnParams &p, int b) {
 // is read from there), O at 256 and 384. V is used as it lies, [keys x d], as an
 // MN-major operand, so no transposed copy is made. The running reference maximum
 // m moves only on a split's first block or when a block's sum of p passes 2^64.
+// A block step of both tiles takes 1.8 us (the MMAs alone 0.55): its period is the chain
+// S, softmax, P V of the two tiles. With the MMAs issued under a branch on the lane
+// index, which holds operands outside the uniform registers, it took 2.0 us.
 // ---------------------------------------------------------------------------
 constexpr int kPrefThreads = 320;
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
@@ -485,6 +488,11 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
 // stages, the four warps take 16 keys each and keep their own m, l and O, which
 // are joined at the end. Keys past the length are zero-filled in shared memory,
 // never read from the cache (stale values there may be anything), and masked.
+// Bound by memory on all SMs (268 MB in 45 us, 6 TB/s) and by the steps' latency, 62
+// KB/us an SM with two CTAs, on the SMs that the prefix part leaves. Measured and
+// slower: eight warps that share a step's maximum and P and own output columns (three
+// barriers a step, 23 KB/us); runs of steps across sequences in place of a CTA a
+// split (no better balance than the scheduler's, and a join and a q load in the run).
 // ---------------------------------------------------------------------------
 constexpr int kOwnThreads = 128;
 constexpr int kOwnKeys = 64;
@@ -723,7 +731,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
 
 // ---------------------------------------------------------------------------
 // Joins the splits of a (sequence, kv head): one warp per head of the group, then
-// the own keys' weights.
+// the own keys' weights. Bound by latency: 5 us for 61 sequences' 488 heads of six
+// splits, and 4 us for their weights.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
@@ -818,10 +827,11 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
     const long long bases = heads_kv * s.pairs;
     if (cap > 0) {
       // The prefix part leaves SMs to the own part, which runs beside it: its share of
-      // the two parts' SM time, 2.4 us for a block step (1.2 with one tile of rows) and
-      // 0.55 us for 64 own keys, if the caches are half full (the lengths are the
-      // device's). Fuller caches go on after the prefix, on all SMs. 128 sequences,
-      // 32768 + 1025 keys on average: 94 us on 96 SMs, 98 on 112, 108 on 128, 111 on all.
+      // the two parts' SM time, 2.4 us for a block step with its part of an item's start
+      // and end (1.2 with one tile of rows) and 0.55 us for 64 own keys, if the caches are
+      // half full (the lengths are the device's). Fuller caches go on after the prefix,
+      // on all SMs. 128 sequences, 32768 + 1025 keys on average: 84 us on 96 SMs, 96 on
+      // 80, 98 on 112, 110 on all; 61 sequences, 4099 + 256 keys: 36 on 80, 38 on 112, 42.
       const double t_p = bases * s.blocks * (rows > 128 ? 2.4 : 1.2);
       const double t_o = 0.5 * batch * heads_kv * ((group + 15) / 16) * cap / 64 * 0.55 * d / 128;
       s.ctas_p = static_cast<int>(kSms * t_p / (t_p + t_o) + 0.5);

@@ -19,6 +19,9 @@
 // leaves some SMs free, and k_own_part, which shares nothing with it, does not wait
 // for it: it starts on those SMs, goes on where that kernel's CTAs leave, and waits
 // for it only in its last CTA, so that what follows it on the stream follows both.
+//
+// Few keys and sequences, where three launches cost more than the work, take one:
+// k_direct.
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -41,6 +44,7 @@ struct PrefixAttnParams {
   int prefix, blocks, split_p, pairs, ctas_p;  // 128-key blocks; key splits; 256-row tile pairs per kv head; CTAs
   int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
   int has_prev;                        // k_own_part runs behind k_prefix_part
+  int direct;                          // above 0: k_direct runs instead, with this many CTAs a cluster
   int one_prefix;                      // every source's prefix lies in one tensor, in head order: one map of each
   float scale_log2;
   const int *lengths;
@@ -53,6 +57,8 @@ struct PrefixAttnParams {
   long long q_ld[kMaxRanks32];
   const void *k_own[kMaxRanks32], *v_own[kMaxRanks32];
   long long ko_ld[kMaxRanks32], vo_ld[kMaxRanks32];
+  const void *k_prefix[kMaxRanks32], *v_prefix[kMaxRanks32];
+  long long kp_ld[kMaxRanks32], vp_ld[kMaxRanks32];
   void *a[kMaxRanks32];
   long long a_ld[kMaxRanks32];
   const float *w_in[kMaxRanks32];
@@ -528,6 +534,177 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// One warp's share of a head tile: the q rows as the A operand (rows lane/4 and lane/4
+// + 8), the outputs over all of D, and the rows' running maximum and sum.
+template <int D>
+struct WarpRows {
+  uint32_t qa[D / 16][4];
+  float o[D / 8][4];
+  float m[2], l[2];
+
+  __device__ __forceinline__ void start(const PrefixAttnParams &p, int b, int kv, int g0) {
+    const int lane = threadIdx.x & 31, r_lo = g0 + (lane >> 2), r_hi = r_lo + 8;
+    const uint32_t *q_lo = r_lo < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_lo)) : nullptr;
+    const uint32_t *q_hi = r_hi < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_hi)) : nullptr;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const int at = kk * 8 + (lane & 3);
+      qa[kk][0] = q_lo ? __ldg(q_lo + at) : 0u;
+      qa[kk][1] = q_hi ? __ldg(q_hi + at) : 0u;
+      qa[kk][2] = q_lo ? __ldg(q_lo + at + 4) : 0u;
+      qa[kk][3] = q_hi ? __ldg(q_hi + at + 4) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // Scores of the 16 keys at stage rows row0 .. row0 + 15, in log2 units; keys from the
+  // `left`-th on are masked. s[n][0,1]: row lane/4, keys 8n + 2 (lane%4) + {0, 1};
+  // s[n][2,3]: row lane/4 + 8.
+  __device__ __forceinline__ void scores(uint32_t ks, int row0, int left, float scale_log2, float (&s)[2][4]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const int r = row0 + ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
+      uint32_t kb[4];
+      ldsm4(ks + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), kb);
+      mma16816(s[0], qa[kk], kb[0], kb[1]);
+      mma16816(s[1], qa[kk], kb[2], kb[3]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[n][i] = 8 * n + 2 * (lane & 3) + (i & 1) < left ? s[n][i] * scale_log2 : -INFINITY;
+  }
+
+  // The keys' softmax terms and their part of the outputs; at least one key is there.
+  __device__ __forceinline__ void absorb(uint32_t vs, int row0, float (&s)[2][4]) {
+    const int lane = threadIdx.x & 31;
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float m_new = fmaxf(m[h], mx);
+      // m_new is above -inf unless a score is not a number
+      alpha[h] = m[h] == m_new ? 1.f : ex2(m[h] - m_new);
+      l[h] *= alpha[h];
+      m[h] = m_new;
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= alpha[0];
+        o[i][1] *= alpha[0];
+        o[i][2] *= alpha[1];
+        o[i][3] *= alpha[1];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[n][i] = ex2(s[n][i] - m[i >> 1]);
+        l[i >> 1] += s[n][i];
+      }
+    // P rounded to bf16 for the product, as every GEMM operand here; l sums the unrounded p
+    const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                            pack_bf16(s[1][2], s[1][3])};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int r = row0 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * i + (lane >> 4);
+      uint32_t vb[4];
+      ldsm4_t(vs + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), vb);
+      mma16816(o[2 * i], pa, vb[0], vb[1]);
+      mma16816(o[2 * i + 1], pa, vb[2], vb[3]);
+    }
+  }
+
+  // Puts the warp's m and l into ml[16] and its outputs into so[16][D].
+  __device__ __forceinline__ void put(float2 *ml, float *so) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int r = (lane >> 2) + 8 * h;
+      if ((lane & 3) == 0) ml[r] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2 *>(so + r * D + i * 8 + 2 * (lane & 3)) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+    }
+  }
+};
+// 2^(m - top) for a part (m, l) of a row, 0 for one without keys.
+__device__ __forceinline__ float part_factor(float2 ml, float top) {
+  return ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - top);
+}
+// Four columns of a row over the CTA's four warps: their common maximum, sum and outputs.
+template <int D>
+__device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const float *so, int r, int c, float2 &ml) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][r].x);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = part_factor(s_ml[w][r], top);
+    if (f == 0.f) continue;  // a warp without keys (its outputs may be anything times 0)
+    const float4 ov = *reinterpret_cast<const float4 *>(so + (w * 16 + r) * D + c);
+    sum += f * s_ml[w][r].y;
+    acc.x += f * ov.x;
+    acc.y += f * ov.y;
+    acc.z += f * ov.z;
+    acc.w += f * ov.w;
+  }
+  ml = make_float2(top, sum);
+  return acc;
+}
+// A thread's walk over 64-key tiles of a cache: 16-byte pieces of rows r0, r0 + kRows,
+// ... of K and V into a stage, zeros past the last key.
+template <int D>
+struct TileLoader {
+  static constexpr int kPieces = D / 8;                // 16-byte pieces of a row
+  static constexpr int kRows = kOwnThreads / kPieces;  // rows that the CTA loads at a time: 8 or 16
+  const char *k, *v;
+  long long k_step, v_step;  // bytes of kRows rows
+  int left;                  // keys from this thread's next row on
+  uint32_t to0;              // its place in a stage (rows kRows apart share the swizzle)
+
+  // `row` is the first key's row; `keys` follow.
+  __device__ __forceinline__ void start(const void *kc, long long k_ld, const void *vc, long long v_ld, long long col,
+                                        long long row, int keys) {
+    const int c0 = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
+    k = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(kc) + (row + r0) * k_ld + col + c0 * 8);
+    v = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(vc) + (row + r0) * v_ld + col + c0 * 8);
+    k_step = kRows * k_ld * 2;
+    v_step = kRows * v_ld * 2;
+    left = keys - r0;
+    to0 = static_cast<uint32_t>(r0 * D * 2 + (c0 ^ (r0 & 7)) * 16);
+  }
+  // safe: any readable address, for the copies that read nothing.
+  __device__ __forceinline__ void tile(uint32_t stage, const void *safe) {
+    const uint32_t to = stage + to0;
+#pragma unroll
+    for (int i = 0; i < kOwnKeys / kRows; ++i) {
+      const bool valid = left > 0;
+      cp_async16(to + i * kRows * D * 2, valid ? static_cast<const void *>(k) : safe, valid);
+      cp_async16(to + OwnCfg<D>::kMat + i * kRows * D * 2, valid ? static_cast<const void *>(v) : safe, valid);
+      k += k_step;
+      v += v_step;
+      left -= kRows;
+    }
+  }
+};
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
 template <int D>
 __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_constant__ PrefixAttnParams p) {
   using C = OwnCfg<D>;
@@ -544,58 +721,22 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
   if (j0 < j1) {
     const int src = kv / p.heads_per_source;
     const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
-    const __nv_bfloat16 *k0 = static_cast<const __nv_bfloat16 *>(p.k_own[src]) + static_cast<long long>(b) * p.cap * p.ko_ld[src] + col;
-    const __nv_bfloat16 *v0 = static_cast<const __nv_bfloat16 *>(p.v_own[src]) + static_cast<long long>(b) * p.cap * p.vo_ld[src] + col;
-    const long long k_ld = p.ko_ld[src], v_ld = p.vo_ld[src];
     const uint32_t sbase = ptx::smem_addr(own_smem);
     const int steps = (j1 - j0 + kOwnKeys - 1) / kOwnKeys;
-    constexpr int kPieces = D / 8;                // 16-byte pieces of a row
-    constexpr int kRows = kOwnThreads / kPieces;  // rows that the CTA loads at a time
-    const int c0 = tid % kPieces, r0 = tid / kPieces;
-    // this thread's piece of rows r0, r0 + kRows, ...: pointers walk, nothing is multiplied
-    const char *kp = reinterpret_cast<const char *>(k0 + (j0 + r0) * k_ld + c0 * 8);
-    const char *vp = reinterpret_cast<const char *>(v0 + (j0 + r0) * v_ld + c0 * 8);
-    const long long k_step = kRows * k_ld * 2, v_step = kRows * v_ld * 2;
-    // rows r0 + i kRows share r & 7 where kRows is a multiple of 8 (always: 8 or 16)
-    const uint32_t to0 = static_cast<uint32_t>(r0 * D * 2 + (c0 ^ (r0 & 7)) * 16);
-    int load_stage = 0, load_key = j0 + r0;
+    TileLoader<D> loader;
+    loader.start(p.k_own[src], p.ko_ld[src], p.v_own[src], p.vo_ld[src], col, static_cast<long long>(b) * p.cap + j0, j1 - j0);
+    int load_stage = 0;
     auto load = [&](int step) {
       if (step < steps) {
-        const uint32_t ks = sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat + to0;
+        loader.tile(sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat, p.k_own[src]);
         if (++load_stage == kOwnStages) load_stage = 0;
-#pragma unroll
-        for (int i = 0; i < kOwnKeys / kRows; ++i) {
-          const bool valid = load_key < j1;
-          cp_async16(ks + i * kRows * D * 2, valid ? kp : reinterpret_cast<const char *>(k0), valid);
-          cp_async16(ks + C::kMat + i * kRows * D * 2, valid ? vp : reinterpret_cast<const char *>(v0), valid);
-          kp += k_step;
-          vp += v_step;
-          load_key += kRows;
-        }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < kOwnStages - 1; ++s) load(s);
-    // q as the A operand: rows lane/4 and lane/4 + 8 are heads g0 + ...
-    const int r_lo = g0 + (lane >> 2), r_hi = r_lo + 8;
-    uint32_t qa[D / 16][4];
-    {
-      const uint32_t *q_lo = r_lo < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_lo)) : nullptr;
-      const uint32_t *q_hi = r_hi < p.group ? reinterpret_cast<const uint32_t *>(q_row(p, b, kv * p.group + r_hi)) : nullptr;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const int at = kk * 8 + (lane & 3);
-        qa[kk][0] = q_lo ? __ldg(q_lo + at) : 0u;
-        qa[kk][1] = q_hi ? __ldg(q_hi + at) : 0u;
-        qa[kk][2] = q_lo ? __ldg(q_lo + at + 4) : 0u;
-        qa[kk][3] = q_hi ? __ldg(q_hi + at + 4) : 0u;
-      }
-    }
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int i = 0; i < kOwnStages - 1; ++i) load(i);
+    WarpRows<D> rows;
+    rows.start(p, b, kv, g0);
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
@@ -605,29 +746,12 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
       const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
       if (++stage == kOwnStages) stage = 0;
       if (key0 >= j1) continue;
-      float s[2][4] = {};
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const int r = warp * 16 + ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
-        uint32_t kb[4];
-        ldsm4(ks + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), kb);
-        mma16816(s[0], qa[kk], kb[0], kb[1]);
-        mma16816(s[1], qa[kk], kb[2], kb[3]);
-      }
-      // s[n][0,1]: row r_lo, keys key0 + 8n + 2 (lane%4) + {0, 1}; s[n][2,3]: row r_hi
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + 8 * n + 2 * (lane & 3) + (i & 1);
-          s[n][i] = key < j1 ? s[n][i] * p.scale_log2 : -INFINITY;
-          mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
-        }
+      float s[2][4];
+      rows.scores(ks, warp * 16, j1 - key0, p.scale_log2, s);
       if (p.scores) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int g = h ? r_hi : r_lo;
+          const int g = g0 + (lane >> 2) + 8 * h;
           if (g < p.group) {
             float *dst = p.scores + part_row(p, kv, b, g) * p.cap;
 #pragma unroll
@@ -640,88 +764,21 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
           }
         }
       }
-      float m_new[2], alpha[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        m_new[h] = fmaxf(m[h], mx[h]);
-        // the step holds at least one key, so m_new is above -inf unless a score is not a number
-        alpha[h] = m[h] == m_new[h] ? 1.f : ex2(m[h] - m_new[h]);
-        l[h] *= alpha[h];
-        m[h] = m_new[h];
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[n][i] = ex2(s[n][i] - m[i >> 1]);
-          l[i >> 1] += s[n][i];
-        }
-      // P rounded to bf16 for the product, as every GEMM operand here; l sums the unrounded p
-      const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                              pack_bf16(s[1][2], s[1][3])};
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int r = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * i + (lane >> 4);
-        uint32_t vb[4];
-        ldsm4_t(vs + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), vb);
-        mma16816(o[2 * i], pa, vb[0], vb[1]);
-        mma16816(o[2 * i + 1], pa, vb[2], vb[3]);
-      }
-    }
-    // join the four warps
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      rows.absorb(vs, warp * 16, s);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // every stage has been read
     float *so = reinterpret_cast<float *>(own_smem);  // [warp][16 rows][D]
-    if ((lane & 3) == 0) {
-      s_ml[warp][lane >> 2] = make_float2(m[0], l[0]);
-      s_ml[warp][(lane >> 2) + 8] = make_float2(m[1], l[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const int c = i * 8 + 2 * (lane & 3);
-      *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2)) * D + c) = make_float2(o[i][0], o[i][1]);
-      *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2) + 8) * D + c) = make_float2(o[i][2], o[i][3]);
-    }
+    rows.put(s_ml[warp], so + warp * 16 * D);
     __syncthreads();
     const int n_rows = min(16, p.group - g0);
     for (int i = tid; i < n_rows * (D / 4); i += kOwnThreads) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-      float mt = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mt = fmaxf(mt, s_ml[w][r].x);
-      float lt = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 ml = s_ml[w][r];
-        if (ml.y == 0.f && ml.x == -INFINITY) continue;  // a warp without keys
-        const float f = ex2(ml.x - mt);
-        const float4 ov = *reinterpret_cast<const float4 *>(so + (w * 16 + r) * D + c);
-        lt += f * ml.y;
-        acc.x += f * ov.x;
-        acc.y += f * ov.y;
-        acc.z += f * ov.z;
-        acc.w += f * ov.w;
-      }
+      float2 ml;
+      const float4 acc = join_warps<D>(s_ml, so, r, c, ml);
       const long long at = static_cast<long long>(p.split_p + split) * p.batch * p.heads_q + part_row(p, kv, b, g0 + r);
       *reinterpret_cast<float4 *>(p.part_o + at * D + c) = acc;
-      if (c == 0) p.part_ml[at] = make_float2(mt, lt);
+      if (c == 0) p.part_ml[at] = ml;
     }
   }
   // What follows this kernel on the stream follows the prefix kernel too: the grid
@@ -730,13 +787,179 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
+// Few keys and few sequences: one launch in place of three. A cluster of CTAs takes a
+// (sequence, kv head); its CTAs share the 64-key tiles of the prefix and then of
+// the own cache (each sequence reads the prefix by itself, from L2 after the first),
+// join through distributed shared memory in cluster order, and finish: outputs by
+// columns, weights by the CTA whose keys they are, from the scores it kept. Bound by
+// latency: 6.6 us for one sequence of 16 heads on 4 kv heads behind 100 + 64 keys, of
+// which a launch and the first loads are about 4.
+// ---------------------------------------------------------------------------
+constexpr int kDirectTiles = 16;                           // tiles of a CTA at most
+constexpr int kScoreRow = kDirectTiles * kOwnKeys + 4;     // floats of a row of kept scores
+
+template <int D>
+struct DirectCfg {
+  static constexpr int kStages = kOwnStages * 2 * OwnCfg<D>::kMat;
+  static constexpr int kSmem = kStages + 16 * kScoreRow * 4;
+  static_assert(kStages >= 5 * 16 * D * 4, "the warps' and the CTA's outputs fit over the stages");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant__ PrefixAttnParams p) {
+  using C = OwnCfg<D>;
+  extern __shared__ __align__(128) uint8_t own_smem[];
+  __shared__ float2 s_ml[4][16];
+  __shared__ __align__(16) float4 s_cta[16];  // the CTA's (m, l) of each row; 16 bytes for the cluster's loads
+  __shared__ float s_lse[16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int parts = p.direct;
+  const int part = parts > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / parts, kv = unit % p.heads_kv, b = unit / p.heads_kv;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int len = own_length(p, b);
+  if (kv == 0 && part == 0 && tid == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  const int tiles_p = (p.prefix + kOwnKeys - 1) / kOwnKeys, tiles = tiles_p + (len + kOwnKeys - 1) / kOwnKeys;
+  const int t0 = tiles * part / parts, t1 = tiles * (part + 1) / parts;
+  const int own0 = max(t0, tiles_p);  // the CTA's first own tile
+  const int src = kv / p.heads_per_source;
+  const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
+  const uint32_t sbase = ptx::smem_addr(own_smem);
+  float *s_scores = reinterpret_cast<float *>(own_smem + DirectCfg<D>::kStages);  // [16][kScoreRow] of the own tiles
+  TileLoader<D> loader;
+  int load_stage = 0;
+  auto load = [&](int t) {
+    if (t < t1) {
+      if (t < tiles_p) {
+        if (t == t0)
+          loader.start(p.k_prefix[src], p.kp_ld[src], p.v_prefix[src], p.vp_ld[src], col, static_cast<long long>(t) * kOwnKeys,
+                       p.prefix - t * kOwnKeys);
+      } else if (t == own0) {
+        const int j = (t - tiles_p) * kOwnKeys;
+        loader.start(p.k_own[src], p.ko_ld[src], p.v_own[src], p.vo_ld[src], col, static_cast<long long>(b) * p.cap + j, len - j);
+      }
+      loader.tile(sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat, t < tiles_p ? p.k_prefix[src] : p.k_own[src]);
+      if (++load_stage == kOwnStages) load_stage = 0;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kOwnStages - 1; ++i) load(t0 + i);
+  WarpRows<D> rows;
+  rows.start(p, b, kv, 0);
+  int stage = 0;
+  for (int t = t0; t < t1; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
+    __syncthreads();
+    load(t + kOwnStages - 1);
+    const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
+    if (++stage == kOwnStages) stage = 0;
+    const int left = (t < tiles_p ? p.prefix - t * kOwnKeys : len - (t - tiles_p) * kOwnKeys) - warp * 16;
+    if (left <= 0) continue;
+    float s[2][4];
+    rows.scores(ks, warp * 16, left, p.scale_log2, s);
+    if (p.w_out[0] && t >= tiles_p) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<float2 *>(s_scores + ((lane >> 2) + 8 * h) * kScoreRow + (t - own0) * kOwnKeys + warp * 16 + 8 * n +
+                                      2 * (lane & 3)) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
+    }
+    rows.absorb(vs, warp * 16, s);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float *so = reinterpret_cast<float *>(own_smem);  // [warp][16][D], then the CTA's [16][D]
+  float *cta_o = so + 4 * 16 * D;
+  rows.put(s_ml[warp], so + warp * 16 * D);
+  __syncthreads();
+  for (int i = tid; i < 16 * (D / 4); i += kOwnThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float2 ml;
+    *reinterpret_cast<float4 *>(cta_o + r * D + c) = join_warps<D>(s_ml, so, r, c, ml);
+    if (c == 0) s_cta[r] = make_float4(ml.x, ml.y, 0.f, 0.f);
+  }
+  if (parts > 1) ptx::cluster_sync();
+  else __syncthreads();
+  // Every CTA sees every part; the outputs are dealt by column groups, in cluster order.
+  const uint32_t ml_addr = ptx::smem_addr(s_cta), o_addr = ptx::smem_addr(cta_o);
+  auto far = [&](uint32_t addr, int q) { return ptx::ld_shared_cluster_f4(ptx::mapa_shared(addr, static_cast<uint32_t>(q))); };
+  const bool any = tiles > 0;
+  const int pieces = p.group * (D / 4);
+  for (int i = part * kOwnThreads + tid; i < pieces; i += parts * kOwnThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float2 ml[8];
+    float4 ov[8];
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < parts) {
+        const float4 v = far(ml_addr + r * 16, q);
+        ml[q] = make_float2(v.x, v.y);
+        ov[q] = far(o_addr + static_cast<uint32_t>(r * D + c) * 4u, q);
+      }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < parts) top = fmaxf(top, ml[q].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < parts) {
+        const float f = part_factor(ml[q], top);
+        sum += f * ml[q].y;
+        acc.x += f * ov[q].x;
+        acc.y += f * ov[q].y;
+        acc.z += f * ov[q].z;
+        acc.w += f * ov[q].w;
+      }
+    // no key at all: the row is zero
+    const float inv = any ? 1.f / sum : 0.f;
+    const int h = kv * p.group + r, rank = h / p.heads_per_rank;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
+                         static_cast<long long>(h - rank * p.heads_per_rank) * D + c;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+  if (p.w_out[0]) {
+    if (tid < p.group) {
+      float top = -INFINITY, sum = 0.f;
+      for (int q = 0; q < parts; ++q) top = fmaxf(top, far(ml_addr + tid * 16, q).x);
+      for (int q = 0; q < parts; ++q) {
+        const float4 v = far(ml_addr + tid * 16, q);
+        sum += part_factor(make_float2(v.x, v.y), top) * v.y;
+      }
+      s_lse[tid] = top + log2f(sum);
+    }
+    __syncthreads();
+    const long long wrow = static_cast<long long>(b) * p.heads_per_source + (kv - src * p.heads_per_source);
+    const float *wi = p.w_in[src] ? p.w_in[src] + wrow * p.wi_ld[src] : nullptr;
+    float *wo = p.w_out[src] + wrow * p.wo_ld[src];
+    const int first = (own0 - tiles_p) * kOwnKeys, keys = t1 > own0 ? min(len, (t1 - tiles_p) * kOwnKeys) - first : 0;
+    for (int x = tid; x < keys; x += kOwnThreads) {
+      float w = 0.f;
+#pragma unroll 8
+      for (int g = 0; g < p.group; ++g) w += ex2(s_scores[g * kScoreRow + x] - s_lse[g]);
+      if (wi) w += wi[first + x];
+      wo[first + x] = w;
+    }
+    for (int j = len + part * kOwnThreads + tid; j < p.cap; j += parts * kOwnThreads) wo[j] = 0.f;
+  }
+  __syncwarp();
+  if (parts > 1) ptx::cluster_sync_relaxed();  // the other CTAs have read this one's results
+}
+
+// ---------------------------------------------------------------------------
 // Joins the splits of a (sequence, kv head): one warp per head of the group, then
 // the own keys' weights. Bound by latency: 5 us for 61 sequences' 488 heads of six
-// splits, and 4 us for their weights.
+// splits, and 4 us for their weights. With few (sequence, kv head)s, SHARED spreads the
+// weights over blockIdx.y, each CTA with the sums of its own reading (two heads, 2048
+// own keys: the call takes 10.3 us in place of 17.6; a form for both costs 61
+// sequences 0.3 us).
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant__ PrefixAttnParams p) {
   constexpr int kPer = D / 32;  // output columns of a lane
   __shared__ float s_lse[kJoinThreads];
@@ -744,15 +967,35 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
   // began after them: they can be read while the last of them still runs.
   if (p.split_p + p.split_o == 0) grid_dep_wait();
   const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
+  const int share = SHARED ? gridDim.y : 1, at = SHARED ? blockIdx.y : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = own_length(p, b);
   grid_dep_wait();
   grid_dep_launch();
-  if (p.split_o == 0 && kv == 0 && threadIdx.x == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  if (p.split_o == 0 && kv == 0 && at == 0 && threadIdx.x == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
   const int own = len > 0 ? (len + p.chunk - 1) / p.chunk : 0;
   const int n = p.split_p + own;
   const long long stride = static_cast<long long>(p.batch) * p.heads_q;
-  for (int g = warp; g < p.group; g += kJoinThreads / 32) {
+  if (at > 0) {  // the weights need the sums alone
+    for (int g = warp; g < p.group; g += kJoinThreads / 32) {
+      const long long row = part_row(p, kv, b, g);
+      float m = -INFINITY, l = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float2 ml = p.part_ml[i * stride + row];
+        const float m_new = fmaxf(m, ml.x);
+        l = (m == m_new ? l : l * ex2(m - m_new)) + ex2(ml.x - m_new) * ml.y;
+        m = m_new;
+      }
+      float mt = m;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      l *= m == mt ? 1.f : ex2(m - mt);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) s_lse[g] = mt + log2f(l);
+    }
+  }
+  for (int g = warp; g < p.group && at == 0; g += kJoinThreads / 32) {
     const long long row = part_row(p, kv, b, g);
     float mt = -INFINITY, lt = 0.f, acc[kPer] = {};
     for (int s0 = 0; s0 < n; s0 += 32) {  // a lane per split, then every lane its columns of all of them
@@ -801,7 +1044,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
   const float *wi = p.w_in[src] ? p.w_in[src] + wrow * p.wi_ld[src] : nullptr;
   float *wo = p.w_out[src] + wrow * p.wo_ld[src];
   const float *sc = p.scores + part_row(p, kv, b, 0) * p.cap;
-  for (int j = threadIdx.x; j < p.cap; j += kJoinThreads) {
+  for (int j = at * kJoinThreads + threadIdx.x; j < p.cap; j += share * kJoinThreads) {
     float w = 0.f;
     if (j < len) {
       const float old = wi ? wi[j] : 0.f;
@@ -889,8 +1132,14 @@ cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
 
 template <int D>
 tp_status launch_all(const PrefixAttnParams &p, const PrefixMaps &maps, cudaStream_t s) {
-  static unsigned mask_p = 0, mask_o = 0;
+  static unsigned mask_p = 0, mask_o = 0, mask_d = 0;
   static std::mutex mu;
+  if (p.direct > 0) {
+    const cudaError_t de = allow_smem(k_direct<D>, DirectCfg<D>::kSmem, mask_d, mu);
+    if (de != cudaSuccess) return cuda_fail(de);
+    return launched(launch_kernel(k_direct<D>, dim3(static_cast<unsigned>(p.batch * p.heads_kv * p.direct)),
+                                  dim3(kOwnThreads), DirectCfg<D>::kSmem, s, static_cast<unsigned>(p.direct), p));
+  }
   cudaError_t e = allow_smem(k_prefix_part<D>, static_cast<int>(PrefCfg<D>::kSmem), mask_p, mu);
   if (e == cudaSuccess) e = allow_smem(k_own_part<D>, OwnCfg<D>::kSmem, mask_o, mu);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -907,8 +1156,30 @@ tp_status launch_all(const PrefixAttnParams &p, const PrefixMaps &maps, cudaStre
     st = launched(launch_kernel(k_own_part<D>, grid, dim3(kOwnThreads), OwnCfg<D>::kSmem, s, 1, p));
     if (st != TP_OK) return st;
   }
-  return launched(launch_kernel(k_combine<D>, dim3(static_cast<unsigned>(p.batch * p.heads_kv)), dim3(kJoinThreads), 0, s,
+  // CTAs a (sequence, kv head): they share the weights while SMs are idle
+  const long long units = static_cast<long long>(p.batch) * p.heads_kv;
+  const int most = p.w_out[0] ? (p.cap + kJoinThreads - 1) / kJoinThreads : 1;
+  int share = 1;
+  while (share < most && share < 32 && units * share * 2 <= 2 * kSms) share *= 2;
+  return launched(launch_kernel(share > 1 ? k_combine<D, true> : k_combine<D, false>,
+                                dim3(static_cast<unsigned>(units), static_cast<unsigned>(share)), dim3(kJoinThreads), 0, s,
                                 1, p));
+}
+
+// CTAs a (sequence, kv head) for k_direct, or 0 where the three kernels run: all
+// clusters resident at once, one 16-head tile, and few tiles a CTA, since every
+// sequence reads the prefix again. Groups of four, d = 128, us here and with the three
+// kernels: 1 sequence of 8 kv heads, 100 + 64 keys 6.7 and 8.5, 4032 + 64 keys 11.1
+// and 14.7; 9 sequences, 1024 + 64 keys (9 tiles a CTA) 11.0 and 12.0, 512 own
+// keys 10.8 and 15.2; 18 sequences, 512 + 64 keys (9) 10.5 and 12.7, 1024 + 64 keys
+// (17) 15.3 and 13.4.
+int direct_parts(long long units, long long group, long long prefix, long long cap) {
+  const long long tiles = (prefix + kOwnKeys - 1) / kOwnKeys + (cap + kOwnKeys - 1) / kOwnKeys;
+  if (group > 16 || tiles == 0 || units > num_sms()) return 0;
+  int parts = 1;
+  for (int c = 2; c <= 8; c *= 2)
+    if (c <= tiles && units * c <= num_sms() && units <= max_active_clusters(c)) parts = c;
+  return (tiles + parts - 1) / parts <= kDirectTiles ? parts : 0;
 }
 
 // Sizes that the launch shape's 32-bit arithmetic and the kernels take.
@@ -994,13 +1265,18 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
     p.a[r] = a[r].ptr;
     p.a_ld[r] = a[r].ld;
   }
+  p.direct = direct_parts(batch * dims.num_kv_heads, group, P, cap);
   // Sources whose prefixes are neighbouring columns of one tensor need one map together.
   p.one_prefix = 1;
   for (int r = 1; r < sources; ++r)
     for (const tp_tensor *t : {k_prefix, v_prefix})
       if (t[r].ld != t[0].ld || static_cast<const char *>(t[0].ptr) + r * kvc * 2 != t[r].ptr) p.one_prefix = 0;
   for (int r = 0; r < sources; ++r) {
-    if (P > 0 && (r == 0 || !p.one_prefix)) {
+    p.k_prefix[r] = k_prefix[r].ptr;
+    p.v_prefix[r] = v_prefix[r].ptr;
+    p.kp_ld[r] = k_prefix[r].ld;
+    p.vp_ld[r] = v_prefix[r].ld;
+    if (p.direct == 0 && P > 0 && (r == 0 || !p.one_prefix)) {
       tp_tensor k = k_prefix[r], v = v_prefix[r];
       if (p.one_prefix) k.cols = v.cols = kvc * sources;
       if (P == 1) k.ld = v.ld = kvc * sources;  // the pitch of a single row is free

@@ -188,6 +188,76 @@ def test_other_stream_and_captured_graph():
         assert torch.equal(torch.cat(a, 1), want[0])
 
 
+# Which kernels a call takes goes by its sizes: one launch of clusters for few keys and sequences
+# with at most 16 heads a group, else the prefix, own and joining kernels. Both sides of each limit.
+EDGES = [
+    (1, 16, 1, 128, 1, 8128, 64, [64]),                     # 128 tiles over eight CTAs: the most
+    (1, 16, 1, 64, 1, 8129, 64, [64]),                      # one more
+    (1, 4, 1, 128, 1, 0, 8192, [8191]), (1, 4, 1, 64, 2, 0, 8193, [8193, 0]),
+    (1, 8, 1, 128, 150, 700, 270, [i * 9 % 271 for i in range(150)]),   # a CTA a sequence, 16 tiles
+    (2, 16, 2, 64, 77, 960, 128, [i * 5 % 129 for i in range(77)]),     # more units than SMs
+    (1, 17, 1, 128, 3, 200, 300, [0, 300, 65]),             # 17 heads
+    (1, 8, 4, 128, 1, 65, 64 * 11 + 1, [64 * 11]),          # tiles that do not divide by the CTAs
+    (8, 16, 4, 64, 3, 64, 64, [0, 64, 1]), (1, 3, 3, 128, 2, 128, 2048, [1, 2047]),
+]
+
+
+@pytest.mark.parametrize("shape", EDGES, ids=lambda s: "-".join(map(str, s[:7])))
+def test_both_sides_of_the_kernels_limits(shape):
+    need_gpu()
+    c = Case(*shape, seed=21, views=True)
+    a, w = c.run()
+    c.check(a, w)
+    a2, w2 = c.run(alias=True)
+    assert torch.equal(a, a2) and torch.equal(w, w2)
+    a3, _ = c.run(weights=False)
+    assert torch.equal(a, a3)
+    c.check(*c.run(first=True), first=True)
+    assert tp.tp_device_status()[0] == tp.TP_OK
+
+
+WAYS = [(1, 8, 2, 128, 5, 300, 130), (1, 34, 2, 128, 5, 300, 130), (1, 8, 2, 64, 5, 0, 130), (1, 34, 2, 64, 5, 0, 130)]
+
+
+@pytest.mark.parametrize("shape", WAYS, ids=lambda s: "-".join(map(str, s)))
+def test_stale_rows_bad_lengths_and_nan_in_both_ways(shape):
+    need_gpu()
+    c = Case(*shape, [0, 13, 64, 130, 99], seed=22)
+    want = c.run()
+    for b, n in enumerate(c.lens.tolist()):
+        c.ko[b * 130 + n:(b + 1) * 130] = float("inf")
+        c.vo[b * 130 + n:(b + 1) * 130] = float("nan")
+        c.w[:, b * 2:(b + 1) * 2, n:] = float("nan")
+    got = c.run()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert tp.tp_device_status()[0] == tp.TP_OK
+    c.lens[0] = -7
+    c.lens[3] = 131
+    got = c.run()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])  # clamped to 0 and to the capacity
+    assert tp.tp_device_status()[0] == tp.TP_ERR_BAD_LENGTH
+    assert tp.tp_device_status()[0] == tp.TP_OK
+    c.lens[0], c.lens[3] = 0, 130
+    c.ko[2 * 130 + 63, 7] = float("nan")     # sequence 2, kv head 0
+    a, w = c.run()
+    group = c.hq // 2
+    assert torch.isnan(a[2].view(c.hq, c.d)[:group].float()).all()
+    keep = torch.ones(5, c.hq, dtype=torch.bool, device="cuda")
+    keep[2, :group] = False
+    assert torch.equal(a.view(5, c.hq, c.d)[keep], want[0].view(5, c.hq, c.d)[keep])
+
+
+def test_long_scores_that_jump_in_both_ways():
+    """The maxima rise from tile to tile by tens of log2 units, over the CTAs of a cluster and over splits."""
+    need_gpu()
+    for hq in (4, 17):
+        c = Case(1, hq, 1, 128, 2, 64 * 9, 64 * 7, [64 * 7, 100], seed=23)
+        ramp = torch.arange(9, device="cuda").repeat_interleave(64)[:, None] * 1.3
+        c.kp += (ramp * torch.sign(c.q[0, :128].float())).to(BF16)
+        c.ko += (torch.linspace(8, 0, c.B * c.C, device="cuda")[:, None] * torch.sign(c.q[1, :128].float())).to(BF16)
+        c.check(*c.run())
+
+
 def test_eviction_reads_the_accumulated_weights():
     need_gpu()
     c = Case(2, 8, 2, 128, 3, 100, 64, [64, 50, 10], seed=11)

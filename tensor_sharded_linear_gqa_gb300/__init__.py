@@ -516,7 +516,15 @@ class _Scratch:
 
     def row(self, t):
         """A vector: its 1-D tensor is the [1 x n] view that the library takes."""
-        return self.one(t if t is None or type(t) is TpTensor or t.dim() == 2 else t.unsqueeze(0))
+        if t is None or type(t) is TpTensor or t.dim() != 1:
+            return self.one(t)
+        n, dt = len(t), _DTYPES.get(t.dtype)
+        if dt is None or not n or not t.is_cuda or t.stride(0) != 1:
+            return self.one(t.unsqueeze(0))
+        at = self.used
+        self.used = at + _DESC_SIZE
+        _PACK(self.buf, at, t.data_ptr(), dt, 0, 1, n, n)
+        return self.base + at
 
 
 _DESC_SIZE, _PACK = _DESC.size, _DESC.pack_into

@@ -43,6 +43,7 @@ struct PrefixAttnParams {
   int batch, heads_q, heads_kv, group, heads_per_rank, heads_per_source, d;
   int prefix, blocks, split_p, pairs, ctas_p;  // 128-key blocks; key splits; 256-row tile pairs per kv head; CTAs
   int cap, chunk, split_o;             // own cache: rows a sequence, keys a split, splits
+  int score_ld;                        // floats of a row of scores: a multiple of four
   int has_prev;                        // k_own_part runs behind k_prefix_part
   int direct;                          // above 0: k_direct runs instead, with this many CTAs a cluster
   int one_prefix;                      // every source's prefix lies in one tensor, in head order: one map of each
@@ -50,7 +51,7 @@ struct PrefixAttnParams {
   const int *lengths;
   float *part_o;    // [split][row][d]
   float2 *part_ml;  // [split][row] (m in log2 units, l)
-  float *scores;    // [row][capacity], s * log2(e) / sqrt(d) of the own keys; null: not wanted
+  float *scores;    // [row][score_ld], s * log2(e) / sqrt(d) of the own keys; null: not wanted
   int *status;
   long long wait_ns;
   const void *q[kMaxRanks32];
@@ -502,12 +503,12 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
 // ---------------------------------------------------------------------------
 constexpr int kOwnThreads = 128;
 constexpr int kOwnKeys = 64;
-constexpr int kOwnStages = 3;
 
 template <int D>
 struct OwnCfg {
   static constexpr int kMat = kOwnKeys * D * 2;  // bytes of a stage's K (or V)
-  static constexpr int kSmem = kOwnStages * 2 * kMat;
+  static constexpr int kStages = 3;
+  static constexpr int kSmem = kStages * 2 * kMat;
   static_assert(kSmem >= 4 * 16 * D * 4, "the warps' outputs fit over the stages");
 };
 
@@ -729,22 +730,22 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
     auto load = [&](int step) {
       if (step < steps) {
         loader.tile(sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat, p.k_own[src]);
-        if (++load_stage == kOwnStages) load_stage = 0;
+        if (++load_stage == C::kStages) load_stage = 0;
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kOwnStages - 1; ++i) load(i);
+    for (int i = 0; i < C::kStages - 1; ++i) load(i);
     WarpRows<D> rows;
     rows.start(p, b, kv, g0);
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
       __syncthreads();  // the stage is there for every thread, and the one loaded next is free
-      load(step + kOwnStages - 1);
+      load(step + C::kStages - 1);
       const int key0 = j0 + step * kOwnKeys + warp * 16;
       const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
-      if (++stage == kOwnStages) stage = 0;
+      if (++stage == C::kStages) stage = 0;
       if (key0 >= j1) continue;
       float s[2][4];
       rows.scores(ks, warp * 16, j1 - key0, p.scale_log2, s);
@@ -753,14 +754,12 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
         for (int h = 0; h < 2; ++h) {
           const int g = g0 + (lane >> 2) + 8 * h;
           if (g < p.group) {
-            float *dst = p.scores + part_row(p, kv, b, g) * p.cap;
+            float *dst = p.scores + part_row(p, kv, b, g) * p.score_ld;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int key = key0 + 8 * n + 2 * (lane & 3) + i;
-                if (key < j1) dst[key] = s[n][2 * h + i];
-              }
+            for (int n = 0; n < 2; ++n) {
+              const int key = key0 + 8 * n + 2 * (lane & 3);  // even, and so is the row's pitch
+              if (key < j1) *reinterpret_cast<float2 *>(dst + key) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
+            }
           }
         }
       }
@@ -800,9 +799,9 @@ constexpr int kScoreRow = kDirectTiles * kOwnKeys + 4;     // floats of a row of
 
 template <int D>
 struct DirectCfg {
-  static constexpr int kStages = kOwnStages * 2 * OwnCfg<D>::kMat;
-  static constexpr int kSmem = kStages + 16 * kScoreRow * 4;
-  static_assert(kStages >= 5 * 16 * D * 4, "the warps' and the CTA's outputs fit over the stages");
+  static constexpr int kTiles = OwnCfg<D>::kSmem;
+  static constexpr int kSmem = kTiles + 16 * kScoreRow * 4;
+  static_assert(kTiles >= 5 * 16 * D * 4, "the warps' and the CTA's outputs fit over the stages");
 };
 
 template <int D>
@@ -826,7 +825,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
   const int src = kv / p.heads_per_source;
   const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
   const uint32_t sbase = ptx::smem_addr(own_smem);
-  float *s_scores = reinterpret_cast<float *>(own_smem + DirectCfg<D>::kStages);  // [16][kScoreRow] of the own tiles
+  float *s_scores = reinterpret_cast<float *>(own_smem + DirectCfg<D>::kTiles);  // [16][kScoreRow] of the own tiles
   TileLoader<D> loader;
   int load_stage = 0;
   auto load = [&](int t) {
@@ -840,21 +839,21 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
         loader.start(p.k_own[src], p.ko_ld[src], p.v_own[src], p.vo_ld[src], col, static_cast<long long>(b) * p.cap + j, len - j);
       }
       loader.tile(sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat, t < tiles_p ? p.k_prefix[src] : p.k_own[src]);
-      if (++load_stage == kOwnStages) load_stage = 0;
+      if (++load_stage == C::kStages) load_stage = 0;
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kOwnStages - 1; ++i) load(t0 + i);
+  for (int i = 0; i < C::kStages - 1; ++i) load(t0 + i);
   WarpRows<D> rows;
   rows.start(p, b, kv, 0);
   int stage = 0;
   for (int t = t0; t < t1; ++t) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
     __syncthreads();
-    load(t + kOwnStages - 1);
+    load(t + C::kStages - 1);
     const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
-    if (++stage == kOwnStages) stage = 0;
+    if (++stage == C::kStages) stage = 0;
     const int left = (t < tiles_p ? p.prefix - t * kOwnKeys : len - (t - tiles_p) * kOwnKeys) - warp * 16;
     if (left <= 0) continue;
     float s[2][4];
@@ -952,7 +951,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
 // ---------------------------------------------------------------------------
 // Joins the splits of a (sequence, kv head): one warp per head of the group, then
 // the own keys' weights. Bound by latency: 5 us for 61 sequences' 488 heads of six
-// splits, and 4 us for their weights. With few (sequence, kv head)s, SHARED spreads the
+// splits, and 2.5 us for their weights, four keys a thread (4.6 with one: too few loads
+// in flight). With few (sequence, kv head)s, SHARED spreads the
 // weights over blockIdx.y, each CTA with the sums of its own reading (two heads, 2048
 // own keys: the call takes 10.3 us in place of 17.6; a form for both costs 61
 // sequences 0.3 us).
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
 constexpr int kJoinThreads = 256;
 
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant__ PrefixAttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) k_combine(const __grid_constant__ PrefixAttnParams p) {
   constexpr int kPer = D / 32;  // output columns of a lane
   __shared__ float s_lse[kJoinThreads];
   // The lengths were written before the kernels whose results this one joins, and those
@@ -1043,16 +1043,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_combine(const __grid_constant_
   const long long wrow = static_cast<long long>(b) * p.heads_per_source + (kv - src * p.heads_per_source);
   const float *wi = p.w_in[src] ? p.w_in[src] + wrow * p.wi_ld[src] : nullptr;
   float *wo = p.w_out[src] + wrow * p.wo_ld[src];
-  const float *sc = p.scores + part_row(p, kv, b, 0) * p.cap;
-  for (int j = at * kJoinThreads + threadIdx.x; j < p.cap; j += share * kJoinThreads) {
-    float w = 0.f;
+  const float *sc = p.scores + part_row(p, kv, b, 0) * p.score_ld;
+  for (int j = 4 * (at * kJoinThreads + threadIdx.x); j < p.cap; j += 4 * share * kJoinThreads) {
+    float w[4] = {};
     if (j < len) {
-      const float old = wi ? wi[j] : 0.f;
+      float old[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) old[i] = wi && j + i < len ? wi[j + i] : 0.f;
 #pragma unroll 8
-      for (int g = 0; g < p.group; ++g) w += ex2(sc[static_cast<long long>(g) * p.cap + j] - s_lse[g]);
-      w += old;
+      for (int g = 0; g < p.group; ++g) {
+        const float4 v = *reinterpret_cast<const float4 *>(sc + static_cast<long long>(g) * p.score_ld + j);
+        w[0] += ex2(v.x - s_lse[g]);
+        w[1] += ex2(v.y - s_lse[g]);
+        w[2] += ex2(v.z - s_lse[g]);
+        w[3] += ex2(v.w - s_lse[g]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = j + i < len ? w[i] + old[i] : 0.f;
     }
-    wo[j] = w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + i < p.cap) wo[j + i] = w[i];
   }
 }
 
@@ -1104,6 +1115,7 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
   }
   return s;
 }
+long long score_pitch(long long cap) { return (cap + 3) / 4 * 4; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Regions {
   size_t o, ml, scores, total;
@@ -1114,7 +1126,7 @@ Regions regions_of(const Shape &s, long long batch, long long heads_q, long long
   r.o = 0;
   r.ml = round256(rows * d * 4);
   r.scores = r.ml + round256(rows * 8);
-  r.total = r.scores + (weights ? round256(static_cast<size_t>(batch) * heads_q * cap * 4) : 0);
+  r.total = r.scores + (weights ? round256(static_cast<size_t>(batch) * heads_q * score_pitch(cap) * 4) : 0);
   return r;
 }
 
@@ -1158,7 +1170,7 @@ tp_status launch_all(const PrefixAttnParams &p, const PrefixMaps &maps, cudaStre
   }
   // CTAs a (sequence, kv head): they share the weights while SMs are idle
   const long long units = static_cast<long long>(p.batch) * p.heads_kv;
-  const int most = p.w_out[0] ? (p.cap + kJoinThreads - 1) / kJoinThreads : 1;
+  const int most = p.w_out[0] ? (p.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 1;
   int share = 1;
   while (share < most && share < 32 && units * share * 2 <= 2 * kSms) share *= 2;
   return launched(launch_kernel(share > 1 ? k_combine<D, true> : k_combine<D, false>,
@@ -1313,6 +1325,7 @@ extern "C" tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp
   p.pairs = shape.pairs;
   p.ctas_p = shape.ctas_p;
   p.cap = static_cast<int>(cap);
+  p.score_ld = static_cast<int>(score_pitch(cap));
   p.chunk = shape.chunk;
   p.split_o = shape.split_o;
   p.has_prev = p.split_p > 0 && pdl_enabled();

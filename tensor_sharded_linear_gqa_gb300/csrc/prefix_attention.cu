@@ -502,14 +502,16 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
 // split (no better balance than the scheduler's, and a join and a q load in the run).
 // ---------------------------------------------------------------------------
 constexpr int kOwnThreads = 128;
-constexpr int kOwnKeys = 64;
+constexpr int kOwnKeys = 64;   // keys of a k_direct tile; an own split is a multiple of it
+constexpr int kWarpKeys = 32;  // keys of a warp's step in k_own_part
 
+// A warp's ring: three slots of kWarpKeys keys' K or V.
 template <int D>
 struct OwnCfg {
-  static constexpr int kMat = kOwnKeys * D * 2;  // bytes of a stage's K (or V)
-  static constexpr int kStages = 3;
-  static constexpr int kSmem = kStages * 2 * kMat;
-  static_assert(kSmem >= 4 * 16 * D * 4, "the warps' outputs fit over the stages");
+  static constexpr int kSlot = kWarpKeys * D * 2;
+  static constexpr int kRing = 3 * kSlot;
+  static constexpr int kSmem = 4 * kRing;
+  static_assert(kRing >= 16 * D * 4, "a warp's outputs fit over its ring");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
@@ -561,35 +563,40 @@ struct WarpRows {
     l[0] = l[1] = 0.f;
   }
 
-  // Scores of the 16 keys at stage rows row0 .. row0 + 15, in log2 units; keys from the
+  // Scores of the KEYS keys at shared-memory rows row0 .., in log2 units; keys from the
   // `left`-th on are masked. s[n][0,1]: row lane/4, keys 8n + 2 (lane%4) + {0, 1};
   // s[n][2,3]: row lane/4 + 8.
-  __device__ __forceinline__ void scores(uint32_t ks, int row0, int left, float scale_log2, float (&s)[2][4]) const {
+  template <int KEYS>
+  __device__ __forceinline__ void scores(uint32_t ks, int row0, int left, float scale_log2, float (&s)[KEYS / 8][4]) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    for (int n = 0; n < KEYS / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const int r = row0 + ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
-      uint32_t kb[4];
-      ldsm4(ks + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), kb);
-      mma16816(s[0], qa[kk], kb[0], kb[1]);
-      mma16816(s[1], qa[kk], kb[2], kb[3]);
-    }
+    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < KEYS / 8; n += 2) {
+        const int r = row0 + n * 8 + ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
+        uint32_t kb[4];
+        ldsm4(ks + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), kb);
+        mma16816(s[n], qa[kk], kb[0], kb[1]);
+        mma16816(s[n + 1], qa[kk], kb[2], kb[3]);
+      }
+#pragma unroll
+    for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         s[n][i] = 8 * n + 2 * (lane & 3) + (i & 1) < left ? s[n][i] * scale_log2 : -INFINITY;
   }
 
-  // The keys' softmax terms and their part of the outputs; at least one key is there.
-  __device__ __forceinline__ void absorb(uint32_t vs, int row0, float (&s)[2][4]) {
-    const int lane = threadIdx.x & 31;
+  // Turns scores into softmax terms p, rescaling what came before; at least one key is there.
+  template <int KEYS>
+  __device__ __forceinline__ void softmax(float (&s)[KEYS / 8][4]) {
     float alpha[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      float mx = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+      for (int n = 1; n < KEYS / 8; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float m_new = fmaxf(m[h], mx);
@@ -608,22 +615,31 @@ struct WarpRows {
       }
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[n][i] = ex2(s[n][i] - m[i >> 1]);
         l[i >> 1] += s[n][i];
       }
-    // P rounded to bf16 for the product, as every GEMM operand here; l sums the unrounded p
-    const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                            pack_bf16(s[1][2], s[1][3])};
+  }
+
+  // Adds p V. P is rounded to bf16 for the product, as every GEMM operand here; l sums the
+  // unrounded p.
+  template <int KEYS>
+  __device__ __forceinline__ void add_pv(uint32_t vs, int row0, const float (&s)[KEYS / 8][4]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const int r = row0 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * i + (lane >> 4);
-      uint32_t vb[4];
-      ldsm4_t(vs + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), vb);
-      mma16816(o[2 * i], pa, vb[0], vb[1]);
-      mma16816(o[2 * i + 1], pa, vb[2], vb[3]);
+    for (int n = 0; n < KEYS / 8; n += 2) {
+      const uint32_t pa[4] = {pack_bf16(s[n][0], s[n][1]), pack_bf16(s[n][2], s[n][3]), pack_bf16(s[n + 1][0], s[n + 1][1]),
+                              pack_bf16(s[n + 1][2], s[n + 1][3])};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int r = row0 + n * 8 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * i + (lane >> 4);
+        uint32_t vb[4];
+        ldsm4_t(vs + static_cast<uint32_t>(r * D * 2 + (c ^ (r & 7)) * 16), vb);
+        mma16816(o[2 * i], pa, vb[0], vb[1]);
+        mma16816(o[2 * i + 1], pa, vb[2], vb[3]);
+      }
     }
   }
 
@@ -646,9 +662,10 @@ struct WarpRows {
 __device__ __forceinline__ float part_factor(float2 ml, float top) {
   return ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - top);
 }
-// Four columns of a row over the CTA's four warps: their common maximum, sum and outputs.
+// Four columns of a row over the CTA's four warps (`stride` floats apart): their common
+// maximum, sum and outputs.
 template <int D>
-__device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const float *so, int r, int c, float2 &ml) {
+__device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const float *so, int stride, int r, int c, float2 &ml) {
   float top = -INFINITY;
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][r].x);
@@ -658,7 +675,7 @@ __device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const flo
   for (int w = 0; w < 4; ++w) {
     const float f = part_factor(s_ml[w][r], top);
     if (f == 0.f) continue;  // a warp without keys (its outputs may be anything times 0)
-    const float4 ov = *reinterpret_cast<const float4 *>(so + (w * 16 + r) * D + c);
+    const float4 ov = *reinterpret_cast<const float4 *>(so + w * stride + r * D + c);
     sum += f * s_ml[w][r].y;
     acc.x += f * ov.x;
     acc.y += f * ov.y;
@@ -697,14 +714,51 @@ struct TileLoader {
     for (int i = 0; i < kOwnKeys / kRows; ++i) {
       const bool valid = left > 0;
       cp_async16(to + i * kRows * D * 2, valid ? static_cast<const void *>(k) : safe, valid);
-      cp_async16(to + OwnCfg<D>::kMat + i * kRows * D * 2, valid ? static_cast<const void *>(v) : safe, valid);
+      cp_async16(to + kOwnKeys * D * 2 + i * kRows * D * 2, valid ? static_cast<const void *>(v) : safe, valid);
       k += k_step;
       v += v_step;
       left -= kRows;
     }
   }
 };
+// A warp's walk down one matrix of a cache, kWarpKeys of every 4 kWarpKeys keys: copies
+// into a slot, zeros past the last key.
+template <int D>
+struct KeyWalk {
+  static constexpr int kPieces = D / 8;        // 16-byte pieces of a row
+  static constexpr int kRows = 32 / kPieces;   // rows that a warp copies at a time: 2 or 4
+  const char *at;
+  long long step;  // bytes of kRows rows
+  int left;        // keys from this lane's next row on
+  uint32_t to0;    // the lane's place in a slot, of its first row
+
+  // `row` is the warp's first row; `keys` follow it, others' among them.
+  __device__ __forceinline__ void start(const void *cache, long long ld, long long col, long long row, int keys) {
+    const int lane = threadIdx.x & 31, c0 = lane % kPieces, r0 = lane / kPieces;
+    at = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(cache) + (row + r0) * ld + col + c0 * 8);
+    step = kRows * ld * 2;
+    left = keys - r0;
+    to0 = static_cast<uint32_t>(r0 * D * 2 + (c0 ^ r0) * 16);
+  }
+  // safe: any readable address, for the copies that read nothing.
+  __device__ __forceinline__ void load(uint32_t slot, const void *safe) {
+#pragma unroll
+    for (int i = 0; i < kWarpKeys / kRows; ++i) {
+      const bool valid = left > i * kRows;
+      // row r0 + i kRows: r0 < kRows, a power of two, so its swizzle is r0's with the bits of i kRows flipped
+      cp_async16(slot + (to0 ^ (((i * kRows) & 7) << 4)) + i * kRows * D * 2, valid ? static_cast<const void *>(at) : safe,
+                 valid);
+      at += step;
+    }
+    at += step * (3 * kWarpKeys / kRows);
+    left -= 4 * kWarpKeys;
+  }
+};
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_constant__ PrefixAttnParams p) {
@@ -723,32 +777,30 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
     const int src = kv / p.heads_per_source;
     const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
     const uint32_t sbase = ptx::smem_addr(own_smem);
-    const int steps = (j1 - j0 + kOwnKeys - 1) / kOwnKeys;
-    TileLoader<D> loader;
-    loader.start(p.k_own[src], p.ko_ld[src], p.v_own[src], p.vo_ld[src], col, static_cast<long long>(b) * p.cap + j0, j1 - j0);
-    int load_stage = 0;
-    auto load = [&](int step) {
-      if (step < steps) {
-        loader.tile(sbase + static_cast<uint32_t>(load_stage) * 2 * C::kMat, p.k_own[src]);
-        if (++load_stage == C::kStages) load_stage = 0;
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) load(i);
+    const int mine = j1 - j0 - warp * kWarpKeys;  // keys from the warp's first on
+    const int steps = mine > 0 ? (mine + 4 * kWarpKeys - 1) / (4 * kWarpKeys) : 0;
+    KeyWalk<D> kw, vw;
+    kw.start(p.k_own[src], p.ko_ld[src], col, static_cast<long long>(b) * p.cap + j0 + warp * kWarpKeys, mine);
+    vw.start(p.v_own[src], p.vo_ld[src], col, static_cast<long long>(b) * p.cap + j0 + warp * kWarpKeys, mine);
+    // K and V of a step take the ring's next two slots; what follows them goes where they were
+    uint32_t ks = sbase + static_cast<uint32_t>(warp * C::kRing), vs = ks + C::kSlot, next = vs + C::kSlot;
+    if (steps > 0) kw.load(ks, p.k_own[src]);
+    cp_async_commit();
+    if (steps > 0) vw.load(vs, p.k_own[src]);
+    cp_async_commit();
+    if (steps > 1) kw.load(next, p.k_own[src]);
+    cp_async_commit();
     WarpRows<D> rows;
     rows.start(p, b, kv, g0);
-    int stage = 0;
     for (int step = 0; step < steps; ++step) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      __syncthreads();  // the stage is there for every thread, and the one loaded next is free
-      load(step + C::kStages - 1);
-      const int key0 = j0 + step * kOwnKeys + warp * 16;
-      const uint32_t ks = sbase + static_cast<uint32_t>(stage) * 2 * C::kMat, vs = ks + C::kMat;
-      if (++stage == C::kStages) stage = 0;
-      if (key0 >= j1) continue;
-      float s[2][4];
-      rows.scores(ks, warp * 16, j1 - key0, p.scale_log2, s);
+      const int key0 = j0 + (step * 4 + warp) * kWarpKeys;
+      cp_async_wait<2>();  // this K
+      __syncwarp();
+      float s[kWarpKeys / 8][4];
+      rows.template scores<kWarpKeys>(ks, 0, j1 - key0, p.scale_log2, s);
+      __syncwarp();  // every lane has read the slot
+      if (step + 1 < steps) vw.load(ks, p.k_own[src]);
+      cp_async_commit();
       if (p.scores) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -756,25 +808,35 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
           if (g < p.group) {
             float *dst = p.scores + part_row(p, kv, b, g) * p.score_ld;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < kWarpKeys / 8; ++n) {
               const int key = key0 + 8 * n + 2 * (lane & 3);  // even, and so is the row's pitch
               if (key < j1) *reinterpret_cast<float2 *>(dst + key) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
             }
           }
         }
       }
-      rows.absorb(vs, warp * 16, s);
+      rows.template softmax<kWarpKeys>(s);
+      cp_async_wait<2>();  // this V
+      __syncwarp();
+      rows.template add_pv<kWarpKeys>(vs, 0, s);
+      __syncwarp();
+      if (step + 2 < steps) kw.load(vs, p.k_own[src]);
+      cp_async_commit();
+      const uint32_t k_next = next;
+      next = vs;
+      vs = ks;
+      ks = k_next;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // every stage has been read
-    float *so = reinterpret_cast<float *>(own_smem);  // [warp][16 rows][D]
-    rows.put(s_ml[warp], so + warp * 16 * D);
+    cp_async_wait<0>();
+    __syncwarp();  // the ring is read and nothing is on its way to it
+    float *so = reinterpret_cast<float *>(own_smem);  // each warp's [16][D] over its ring
+    rows.put(s_ml[warp], so + warp * (C::kRing / 4));
     __syncthreads();
     const int n_rows = min(16, p.group - g0);
     for (int i = tid; i < n_rows * (D / 4); i += kOwnThreads) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       float2 ml;
-      const float4 acc = join_warps<D>(s_ml, so, r, c, ml);
+      const float4 acc = join_warps<D>(s_ml, so, C::kRing / 4, r, c, ml);
       const long long at = static_cast<long long>(p.split_p + split) * p.batch * p.heads_q + part_row(p, kv, b, g0 + r);
       *reinterpret_cast<float4 *>(p.part_o + at * D + c) = acc;
       if (c == 0) p.part_ml[at] = ml;
@@ -799,14 +861,16 @@ constexpr int kScoreRow = kDirectTiles * kOwnKeys + 4;     // floats of a row of
 
 template <int D>
 struct DirectCfg {
-  static constexpr int kTiles = OwnCfg<D>::kSmem;
+  static constexpr int kMat = kOwnKeys * D * 2;  // bytes of a stage's K (or V)
+  static constexpr int kStages = 3;
+  static constexpr int kTiles = kStages * 2 * kMat;
   static constexpr int kSmem = kTiles + 16 * kScoreRow * 4;
   static_assert(kTiles >= 5 * 16 * D * 4, "the warps' and the CTA's outputs fit over the stages");
 };
 
 template <int D>
 __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant__ PrefixAttnParams p) {
-  using C = OwnCfg<D>;
+  using C = DirectCfg<D>;
   extern __shared__ __align__(128) uint8_t own_smem[];
   __shared__ float2 s_ml[4][16];
   __shared__ __align__(16) float4 s_cta[16];  // the CTA's (m, l) of each row; 16 bytes for the cluster's loads
@@ -825,7 +889,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
   const int src = kv / p.heads_per_source;
   const long long col = static_cast<long long>(kv - src * p.heads_per_source) * D;
   const uint32_t sbase = ptx::smem_addr(own_smem);
-  float *s_scores = reinterpret_cast<float *>(own_smem + DirectCfg<D>::kTiles);  // [16][kScoreRow] of the own tiles
+  float *s_scores = reinterpret_cast<float *>(own_smem + C::kTiles);  // [16][kScoreRow] of the own tiles
   TileLoader<D> loader;
   int load_stage = 0;
   auto load = [&](int t) {
@@ -857,7 +921,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
     const int left = (t < tiles_p ? p.prefix - t * kOwnKeys : len - (t - tiles_p) * kOwnKeys) - warp * 16;
     if (left <= 0) continue;
     float s[2][4];
-    rows.scores(ks, warp * 16, left, p.scale_log2, s);
+    rows.template scores<16>(ks, warp * 16, left, p.scale_log2, s);
     if (p.w_out[0] && t >= tiles_p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -866,7 +930,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
           *reinterpret_cast<float2 *>(s_scores + ((lane >> 2) + 8 * h) * kScoreRow + (t - own0) * kOwnKeys + warp * 16 + 8 * n +
                                       2 * (lane & 3)) = make_float2(s[n][2 * h], s[n][2 * h + 1]);
     }
-    rows.absorb(vs, warp * 16, s);
+    rows.template softmax<16>(s);
+    rows.template add_pv<16>(vs, warp * 16, s);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
@@ -877,7 +942,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
   for (int i = tid; i < 16 * (D / 4); i += kOwnThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float2 ml;
-    *reinterpret_cast<float4 *>(cta_o + r * D + c) = join_warps<D>(s_ml, so, r, c, ml);
+    *reinterpret_cast<float4 *>(cta_o + r * D + c) = join_warps<D>(s_ml, so, 16 * D, r, c, ml);
     if (c == 0) s_cta[r] = make_float4(ml.x, ml.y, 0.f, 0.f);
   }
   if (parts > 1) ptx::cluster_sync();

@@ -1152,7 +1152,7 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
       // on all SMs. 128 sequences, 32768 + 1025 keys on average: 84 us on 96 SMs, 96 on
       // 80, 98 on 112, 110 on all; 61 sequences, 4099 + 256 keys: 36 on 80, 38 on 112, 42.
       const double t_p = bases * s.blocks * (rows > 128 ? 2.4 : 1.2);
-      const double t_o = 0.5 * batch * heads_kv * ((group + 15) / 16) * cap / 64 * 0.55 * d / 128;
+      const double t_o = 0.5 * batch * heads_kv * ((group + 15) / 16) * cap / 64 * 0.50 * d / 128;
       s.ctas_p = static_cast<int>(kSms * t_p / (t_p + t_o) + 0.5);
       if (s.ctas_p < kSms / 4) s.ctas_p = kSms / 4;
     }

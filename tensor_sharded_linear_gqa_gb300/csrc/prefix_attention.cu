@@ -103,7 +103,10 @@ __device__ __forceinline__ int own_length(const PrefixAttnParams &p, int b) {
 // m moves only on a split's first block or when a block's sum of p passes 2^64.
 // A block step of both tiles takes 1.8 us (the MMAs alone 0.55): its period is the chain
 // S, softmax, P V of the two tiles. With the MMAs issued under a branch on the lane
-// index, which holds operands outside the uniform registers, it took 2.0 us.
+// index, which holds operands outside the uniform registers, it took 2.0 us. Halving
+// the chain costs more than it hides: products of P's halves 2.0 us, S by halves of
+// 64 keys too (four chains) 2.3. An item's start and end move q and O between rows
+// and threads through shared memory (61 sequences, 4099 keys: 28.9 -> 26.1 us a call).
 // ---------------------------------------------------------------------------
 constexpr int kPrefThreads = 320;
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
@@ -145,6 +148,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 template <int D>
@@ -332,6 +344,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
     const uint32_t sb = tmem + lane_off + static_cast<uint32_t>(x * 128);
     const uint32_t ob = tmem + lane_off + 256u + static_cast<uint32_t>(x * 128);
     const uint32_t s_full = s_full0 + 8 * x, p_full = p_full0 + 8 * x;
+    const uint32_t warp_q = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(qw) * 4096u;  // its 32 rows
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       const bool ready = ptx::mbar_wait(bar, parity, p.wait_ns);
@@ -351,19 +364,19 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       const int nb = b1 - b0;
       const int m_row = (2 * pair + x) * 128 + row;  // row of the kv head: sequence * group + head
       if ((2 * pair + x) * 128 >= rows) continue;
-      // this thread's q row into the Q tile; the previous item's products have read
-      // it (its o_full was waited for)
+      // the warp's q rows into the Q tile, a row's 16-byte pieces by neighbouring lanes; the
+      // previous item's products have read it (its o_full was waited for)
       {
-        const uint32_t dst = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(row) * 128u;
-        const bool there = m_row < rows;
-        const int b = there ? m_row / p.group : 0, gq = there ? m_row - b * p.group : 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(q_row(p, b, kv * p.group + gq));
+        constexpr int kPieces = D / 8;
+        const int b = m_row < rows ? m_row / p.group : 0, gq = m_row < rows ? m_row - b * p.group : 0;
+        const unsigned long long mine = m_row < rows ? reinterpret_cast<unsigned long long>(q_row(p, b, kv * p.group + gq)) : 0;
+        const int c = lane % kPieces;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = there ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t at = dst + (c >> 3) * kSubTile + static_cast<uint32_t>(((c & 7) ^ (row & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = i * (32 / kPieces) + lane / kPieces;
+          const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, mine, r));
+          const uint4 v = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          st_shared(warp_q + (c >> 3) * kSubTile + r * 128 + ((c & 7) ^ (r & 7)) * 16, v);
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(q_full0 + 8 * x);
@@ -458,19 +471,26 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       ptx::tc_fence_after();
       const long long at = static_cast<long long>(split) * p.batch * p.heads_q + static_cast<long long>(kv) * rows + m_row;
       if (m_row < rows) p.part_ml[at] = make_float2(m, l);
+      // out by rows of 128 bytes, turned in the warp's part of the Q tile, which nothing
+      // reads any more: a lane that stores its own row touches 32 lines an instruction
+      const int there = rows - (m_row - lane);  // of the warp's rows
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         ptx::tmem_ld_32cols(ob + c * 32, v);
         ptx::tmem_ld_wait();
         ptx::tmem_regs_ready(v);
-        if (m_row < rows) {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + c * 32);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                 __uint_as_float(v[4 * i + 3]));
+        for (int i = 0; i < 8; ++i)
+          st_shared(warp_q + lane * 128 + (i ^ (lane & 7)) * 16, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), q = lane & 7;
+          const uint4 w = ld_shared(warp_q + r * 128 + (q ^ (r & 7)) * 16);
+          if (r < there) *reinterpret_cast<uint4 *>(p.part_o + (at - lane + r) * D + c * 32 + q * 4) = w;
         }
+        __syncwarp();
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(o_free0 + 8 * x);
@@ -491,15 +511,21 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
-// The own caches. CTA (sequence and kv head, key split, 16-head tile); 64-key
-// stages, the four warps take 16 keys each and keep their own m, l and O, which
+// The own caches. CTA (sequence and kv head, key split, 16-head tile). The four
+// warps walk by themselves, 32 keys a step, each through its own ring of three slots (K
+// of the step, V of the step, K of the next), and keep their own m, l and O, which
 // are joined at the end. Keys past the length are zero-filled in shared memory,
 // never read from the cache (stale values there may be anything), and masked.
-// Bound by memory on all SMs (268 MB in 45 us, 6 TB/s) and by the steps' latency, 62
-// KB/us an SM with two CTAs, on the SMs that the prefix part leaves. Measured and
-// slower: eight warps that share a step's maximum and P and own output columns (three
-// barriers a step, 23 KB/us); runs of steps across sequences in place of a CTA a
-// split (no better balance than the scheduler's, and a join and a q load in the run).
+// Bound by memory on all SMs (268 MB in 45 us, 6 TB/s) and by latency on the SMs that
+// the prefix part leaves: a step's chain (85 KB/us an SM with two CTAs of 1000
+// keys), a CTA's start and join (44 KB/us with 256 keys). Measured and slower: stages
+// of 64 keys shared by the warps, 16 a warp (62 KB/us; 61 sequences 36.1 us in place
+// of 33.4: twice the shuffles and dependent products a key, and a barrier); rings of
+// 16 keys (35.6); three CTAs an SM with two shared stages (33.9, but 90 in place of 85
+// for 128 sequences of 1025 keys: too little in flight); eight warps that share
+// a step's maximum and P and own output columns (three barriers a step, 23 KB/us); runs
+// of steps across sequences in place of a CTA a split (no better balance than the
+// scheduler's, and a join and a q load in the run).
 // ---------------------------------------------------------------------------
 constexpr int kOwnThreads = 128;
 constexpr int kOwnKeys = 64;   // keys of a k_direct tile; an own split is a multiple of it
@@ -1147,11 +1173,11 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
     if (cap > 0) {
       // The prefix part leaves SMs to the own part, which runs beside it: its share of
       // the two parts' SM time, 2.4 us for a block step with its part of an item's start
-      // and end (1.2 with one tile of rows) and 0.55 us for 64 own keys, if the caches are
+      // and end (1.5 with one tile of rows) and 0.5 us for 64 own keys, if the caches are
       // half full (the lengths are the device's). Fuller caches go on after the prefix,
-      // on all SMs. 128 sequences, 32768 + 1025 keys on average: 84 us on 96 SMs, 96 on
-      // 80, 98 on 112, 110 on all; 61 sequences, 4099 + 256 keys: 36 on 80, 38 on 112, 42.
-      const double t_p = bases * s.blocks * (rows > 128 ? 2.4 : 1.2);
+      // on all SMs. 128 sequences, 32768 + 1025 keys on average: 85 us on 96 SMs, 108 on
+      // 112; 61 sequences, 4099 + 256 keys: 34 on 64 or 80, 39 on 96.
+      const double t_p = bases * s.blocks * (rows > 128 ? 2.4 : 1.5);
       const double t_o = 0.5 * batch * heads_kv * ((group + 15) / 16) * cap / 64 * 0.50 * d / 128;
       s.ctas_p = static_cast<int>(kSms * t_p / (t_p + t_o) + 0.5);
       if (s.ctas_p < kSms / 4) s.ctas_p = kSms / 4;

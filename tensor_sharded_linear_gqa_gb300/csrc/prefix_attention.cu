@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       ptx::mbar_init(v_full0 + 8 * s, 1);
       ptx::mbar_init(v_empty0 + 8 * s, 1);
       ptx::mbar_init(s_full0 + 8 * s, 1);
-      ptx::mbar_init(p_full0 + 8 * s, 128);
+      ptx::mbar_init(p_full0 + 8 * s, 4);
       ptx::mbar_init(o_full0 + 8 * s, 1);
       ptx::mbar_init(o_free0 + 8 * s, 128);
     }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
     const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, p.wait_ns) && *abort_flag == 0)) return true;
+      if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, p.wait_ns))) return true;  // an abort elsewhere ends in a timeout here
       if (*abort_flag == 0) record(p.status, kDevTimeoutMma);
       ok = false;
       return false;
@@ -304,28 +304,21 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       commit(k_empty0 + 8 * (g & 1));
       for (int j = 0; ok && j < nb; ++j) {
         const int gj = g + j;
+        const bool last = j + 1 == nb;
         if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
-        bool next_k = false;
+        if (!last && !wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
         for (int x = 0; ok && x < tiles; ++x) {
           if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
           ++np[x];
           if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
           ptx::tc_fence_after();
           issue_pv(x, gj, j == 0);
-          if (j + 1 == nb) {
-            commit(o_full0 + 8 * x);
-          } else {
-            if (!next_k) {
-              if (!wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
-              ptx::tc_fence_after();
-              next_k = true;
-            }
-            issue_s(x, gj + 1);
-          }
+          if (last) commit(o_full0 + 8 * x);
+          else issue_s(x, gj + 1);
         }
         if (!ok) break;
         commit(v_empty0 + 8 * (gj & 1));
-        if (next_k) commit(k_empty0 + 8 * ((gj + 1) & 1));
+        if (!last) commit(k_empty0 + 8 * ((gj + 1) & 1));
       }
       for (int x = 0; x < tiles; ++x) ++nact[x];
       g += nb;
@@ -348,14 +341,12 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       const bool ready = ptx::mbar_wait(bar, parity, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ready && *abort_flag == 0)) {
-        if (lane == 0) {
-          if (!ready) record(p.status, kDevTimeoutEpilogue);
-          *abort_flag = 1;
-        }
-        return false;
+      if (__all_sync(0xffffffffu, ready)) return true;  // an abort elsewhere ends in a timeout here
+      if (lane == 0) {
+        if (*abort_flag == 0) record(p.status, kDevTimeoutEpilogue);
+        *abort_flag = 1;
       }
-      return true;
+      return false;
     };
     uint32_t gs = 0, nact = 0;
     for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
@@ -460,7 +451,8 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full);
       }
       if (!ok) break;
       if (!wait_all(o_full0 + 8 * x, nact & 1)) {

@@ -101,11 +101,13 @@ __device__ __forceinline__ int own_length(const PrefixAttnParams &p, int b) {
 // is read from there), O at 256 and 384. V is used as it lies, [keys x d], as an
 // MN-major operand, so no transposed copy is made. The running reference maximum
 // m moves only on a split's first block or when a block's sum of p passes 2^64.
-// A block step of both tiles takes 1.8 us (the MMAs alone 0.55): its period is the chain
+// A block step of both tiles takes 1.6 us (the MMAs alone 1.1): its period is the chain
 // S, softmax, P V of the two tiles. With the MMAs issued under a branch on the lane
-// index, which holds operands outside the uniform registers, it took 2.0 us. Halving
-// the chain costs more than it hides: products of P's halves 2.0 us, S by halves of
-// 64 keys too (four chains) 2.3. An item's start and end move q and O between rows
+// index, which holds operands outside the uniform registers, it took 0.2
+// us more. Halving the chain costs more than it hides: products of P's halves 0.2 us, S
+// by halves of 64 keys too (four chains) 0.5. P stored 16 keys at a time in place of
+// 32, for the registers, is worth 3%; columns loaded under the exponentials of those
+// before cost 10% (spills). An item's start and end move q and O between rows
 // and threads through shared memory (61 sequences, 4099 keys: 28.9 -> 26.1 us a call).
 // ---------------------------------------------------------------------------
 constexpr int kPrefThreads = 320;
@@ -382,10 +384,8 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
         const int lim = p.prefix - (b0 + j) * 128;  // keys of the block that exist
         uint32_t v[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&vc)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]);
-          ptx::tmem_ld_32cols(sb + 32 * c, vc);
-        }
+        for (int c = 0; c < 8; ++c)
+          ptx::tmem_ld_16cols(sb + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * c]));
         ptx::tmem_ld_wait();
         ptx::tmem_regs_ready(v);
         if (lim < 128) {
@@ -418,16 +418,20 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
           for (int h = 0; h < 4; ++h) {
             uint64_t &sum2 = sumh[h];
             sum2 = pack2(0.f, 0.f);
-            uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float y0, y1;
-              unpack2(fma2(pack2(__uint_as_float(v[32 * h + i]), __uint_as_float(v[32 * h + i + 1])), c2, nm2), y0, y1);
-              const float a0 = ex2(y0), a1 = ex2(y1);
-              sum2 = add2(sum2, pack2(a0, a1));
-              pk[i >> 1] = pack_bf16(a0, a1);
+            for (int e = 0; e < 32; e += 16) {  // P leaves in pieces of 16 keys: v holds most registers
+              uint32_t pk[8];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const int k = 32 * h + e + i;
+                float y0, y1;
+                unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, nm2), y0, y1);
+                const float a0 = ex2(y0), a1 = ex2(y1);
+                sum2 = add2(sum2, pack2(a0, a1));
+                pk[i >> 1] = pack_bf16(a0, a1);
+              }
+              ptx::tmem_st_8cols(sb + 16 * h + e / 2, pk);
             }
-            ptx::tmem_st_16cols(sb + 16 * h, pk);
           }
           unpack2(add2(add2(sumh[0], sumh[1]), add2(sumh[2], sumh[3])), s0, s1);
           if (find_max || !__any_sync(0xffffffffu, !(s0 + s1 <= kSumLimit))) break;
@@ -435,9 +439,9 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
           ptx::tmem_st_wait();
         }
         const float alpha = move ? exp2f(m - m_new) : 1.f;
-        l = l * alpha + (s0 + s1);
         m = m_new;
-        if (j > 0 && __any_sync(0xffffffffu, move)) {
+        if (find_max && j > 0 && __any_sync(0xffffffffu, move)) {
+          l *= alpha;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -453,6 +457,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_full);
+        l += s0 + s1;
       }
       if (!ok) break;
       if (!wait_all(o_full0 + 8 * x, nact & 1)) {

@@ -177,12 +177,18 @@ def _check(status: int, where: str) -> None:
 # field through ctypes costs about as long as the rest of a small call.
 _DESC = struct.Struct("=Qiiqqq")
 _DTYPES: dict = {}
+try:
+    from . import _describe  # the same in C, for plain tensors: a small call's issue time is mostly this
+except ImportError:  # not built (an interpreter without its headers): interpreted code does it all
+    _describe = None
 
 
 def _dtypes() -> dict:
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3})
+        if _describe is not None:
+            _describe.dtypes(*_DTYPES)
     return _DTYPES
 
 
@@ -490,16 +496,8 @@ class _Scratch:
             return None
         at = self.used
         self.used = at + _DESC_SIZE
-        if type(t) is TpTensor:
-            _PACK(self.buf, at, *_fields(t))
-            return self.base + at
-        rows, cols = t.shape
-        ld, step = t.stride()
-        dt = _DTYPES.get(t.dtype)
-        if step != 1 or dt is None or not rows or not cols or not t.is_cuda:
-            _PACK(self.buf, at, *_fields(t))  # an empty tensor, the first of all, or an error's words
-        else:
-            _PACK(self.buf, at, t.data_ptr(), dt, 0, rows, cols, ld if rows > 1 or ld > cols else cols)
+        if not _matrix(t, self.base + at):
+            _PACK(self.buf, at, *_fields(t))  # no plain tensor, the first of all, or an error's words
         return self.base + at
 
     def many(self, seq, n: int):
@@ -509,25 +507,29 @@ class _Scratch:
         if isinstance(seq, ctypes.Array):
             return seq
         first = self.base + self.used
-        one = self.one
-        for i in range(n):
-            one(seq[i])
+        done = _matrices(seq, n, first)
+        self.used += done * _DESC_SIZE
+        for i in range(done, n):
+            self.one(seq[i])
         return first
 
     def row(self, t):
         """A vector: its 1-D tensor is the [1 x n] view that the library takes."""
-        if t is None or type(t) is TpTensor or t.dim() != 1:
-            return self.one(t)
-        n, dt = len(t), _DTYPES.get(t.dtype)
-        if dt is None or not n or not t.is_cuda or t.stride(0) != 1:
-            return self.one(t.unsqueeze(0))
+        if t is None:
+            return None
         at = self.used
+        if not _row(t, self.base + at):
+            return self.one(t if type(t) is TpTensor or t.dim() != 1 else t.unsqueeze(0))
         self.used = at + _DESC_SIZE
-        _PACK(self.buf, at, t.data_ptr(), dt, 0, 1, n, n)
         return self.base + at
 
 
 _DESC_SIZE, _PACK = _DESC.size, _DESC.pack_into
+if _describe is not None:
+    _matrix, _matrices, _row = _describe.matrix, _describe.matrices, _describe.row
+else:
+    _matrix = _row = lambda t, to: False  # noqa: E731
+    _matrices = lambda seq, n, to: 0  # noqa: E731
 _local = threading.local()
 
 

@@ -4,7 +4,8 @@ Each translation unit is compiled in parallel into ``_build/`` and linked into
 ``tensor_sharded_linear_gqa_gb300/libtpgqa.so`` (static CUDA runtime; the driver
 API is reached through cudaGetDriverEntryPointByVersion, so libcuda is not a
 link dependency). A stamp records the machine and the source hashes, so a
-library built for another machine or from other sources is rebuilt.
+library built for another machine or from other sources is rebuilt. Beside it
+lies ``_describe.so``, an extension module of the Python binding.
 
 Usage: ``python -m tensor_sharded_linear_gqa_gb300.build [--force] [-v]``.
 """
@@ -17,6 +18,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -26,10 +28,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpgqa.so")
 STAMP = os.path.join(BUILD, "stamp.json")
+DESCRIBE = os.path.join(PKG, "_describe.so")  # the binding's extension module
 
 SOURCES = ["plan.cpp", "tp_api.cu", "gemm_tcgen05.cu", "gemm_f32.cu", "combine.cu", "mlp_static.cu", "vocab.cu", "moe.cu", "attention.cu",
            "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu", "prefix_attention.cu"]
-HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h"]
+HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h", "describe.c"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -81,6 +84,24 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_describe(verbose: bool) -> None:
+    """Compiles the extension module that describes tensors; without the interpreter's headers
+    there is none, and the binding does without."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print(f"{include}/Python.h is missing: tensors are described by interpreted code", file=sys.stderr)
+        return
+    tmp = DESCRIBE + ".tmp"
+    cmd = [nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", "-cudart", "none", "-shared", "-I", INCLUDE, "-I", include,
+           os.path.join(CSRC, "describe.c"), "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"nvcc failed on describe.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, DESCRIBE)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compiles and links libtpgqa.so if it is missing or stale; returns its path."""
     if not force and up_to_date():
@@ -96,6 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_describe(verbose)
     with open(STAMP, "w") as fh:
         json.dump(_stamp(), fh)
     return LIB

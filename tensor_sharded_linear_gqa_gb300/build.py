@@ -54,12 +54,18 @@ def _digest() -> str:
     return h.hexdigest()
 
 
+def _python_h() -> str:
+    return os.path.join(sysconfig.get_paths()["include"], "Python.h")
+
+
 def _stamp() -> dict:
-    return {"machine": platform.machine(), "digest": _digest()}
+    return {"machine": platform.machine(), "digest": _digest(), "python": sysconfig.get_config_var("SOABI")}
 
 
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(STAMP):
+        return False
+    if os.path.exists(_python_h()) and not os.path.exists(DESCRIBE):
         return False
     try:
         with open(STAMP) as fh:
@@ -87,13 +93,12 @@ def _compile(src: str, verbose: bool) -> str:
 def _build_describe(verbose: bool) -> None:
     """Compiles the extension module that describes tensors; without the interpreter's headers
     there is none, and the binding does without."""
-    include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
-        print(f"{include}/Python.h is missing: tensors are described by interpreted code", file=sys.stderr)
+    if not os.path.exists(_python_h()):
+        print(f"{_python_h()} is missing: tensors are described by interpreted code", file=sys.stderr)
         return
     tmp = DESCRIBE + ".tmp"
-    cmd = [nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", "-cudart", "none", "-shared", "-I", INCLUDE, "-I", include,
-           os.path.join(CSRC, "describe.c"), "-o", tmp]
+    cmd = [nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", "-cudart", "none", "-shared", "-I", INCLUDE,
+           "-I", os.path.dirname(_python_h()), os.path.join(CSRC, "describe.c"), "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -686,7 +686,8 @@ __device__ __forceinline__ float part_factor(float2 ml, float top) {
   return ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - top);
 }
 // Four columns of a row over the CTA's four warps (`stride` floats apart): their common
-// maximum, sum and outputs.
+// maximum, sum and outputs. A warp without keys has zeros, and a factor of 0 still multiplies: a warp
+// whose only scores are no numbers has a maximum of -inf (fmaxf passes over them) and such a sum.
 template <int D>
 __device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const float *so, int stride, int r, int c, float2 &ml) {
   float top = -INFINITY;
@@ -697,7 +698,6 @@ __device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const flo
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const float f = part_factor(s_ml[w][r], top);
-    if (f == 0.f) continue;  // a warp without keys (its outputs may be anything times 0)
     const float4 ov = *reinterpret_cast<const float4 *>(so + w * stride + r * D + c);
     sum += f * s_ml[w][r].y;
     acc.x += f * ov.x;

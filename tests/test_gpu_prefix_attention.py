@@ -273,3 +273,23 @@ def test_eviction_reads_the_accumulated_weights():
     for s in range(2):
         at = kept[s, 1].long()
         assert torch.equal(kv[0][s][64:96], before[s][64 + at])
+
+
+# One prefix-free batch per kernel route: clusters of one launch (groups of at most 16 heads), and the
+# three kernels (17 heads). The last own key is alone in its warp's share, with every count of keys.
+@pytest.mark.parametrize("length", [1, 17, 33, 49, 65, 97, 129, 130])
+@pytest.mark.parametrize("hq, P", [(8, 0), (34, 0), (8, 70), (34, 70)])
+def test_a_nan_in_the_last_own_key_reaches_the_output(hq, P, length):
+    need_gpu()
+    c = Case(1, hq, 2, 128, 5, P, 130, [64, length, 130, length, 13], seed=31)
+    want, w_want = c.run()
+    c.ko[130 + length - 1, 5] = float("nan")   # sequence 1, kv head 0
+    a, w = c.run()
+    group = hq // 2
+    assert torch.isnan(a[1].view(hq, 128)[:group].float()).all()
+    assert torch.isnan(w[0, 2, :length]).all() and (w[0, 2, length:] == 0).all()
+    keep = torch.ones(5, hq, dtype=torch.bool, device="cuda")
+    keep[1, :group] = False
+    assert torch.equal(a.view(5, hq, 128)[keep], want.view(5, hq, 128)[keep])
+    rows = [i for i in range(10) if i != 2]
+    assert torch.equal(w[0, rows], w_want[0, rows])

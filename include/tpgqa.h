@@ -603,7 +603,8 @@ size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t
  *   a[b, h] = softmax(q[b, h] [Kp_g ; Ko_b,g]^T / sqrt(d)) [Vp_g ; Vo_b,g]
  * over all P prefix keys and the own keys in rows 0 .. lengths[b]-1 of the
  * sequence's C cache rows (the new token's own key among them, if it is to see
- * itself). No position encoding is applied. A row without any key is zero.
+ * itself). No position encoding is applied. A row without any key is zero. A key
+ * that scores -inf has weight 0; a row of such keys alone is NaN, as 0 / 0.
  *  q[r], a[r] : [batch x Hq_r*d] bf16, rank r's q heads and output columns.
  *  k_prefix, v_prefix : per kv source (one per rank, or one when the plan
  *               replicates K/V) bf16 [P x heads*d]; P may be 0.

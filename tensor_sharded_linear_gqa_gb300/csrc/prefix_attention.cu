@@ -13,7 +13,9 @@
 // m16n8k16 products whose 16 rows are the group's heads; P stays in registers.
 // Both leave unnormalised f32 sums with their reference maximum m and sum l per
 // (split, row); k_combine joins them: sum of 2^(m_s - M) O_s over sum of
-// 2^(m_s - M) l_s, which is the softmax over all keys, whatever the split.
+// 2^(m_s - M) l_s, which is the softmax over all keys, whatever the split. No m is below
+// f32's lowest value: with it in place of -inf, keys that score -inf (and masked ones) get
+// weight 0 where no other has been seen yet, and what is seen later moves m as usual.
 //
 // The two parts bound different things, so they run at the same time: k_prefix_part
 // leaves some SMs free, and k_own_part, which shares nothing with it, does not wait
@@ -22,6 +24,7 @@
 //
 // Few keys and sequences, where three launches cost more than the work, take one:
 // k_direct.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
                 mq[q] = max3(mq[q], __uint_as_float(v[32 * q + i]), __uint_as_float(v[32 * q + i + 1]));
               mq[q] = fmaxf(mq[q], __uint_as_float(v[32 * q + 30]));
             }
-            const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * p.scale_log2;
+            const float m_blk = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * p.scale_log2, -FLT_MAX);
             move = m_blk > m + 8.f;
             m_new = move ? m_blk : m;
           }
@@ -582,7 +585,7 @@ struct WarpRows {
     }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    m[0] = m[1] = -INFINITY;
+    m[0] = m[1] = -FLT_MAX;
     l[0] = l[1] = 0.f;
   }
 
@@ -623,7 +626,6 @@ struct WarpRows {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float m_new = fmaxf(m[h], mx);
-      // m_new is above -inf unless a score is not a number
       alpha[h] = m[h] == m_new ? 1.f : ex2(m[h] - m_new);
       l[h] *= alpha[h];
       m[h] = m_new;
@@ -681,13 +683,9 @@ struct WarpRows {
     }
   }
 };
-// 2^(m - top) for a part (m, l) of a row, 0 for one without keys.
-__device__ __forceinline__ float part_factor(float2 ml, float top) {
-  return ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - top);
-}
 // Four columns of a row over the CTA's four warps (`stride` floats apart): their common
 // maximum, sum and outputs. A warp without keys has zeros, and a factor of 0 still multiplies: a warp
-// whose only scores are no numbers has a maximum of -inf (fmaxf passes over them) and such a sum.
+// whose only scores are no numbers has the lowest maximum (fmaxf passes over them) and such a sum.
 template <int D>
 __device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const float *so, int stride, int r, int c, float2 &ml) {
   float top = -INFINITY;
@@ -697,7 +695,7 @@ __device__ __forceinline__ float4 join_warps(const float2 (*s_ml)[16], const flo
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float f = part_factor(s_ml[w][r], top);
+    const float f = ex2(s_ml[w][r].x - top);
     const float4 ov = *reinterpret_cast<const float4 *>(so + w * stride + r * D + c);
     sum += f * s_ml[w][r].y;
     acc.x += f * ov.x;
@@ -994,7 +992,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       if (q < parts) {
-        const float f = part_factor(ml[q], top);
+        const float f = ex2(ml[q].x - top);
         sum += f * ml[q].y;
         acc.x += f * ov[q].x;
         acc.y += f * ov[q].y;
@@ -1014,7 +1012,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
       for (int q = 0; q < parts; ++q) top = fmaxf(top, far(ml_addr + tid * 16, q).x);
       for (int q = 0; q < parts; ++q) {
         const float4 v = far(ml_addr + tid * 16, q);
-        sum += part_factor(make_float2(v.x, v.y), top) * v.y;
+        sum += ex2(v.x - top) * v.y;
       }
       s_lse[tid] = top + log2f(sum);
     }

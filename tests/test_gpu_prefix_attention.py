@@ -293,3 +293,62 @@ def test_a_nan_in_the_last_own_key_reaches_the_output(hq, P, length):
     assert torch.equal(a.view(5, hq, 128)[keep], want.view(5, hq, 128)[keep])
     rows = [i for i in range(10) if i != 2]
     assert torch.equal(w[0, rows], w_want[0, rows])
+
+
+def check_hidden(c, hide_prefix, hide_own):
+    """Keys that every q row scores with -inf (through channel 0) have weight 0, as in the definition;
+    rows of such keys alone divide 0 by 0. hide_prefix: [P], hide_own: [B, C] truth values."""
+    d, G, hr = c.d, c.hq // c.hkv, c.hkv // c.s
+    c.q.view(c.B, c.hq, d)[:, :, 0] = 1.0
+    finite = c.kp.clone(), c.ko.clone()
+    c.kp.view(c.P, c.hkv, d)[hide_prefix, :, 0] = float("-inf")
+    c.ko.view(c.B, c.C, c.hkv, d)[hide_own, :, 0] = float("-inf")
+    a, w = c.run(first=True)
+    for b in range(c.B):
+        n = min(max(int(c.lens[b]), 0), c.C)
+        hidden = torch.cat([hide_prefix, hide_own[b, :n]])
+        for h in range(c.hkv):
+            cols = slice(h * d, (h + 1) * d)
+            own = slice(b * c.C, b * c.C + n)
+            k = torch.cat([finite[0][:, cols], finite[1][own, cols]]).double()
+            v = torch.cat([c.vp[:, cols], c.vo[own, cols]]).double()
+            q = c.q[b].view(c.hq, d)[h * G:(h + 1) * G].double()
+            got = a[b].view(c.hq, d)[h * G:(h + 1) * G].double()
+            row = w[h // hr, b * hr + h % hr].double()
+            if len(hidden) == 0:
+                assert (got == 0).all() and (row == 0).all()
+                continue
+            if bool(hidden.all()):
+                assert torch.isnan(got).all() and torch.isnan(row[:n]).all()
+                continue
+            s = q @ k.t() / d ** 0.5
+            ds = ((d / 16 + 16) * 2 * U * (q.abs() @ k.abs().t()) / d ** 0.5 + 4 * U * s.abs()).amax(1, keepdim=True)
+            rel = 2 * ds + 2.0 ** -18
+            p = torch.softmax(s.masked_fill(hidden, float("-inf")), dim=1)
+            out = p @ v
+            tol = (2.0 ** -8 + rel) * (p @ v.abs()) + 2.0 ** -8 * out.abs()
+            assert ((got - out).abs() <= 1.02 * tol + 1e-30).all(), (b, h)
+            ref = p[:, c.P:].sum(0)
+            tol = (p[:, c.P:] * rel).sum(0) + (G + 2) * U * ref
+            assert ((row[:n] - ref).abs() <= 1.02 * tol + 1e-30).all(), (b, h)
+            assert (row[n:] == 0).all()
+
+
+# What is hidden: the prefix's first keys (a whole first block and more splits than a warp joins at a
+# time), runs of own keys that fill a warp's share or a whole split, and every key of one sequence.
+@pytest.mark.parametrize("shape, first, own", [
+    ((1, 8, 2, 128, 3, 300, 130, [130, 77, 0]), 200, (0, 64)),
+    ((1, 8, 2, 64, 3, 0, 130, [130, 77, 64]), 0, (0, 64)),              # the third sequence has hidden keys alone
+    ((1, 34, 2, 128, 5, 300, 130, [130, 77, 64, 0, 33]), 200, (0, 64)),
+    ((1, 34, 2, 64, 5, 0, 130, [130, 77, 64, 0, 33]), 0, (0, 64)),
+    ((1, 34, 2, 128, 5, 300, 130, [130, 77, 64, 0, 33]), 300, (32, 96)),
+    ((1, 20, 1, 128, 100, 6000, 64, [i % 65 for i in range(100)]), 140, (0, 32)),   # three blocks of keys an item
+    ((2, 2, 2, 128, 1, 20000, 64, [50]), 16000, (0, 50)),               # over 32 splits of the prefix are hidden
+    ((1, 2, 1, 128, 1, 0, 20000, [19990]), 0, (0, 15000)),              # and of the own keys
+], ids=lambda v: "-".join(map(str, v[:7] if type(v) is tuple else [v])))
+def test_keys_that_score_minus_infinity_have_no_weight(shape, first, own):
+    need_gpu()
+    c = Case(*shape, seed=32)
+    hide_prefix = torch.arange(c.P, device="cuda") < first
+    at = torch.arange(c.C, device="cuda")
+    check_hidden(c, hide_prefix, ((at >= own[0]) & (at < own[1])).expand(c.B, -1))

@@ -114,6 +114,18 @@ struct IsFp8<__nv_fp8_e4m3> {
   static constexpr bool value = true;
 };
 
+// The larger of two; NaN if either is (fmaxf would pass over it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+// A token's scale from its largest |z w| and its factor. A row whose largest |y| is
+// no number (a NaN, or an infinity times the factor 0 of an infinite mean) has no scale.
+__device__ __forceinline__ float row_scale(float top, float rstd) {
+  return max_nan(top * rstd, kScaleFloor) / kE4m3Max;
+}
+
 // Sum and maximum over the CTA, in every thread. The order of the additions is
 // fixed by the thread count, so results do not change from run to run.
 __device__ __forceinline__ float2 block_sum_max(float sum, float mx) {
@@ -121,7 +133,7 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   const int warps = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(sum, mx);
@@ -130,7 +142,7 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     r.x += __shfl_xor_sync(0xffffffffu, r.x, o);
-    r.y = fmaxf(r.y, __shfl_xor_sync(0xffffffffu, r.y, o));
+    r.y = max_nan(r.y, __shfl_xor_sync(0xffffffffu, r.y, o));
   }
   return r;
 }
@@ -199,7 +211,7 @@ __global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_c
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum = fmaf(z[j][i], z[j][i], sum);
-        if (IsFp8<YT>::value) mx = fmaxf(mx, fabsf(z[j][i] * w[j][i]));
+        if (IsFp8<YT>::value) mx = max_nan(mx, fabsf(z[j][i] * w[j][i]));
       }
     }
   }
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_c
   const float rstd = rsqrtf(st.x / static_cast<float>(p.cols) + p.eps);
   float inv = 1.0f;
   if (IsFp8<YT>::value) {
-    const float scale = fmaxf(st.y * rstd, kScaleFloor) / kE4m3Max;
+    const float scale = row_scale(st.y, rstd);
     inv = 1.0f / scale;
     if (threadIdx.x == 0) p.scale[row] = scale;
   }
@@ -248,13 +260,13 @@ __global__ void __launch_bounds__(512) k_add_rmsnorm_elems(const __grid_constant
   for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
     const float z = z_at(c);
     sum = fmaf(z, z, sum);
-    if (IsFp8<YT>::value) mx = fmaxf(mx, fabsf(z * w_at(c)));
+    if (IsFp8<YT>::value) mx = max_nan(mx, fabsf(z * w_at(c)));
   }
   const float2 st = block_sum_max(sum, mx);
   const float rstd = rsqrtf(st.x / static_cast<float>(p.cols) + p.eps);
   float inv = 1.0f;
   if (IsFp8<YT>::value) {
-    const float scale = fmaxf(st.y * rstd, kScaleFloor) / kE4m3Max;
+    const float scale = row_scale(st.y, rstd);
     inv = 1.0f / scale;
     if (threadIdx.x == 0) p.scale[row] = scale;
   }

@@ -153,3 +153,30 @@ def test_empty_and_other_stream():
     tp.tp_add_rmsnorm(x, None, w, EPS, None, y, stream=side)
     side.synchronize()
     check([x], None, w, "bf16", None, y, None)
+
+
+@pytest.mark.parametrize("D, n, lead, pad", [(512, 1, 0, None), (512, 3, 0, None), (16384, 1, 0, None), (250, 1, 1, 3),
+                                             (20000, 1, 0, None)])
+def test_nan_and_infinities_reach_the_scale(D, n, lead, pad):
+    """The largest |y| of such a row is not a number, so its scale is none, and neither is any code."""
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(D + n)
+    xs = []
+    for _ in range(n):
+        x = padded(6, D, torch.float32, lead, pad)
+        x.copy_(torch.randn(6, D, generator=g, device="cuda"))
+        xs.append(x)
+    xs[-1][1, D - 3] = float("inf")
+    xs[0][2, 4] = float("-inf")
+    xs[0][4, D // 2] = float("nan")
+    w = 1.0 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    y, scale = padded(6, D, TYPES["e4m3"], lead, pad), torch.zeros(6, device="cuda")
+    tp.tp_add_rmsnorm(xs if n > 1 else xs[0], None, w, EPS, None, y, scale)
+    torch.cuda.synchronize()
+    for row in (1, 2, 4):
+        assert torch.isnan(scale[row]) and torch.isnan(y[row].float()).all()
+    rest = [0, 3, 5]
+    check([x[rest] for x in xs], None, w, "e4m3", None, y.view(torch.uint8)[rest].view(TYPES["e4m3"]), scale[rest])
+    w[7] = float("nan")
+    tp.tp_add_rmsnorm(xs if n > 1 else xs[0], None, w, EPS, None, y, scale)
+    assert torch.isnan(scale).all() and torch.isnan(y.float()).all()

@@ -405,13 +405,22 @@ def tp_moe_workspace_size(dims: TpMoeDims, tokens: int) -> int:
 _DTYPE_NAMES: dict = {}  # str(dtype) by dtype: formatting it costs more than the rest of the check
 
 
-def _dev_ptr(t, dtype: str) -> int:
+def _dev_ptr(t, dtype: str, n: int | None = None, what: str = "") -> int:
+    """Address of a contiguous CUDA tensor (0 when empty). The library sees no length, so where it
+    takes one from elsewhere (n), the tensor's is held against it here."""
     name = _DTYPE_NAMES.get(t.dtype)
     if name is None:
         name = _DTYPE_NAMES[t.dtype] = str(t.dtype)
     if name != dtype or not t.is_contiguous():
         raise TypeError(f"expected a contiguous {dtype} tensor")
-    return t.data_ptr() if t.numel() else 0
+    have = t.numel()
+    if n is not None and have != n:
+        raise ValueError(f"{what} must have {n} entries, not {have}")
+    if have == 0:
+        return 0
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
 
 
 def tp_moe_block(dims: TpMoeDims, x, topk_ids, topk_w, w_gate, w_up, w_down, y, combine: int, workspace,
@@ -542,8 +551,12 @@ def _args(most: int) -> _Scratch:
     return s
 
 
-def _opt_ptr(t, dtype: str):
-    return None if t is None else _dev_ptr(t, dtype)
+def _scale_ptr(t, of, dim: int, what: str):
+    """Address of the scales of `of`'s rows (dim 0) or columns (1); None for None."""
+    if t is None:
+        return None
+    n = (of.rows, of.cols)[dim] if isinstance(of, TpTensor) else of.shape[dim]
+    return _dev_ptr(t, "torch.float32", n, what)
 
 
 def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=None, stream=None) -> None:
@@ -553,7 +566,7 @@ def tp_add_rmsnorm(x, residual, weight, eps: float, residual_out, y, y_scale=Non
     n = len(x) if many else 1
     a = _args(n + 4)
     st = _lib.tp_add_rmsnorm(n, a.many(x, n) if many else a.one(x), a.one(residual), a.row(weight), eps,
-                             a.one(residual_out), a.one(y), _opt_ptr(y_scale, "torch.float32"), _stream(stream))
+                             a.one(residual_out), a.one(y), _scale_ptr(y_scale, y, 0, "y_scale"), _stream(stream))
     if st:
         raise TPError(st, "tp_add_rmsnorm")
 
@@ -563,9 +576,10 @@ def tp_linear_epilogue(tp_size: int, shard: int, x, w, y, bias=None, activation:
     """y = activation(x w^T * x_scale * w_scale + bias) + residual. shard: TP_SHARD_COLUMN (x: [X],
     w: the ranks' weight rows) or TP_SHARD_ROW (x, w: the ranks' slices of the input features)."""
     a = _args(2 * tp_size + 3 if tp_size > 0 else 3)
+    to = a.one(y)
     st = _lib.tp_linear_epilogue(tp_size, shard, a.many(x, tp_size if shard == TP_SHARD_ROW else 1),
-                                 _opt_ptr(x_scale, "torch.float32"), a.many(w, tp_size), _opt_ptr(w_scale, "torch.float32"),
-                                 a.row(bias), activation, a.one(residual), a.one(y), _stream(stream))
+                                 _scale_ptr(x_scale, y, 0, "x_scale"), a.many(w, tp_size), _scale_ptr(w_scale, y, 1, "w_scale"),
+                                 a.row(bias), activation, a.one(residual), to, _stream(stream))
     if st:
         raise TPError(st, "tp_linear_epilogue")
 
@@ -582,6 +596,8 @@ def tp_prefix_attn(plan: Plan, q, k_prefix, v_prefix, k_own, v_own, lengths, a, 
                    stream=None) -> None:
     """One new token per sequence over the shared prefix and the sequence's own cache. q, a: one
     entry per rank; caches and weights: one per kv source; workspace: a CUDA byte tensor."""
+    if not workspace.is_contiguous() or not (workspace.is_cuda or workspace.numel() == 0):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     n, src = plan.dims.tp_size, _kv_sources(plan)
     g = _args(2 * n + 6 * src)
     st = _lib.tp_prefix_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_prefix, src), g.many(v_prefix, src),
@@ -598,15 +614,11 @@ def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int,
     """Keeps `budget` positions of every sequence and kv head: the first n_first, the last
     n_recent and the heaviest between. k, v, weight and their outputs: one entry per kv source."""
     batch, src = lengths.numel(), _kv_sources(plan)
-    if kept.numel() != batch * plan.dims.num_kv_heads * budget:
-        raise ValueError("kept must hold sources * batch * heads * budget entries")
-    if lengths_out.numel() != batch:
-        raise ValueError("lengths_out must have one entry per sequence")
     a = _args(6 * src)
     st = _lib.tp_cache_evict(plan.handle, batch, _dev_ptr(lengths, "torch.int32"), a.many(k, src), a.many(v, src),
                              a.many(weight, src), budget, n_first, n_recent, a.many(k_out, src), a.many(v_out, src),
-                             a.many(weight_out, src), _dev_ptr(lengths_out, "torch.int32"), _dev_ptr(kept, "torch.int32"),
-                             _stream(stream))
+                             a.many(weight_out, src), _dev_ptr(lengths_out, "torch.int32", batch, "lengths_out"),
+                             _dev_ptr(kept, "torch.int32", batch * plan.dims.num_kv_heads * budget, "kept"), _stream(stream))
     if st:
         raise TPError(st, "tp_cache_evict")
 

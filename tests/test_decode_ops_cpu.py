@@ -189,3 +189,90 @@ def test_attn_unsupported_empty_and_workspace():
     assert attn_status(ws_bytes=size(PLAN, 3, 50, 10, False) - 1) == tp.TP_ERR_WORKSPACE
     assert size(PLAN, 1 << 40, 1, 1, False) == 0
     assert attn_status(batch=1 << 40, q=T(BF, 1 << 30, 256)) == tp.TP_ERR_INVALID_ARG
+
+
+# ---- the binding's own checks: what the library sees as bare addresses ------------------
+class FakeTensor:
+    """What the binding reads of a torch tensor on the GPU."""
+
+    def __init__(self, n, dtype="float32", cuda=True, contiguous=True):
+        import torch
+        self.n, self.dtype, self.is_cuda, self.contiguous = n, getattr(torch, dtype), cuda, contiguous
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    class Unreachable:
+        def __getattr__(self, name):
+            def entry(*args):
+                raise AssertionError(f"{name} was called")
+            return entry
+
+    monkeypatch.setattr(tp, "_lib", Unreachable())
+    return PLAN
+
+
+def e4m3_norm(scale):
+    tp.tp_add_rmsnorm(T(F32, 4, 64), None, T(F32, 1, 64), 1e-5, None, T(E4, 4, 64), scale, stream=1)
+
+
+def e4m3_linear(xs, ws):
+    tp.tp_linear_epilogue(1, tp.TP_SHARD_COLUMN, [T(E4, 4, 64)], [T(E4, 96, 64)], T(BF, 4, 96), x_scale=xs, w_scale=ws, stream=1)
+
+
+@pytest.mark.parametrize("n", [0, 1, 3, 5])
+def test_scales_have_one_entry_a_token_or_feature(no_library, n):
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="y_scale"):
+        e4m3_norm(FakeTensor(n))
+    with pytest.raises(ValueError, match="x_scale"):
+        e4m3_linear(FakeTensor(n), FakeTensor(96))
+    with pytest.raises(ValueError, match="w_scale"):
+        e4m3_linear(FakeTensor(4), FakeTensor(n))
+
+
+def attn(plan, lengths, ws):
+    q, kp, ko = [T(BF, 3, 256)] * 2, [T(BF, 50, 128)] * 2, [T(BF, 30, 128)] * 2
+    tp.tp_prefix_attn(plan, q, kp, kp, ko, ko, lengths, q, ws, stream=1)
+
+
+def evict(plan, lengths, lengths_out, kept):
+    k, w = [T(BF, 30, 128)] * 2, [T(F32, 3, 10)] * 2
+    tp.tp_cache_evict(plan, lengths, k, k, w, 5, 1, 1, k, k, w, lengths_out, kept, stream=1)
+
+
+def test_addresses_must_be_the_gpus(no_library):
+    pytest.importorskip("torch")
+    f, i = lambda n: FakeTensor(n), lambda n: FakeTensor(n, "int32")  # noqa: E731
+    host = {"float32": lambda n: FakeTensor(n, cuda=False), "int32": lambda n: FakeTensor(n, "int32", cuda=False)}
+    calls = [lambda: e4m3_norm(host["float32"](4)), lambda: e4m3_linear(host["float32"](4), f(96)),
+             lambda: e4m3_linear(f(4), host["float32"](96)),
+             lambda: attn(no_library, host["int32"](3), FakeTensor(1 << 30, "uint8")),
+             lambda: attn(no_library, i(3), FakeTensor(1 << 30, "uint8", cuda=False)),
+             lambda: attn(no_library, i(3), FakeTensor(1 << 30, "uint8", contiguous=False)),  # an expanded byte, say
+             lambda: evict(no_library, host["int32"](3), i(3), i(30)), lambda: evict(no_library, i(3), host["int32"](3), i(30)),
+             lambda: evict(no_library, i(3), i(3), host["int32"](30))]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_right_sizes_reach_the_library(no_library):
+    pytest.importorskip("torch")
+    i = lambda n: FakeTensor(n, "int32")  # noqa: E731
+    for call in (lambda: e4m3_norm(FakeTensor(4)), lambda: e4m3_linear(FakeTensor(4), FakeTensor(96)),
+                 lambda: attn(no_library, i(3), FakeTensor(1 << 30, "uint8")), lambda: evict(no_library, i(3), i(3), i(30))):
+        with pytest.raises(AssertionError, match="was called"):
+            call()

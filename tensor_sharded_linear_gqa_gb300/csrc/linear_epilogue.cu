@@ -26,7 +26,10 @@
 // TMEM has room: k_linear_pair's epilogue adds each chunk to the sum in registers,
 // k_linear_split gives each chunk its own columns and adds them at the end, both
 // rounding to nearest. Over K = 8192 in bf16 this takes the error of an f32
-// output, relative to its size, from 8e-6 to about 1e-6.
+// output, relative to its size, from 8e-6 to about 1e-6. k_linear_split's room is
+// 256 columns where two CTAs share an SM (up to 128 tokens: two accumulators at 65 to
+// 128) and 512 where one has it (two): where K, over the cluster, needs more, each runs
+// longer, 128 steps and 2.2e-6 for 200 x 8192 x 8192 in bf16.
 // Warp roles in both: warp 0 loads (TMA), warp 1 issues the MMAs, the others are
 // the epilogue. Every wait is bounded, as in the grouped GEMM.
 #include <cstdlib>
@@ -952,12 +955,13 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     for (int c = 2; c <= 8; ++c)
       if (tiles * c <= num_sms() * per_sm && tiles <= max_active_clusters(c) * per_sm && p.kt_total >= 2 * c) p.split = c;
     if (tiles * p.split > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
-    // accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation
+    // accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation, in
+    // the columns that a CTA has: half of the SM's where two share it
     p.region_cols = 32;
     while (p.region_cols < p.tok_tile) p.region_cols *= 2;
     const int steps = (p.kt_total + p.split - 1) / p.split * 4;
     p.regions = 1;
-    while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= 256) p.regions *= 2;
+    while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= (two ? 256 : 512)) p.regions *= 2;
   }
   // A copy costs its issue whatever its size, so where every slice is whole k-tiles one
   // box spans a stage's k-tiles (2048 x 4096 x 8192 in e4m3: 56.1 us, 57.8 with one copy

@@ -180,3 +180,25 @@ def test_norm_feeds_the_8_bit_product():
     tp.tp_linear_epilogue(1, tp.TP_SHARD_COLUMN, [x], [w], y, x_scale=xs, w_scale=ws)
     torch.cuda.synchronize()
     check(y, x, w, xs, ws, None, "none", None)
+
+
+# Steps of the tensor core's f32 accumulation (32 bytes of K each) in one accumulator, by the launch rules:
+# K / 16 (bf16) or K / 32 (e4m3) over the split and over the accumulators that fit in tensor memory, 64 at
+# least as a bound. One accumulator of n steps is off by 1.6e-8 n of the result's norm (it truncates: 8e-6
+# over 512 steps); the limit is one and a half times that plus the f32 output's 2^-24.
+@pytest.mark.parametrize("T, K, N, dtype, steps", [
+    (1, 8192, 8192, BF16, 64), (64, 8192, 8192, BF16, 64), (128, 8192, 8192, BF16, 64), (61, 5000, 14336, BF16, 64),
+    (128, 16384, 2048, E4M3, 64), (64, 8192, 28672, E4M3, 64),
+    (200, 8192, 8192, BF16, 128), (300, 8192, 4096, BF16, 128), (256, 8192, 4096, E4M3, 64),
+    (1000, 8192, 4096, BF16, 64), (1030, 5000, 2560, BF16, 64), (1000, 16384, 4096, E4M3, 64),
+])
+def test_f32_sums_over_a_long_k(T, K, N, dtype, steps):
+    need_gpu()
+    p = Problem(T, K, N, dtype, K + T)
+    y = padded(T, N, F32)
+    tp.tp_linear_epilogue(1, tp.TP_SHARD_COLUMN, p.xr, p.wr, y, x_scale=p.xs, w_scale=p.ws)
+    want = p.x.double() @ p.w.double().t()
+    if dtype == E4M3:
+        want = want * p.xs.double()[:, None] * p.ws.double()
+    err = float((y.double() - want).norm() / want.norm())
+    assert err <= 1.5 * 1.6e-8 * steps + U

@@ -202,3 +202,24 @@ def test_f32_sums_over_a_long_k(T, K, N, dtype, steps):
         want = want * p.xs.double()[:, None] * p.ws.double()
     err = float((y.double() - want).norm() / want.norm())
     assert err <= 1.5 * 1.6e-8 * steps + U
+
+
+def one_value_a_row(v, act):
+    """act(v) for every element of a row, through a product that gives v exactly."""
+    T = len(v)
+    x, w, y = padded(T, 64, BF16), padded(1544, 64, BF16), padded(T, 1544, F32)
+    x[:, 3] = v
+    w[:, 3] = 1.0
+    tp.tp_linear_epilogue(1, tp.TP_SHARD_COLUMN, [x], [w], y, activation=act)
+    return y.double()
+
+
+# x Phi(x) = x/2 erfc(-x / sqrt 2): the argument is off by 2u of itself, which moves erfc by at most
+# x^2 + 1 times that, erfc by 8u, and two products by u.
+@pytest.mark.parametrize("T", [40, 1200])
+def test_gelu_far_in_its_tail(T):
+    need_gpu()
+    v = torch.linspace(-12.0, 12.0, T, device="cuda").to(BF16)
+    y, f = one_value_a_row(v, tp.TP_ACT_GELU), v.double()
+    want, rel = 0.5 * f * torch.erfc(-f / math.sqrt(2)), (2 * (f.square() + 1) + 10) * U
+    assert ((y - want[:, None]).abs() <= (1.01 * rel * want.abs())[:, None]).all()

@@ -112,19 +112,42 @@ __device__ __forceinline__ void gelu2(float &x0, float &x1) {
   x0 *= x0 < 0.0f ? h0 : 1.0f - h0;
   x1 *= x1 < 0.0f ? h1 : 1.0f - h1;
 }
+// x / (1 + e^-x) of two values for an f32 output, within 6 2^-24 of it: e^-x is 2^t, and the rounding of
+// t = -x log2(e), up to 2^-18 of e^-x, is brought in again behind it; the quotient is corrected
+// by its remainder. From 20 on it is x; t stops at 126, so below -88 it is 2^-126 x.
+__device__ __forceinline__ void silu2(float &x0, float &x1) {
+  const float c = 1.442695041f, c_low = 1.925963033e-8f, ln2 = 0.6931471806f;  // log2(e): c and what f32 leaves of it
+  const uint64_t x = pack2(x0, x1), minus_x = pack2(-x0, -x1), t = mul2(minus_x, pack2(c, c));
+  float t0, t1, d0, d1, y0, y1;
+  unpack2(t, t0, t1);
+  const uint64_t e = pack2(ex2(fminf(t0, 126.0f)), ex2(fminf(t1, 126.0f)));
+  const uint64_t minus_low = fma2(x, pack2(c_low, c_low), fma2(x, pack2(c, c), t));
+  const uint64_t d = add2(fma2(e, mul2(minus_low, pack2(-ln2, -ln2)), e), pack2(1.0f, 1.0f));
+  unpack2(d, d0, d1);
+  const uint64_t r = pack2(rcp(d0), rcp(d1));
+  unpack2(fma2(fma2(mul2(minus_x, r), d, x), r, mul2(x, r)), y0, y1);
+  x0 = x0 > 20.0f ? x0 : y0;
+  x1 = x1 > 20.0f ? x1 : y1;
+}
 
-// The activations by their formulas, in f32: relu, x Phi(x), x / (1 + e^-x) (at x < -88 the quotient is -0, its limit).
+// The activations by their formulas, in f32: relu, x Phi(x), x / (1 + e^-x). For a bf16 output
+// the last by the hardware's exponential and reciprocal alone, off by up to 2^-23 |x| of its
+// value (at x < -88 it is -0, its limit): far below bf16's half step of 2^-9, and the exact
+// form costs 4096 x 8192 x 28672 in e4m3 5%.
 template <int N>
-__device__ __forceinline__ void activate(float (&f)[N], int act) {
+__device__ __forceinline__ void activate(float (&f)[N], int act, bool f32) {
   if (act == TP_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = f[i] < 0.0f ? 0.0f : f[i];  // keeps NaN
   } else if (act == TP_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) gelu2(f[i], f[i + 1]);
+  } else if (act == TP_ACT_SILU && f32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) silu2(f[i], f[i + 1]);
   } else if (act == TP_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = __fdividef(f[i], 1.0f + __expf(-f[i]));
+    for (int i = 0; i < N; ++i) f[i] *= rcp(1.0f + ex2(f[i] * -1.442695041f));
   }
 }
 
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
         if (t0 + u * kWarps >= t1 || left <= 0) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[u][i] = f[u][i] * (sx[u] * terms[i].x) + terms[i].y;
-        activate(f[u], p.act);
+        activate(f[u], p.act, p.y_f32);
         if (p.res) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[u][i] += res[u][i];
@@ -520,7 +543,9 @@ __device__ __forceinline__ void pair_tile(const LinearParams &p, int tile, int &
   nt = r / rows;
 }
 
-template <bool F8, int BN>
+// Y32: an f32 output. As a template parameter it halves the epilogue's unrolled code, whose length
+// shows: with both kinds of output in one kernel the widest product takes 2% more.
+template <bool F8, int BN, bool Y32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ LinearParams p) {
   using C = PairCfg<BN>;
@@ -736,13 +761,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             f[i] = sum[c + i] * (sx * t.x) + t.y;
             f[i + 1] = sum[c + i + 1] * (sx * t.z) + t.w;
           }
-          activate(f, p.act);
+          activate(f, p.act, Y32);
           if (p.res) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] += res[i];
           }
-          if (wide && p.y_f32) store32(static_cast<float *>(p.y) + tok * p.y_ld + col + c, f);
-          else store_row(p.y, p.y_f32, tok * p.y_ld + col + c, n_left - c, f);
+          if (wide && Y32) store32(static_cast<float *>(p.y) + tok * p.y_ld + col + c, f);
+          else store_row(p.y, Y32, tok * p.y_ld + col + c, n_left - c, f);
         }
       }
     }
@@ -784,24 +809,28 @@ tp_status launch_split(const LinearParams &p, size_t smem, cudaStream_t s) {
   return launched(launch_kernel(k_linear_split<F8>, dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split)),
                                 dim3(kThreads), smem, s, static_cast<unsigned>(p.split), p));
 }
-template <bool F8, int BN>
+template <bool F8, int BN, bool Y32>
 tp_status launch_pair(const LinearParams &p, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_linear_pair<F8, BN>, mask, mu);
+  const cudaError_t e = allow_smem(k_linear_pair<F8, BN, Y32>, mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
   const int tiles = p.m_tiles * p.n_tiles, most = num_sms() / 2;
-  return launched(launch_kernel(k_linear_pair<F8, BN>, dim3(2u * static_cast<unsigned>(tiles < most ? tiles : most)),
+  return launched(launch_kernel(k_linear_pair<F8, BN, Y32>, dim3(2u * static_cast<unsigned>(tiles < most ? tiles : most)),
                                 dim3(kPairThreads), PairCfg<BN>::kSmem, s, 1, p));
 }
-template <bool F8>
+template <bool F8, bool Y32>
 tp_status launch_pair_bn(const LinearParams &p, int bn, cudaStream_t s) {
   switch (bn) {
-    case 128: return launch_pair<F8, 128>(p, s);
-    case 160: return launch_pair<F8, 160>(p, s);
-    case 192: return launch_pair<F8, 192>(p, s);
-    default: return launch_pair<F8, 224>(p, s);
+    case 128: return launch_pair<F8, 128, Y32>(p, s);
+    case 160: return launch_pair<F8, 160, Y32>(p, s);
+    case 192: return launch_pair<F8, 192, Y32>(p, s);
+    default: return launch_pair<F8, 224, Y32>(p, s);
   }
+}
+template <bool F8>
+tp_status launch_pair_y(const LinearParams &p, int bn, cudaStream_t s) {
+  return p.y_f32 ? launch_pair_bn<F8, true>(p, bn, s) : launch_pair_bn<F8, false>(p, bn, s);
 }
 
 // Whether view b continues view a to the right (same rows, next columns) or below.
@@ -1003,7 +1032,7 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     if (!encode(&p.x[i], xs[i], x_box)) return TP_ERR_INVALID_ARG;
   for (int i = 0; i < parts; ++i)
     if (!encode(&p.w[i], ws[i], w_box)) return TP_ERR_INVALID_ARG;
-  if (pair) return dt == TP_E4M3 ? launch_pair_bn<true>(p, bn, s) : launch_pair_bn<false>(p, bn, s);
+  if (pair) return dt == TP_E4M3 ? launch_pair_y<true>(p, bn, s) : launch_pair_y<false>(p, bn, s);
   size_t smem = 1024 + static_cast<size_t>(p.stages) * (kWTile + p.tok_tile * 128);
   const size_t out = 1024 + static_cast<size_t>(p.tok_tile) * 512;  // the partials lie over the stages
   smem = (smem > out ? smem : out) + 8 * (2 * p.stages + 2) + p.tok_tile * 4 + 64;

@@ -223,3 +223,13 @@ def test_gelu_far_in_its_tail(T):
     y, f = one_value_a_row(v, tp.TP_ACT_GELU), v.double()
     want, rel = 0.5 * f * torch.erfc(-f / math.sqrt(2)), (2 * (f.square() + 1) + 10) * U
     assert ((y - want[:, None]).abs() <= (1.01 * rel * want.abs())[:, None]).all()
+
+
+# x / (1 + e^-x): the exponential is off by 2u, the sum by u, the quotient by u; 2u are left for their forms.
+@pytest.mark.parametrize("T", [40, 1200])
+def test_silu_far_in_its_tail(T):
+    need_gpu()
+    v = torch.linspace(-80.0, 40.0, T, device="cuda").to(BF16)
+    y, f = one_value_a_row(v, tp.TP_ACT_SILU), v.double()
+    want = f / (1 + torch.exp(-f))
+    assert ((y - want[:, None]).abs() <= (1.01 * 6 * U * want.abs())[:, None]).all()

@@ -15,6 +15,7 @@ None for the current torch stream.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import struct
 import threading
@@ -177,19 +178,53 @@ def _check(status: int, where: str) -> None:
 # field through ctypes costs about as long as the rest of a small call.
 _DESC = struct.Struct("=Qiiqqq")
 _DTYPES: dict = {}
-try:
-    from . import _describe  # the same in C, for plain tensors: a small call's issue time is mostly this
-except ImportError:  # not built (an interpreter without its headers): interpreted code does it all
-    _describe = None
+
+
+def _load_describe():
+    """The same in C, for plain tensors (a small call's issue time is mostly this), loaded by the first
+    tensor that is described: importing the package maps no object. None where it is not built (an
+    interpreter without its headers): interpreted code does it all."""
+    global _describe, _matrix, _matrices, _row
+    if "_describe" not in globals():
+        try:
+            _describe = importlib.import_module("._describe", __name__)
+            _matrix, _matrices, _row = _describe.matrix, _describe.matrices, _describe.row
+        except ImportError:
+            _describe = None
+            _matrix = _row = lambda t, to: False  # noqa: E731
+            _matrices = lambda seq, n, to: 0  # noqa: E731
+    return _describe
+
+
+def __getattr__(name):
+    if name == "_describe":
+        return _load_describe()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _dtypes() -> dict:
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3})
-        if _describe is not None:
+        if _load_describe() is not None:
             _describe.dtypes(*_DTYPES)
     return _DTYPES
+
+
+def _matrix(t, to):
+    """_describe.matrix; _load_describe puts it in this one's place, as for the next two."""
+    _dtypes()
+    return _matrix(t, to)
+
+
+def _matrices(seq, n, to):
+    _dtypes()
+    return _matrices(seq, n, to)
+
+
+def _row(t, to):
+    _dtypes()
+    return _row(t, to)
 
 
 def _fields(t) -> tuple:
@@ -534,11 +569,6 @@ class _Scratch:
 
 
 _DESC_SIZE, _PACK = _DESC.size, _DESC.pack_into
-if _describe is not None:
-    _matrix, _matrices, _row = _describe.matrix, _describe.matrices, _describe.row
-else:
-    _matrix = _row = lambda t, to: False  # noqa: E731
-    _matrices = lambda seq, n, to: 0  # noqa: E731
 _local = threading.local()
 
 

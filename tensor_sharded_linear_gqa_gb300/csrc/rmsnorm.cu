@@ -152,11 +152,13 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx) {
 // be partial and is moved by elements.
 // ONE: a single x, whose few registers let three CTAs share an SM: with rows that
 // load, reduce and store at different times memory stays busy (4096 x 8192, f32 x and
-// bf16 residual: 56 us, 5.95 TB/s, against 69 us with two CTAs of up to 64 registers). The loads
-// of several partials need those registers (64 x 4096, eight partials: 5.4 us, 8.3
-// with three CTAs).
+// bf16 residual: 56 us, 5.95 TB/s, against 69 us with two CTAs of up to 64 registers). Four
+// groups a thread (rows of 8193 to 16384) leave room for two, and read the weight again, from
+// L1, where it would take half of the registers: 2048 x 16384 takes 64 us, 69 with the weight
+// kept (spills) and 84 with three CTAs (more of them). The loads of several partials
+// need more registers (64 x 4096, eight partials: 5.4 us, 8.3 with three CTAs).
 template <typename XT, typename RT, typename YT, int ITEMS, bool ONE>
-__global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(512, ONE ? (ITEMS <= 2 ? 3 : 2) : 1) k_add_rmsnorm(const __grid_constant__ NormParams p) {
   constexpr bool kRes = !std::is_same<RT, NoRes>::value;
   grid_dep_wait();
   grid_dep_launch();
@@ -200,18 +202,23 @@ __global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_c
       }
     }
   }
-  float w[ITEMS][8];
+  constexpr bool kKeep = ITEMS <= 2;  // the weight in registers
+  float kept[kKeep ? ITEMS : 1][8];
+  auto weight = [&](int c, float (&w)[8]) {
+    if (p.w_f32) load8(static_cast<const float *>(p.w) + c, p.cols - c, w);
+    else load8(static_cast<const __nv_bfloat16 *>(p.w) + c, p.cols - c, w);
+  };
   float sum = 0.0f, mx = 0.0f;
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
     const int c = (threadIdx.x + j * blockDim.x) * 8;
     if (c < p.cols) {
-      if (p.w_f32) load8(static_cast<const float *>(p.w) + c, p.cols - c, w[j]);
-      else load8(static_cast<const __nv_bfloat16 *>(p.w) + c, p.cols - c, w[j]);
+      float (&w)[8] = kept[kKeep ? j : 0];
+      if (kKeep || IsFp8<YT>::value) weight(c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum = fmaf(z[j][i], z[j][i], sum);
-        if (IsFp8<YT>::value) mx = max_nan(mx, fabsf(z[j][i] * w[j][i]));
+        if (IsFp8<YT>::value) mx = max_nan(mx, fabsf(z[j][i] * w[i]));
       }
     }
   }
@@ -230,9 +237,11 @@ __global__ void __launch_bounds__(512, ONE ? 3 : 1) k_add_rmsnorm(const __grid_c
       if constexpr (kRes) {
         if (p.res_out) store8(static_cast<RT *>(p.res_out) + row * p.res_out_ld + c, p.cols - c, z[j]);
       }
+      float (&w)[8] = kept[kKeep ? j : 0];
+      if (!kKeep) weight(c, w);
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = z[j][i] * rstd * w[j][i] * inv;
+      for (int i = 0; i < 8; ++i) v[i] = z[j][i] * rstd * w[i] * inv;
       store8(static_cast<YT *>(p.y) + row * p.y_ld + c, p.cols - c, v);
     }
   }

@@ -594,8 +594,10 @@ tp_status tp_linear_epilogue(int32_t tp_size, int32_t shard, const tp_tensor *x,
                              const tp_tensor *residual, tp_tensor *y, tp_stream_t stream);
 
 /* Workspace bytes tp_prefix_attn needs for these sizes: the splits' f32 partial
- * results and, with weights != 0, the own keys' scores. 0 for a null plan,
- * negative or unsupported sizes, and where none is needed. */
+ * results and, with weights != 0, the own keys' scores. It goes by the sizes, not by
+ * the lengths, and holds for every kernel that they may take (few keys and sequences
+ * go through one that uses none of it). 0 for a null plan, negative or unsupported
+ * sizes, an empty batch and where there are no keys. */
 size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t prefix, int64_t capacity,
                                      int32_t weights);
 
@@ -620,7 +622,8 @@ size_t tp_prefix_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t
  *  workspace  : at least tp_prefix_attn_workspace_size bytes, 16-byte aligned.
  * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16.
  * d must be 64 or 128, tp_size at most 32, a kv head's group at most 256 q heads,
- * else TP_ERR_UNSUPPORTED. Outputs overlap no input except weight_out = weight_in.
+ * C at most 4194240, P at most 2^31 - 257 and batch * q heads at most 8388607, else
+ * TP_ERR_UNSUPPORTED. Outputs overlap no input except weight_out = weight_in.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
  * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
 tp_status tp_prefix_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_prefix,

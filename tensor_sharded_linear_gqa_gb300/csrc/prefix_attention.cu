@@ -1259,8 +1259,9 @@ int direct_parts(long long units, long long group, long long prefix, long long c
 // Sizes that the launch shape's 32-bit arithmetic and the kernels take.
 bool sizes_ok(const tp_dims &d, long long batch, long long prefix, long long cap) {
   const long long group = d.num_q_heads / d.num_kv_heads;
-  return batch <= 0x7fffffffLL / 256 / d.num_q_heads && prefix <= 0x7fffffffLL - 256 && cap <= 0x7fffffffLL - 1024 &&
-         group <= kJoinThreads && (cap + kOwnKeys - 1) / kOwnKeys <= 65535;
+  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kMaxRanks32 && group <= kJoinThreads &&
+         batch <= 0x7fffffffLL / 256 / d.num_q_heads && prefix <= 0x7fffffffLL - 256 &&
+         (cap + kOwnKeys - 1) / kOwnKeys <= 65535;
 }
 
 }  // namespace

@@ -276,3 +276,14 @@ def test_right_sizes_reach_the_library(no_library):
                  lambda: attn(no_library, i(3), FakeTensor(1 << 30, "uint8")), lambda: evict(no_library, i(3), i(3), i(30))):
         with pytest.raises(AssertionError, match="was called"):
             call()
+
+
+def test_attn_workspace_size_of_unsupported_sizes():
+    size = tp.tp_prefix_attn_workspace_size
+    plans = {"d 96": tp.tp_plan_create(2, 512, 4, 2, 96, 64), "64 ranks": tp.tp_plan_create(64, 64, 64, 64, 64, 64),
+             "257 heads a group": tp.tp_plan_create(1, 64, 257, 1, 64, 64)}
+    for name, plan in plans.items():
+        assert size(plan, 2, 100, 10, False) == 0, name
+    assert size(PLAN, 1, 100, 4194240, False) > 0 and size(PLAN, 1, 100, 4194241, False) == 0
+    assert size(PLAN, 1, (1 << 31) - 257, 0, False) > 0 and size(PLAN, 1, (1 << 31) - 256, 0, False) == 0
+    assert size(PLAN, 8388607 // 4, 100, 0, False) > 0 and size(PLAN, 8388607 // 4 + 1, 100, 0, False) == 0

@@ -352,3 +352,50 @@ def test_keys_that_score_minus_infinity_have_no_weight(shape, first, own):
     hide_prefix = torch.arange(c.P, device="cuda") < first
     at = torch.arange(c.C, device="cuda")
     check_hidden(c, hide_prefix, ((at >= own[0]) & (at < own[1])).expand(c.B, -1))
+
+
+# Shapes by the path of the prefix kernel that they take, with the launches of a call: items of several
+# 128-key blocks, two row tiles or one in the last pair, and more items than CTAs (a CTA's second item
+# uses the Q tiles, the O columns and the barriers again).
+ROUTES = [  # tp, Hq, Hkv, d, B, P, C, launches
+    (1, 20, 1, 128, 100, 6000, 64, 3),     # 47 blocks in 16 splits, 2000 rows: 8 pairs, the last of 208 rows
+    (2, 24, 4, 64, 170, 4000, 20, 3),      # 32 blocks in 8 splits, 1020 rows
+    (1, 8, 2, 64, 180, 9000, 32, 3),       # 71 blocks in 24 splits, 720 rows: 208 in the last pair
+    (4, 4, 4, 128, 340, 5000, 0, 2),       # no own caches: 40 blocks in 14 splits, 340 rows: 84 in the last pair
+    (8, 128, 8, 64, 330, 400, 8, 3),       # 168 items of four blocks: some CTAs take two
+    (1, 128, 8, 128, 322, 500, 8, 3),      # the same, one row tile in a head's last pair
+    (1, 320, 8, 128, 37, 1500, 2000, 3),   # long own caches leave the prefix 38 CTAs
+    (1, 4, 1, 128, 1, 100, 30, 1),
+]
+
+
+@pytest.mark.parametrize("shape", ROUTES, ids=lambda s: "-".join(map(str, s)))
+def test_prefix_items_of_several_blocks_and_several_items(shape):
+    need_gpu()
+    *sizes, launches = shape
+    B, C = sizes[4], sizes[6]
+    c = Case(*sizes, [(i * 37 + 5) % (C + 1) for i in range(B)], seed=41)
+    # the maxima of neighbouring blocks rise by over 64 log2 units for the first sequence's first head
+    # and move up and down by less for the others
+    ramp = ((torch.arange(c.P, device="cuda") // 128) % 3)[:, None] * 6.0
+    for h in range(c.hkv):
+        cols = slice(h * c.d, (h + 1) * c.d)
+        q = c.q[0, h * (c.hq // c.hkv) * c.d:][:c.d].float()
+        c.kp[:, cols] += (ramp * torch.sign(q)).to(BF16)
+    before = tp.tp_launch_count()
+    a, w = c.run()
+    assert tp.tp_launch_count() - before == launches
+    c.check(a, w)
+    a2, w2 = c.run(alias=True)
+    assert torch.equal(a, a2) and torch.equal(w, w2)
+    assert tp.tp_device_status()[0] == tp.TP_OK
+
+
+@pytest.mark.parametrize("q_std", [4.0, 30.0])
+def test_sharp_scores_through_the_three_kernels(q_std):
+    need_gpu()
+    c = Case(2, 36, 2, 128, 90, 7000, 150, [(i * 29) % 151 for i in range(90)], seed=42, q_std=q_std)
+    before = tp.tp_launch_count()
+    a, w = c.run()
+    assert tp.tp_launch_count() - before == 3
+    c.check(a, w)

@@ -30,7 +30,11 @@
  *    on the same stream (put an event wait, a host synchronisation or other
  *    work in between), or set the environment variable TPGQA_EARLY_B=0 (read at
  *    every launch) to make weight loads wait as well. Block-table (MoE) GEMMs
- *    never read weights early.
+ *    never read weights early. tp_prefix_attn's kernel over the own caches runs
+ *    beside its kernel over the prefix, which has waited for everything before
+ *    the call; the former relies on that and reads q, the lengths and the caches
+ *    from L2 without a wait of its own. TPGQA_PDL=0 (read once) turns dependent
+ *    launches off: every kernel then starts after the one before it.
  *  - Pointers: tp_tensor.ptr is a device pointer. Arrays of tp_tensor
  *    (per-rank arguments) are host arrays, read during the call only.
  *  - Errors: every call returns a tp_status and never aborts. Arguments are

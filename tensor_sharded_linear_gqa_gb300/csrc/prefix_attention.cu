@@ -21,6 +21,10 @@
 // leaves some SMs free, and k_own_part, which shares nothing with it, does not wait
 // for it: it starts on those SMs, goes on where that kernel's CTAs leave, and waits
 // for it only in its last CTA, so that what follows it on the stream follows both.
+// Its inputs were written before k_prefix_part, whose every CTA has waited for what is
+// before it on the stream when the first CTA of k_own_part starts: they are in L2, and
+// what reads them without a wait of its own (k_own_part, and k_combine the lengths)
+// reads them there, past L1 (61 sequences: 33.1 us, 32.4 through L1).
 //
 // Few keys and sequences, where three launches cost more than the work, take one:
 // k_direct.
@@ -84,7 +88,7 @@ __device__ __forceinline__ long long part_row(const PrefixAttnParams &p, int kv,
   return (static_cast<long long>(kv) * p.batch + b) * p.group + g;
 }
 __device__ __forceinline__ int own_length(const PrefixAttnParams &p, int b) {
-  return min(max(__ldg(p.lengths + b), 0), p.cap);
+  return min(max(__ldcg(p.lengths + b), 0), p.cap);
 }
 
 // ---------------------------------------------------------------------------
@@ -554,10 +558,10 @@ struct WarpRows {
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const int at = kk * 8 + (lane & 3);
-      qa[kk][0] = q_lo ? __ldg(q_lo + at) : 0u;
-      qa[kk][1] = q_hi ? __ldg(q_hi + at) : 0u;
-      qa[kk][2] = q_lo ? __ldg(q_lo + at + 4) : 0u;
-      qa[kk][3] = q_hi ? __ldg(q_hi + at + 4) : 0u;
+      qa[kk][0] = q_lo ? __ldcg(q_lo + at) : 0u;
+      qa[kk][1] = q_hi ? __ldcg(q_hi + at) : 0u;
+      qa[kk][2] = q_lo ? __ldcg(q_lo + at + 4) : 0u;
+      qa[kk][3] = q_hi ? __ldcg(q_hi + at + 4) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) k_own_part(const __grid_consta
   if (!p.has_prev) grid_dep_wait();
   grid_dep_launch();
   const int len = own_length(p, b);
-  if (kv == 0 && split == 0 && g0 == 0 && tid == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  if (kv == 0 && split == 0 && g0 == 0 && tid == 0 && len != __ldcg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
   const int j0 = split * p.chunk, j1 = min(len, j0 + p.chunk);
   if (j0 < j1) {
     const int src = kv / p.heads_per_source;
@@ -879,7 +883,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) k_direct(const __grid_constant
   grid_dep_wait();
   grid_dep_launch();
   const int len = own_length(p, b);
-  if (kv == 0 && part == 0 && tid == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  if (kv == 0 && part == 0 && tid == 0 && len != __ldcg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
   const int tiles_p = (p.prefix + kOwnKeys - 1) / kOwnKeys, tiles = tiles_p + (len + kOwnKeys - 1) / kOwnKeys;
   const int t0 = tiles * part / parts, t1 = tiles * (part + 1) / parts;
   const int own0 = max(t0, tiles_p);  // the CTA's first own tile
@@ -1034,7 +1038,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) k_combine(const __grid_consta
   const int len = own_length(p, b);
   grid_dep_wait();
   grid_dep_launch();
-  if (p.split_o == 0 && kv == 0 && at == 0 && threadIdx.x == 0 && len != __ldg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
+  if (p.split_o == 0 && kv == 0 && at == 0 && threadIdx.x == 0 && len != __ldcg(p.lengths + b)) atomicCAS(p.status, 0, kDevBadLength);
   const int own = len > 0 ? (len + p.chunk - 1) / p.chunk : 0;
   const int n = p.split_p + own;
   const long long stride = static_cast<long long>(p.batch) * p.heads_q;

@@ -68,6 +68,8 @@ class Layer:
 
     def step(self, residual):
         """One token of every sequence: `residual` [batch x hidden] f32 is updated in place."""
+        if self.longest == self.capacity:  # the new rows would lie in the next sequence's cache
+            raise RuntimeError("the caches are full: evict first")
         n, s = self.ranks, self.sources
         tp.tp_add_rmsnorm(residual, None, self.norm1, EPS, None, self.x8, self.x8_scale)
         tp.tp_linear_epilogue(n, tp.TP_SHARD_COLUMN, [self.x8], self.shards(self.w_qkv, n, 0), self.qkv, bias=self.b_qkv,

@@ -287,3 +287,18 @@ def test_attn_workspace_size_of_unsupported_sizes():
     assert size(PLAN, 1, 100, 4194240, False) > 0 and size(PLAN, 1, 100, 4194241, False) == 0
     assert size(PLAN, 1, (1 << 31) - 257, 0, False) > 0 and size(PLAN, 1, (1 << 31) - 256, 0, False) == 0
     assert size(PLAN, 8388607 // 4, 100, 0, False) > 0 and size(PLAN, 8388607 // 4 + 1, 100, 0, False) == 0
+
+
+def test_the_example_refuses_a_step_on_full_caches():
+    pytest.importorskip("torch")
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_step.py")
+    spec = importlib.util.spec_from_file_location("decode_step_cpu", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    layer = m.Layer.__new__(m.Layer)  # no weights: the refusal comes first
+    layer.longest = layer.capacity = 12
+    with pytest.raises(RuntimeError, match="full"):
+        layer.step(None)

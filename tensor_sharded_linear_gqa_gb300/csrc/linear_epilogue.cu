@@ -22,14 +22,13 @@
 //
 // The tensor core truncates where it adds a step's products into the f32
 // accumulator: an error of one sign that grows with the steps. So no accumulator
-// runs for more than kChunkSteps steps (1024 bf16 or 2048 e4m3 values of K) where
-// TMEM has room: k_linear_pair's epilogue adds each chunk to the sum in registers,
-// k_linear_split gives each chunk its own columns and adds them at the end, both
-// rounding to nearest. Over K = 8192 in bf16 this takes the error of an f32
-// output, relative to its size, from 8e-6 to about 1e-6. k_linear_split's room is
-// 256 columns where two CTAs share an SM (up to 128 tokens: two accumulators at 65 to
-// 128) and 512 where one has it (two): where K, over the cluster, needs more, each runs
-// longer, 128 steps and 2.2e-6 for 200 x 8192 x 8192 in bf16.
+// runs for more than kChunkSteps steps (1024 bf16 or 2048 e4m3 values of K): both
+// kernels add a chunk's products to the sum outside the tensor core, rounding to
+// nearest. k_linear_pair's epilogue keeps the sum in registers. k_linear_split gives
+// each chunk its own columns of TMEM and adds them at the end; what does not fit (half
+// of the columns, where two CTAs share an SM) is added to the first chunk's columns
+// under the products. Over K = 8192 in bf16 this takes the error of an f32 output,
+// relative to its size, from 8e-6 to 1e-6, an f32 sum's.
 // Warp roles in both: warp 0 loads (TMA), warp 1 issues the MMAs, the others are
 // the epilogue. Every wait is bounded, as in the grouped GEMM.
 #include <cstdlib>
@@ -46,6 +45,7 @@ using namespace op;
 
 constexpr int kThreads = 256;       // k_linear_split
 constexpr int kChunkSteps = 64;     // MMA steps (32 bytes of K each) of one accumulator
+constexpr int kMaxRegions = 8;      // accumulators of k_linear_split: 256 columns of 32
 constexpr int kMaxParts = 16;  // weight shards (column) or K slices (row)
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kWTile = 128 * 128;  // bytes of one 128-row, 128-byte-wide box
@@ -55,7 +55,7 @@ constexpr int kWTile = 128 * 128;  // bytes of one 128-row, 128-byte-wide box
 struct LinearParams {
   int tok_tile, stages, split;       // k_linear_split: token tile, stages (one k-tile each), CTAs sharing K
   int box3;                          // k_linear_pair: one copy of a 3-D box brings a stage's k-tiles of an operand
-  int regions, region_cols;          // its accumulators in TMEM and their stride
+  int regions, region_cols, tmem_cols;  // its accumulators in TMEM, their stride, and what it allocates
   int early_w;                       // W loads before the dependency wait
   int n_slices, n_shards, kt_total, n_tiles, rows, m_tiles;
   int act, y_f32, res_f32, bias_f32, wide32;  // wide32: f32 rows of residual and y in 32-byte accesses
@@ -245,7 +245,8 @@ __device__ __forceinline__ float2 column_terms(const LinearParams &p, long long 
 // 7 us (8 TB/s), the rest is the start (2 us to the first stage), the partials'
 // exchange (2 us) and the output (2.5 us). One token, 4096 -> 4096 in bf16: 9.0 us.
 // ---------------------------------------------------------------------------
-template <bool F8>
+// ADD: a CTA's K has more chunks than accumulators (a kernel of its own: the code costs the others 0.15 us).
+template <bool F8, bool ADD>
 __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_constant__ LinearParams p) {
   constexpr int kElems = F8 ? 128 : 64;  // values of a 128-byte box row
   extern __shared__ uint8_t smem_raw[];
@@ -260,9 +261,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   auto full_bar = [&](int i) { return bar0 + 8u * i; };
   auto empty_bar = [&](int i) { return bar0 + 8u * (S + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * S);
-  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 8 * (2 * S + 1));
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 8 * (2 * S + 1) + 4);
-  float *s_scale = reinterpret_cast<float *>(bar_area + 8 * (2 * S + 2));  // [token]
+  auto chunk_bar = [&](int r) { return bar0 + 8u * (2 * S + 1 + r); };  // an accumulator is whole
+  auto added_bar = [&](int r) { return bar0 + 8u * (2 * S + 1 + kMaxRegions + r); };  // and added to the first
+  constexpr int kBars = 1 + 2 * kMaxRegions;  // beside the stages'
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 8 * (2 * S + kBars));
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 8 * (2 * S + kBars) + 4);
+  float *s_scale = reinterpret_cast<float *>(bar_area + 8 * (2 * S + kBars + 1));  // [token]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
@@ -272,9 +276,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   const int feat0 = (nt - p.shard[shard].tile0) * 128;  // within the shard
   const int kb0 = static_cast<int>(static_cast<long long>(p.kt_total) * part / p.split);
   const int kb1 = static_cast<int>(static_cast<long long>(p.kt_total) * (part + 1) / p.split);
-  const uint32_t tmem_cols = static_cast<uint32_t>(p.regions * p.region_cols);
+  const uint32_t tmem_cols = static_cast<uint32_t>(p.tmem_cols);
   const int nkb = kb1 - kb0;
-  const int per_region = (nkb + p.regions - 1) / p.regions;  // k-tiles of an accumulator
+  // Chunks of K. The first p.regions of them have an accumulator each. Accumulator 0 keeps the
+  // first; a later chunk takes the place of an earlier one in the others, which warps 4 to 7
+  // have added to accumulator 0 by then: chunks 1 to to_add.
+  constexpr int kChunkKt = kChunkSteps / 4;
+  const int to_add = ADD ? max((nkb + kChunkKt - 1) / kChunkKt - p.regions, 0) : 0;
+  const int chunk_kt = ADD ? kChunkKt : (nkb + p.regions - 1) / p.regions;
 
   // The loading thread's cursors over the k-tiles, (slice, k-tile in it), of W and of X.
   struct Cursor {
@@ -314,6 +323,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
         ptx::mbar_init(empty_bar(i), 1);
       }
       ptx::mbar_init(done_bar, 1);
+      if (ADD)
+        for (int r = 1; r < p.regions; ++r) {
+          ptx::mbar_init(chunk_bar(r), 1);
+          ptx::mbar_init(added_bar(r), 4);
+        }
       *abort_flag = 0;
       ptx::fence_barrier_init();
       ptx::fence_proxy_async_smem();
@@ -359,37 +373,90 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
       const long long tok = static_cast<long long>(mt) * NT + t;
       s_scale[t] = p.x_scale && tok < p.rows ? __ldg(p.x_scale + tok) : 1.f;
     }
+    if (ADD && warp >= 4) {  // a warp per quarter of the TMEM lanes
+      const uint32_t sum_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      int region = 1;
+      uint32_t parity = 0;
+      for (int i = 0; i < to_add; ++i) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(chunk_bar(region), parity, p.wait_ns))) {
+          record(p.status, kDevTimeoutEpilogue);
+          *abort_flag = 1;
+          break;
+        }
+        ptx::tc_fence_after();
+        for (int c = 0; c < NT; c += 32) {  // 32 columns' loads in flight; an odd 16 at the end twice
+          const int c2 = c + 16 < NT ? c + 16 : c;
+          uint32_t v[2][16], sum[2][16];
+          ptx::tmem_ld_16cols(sum_at + region * p.region_cols + c, v[0]);
+          ptx::tmem_ld_16cols(sum_at + c, sum[0]);
+          ptx::tmem_ld_16cols(sum_at + region * p.region_cols + c2, v[1]);
+          ptx::tmem_ld_16cols(sum_at + c2, sum[1]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ptx::tmem_regs_ready(v[h]);
+            ptx::tmem_regs_ready(sum[h]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[h][j] = __float_as_uint(__uint_as_float(sum[h][j]) + __uint_as_float(v[h][j]));
+            ptx::tmem_st_16cols(sum_at + (h ? c2 : c), sum[h]);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(added_bar(region));
+        if (++region == p.regions) {
+          region = 1;
+          parity ^= 1;
+        }
+      }
+    }
   }
   if (warp == 1) {  // the whole warp walks the stages, one lane issues
     const uint32_t idesc = F8 ? ptx::idesc_e4m3_f32(128, NT) : ptx::idesc_bf16_f32(128, NT);
     const bool leader = ptx::elect_one();
-    int st = 0, in_region = 0;
-    uint32_t parity = 0, d = tmem;
-    for (int i = 0; i < nkb; ++i) {
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait(full_bar(st), parity, p.wait_ns))) {
+    int st = 0, region = 0;
+    uint32_t parity = 0, reuse = 1, d = tmem;  // reuse: parity of the additions that the present accumulator waits for
+    bool go = true;
+    for (int i = 0, chunk = 0; go && i < nkb; ++chunk) {
+      if (ADD && chunk >= p.regions && !__all_sync(0xffffffffu, ptx::mbar_wait(added_bar(region), reuse, p.wait_ns))) {
         record(p.status, kDevTimeoutMma);
         *abort_flag = 1;
         break;
       }
-      ptx::tc_fence_after();
-      const uint64_t wd = ptx::smem_desc_sw128(w_slot(st)), xd = ptx::smem_desc_sw128(w_slot(st) + kWTile);
-      const uint32_t more = in_region != 0 ? 1u : 0u;
-      if (leader) {
+      const int end = min(nkb, i + chunk_kt);
+      for (uint32_t more = 0; i < end; ++i, more = 1) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(full_bar(st), parity, p.wait_ns))) {
+          record(p.status, kDevTimeoutMma);
+          *abort_flag = 1;
+          go = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint64_t wd = ptx::smem_desc_sw128(w_slot(st)), xd = ptx::smem_desc_sw128(w_slot(st) + kWTile);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (F8) ptx::mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
-          else ptx::mma_bf16(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+          for (int k = 0; k < 4; ++k) {
+            if (F8) ptx::mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+            else ptx::mma_bf16(d, wd + 2 * k, xd + 2 * k, idesc, k != 0 ? 1u : more);
+          }
+        }
+        if (leader) ptx::mma_commit(empty_bar(st));
+        __syncwarp();
+        if (++st == S) {
+          st = 0;
+          parity ^= 1;
         }
       }
-      if (leader) ptx::mma_commit(empty_bar(st));
-      __syncwarp();
-      if (++st == S) {
-        st = 0;
-        parity ^= 1;
-      }
-      if (++in_region == per_region) {  // the next accumulator
-        in_region = 0;
-        d += static_cast<uint32_t>(p.region_cols);
+      d += static_cast<uint32_t>(p.region_cols);  // the next accumulator
+      if (ADD) {
+        if (leader && chunk > 0 && chunk <= to_add) ptx::mma_commit(chunk_bar(region));
+        __syncwarp();
+        if (++region == p.regions) {
+          region = 1;
+          reuse ^= 1;
+          d = tmem + static_cast<uint32_t>(p.region_cols);
+        }
       }
     }
     if (leader) ptx::mma_commit(done_bar);
@@ -411,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
   float *red = reinterpret_cast<float *>(smem);  // [token][128 features] f32
   if (ready) {  // two warps per quarter of the TMEM lanes, every other 16 tokens each
     const int q = warp & 3;
-    const int used = (nkb + per_region - 1) / per_region;
+    const int used = min((nkb + chunk_kt - 1) / chunk_kt, p.regions);
     for (int c = 16 * (warp >> 2); c < NT; c += 32) {
       float f[16];
       for (int r = 0; r < used; r += 2) {  // two accumulators' loads in flight
@@ -800,13 +867,13 @@ cudaError_t allow_smem(K kernel, unsigned &mask, std::mutex &mu) {
   return e;
 }
 
-template <bool F8>
+template <bool F8, bool ADD>
 tp_status launch_split(const LinearParams &p, size_t smem, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_linear_split<F8>, mask, mu);
+  const cudaError_t e = allow_smem(k_linear_split<F8, ADD>, mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
-  return launched(launch_kernel(k_linear_split<F8>, dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split)),
+  return launched(launch_kernel(k_linear_split<F8, ADD>, dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split)),
                                 dim3(kThreads), smem, s, static_cast<unsigned>(p.split), p));
 }
 template <bool F8, int BN, bool Y32>
@@ -975,6 +1042,7 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
   const long long m256 = (T + 255) / 256;
   lay_out(256);
   const bool pair = T > 128 && m256 * p.n_tiles >= num_sms() / 4;
+  bool add = false;
   int x_box = 128, w_box = 128, bn = 224;
   if (pair) {
     // The tile width whose last wave wastes least: the busiest pair's columns,
@@ -1012,13 +1080,22 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     for (int c = 2; c <= 8; ++c)
       if (tiles * c <= num_sms() * per_sm && tiles <= max_active_clusters(c) * per_sm && p.kt_total >= 2 * c) p.split = c;
     if (tiles * p.split > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
-    // accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation, in
-    // the columns that a CTA has: half of the SM's where two share it
+    // Accumulators of kChunkSteps steps each, a power of two of them for TMEM's allocation, in
+    // the columns that a CTA has (half of the SM's where two share it); where they do not
+    // suffice, as many as those columns hold, and chunks are added under the products.
+    const int most = two ? 256 : 512;
     p.region_cols = 32;
     while (p.region_cols < p.tok_tile) p.region_cols *= 2;
     const int steps = (p.kt_total + p.split - 1) / p.split * 4;
     p.regions = 1;
-    while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= (two ? 256 : 512)) p.regions *= 2;
+    while (p.regions * kChunkSteps < steps && 2 * p.regions * p.region_cols <= most) p.regions *= 2;
+    p.tmem_cols = p.regions * p.region_cols;
+    add = p.regions * kChunkSteps < steps;
+    if (add) {
+      p.region_cols = (p.tok_tile + 31) / 32 * 32;
+      p.regions = most / p.region_cols < kMaxRegions ? most / p.region_cols : kMaxRegions;
+      p.tmem_cols = most;
+    }
   }
   // A copy costs its issue whatever its size, so where every slice is whole k-tiles one
   // box spans a stage's k-tiles (2048 x 4096 x 8192 in e4m3: 56.1 us, 57.8 with one copy
@@ -1035,6 +1112,7 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
   if (pair) return dt == TP_E4M3 ? launch_pair_y<true>(p, bn, s) : launch_pair_y<false>(p, bn, s);
   size_t smem = 1024 + static_cast<size_t>(p.stages) * (kWTile + p.tok_tile * 128);
   const size_t out = 1024 + static_cast<size_t>(p.tok_tile) * 512;  // the partials lie over the stages
-  smem = (smem > out ? smem : out) + 8 * (2 * p.stages + 2) + p.tok_tile * 4 + 64;
-  return dt == TP_E4M3 ? launch_split<true>(p, smem, s) : launch_split<false>(p, smem, s);
+  smem = (smem > out ? smem : out) + 8 * (2 * p.stages + 2 + 2 * kMaxRegions) + p.tok_tile * 4 + 64;
+  if (add) return dt == TP_E4M3 ? launch_split<true, true>(p, smem, s) : launch_split<false, true>(p, smem, s);
+  return dt == TP_E4M3 ? launch_split<true, false>(p, smem, s) : launch_split<false, false>(p, smem, s);
 }

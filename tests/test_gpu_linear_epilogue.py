@@ -233,3 +233,24 @@ def test_silu_far_in_its_tail(T):
     y, f = one_value_a_row(v, tp.TP_ACT_SILU), v.double()
     want = f / (1 + torch.exp(-f))
     assert ((y - want[:, None]).abs() <= (1.01 * 6 * U * want.abs())[:, None]).all()
+
+
+# Few tokens and a K of more chunks of 64 steps than fit in tensor memory: they are added under the
+# products, through every accumulator several times over. The limit is that of 64 steps above.
+@pytest.mark.parametrize("T, K, N, dtype", [
+    (128, 8192, 28672, BF16), (100, 28672, 8192, BF16), (200, 8192, 8192, BF16), (300, 20000, 4096, BF16),
+    (17, 16384, 20480, BF16), (61, 20000, 14336, BF16), (1, 28672, 4096, BF16), (128, 16384, 28672, E4M3), (256, 28672, 8192, E4M3),
+])
+def test_f32_sums_that_outgrow_tensor_memory(T, K, N, dtype):
+    need_gpu()
+    p = Problem(T, K, N, dtype, K + T)
+    y, again = padded(T, N, F32), padded(T, N, F32)
+    for out in (y, again):
+        tp.tp_linear_epilogue(1, tp.TP_SHARD_COLUMN, p.xr, p.wr, out, x_scale=p.xs, w_scale=p.ws)
+    assert torch.equal(y, again)
+    want = torch.cat([p.x.double() @ w.double().t() for w in p.w.split(4096)], 1)
+    if dtype == E4M3:
+        want = want * p.xs.double()[:, None] * p.ws.double()
+    err = float((y.double() - want).norm() / want.norm())
+    assert err <= 1.5 * 1.6e-8 * 64 + U
+    assert tp.tp_device_status()[0] == tp.TP_OK

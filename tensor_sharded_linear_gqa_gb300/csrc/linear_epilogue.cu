@@ -112,28 +112,21 @@ __device__ __forceinline__ void gelu2(float &x0, float &x1) {
   x0 *= x0 < 0.0f ? h0 : 1.0f - h0;
   x1 *= x1 < 0.0f ? h1 : 1.0f - h1;
 }
-// x / (1 + e^-x) of two values for an f32 output, within 6 2^-24 of it: e^-x is 2^t, and the rounding of
+// x / (1 + e^-x) for an f32 output, within 6 2^-24 of it: e^-x is 2^t, and the rounding of
 // t = -x log2(e), up to 2^-18 of e^-x, is brought in again behind it; the quotient is corrected
 // by its remainder. From 20 on it is x; t stops at 126, so below -88 it is 2^-126 x.
-__device__ __forceinline__ void silu2(float &x0, float &x1) {
-  const float c = 1.442695041f, c_low = 1.925963033e-8f, ln2 = 0.6931471806f;  // log2(e): c and what f32 leaves of it
-  const uint64_t x = pack2(x0, x1), minus_x = pack2(-x0, -x1), t = mul2(minus_x, pack2(c, c));
-  float t0, t1, d0, d1, y0, y1;
-  unpack2(t, t0, t1);
-  const uint64_t e = pack2(ex2(fminf(t0, 126.0f)), ex2(fminf(t1, 126.0f)));
-  const uint64_t minus_low = fma2(x, pack2(c_low, c_low), fma2(x, pack2(c, c), t));
-  const uint64_t d = add2(fma2(e, mul2(minus_low, pack2(-ln2, -ln2)), e), pack2(1.0f, 1.0f));
-  unpack2(d, d0, d1);
-  const uint64_t r = pack2(rcp(d0), rcp(d1));
-  unpack2(fma2(fma2(mul2(minus_x, r), d, x), r, mul2(x, r)), y0, y1);
-  x0 = x0 > 20.0f ? x0 : y0;
-  x1 = x1 > 20.0f ? x1 : y1;
+__device__ __forceinline__ float silu_f32(float x) {
+  const float c = 1.442695041f, c_low = 1.925963033e-8f;  // log2(e), and what f32 leaves of it
+  const float t = x * -c, e0 = ex2(fminf(t, 126.0f));
+  const float low = fmaf(x, -c_low, fmaf(x, -c, -t)) * 0.6931471806f;
+  const float d = 1.0f + fmaf(e0, low, e0), r = rcp(d), q = x * r;
+  return x > 20.0f ? x : fmaf(fmaf(-q, d, x), r, q);
 }
 
 // The activations by their formulas, in f32: relu, x Phi(x), x / (1 + e^-x). For a bf16 output
 // the last by the hardware's exponential and reciprocal alone, off by up to 2^-23 |x| of its
 // value (at x < -88 it is -0, its limit): far below bf16's half step of 2^-9, and the exact
-// form costs 4096 x 8192 x 28672 in e4m3 5%.
+// form costs 4096 x 8192 x 28672 in e4m3 7%.
 template <int N>
 __device__ __forceinline__ void activate(float (&f)[N], int act, bool f32) {
   if (act == TP_ACT_RELU) {
@@ -144,7 +137,7 @@ __device__ __forceinline__ void activate(float (&f)[N], int act, bool f32) {
     for (int i = 0; i < N; i += 2) gelu2(f[i], f[i + 1]);
   } else if (act == TP_ACT_SILU && f32) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) silu2(f[i], f[i + 1]);
+    for (int i = 0; i < N; ++i) f[i] = silu_f32(f[i]);
   } else if (act == TP_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] *= rcp(1.0f + ex2(f[i] * -1.442695041f));

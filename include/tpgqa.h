@@ -553,6 +553,7 @@ tp_status tp_attn_proj(const tp_plan *plan, const tp_tensor *x, const tp_tensor 
  *                 (same base and pitch), and overlaps nothing else. Needs a residual.
  *  y            : [T x D] bf16 or e4m3; overlaps no input.
  *  y_scale      : f32 [T] device array with an e4m3 y, else NULL.
+ * A row whose sum of squares is above f32's range (|z| near 10^19) gives zeros.
  * A row with a NaN gives a row of NaN; with an e4m3 y so does a row with an infinity,
  * and the scale of either is NaN. Bases are aligned to their element; bases
  * and pitches on 16 bytes take the vector path.

@@ -11,7 +11,7 @@
 //   k_linear_split  few tokens. Bound by streaming W, so the 128 rows of the MMA's
 //                   M are output features and the tokens are its N (16..256): no
 //                   accumulator row is padding, and a stage is 16 KB of W and 128
-//                   bytes a token of X, about 200 KB in flight per SM. Too few
+//                   bytes a token of X, 170 to 220 KB in flight per SM. Too few
 //                   feature tiles to fill the SMs split K over a cluster; the f32
 //                   partials are summed through distributed shared memory in rank
 //                   order, so results repeat.
@@ -234,9 +234,9 @@ __device__ __forceinline__ float2 column_terms(const LinearParams &p, long long 
 
 // ---------------------------------------------------------------------------
 // Few tokens: features on the MMA's M, tokens on its N, K split over a cluster.
-// 61 tokens, 4096 -> 14336 in e4m3 with GELU: 15.6 us for 61 MB; its weights stream in
+// 61 tokens, 4096 -> 14336 in e4m3 with GELU: 15.3 us for 61 MB; its weights stream in
 // 7 us (8 TB/s), the rest is the start (2 us to the first stage), the partials'
-// exchange (2 us) and the output (2.5 us). One token, 4096 -> 4096 in bf16: 9.0 us.
+// exchange (2 us) and the output (2 us). One token, 4096 -> 4096 in bf16: 9.0 us.
 // ---------------------------------------------------------------------------
 // ADD: a CTA's K has more chunks than accumulators (a kernel of its own: the code costs the others 0.15 us).
 template <bool F8, bool ADD>
@@ -574,9 +574,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_linear_split(const __grid_const
 // epilogue warps: two per quarter of the TMEM lanes, each with half of the columns.
 // BN is at most 224: the 128 sums a lane of BN = 256 spill (4096 x 8192 x 28672 in e4m3:
 // 638 us against 578). That product runs at 2.9-3.3 PFLOP/s, by the clock the power
-// cap leaves; the tensor pipe is active 59% of the cycles on 2048 x 8192 x 8192, where
+// cap leaves; the tensor pipe is active 66% of the cycles on 2048 x 8192 x 8192, where
 // a CTA takes in 69 bytes a clock, near what its copies bring. 2047 x 8192 x 8192 in
-// bf16 with f32 residual and output: 200 us, 165 without them.
+// bf16: 168 us with an f32 output, 199 with an f32 residual too.
 // ---------------------------------------------------------------------------
 constexpr int kSub = 2;           // k-tiles per stage
 constexpr int kPairThreads = 320;
@@ -1061,8 +1061,8 @@ extern "C" tp_status tp_linear_epilogue(int32_t n, int32_t shard, const tp_tenso
     p.tok_tile = static_cast<int>((per + 15) / 16 * 16);
     x_box = p.tok_tile;
     // Half of an SM's shared memory, so that two CTAs share it (the next kernel's first
-    // weights load beside this one's end), while that leaves four stages and more;
-    // beyond 128 tokens all of it. At 61 tokens, 4096 -> 14336 in e4m3: 15.9 us with two
+    // weights load beside this one's end): six stages for 16 tokens, four for 64, three
+    // from 81 to 128; beyond 128 tokens all of it. At 61 tokens, 4096 -> 14336 in e4m3: 15.9 us with two
     // CTAs an SM of 110 KB, 16.5 with one of 222 KB, 18.7 with three of 72 KB.
     const int stage = kWTile + p.tok_tile * 128;
     const bool two = p.tok_tile <= 128;

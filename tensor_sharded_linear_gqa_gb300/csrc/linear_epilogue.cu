@@ -91,7 +91,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // x Phi(x) of two values, from h = Phi(-|x|) = t P(t) e^(-x^2/2) with t = 1 / (1 + 0.27 |x|):
-// x h below 0, where x/2 (1 + erf) would cancel (at -4 it keeps fewer bits than bf16), x (1 - h)
+// x h below 0, where x/2 (1 + erf) would cancel (below -4.5 it keeps fewer bits than bf16), x (1 - h)
 // above. P is the polynomial of degree 8 nearest to erfc(|x| / sqrt 2) e^(x^2/2) / (2 t)
 // relative to it (2.4e-8), by a weighted least-squares fit over |x| <= 14.
 __device__ __forceinline__ void gelu2(float &x0, float &x1) {

@@ -83,8 +83,8 @@ typedef enum tp_status {
 
 /* TP_E4M3 (8-bit floats: 4 exponent bits, 3 mantissa bits, no infinities) is
  * taken by the calls that name it: tp_add_rmsnorm's output and the operands of
- * tp_linear_epilogue. */
-typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1, TP_E4M3 = 2 } tp_dtype;
+ * tp_linear_epilogue. TP_U8 (bytes) holds the codes of the 4-bit caches. */
+typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1, TP_E4M3 = 2, TP_U8 = 3 } tp_dtype;
 
 /* A 2-D row-major view: element (i, j) lives at ptr + (i * ld + j) * size(dtype).
  * ld >= cols. rows or cols may be 0 (empty); each is below 2^31 (their product,
@@ -666,6 +666,139 @@ tp_status tp_cache_evict(const tp_plan *plan, int64_t batch, const int32_t *leng
                          const tp_tensor *v, const tp_tensor *weight, int32_t budget, int32_t n_first,
                          int32_t n_recent, tp_tensor *k_out, tp_tensor *v_out, tp_tensor *weight_out,
                          int32_t *lengths_out, int32_t *kept, tp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Long contexts: rotary positions between the q/k/v projection and the attention
+ * calls (which apply none themselves), attention over a sliding window and the first
+ * tokens, and caches held in 4 bits.
+ * ------------------------------------------------------------------------- */
+typedef enum tp_rotary_layout {
+  TP_ROTARY_HALVES = 0,    /* pair i of a head is its values i and i + pairs */
+  TP_ROTARY_NEIGHBOURS = 1 /* pair i is its values 2i and 2i + 1             */
+} tp_rotary_layout;
+
+/* Rotary positions with one or several axes (time, height, width). For token t and
+ * pair i of every head of q and k, with the pair's values (a, b):
+ *   angle = positions[axis[i]][t] * freq[i],
+ *   a' = a cos(angle) - b sin(angle),  b' = a sin(angle) + b cos(angle),
+ * computed in f32 from an angle that is reduced without loss, rounded once. The
+ * values of a head past 2 * pairs are copied.
+ *  positions : device int32 [n_axes x tokens], row-major; any value.
+ *  freq      : device f32 [pairs], finite, radians a position (scaled frequencies of
+ *              any kind are given here).
+ *  axis      : host int32 [pairs] with values in [0, n_axes), or NULL (all 0).
+ *  inverse   : 1 turns by the negated angle: the call's own inverse, and the gradient
+ *              of its inputs from that of its outputs. Else 0.
+ *  q[r]      : [tokens x Hq_r*d] per rank; k[r]: [tokens x heads*d] per kv source (one
+ *              per rank, or one when the plan replicates K/V); all f32 or all bf16.
+ *              Either may be NULL together with its output.
+ *  q_out, k_out : as q and k; each may be its input itself (same base and pitch), else
+ *              they overlap no input.
+ * 1 <= pairs <= d / 2. More than 256 pairs, 8 axes or 32 ranks are TP_ERR_UNSUPPORTED.
+ * Bases are aligned to their element; bases, pitches and heads on 16 bytes with a
+ * whole number of 16-byte pieces of pairs take the vector path.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_UNSUPPORTED,
+ * TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_rotary(const tp_plan *plan, int64_t tokens, const int32_t *positions, int32_t n_axes, const float *freq,
+                    int32_t pairs, const int32_t *axis, int32_t layout, int32_t inverse, const tp_tensor *q,
+                    const tp_tensor *k, tp_tensor *q_out, tp_tensor *k_out, tp_stream_t stream);
+
+/* Workspace bytes tp_window_attn needs for these sizes on the current device: the key
+ * splits' f32 partial results where there are too few tokens to fill it, else 0. 0 too
+ * for a null plan and for sizes that the call refuses. */
+size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tokens, int64_t keys, int32_t window, int32_t sinks);
+
+/* Causal attention over a sliding window and the first tokens: the T queries are those
+ * of the last T of S positions; the query at position i = S - T + t sees key j when
+ *   j <= i and (j > i - window or j < sinks),
+ *   a[t, h] = softmax(q[t, h] K_g^T / sqrt(d)) V_g over the keys that it sees,
+ * with g its kv head. A prompt has T = S, a later chunk of it (or a single new token)
+ * T < S behind the keys of what came before. No position encoding is applied.
+ *  q[r], a[r] : [T x Hq_r*d] bf16, rank r's q heads and output columns.
+ *  k, v       : per kv source (one per rank, or one when the plan replicates K/V)
+ *               bf16 [S x heads*d], S >= T.
+ *  window     : >= 1 (1: the token itself); 2^31 - 1 hides nothing.
+ *  sinks      : >= 0, first tokens that stay visible.
+ *  workspace  : at least tp_window_attn_workspace_size bytes, 16-byte aligned; may be
+ *               NULL where that is 0.
+ * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16. Keys
+ * that no query sees are not read, but for those that share a block of 128 with one that
+ * is seen: an infinity or NaN among the latter's values reaches the block's queries.
+ * d must be 64 or 128, tp_size at most 32, S at most 2^31 - 257, T * q heads at
+ * most 2^28, else TP_ERR_UNSUPPORTED. Outputs overlap no input.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
+ * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, const tp_tensor *k, const tp_tensor *v, int32_t window,
+                         int32_t sinks, tp_tensor *a, void *workspace, size_t workspace_bytes, tp_stream_t stream);
+
+/* Caches held in 4 bits. A head's values lie in groups of 32 that share a bf16 scale:
+ *   scale = bf16(max|x| / 7),  code = clamp(round(x / scale), -8, 7) + 8,
+ *   value = (code - 8) * scale
+ * (round half to even; codes 8 where the scale is 0; a group with an infinity or a NaN
+ * has the scale NaN). A cache of `batch` sequences with C positions is four tensors per
+ * kv source (one per rank, or one when the plan replicates K/V), all contiguous, the
+ * codes on 16-byte boundaries, the scales on those of a row (d/16 bytes); row (b * heads + h) * C + j is position j of sequence b's head h,
+ * so a sequence's rows are neighbours and a part of the batch is a part of the rows:
+ *  k_codes, v_codes : TP_U8 [batch*heads*C x d/2], two codes a byte, the first value's in
+ *                     the low half. A group's values are cut into pieces, of 8 values
+ *                     for keys and of 4 for values; a row has the first pieces of all
+ *                     groups, then the second ones, and so on.
+ *  k_scale, v_scale : bf16 [batch*heads*C x d/32].
+ * d is 64 or 128 and tp_size at most 32, else TP_ERR_UNSUPPORTED. */
+
+/* Stores n new tokens of every sequence behind what its cache has.
+ *  lengths : device int32 [batch], the positions held so far: token i of sequence b
+ *            goes to position lengths[b] + i. The call does not change them.
+ *  counts  : device int32 [batch], how many of the n tokens sequence b has (the others
+ *            are padding and not stored), or NULL: all n.
+ *  k, v    : per kv source bf16 [batch*n x heads*d], row b*n + i.
+ * A length outside [0, C], a count outside [0, n] and tokens past position C - 1 are
+ * reported by tp_device_status (TP_ERR_BAD_LENGTH): a sequence with a bad length stores
+ * nothing, one with a bad count as many of its n tokens as the nearer bound allows, and
+ * tokens past the end are dropped.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_UNSUPPORTED,
+ * TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *lengths, const int32_t *counts,
+                          const tp_tensor *k, const tp_tensor *v, tp_tensor *k_codes, tp_tensor *k_scale,
+                          tp_tensor *v_codes, tp_tensor *v_scale, tp_stream_t stream);
+
+/* Reads positions first[b] .. first[b] + n - 1 of every sequence back as the values that
+ * the codes stand for (what tp_window_attn attends over when a prompt goes on behind a
+ * stored part).
+ *  first        : device int32 [batch]. One outside [0, C] is reported by
+ *                 tp_device_status (TP_ERR_BAD_LENGTH).
+ *  k_out, v_out : per kv source [batch*n x heads*d], all f32 (exact) or all bf16 (rounded
+ *                 once). Positions outside the cache give zeros.
+ * Errors: as tp_cache4_store. */
+tp_status tp_cache4_load(const tp_plan *plan, int64_t batch, const int32_t *first, const tp_tensor *k_codes,
+                         const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale, tp_tensor *k_out,
+                         tp_tensor *v_out, tp_stream_t stream);
+
+/* Workspace bytes tp_cache4_attn needs for these sizes on the current device (the key
+ * splits' f32 partial results; 0 where one CTA takes a whole sequence). It goes by the
+ * capacity, not by the lengths. 0 too for a null plan and for sizes that the call refuses. */
+size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t capacity, int32_t window, int32_t sinks);
+
+/* Attention of one new token per sequence over its 4-bit cache: with len = lengths[b],
+ * the token (position len - 1, whose own key is stored already) sees key j < len when
+ *   j >= len - window or j < sinks,
+ *   a[b, h] = softmax(q[b, h] K_g^T / sqrt(d)) V_g over these, K and V the codes' values.
+ * No position encoding is applied. A sequence without any key gives zeros.
+ *  q[r], a[r] : [batch x Hq_r*d] bf16, rank r's q heads and output columns.
+ *  lengths    : device int32 [batch]. One outside [0, C] is taken as the nearer bound
+ *               and reported by tp_device_status (TP_ERR_BAD_LENGTH).
+ *  window, sinks : as tp_window_attn. Keys that the token does not see are not read.
+ *  workspace  : at least tp_cache4_attn_workspace_size bytes, 16-byte aligned; may be
+ *               NULL where that is 0.
+ * Scores are products of q's values (at f16's 11 bits or more of the head's largest) with
+ * whole codes, in f32; the statistics and sums are f32; p * scale is rounded to bf16 for
+ * P V, A to bf16. |q| up to 2^100. Outputs overlap no input.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
+ * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
+tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_codes,
+                         const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale,
+                         const int32_t *lengths, int32_t window, int32_t sinks, tp_tensor *a, void *workspace,
+                         size_t workspace_bytes, tp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status, health and diagnostics.

@@ -7,8 +7,8 @@ the library's CUDA kernels. There is no CPU fallback: the first call loads
 ``python -m tensor_sharded_linear_gqa_gb300.build``).
 
 Tensors are passed either as ``TpTensor`` or as 2-D CUDA ``torch.Tensor`` views
-with unit column stride (float32 or bfloat16; float8_e4m3fn where a call takes
-it). Per-rank arguments are Python
+with unit column stride (float32 or bfloat16; float8_e4m3fn or uint8 where a call
+takes it). Per-rank arguments are Python
 sequences. ``stream`` is a ``torch.cuda.Stream``, a raw ``cudaStream_t`` int, or
 None for the current torch stream.
 """
@@ -32,7 +32,7 @@ STATUS_NAMES = ["TP_OK", "TP_ERR_INVALID_ARG", "TP_ERR_TP_SIZE_NOT_POW2", "TP_ER
                 "TP_ERR_BAD_TOKEN", "TP_ERR_BAD_LENGTH"]
 for _i, _n in enumerate(STATUS_NAMES):
     globals()[_n] = _i
-TP_F32, TP_BF16, TP_E4M3 = 0, 1, 2
+TP_F32, TP_BF16, TP_E4M3, TP_U8 = 0, 1, 2, 3
 TP_SHARD_COLUMN, TP_SHARD_ROW, TP_SHARD_VOCAB, TP_SHARD_REPLICATED = 0, 1, 2, 3
 TP_COMM_NONE, TP_COMM_ALL_REDUCE, TP_COMM_ALL_GATHER, TP_COMM_REDUCE_SCATTER = 0, 1, 2, 3
 TP_W_Q, TP_W_K, TP_W_V, TP_W_O, TP_W_GATE, TP_W_UP, TP_W_DOWN, TP_W_COUNT = range(8)
@@ -42,6 +42,7 @@ TP_RING_STEPS, TP_RING_FUSED, TP_RING_FUSED_SHARED = 0, 1, 2
 TP_ACT_NONE, TP_ACT_RELU, TP_ACT_GELU, TP_ACT_SILU = 0, 1, 2, 3
 ACTIVATIONS = {"none": TP_ACT_NONE, "relu": TP_ACT_RELU, "gelu": TP_ACT_GELU, "silu": TP_ACT_SILU}
 TP_MOE_EXPERT_PARALLEL, TP_MOE_WITHIN_EXPERT = 0, 1
+TP_ROTARY_HALVES, TP_ROTARY_NEIGHBOURS = 0, 1
 
 
 class TpTensor(ctypes.Structure):
@@ -125,6 +126,15 @@ _SIGS = {
     "tp_prefix_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _A, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
     "tp_cache_evict": ([_A, ctypes.c_int64, _A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _A, _A, _A, _A,
                         _A, _S], ctypes.c_int),
+    "tp_rotary": ([_A, ctypes.c_int64, _A, ctypes.c_int32, _A, ctypes.c_int32, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, _A,
+                   _A, _S], ctypes.c_int),
+    "tp_window_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+    "tp_window_attn": ([_A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
+    "tp_cache4_store": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _A, _S], ctypes.c_int),
+    "tp_cache4_load": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _S], ctypes.c_int),
+    "tp_cache4_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+    "tp_cache4_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, ctypes.c_size_t,
+                        _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "tp_last_cuda_error": ([], ctypes.c_int32),
     "tp_set_rank_health": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_int),
@@ -205,7 +215,7 @@ def __getattr__(name):
 def _dtypes() -> dict:
     if not _DTYPES:
         import torch
-        _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3})
+        _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8})
         if _load_describe() is not None:
             _describe.dtypes(*_DTYPES)
     return _DTYPES
@@ -651,6 +661,106 @@ def tp_cache_evict(plan: Plan, lengths, k, v, weight, budget: int, n_first: int,
                              _dev_ptr(kept, "torch.int32", batch * plan.dims.num_kv_heads * budget, "kept"), _stream(stream))
     if st:
         raise TPError(st, "tp_cache_evict")
+
+
+# ---- long contexts ----------------------------------------------------------------
+def rotary_axes(sections) -> ctypes.Array:
+    """The `axis` argument of tp_rotary for axes that take their pairs one after the other:
+    sections[x] pairs of axis x."""
+    axis = [x for x, n in enumerate(sections) for _ in range(n)]
+    return (ctypes.c_int32 * len(axis))(*axis)
+
+
+def _workspace(t) -> tuple:
+    """(address, bytes) of a workspace tensor; None is an empty one."""
+    if t is None:
+        return None, 0
+    size = t.numel() * t.element_size()
+    if not t.is_contiguous() or not (t.is_cuda or size == 0):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), size
+
+
+def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout: int = TP_ROTARY_HALVES,
+              inverse: bool = False, stream=None) -> None:
+    """Rotates pairs of values of q's and k's heads by positions[axis] * freq. positions: int32 [T] or
+    [axes x T]; freq: f32 [pairs]; axis: per pair (rotary_axes), None: all 0. q, q_out: one entry
+    per rank, k, k_out: one per kv source; q or k may be None with its output."""
+    n, src, pairs = plan.dims.tp_size, _kv_sources(plan), freq.numel()
+    if positions.dim() not in (1, 2):
+        raise ValueError("positions must be [T] or [axes x T]")
+    axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
+    if axis is not None:
+        if not isinstance(axis, ctypes.Array):
+            axis = (ctypes.c_int32 * len(axis))(*axis)
+        if axis._type_ is not ctypes.c_int32 or len(axis) != pairs:
+            raise ValueError(f"axis must have {pairs} entries, one per pair")
+    g = _args(2 * n + 2 * src)
+    st = _lib.tp_rotary(plan.handle, tokens, _dev_ptr(positions, "torch.int32"), axes, _dev_ptr(freq, "torch.float32"), pairs,
+                        axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
+                        None if q_out is None else g.many(q_out, n), None if k_out is None else g.many(k_out, src),
+                        _stream(stream))
+    if st:
+        raise TPError(st, "tp_rotary")
+
+
+def tp_window_attn_workspace_size(plan: Plan, tokens: int, keys: int, window: int, sinks: int) -> int:
+    return int(_lib.tp_window_attn_workspace_size(plan.handle, tokens, keys, window, sinks))
+
+
+def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=None, stream=None) -> None:
+    """The last T of S tokens over a sliding window and the first `sinks` tokens. q, a: one entry per
+    rank; k, v: one per kv source; workspace: a CUDA byte tensor."""
+    n, src = plan.dims.tp_size, _kv_sources(plan)
+    ws, size = _workspace(workspace)
+    g = _args(2 * n + 2 * src)
+    st = _lib.tp_window_attn(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
+                             _stream(stream))
+    if st:
+        raise TPError(st, "tp_window_attn")
+
+
+def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scale, counts=None, stream=None) -> None:
+    """Stores the rows of k and v (batch * n tokens) behind the lengths[b] positions that the 4-bit
+    caches hold. All but lengths and counts: one entry per kv source."""
+    batch, src = lengths.numel(), _kv_sources(plan)
+    g = _args(6 * src)
+    st = _lib.tp_cache4_store(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
+                              None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
+                              g.many(v, src), g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src),
+                              g.many(v_scale, src), _stream(stream))
+    if st:
+        raise TPError(st, "tp_cache4_store")
+
+
+def tp_cache4_load(plan: Plan, first, k_codes, k_scale, v_codes, v_scale, k_out, v_out, stream=None) -> None:
+    """Positions first[b] .. of every sequence from the 4-bit caches into k_out and v_out (batch * n
+    rows). All but first: one entry per kv source."""
+    src = _kv_sources(plan)
+    g = _args(6 * src)
+    st = _lib.tp_cache4_load(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
+                             g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
+                             g.many(v_out, src), _stream(stream))
+    if st:
+        raise TPError(st, "tp_cache4_load")
+
+
+def tp_cache4_attn_workspace_size(plan: Plan, batch: int, capacity: int, window: int, sinks: int) -> int:
+    return int(_lib.tp_cache4_attn_workspace_size(plan.handle, batch, capacity, window, sinks))
+
+
+def tp_cache4_attn(plan: Plan, q, k_codes, k_scale, v_codes, v_scale, lengths, window: int, sinks: int, a, workspace=None,
+                   stream=None) -> None:
+    """One new token per sequence over the 4-bit caches, a sliding window and the first `sinks` tokens.
+    q, a: one entry per rank; caches: one per kv source; workspace: a CUDA byte tensor."""
+    n, src = plan.dims.tp_size, _kv_sources(plan)
+    ws, size = _workspace(workspace)
+    g = _args(2 * n + 4 * src)
+    st = _lib.tp_cache4_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),
+                             g.many(v_codes, src), g.many(v_scale, src), _dev_ptr(lengths, "torch.int32"), window, sinks,
+                             g.many(a, n), ws, size, _stream(stream))
+    if st:
+        raise TPError(st, "tp_cache4_attn")
 
 
 # ---- status and diagnostics ---------------------------------------------------

@@ -31,8 +31,9 @@ STAMP = os.path.join(BUILD, "stamp.json")
 DESCRIBE = os.path.join(PKG, "_describe.so")  # the binding's extension module
 
 SOURCES = ["plan.cpp", "tp_api.cu", "gemm_tcgen05.cu", "gemm_f32.cu", "combine.cu", "mlp_static.cu", "vocab.cu", "moe.cu", "attention.cu",
-           "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu", "prefix_attention.cu"]
-HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h", "describe.c"]
+           "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu", "prefix_attention.cu",
+           "rotary.cu", "window_attention.cu", "cache4.cu"]
+HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h", "split_join.cuh", "describe.c"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,875 @@
+// Caches of keys and values held in 4 bits: storing, reading back, and attention of one new token
+// per sequence over them.
+//
+// Format. The 32 neighbouring values of a head that form a group share a bf16 scale,
+//   scale = bf16(max|x| / 7),  code = clamp(rint(x / scale), -8, 7) + 8,  value = (code - 8) * scale
+// (all codes 8 where the scale is 0; a group with an infinity or a NaN has the scale NaN). Row (b * heads + h) * C + j
+// of a kv source's tensors is position j of sequence b's head h: d/2 bytes of codes and d/32
+// scales, 4.5 bits a value. A row's bytes are ordered for the attention kernel's registers: a
+// group's 32 values are cut into pieces (4 of 8 values for keys, 8 of 4 for values), the row
+// holds the first pieces of all groups, then the second ones, and so on, two codes a byte, the
+// lower value's in the lower half.
+//
+// k_cache4_attn. Bound by reading the cache (in theory; see below): 4.5 bits a value leave 41
+// codes a clock and SM at the measured copy rate, so what counts is instructions a code. Tensor products are m16n8k16 with the KEYS as
+// rows: S^T = K q^T (16 keys x 8 heads), O^T += V^T P^T (16 dims x 8 heads). A group of 8 heads then
+// fills a product, where rows of heads would leave half of it empty, and both operands that come
+// from the cache are A fragments made in registers:
+//   K  a word of 8 codes gives four f16 pairs by one shift and four masks: the code's bits in the
+//      low mantissa bits are the subnormal code * 2^-24, or 16 times it, which q makes good
+//      (f16, scaled by a power of two for each head so that its largest value is near 2^14). No -8 is
+//      taken off the codes: the accumulators start at -8 * sum(q). Products of one group
+//      share the key's scale, which multiplies the accumulators, not the codes.
+//   V  codes of two keys are paired by byte permutes, 0x4300 | code is the bf16 128 + code, and
+//      136 is taken off exactly. The values' scales multiply p before it is rounded to bf16,
+//      once a group; movmatrix turns it from S^T's layout into the B operand's.
+// A warp walks 16 keys at a time by itself, through its own ring of cp.async stages; its m, l
+// and O are joined with the other warps' at the end of the CTA's keys, and k_cache4_join joins
+// the CTAs of a (sequence, kv head).
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "op_util.h"
+#include "sm100_ptx.cuh"
+#include "split_join.cuh"
+
+namespace tpgqa {
+namespace {
+
+using namespace op;
+
+constexpr int kC4Ranks = 32;
+constexpr int kGroup = 32;  // values that share a scale
+
+struct Cache4 {
+  uint8_t *k_codes[kC4Ranks], *v_codes[kC4Ranks];
+  __nv_bfloat16 *k_scale[kC4Ranks], *v_scale[kC4Ranks];
+};
+
+// ---------------------------------------------------------------------------
+// Storing and reading back. A thread has 8 neighbouring values (16 bytes of bf16): four threads a
+// group. Bound by memory.
+// ---------------------------------------------------------------------------
+constexpr int kCopyThreads = 256;
+constexpr int kCopyRows = 4;  // rows (token and head) in flight a thread
+
+struct CopyParams {
+  Cache4 cache;
+  const void *in[2][kC4Ranks];   // store: keys and values; load: unused
+  void *out[2][kC4Ranks];        // load: keys and values
+  long long ld[2][kC4Ranks];
+  const int *starts, *counts;
+  int batch, n, cap, heads_kv, heads_per_source;
+  int *status;
+};
+
+// Where piece i of a group's lies in a row of codes with G groups, in bytes.
+template <int G>
+__device__ __forceinline__ int k_byte(int group, int piece) { return (piece * G + group) * 4; }
+template <int G>
+__device__ __forceinline__ int v_byte(int group, int piece) { return (piece * G + group) * 2; }
+
+// Row index -> (token i of sequence b, kv head); consecutive rows are heads of one token.
+struct RowAt {
+  int b, i, kv;
+};
+__device__ __forceinline__ RowAt row_at(long long row, const CopyParams &p) {
+  RowAt r;
+  const long long token = row / p.heads_kv;
+  r.kv = static_cast<int>(row - token * p.heads_kv);
+  r.b = static_cast<int>(token / p.n);
+  r.i = static_cast<int>(token - static_cast<long long>(r.b) * p.n);
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_constant__ CopyParams p) {
+  constexpr int G = D / kGroup, kPer = D / 8;  // groups, threads a row
+  constexpr int kRows = kCopyThreads / kPer;   // rows of a CTA at once
+  grid_dep_wait();
+  grid_dep_launch();
+  const int which = blockIdx.y;  // 0 keys, 1 values
+  const long long rows = static_cast<long long>(p.batch) * p.n * p.heads_kv;
+  const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
+  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kCopyRows) + threadIdx.x / kPer;
+  uint4 raw[kCopyRows];
+  long long to[kCopyRows];  // row of the cache, -1: not stored
+  int src[kCopyRows];
+#pragma unroll
+  for (int u = 0; u < kCopyRows; ++u) {
+    const long long row = r0 + u * kRows;
+    to[u] = -1;
+    src[u] = 0;
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (row >= rows) continue;
+    const RowAt r = row_at(row, p);
+    const int start = p.starts[r.b], count = p.counts ? p.counts[r.b] : p.n;
+    const bool start_ok = start >= 0 && start <= p.cap;
+    const bool good = start_ok && count >= 0 && count <= p.n && count <= p.cap - start;
+    if (!good && r.i == 0 && r.kv == 0 && at == 0 && which == 0) atomicCAS(p.status, 0, kDevBadLength);
+    if (!start_ok || r.i >= count || r.i >= p.cap - start) continue;
+    src[u] = r.kv / p.heads_per_source;
+    const int h = r.kv - src[u] * p.heads_per_source;
+    to[u] = (static_cast<long long>(r.b) * p.heads_per_source + h) * p.cap + start + r.i;
+    const long long token = static_cast<long long>(r.b) * p.n + r.i;
+    raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.in[which][src[u]]) +
+                                              token * p.ld[which][src[u]] + h * D + at * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyRows; ++u) {
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    float x[8], top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+      top = fmaxf(top, fabsf(x[i]));
+      finite = finite && fabsf(x[i]) <= FLT_MAX;
+    }
+    if (!finite) top = INFINITY;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // rounded as the definition says, by true divisions: the codes are the same everywhere
+    const __nv_bfloat16 scale = __float2bfloat16_rn(top <= FLT_MAX ? __fdiv_rn(top, 7.f) : NAN);
+    const float s = __bfloat162float(scale);
+    uint32_t codes = 0;  // 8 codes, the first in the low bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -8.f), 7.f) : 0.f;
+      codes |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * i);
+    }
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);  // the same part of the neighbour group
+    if (to[u] < 0) continue;
+    if (part == 0) (which ? p.cache.v_scale : p.cache.k_scale)[src[u]][to[u] * G + group] = scale;
+    uint8_t *row = (which ? p.cache.v_codes : p.cache.k_codes)[src[u]] + to[u] * (D / 2);
+    if (which == 0) {
+      *reinterpret_cast<uint32_t *>(row + k_byte<G>(group, part)) = codes;
+    } else {
+      // this thread's 8 values are pieces 2 part and 2 part + 1; with the neighbour group's it
+      // writes one of them for both groups, which are neighbours in the row
+      const bool odd = group & 1;
+      const uint32_t word = odd ? __byte_perm(other, codes, 0x7632) : __byte_perm(codes, other, 0x5410);
+      *reinterpret_cast<uint32_t *>(row + v_byte<G>(group & ~1, 2 * part + odd)) = word;
+    }
+  }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_constant__ CopyParams p) {
+  constexpr int G = D / kGroup, kPer = D / 8;
+  constexpr int kRows = kCopyThreads / kPer;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int which = blockIdx.y;
+  const long long rows = static_cast<long long>(p.batch) * p.n * p.heads_kv;
+  const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
+  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kCopyRows) + threadIdx.x / kPer;
+  uint32_t codes[kCopyRows];
+  float scale[kCopyRows];
+  T *dst[kCopyRows];
+#pragma unroll
+  for (int u = 0; u < kCopyRows; ++u) {
+    const long long row = r0 + u * kRows;
+    dst[u] = nullptr;
+    codes[u] = 0x88888888u;
+    scale[u] = 0.f;
+    if (row >= rows) continue;
+    const RowAt r = row_at(row, p);
+    const int src = r.kv / p.heads_per_source, h = r.kv - src * p.heads_per_source;
+    const long long token = static_cast<long long>(r.b) * p.n + r.i;
+    dst[u] = static_cast<T *>(p.out[which][src]) + token * p.ld[which][src] + h * D + at * 8;
+    const int start = p.starts[r.b];
+    if ((start < 0 || start > p.cap) && r.i == 0 && r.kv == 0 && at == 0 && which == 0) atomicCAS(p.status, 0, kDevBadLength);
+    if (start < 0 || r.i >= p.cap - start) continue;  // no such position: zeros
+    const long long from = (static_cast<long long>(r.b) * p.heads_per_source + h) * p.cap + start + r.i;
+    scale[u] = __bfloat162float((which ? p.cache.v_scale : p.cache.k_scale)[src][from * G + group]);
+    const uint8_t *bytes = (which ? p.cache.v_codes : p.cache.k_codes)[src] + from * (D / 2);
+    if (which == 0) {
+      codes[u] = *reinterpret_cast<const uint32_t *>(bytes + k_byte<G>(group, part));
+    } else {
+      const uint32_t lo = *reinterpret_cast<const uint16_t *>(bytes + v_byte<G>(group, 2 * part));
+      const uint32_t hi = *reinterpret_cast<const uint16_t *>(bytes + v_byte<G>(group, 2 * part + 1));
+      codes[u] = lo | hi << 16;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyRows; ++u) {
+    if (!dst[u]) continue;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(static_cast<int>(codes[u] >> (4 * i) & 15u) - 8) * scale[u];
+    if (sizeof(T) == 4) {
+      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention.
+// ---------------------------------------------------------------------------
+constexpr int kAttnWarps = 4, kAttnThreads4 = 32 * kAttnWarps;
+constexpr int kTileKeys = 16;  // keys of a warp's step
+constexpr int kStages = 4;
+
+struct Attn4Params {
+  Cache4 cache;
+  int batch, cap, heads_q, heads_kv, group, heads_per_rank, heads_per_source;
+  int window, sinks;
+  int chunk;               // tiles a split has at most
+  int splits, head_tiles;  // grid y, grid z
+  float scale_log2;
+  const int *lengths;
+  float *part_o;    // [split][row][d], rows kv head by kv head
+  float2 *part_ml;  // [split][row]: m (log2 units), l
+  int *status;
+  const void *q[kC4Ranks];
+  long long q_ld[kC4Ranks];
+  void *a[kC4Ranks];
+  long long a_ld[kC4Ranks];
+};
+
+// The 16-key tiles that a sequence's new token sees: those of the first tokens, then those of the
+// window. One run from 0 where the two meet.
+struct Tiles {
+  int sink_tiles, first, count;
+  __device__ __forceinline__ int at(int j) const { return j < sink_tiles ? j : j - sink_tiles + first; }
+};
+__device__ __forceinline__ Tiles tiles_of(int len, int window, int sinks) {
+  const int w0 = len > window ? len - window : 0;
+  Tiles t;
+  t.first = w0 / kTileKeys;
+  const int st = (min(sinks, w0) + kTileKeys - 1) / kTileKeys;
+  t.sink_tiles = min(st, t.first);
+  t.count = len > 0 ? t.sink_tiles + (len + kTileKeys - 1) / kTileKeys - t.first : 0;
+  return t;
+}
+__device__ __forceinline__ int splits_here(const Tiles &t, int chunk) { return (t.count + chunk - 1) / chunk; }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(there ? N : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// D = A B + C, 16 x 8 x 16.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ void mma_bf(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Four codes in the low nibbles of w's halves (after a shift) as f16 pairs' or bf16 pairs' bits.
+__device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {  // the pair of codes at bits 0-3 and 16-19, less 8
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w));  // (w & a) | b
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xc308), __ushort_as_bfloat16(0xc308));  // -136
+  const __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&r), off);
+  return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+template <int D>
+struct Attn4Cfg {
+  static constexpr int kG = D / kGroup;
+  static constexpr int kRow = D / 2;                             // bytes of a row of codes
+  static constexpr int kV = kTileKeys * kRow, kKs = 2 * kV;      // stage: K codes, V codes, K scales, V scales
+  static constexpr int kVs = kKs + kTileKeys * 2 * kG;
+  static constexpr int kStage = kVs + kTileKeys * 2 * kG;
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kJoinRow = D + 4;                         // floats of a head's sums while warps are joined
+  // Where a tile's K row lies in a stage: rows j and j + 4, read by neighbouring rows of a fragment,
+  // are no multiple of 128 bytes apart.
+  static __device__ __forceinline__ int k_slot(int row) { return row ^ (D == 128 ? row >> 2 & 1 : row >> 1 & 2); }
+};
+
+// NT: products of 8 heads a key fragment serves (the CTA has up to 8 NT heads of the group).
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads4) k_cache4_attn(const __grid_constant__ Attn4Params p) {
+  using C = Attn4Cfg<D>;
+  constexpr int G = C::kG;
+  constexpr int kSums = kAttnWarps * 8 * NT * C::kJoinRow * 4;
+  constexpr int kRing = kAttnWarps * C::kWarp;
+  __shared__ __align__(16) uint8_t smem[kSums > kRing ? kSums : kRing];
+  __shared__ float2 s_ml[kAttnWarps][8 * NT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
+  const int split = blockIdx.y, h0 = blockIdx.z * 8 * NT;  // first head of the group here
+  grid_dep_wait();
+  grid_dep_launch();
+  const int given = p.lengths[b], len = min(max(given, 0), p.cap);
+  if (given != len && kv == 0 && split == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
+  const Tiles tl = tiles_of(len, p.window, p.sinks);
+  const int n_splits = splits_here(tl, p.chunk);
+  if (split >= n_splits) {
+    if (len > 0 || split > 0) return;
+    // no key at all: the heads' outputs are zero
+    for (int i = threadIdx.x; i < 8 * NT * (D / 2); i += kAttnThreads4) {
+      const int g = h0 + i / (D / 2);
+      if (g >= p.group) break;
+      const int head = kv * p.group + g, rank = head / p.heads_per_rank;
+      reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
+                                   static_cast<long long>(head - rank * p.heads_per_rank) * D)[i % (D / 2)] = 0;
+    }
+    return;
+  }
+  const int t0 = static_cast<int>(static_cast<long long>(tl.count) * split / n_splits);
+  const int t1 = static_cast<int>(static_cast<long long>(tl.count) * (split + 1) / n_splits);
+  const int w0 = len > p.window ? len - p.window : 0;
+
+  const int src = kv / p.heads_per_source;
+  const long long row0 = (static_cast<long long>(b) * p.heads_per_source + (kv - src * p.heads_per_source)) * p.cap;
+  const uint8_t *k_codes = p.cache.k_codes[src] + row0 * C::kRow, *v_codes = p.cache.v_codes[src] + row0 * C::kRow;
+  const __nv_bfloat16 *k_scale = p.cache.k_scale[src] + row0 * G, *v_scale = p.cache.v_scale[src] + row0 * G;
+  const uint32_t ring = ptx::smem_addr(smem) + warp * C::kWarp;
+
+  // A tile's rows into a stage; rows that the token does not see are zeros (their scales too), so
+  // that nothing stale is read, however it is encoded.
+  auto seen = [&](int j) { return j < len && (j >= w0 || j < p.sinks); };
+  auto fetch = [&](int t, int stage) {
+    if (t < t1) {
+      const int j0 = tl.at(t) * kTileKeys;
+      const uint32_t to = ring + stage * C::kStage;
+      constexpr int kPieces = kTileKeys * C::kRow / 16;  // 16-byte pieces of a tile's codes: 64 or 32
+#pragma unroll
+      for (int i = 0; i < kPieces / 32; ++i) {
+        const int piece = i * 32 + lane, row = piece / (C::kRow / 16);
+        const bool there = seen(j0 + row);
+        const long long at = there ? static_cast<long long>(j0) * C::kRow + piece * 16 : 0;
+        // K rows and pieces of V rows change places so that the fragments' loads hit every bank once
+        const int in = piece % (C::kRow / 16) * 16;
+        cp16(to + C::k_slot(row) * C::kRow + in, k_codes + at, there);
+        cp16(to + C::kV + row * C::kRow + (D == 128 ? in ^ ((row >> 1 & 1) * 32) : in), v_codes + at, there);
+      }
+      const int row = lane & 15;
+      const bool there = seen(j0 + row);
+      const long long at = there ? static_cast<long long>(j0 + row) * G : 0;
+      cp_small<2 * G>(to + (lane < 16 ? C::kKs : C::kVs) + row * 2 * G, (lane < 16 ? k_scale : v_scale) + at, there);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(t0 + warp + i * kAttnWarps, i);
+
+  // q of the heads as B fragments: step 2g + h of the product over group g takes, from thread c, the
+  // values 8c + 2h, 8c + 2h + 4 (first pair) and 8c + 2h + 1, 8c + 2h + 5 (second), as the codes' masks
+  // bring them up. The second pairs' codes are 16 times as large.
+  uint32_t qf[NT][2 * G][2];
+  float start[NT][G][2];  // the accumulators' first values: -8 * 2^-24 * sum of q over the group, heads 2c and 2c + 1
+  float f[NT][2];         // log2(e) / sqrt(d) * 2^24 / the head's factor
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int g = h0 + 8 * nt + r;
+    uint4 raw[G];
+    float top = 0.f;
+    const int head = kv * p.group + (g < p.group ? g : 0), rank = head / p.heads_per_rank;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q[rank]) + b * p.q_ld[rank] +
+                             static_cast<long long>(head - rank * p.heads_per_rank) * D;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      raw[i] = g < p.group ? *reinterpret_cast<const uint4 *>(q + i * kGroup + c * 8) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the power of two that brings the largest value into [2^14, 2^15); within [2^-100, 2^100] for the
+    // factor's own range
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    const int up = min(max(14 - ex, -100), 100);
+    const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    const float mine = p.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    f[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+    f[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      float x[8], sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = (e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1])) * scale;
+        // what the product will use: values far below the head's largest lose bits in f16
+        x[e] = __half2float(__float2half_rn(e & 1 ? x[e] * 0.0625f : x[e]));
+        sum += e & 1 ? 16.f * x[e] : x[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const __half2 pr = __floats2half2_rn(x[2 * h + e], x[2 * h + e + 4]);
+          qf[nt][2 * i + h][e] = *reinterpret_cast<const uint32_t *>(&pr);
+        }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum *= -8.f * 0x1p-24f;
+      start[nt][i][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+      start[nt][i][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+    }
+  }
+
+  float m[NT][2], l[NT][2], o[NT][2 * G][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -FLT_MAX;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+  }
+
+  // Row r of a fragment's upper half is the tile's key r/2 + 4 (r & 1), of its lower half that key
+  // + 8: the pairs of keys (2c, 2c + 1) of the second product are then the rows c and c + 4, and
+  // each of the values' loads takes four neighbouring rows.
+  const int key = (r >> 1) + 4 * (r & 1);
+  int stage = 0;
+  for (int t = t0 + warp; t < t1; t += kAttnWarps) {
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    const uint8_t *st = smem + warp * C::kWarp + stage * C::kStage;
+    const int j0 = tl.at(t) * kTileKeys;
+    // ---- scores ----
+    uint32_t kw[2][G];
+    float ks[2][G];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t *at = st + C::k_slot(key + 8 * u) * C::kRow + c * 4 * G;
+      if (G == 4) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(at);
+        kw[u][0] = w.x, kw[u][1] = w.y, kw[u][2 % G] = w.z, kw[u][3 % G] = w.w;
+        const uint2 s = *reinterpret_cast<const uint2 *>(st + C::kKs + (key + 8 * u) * 2 * G);
+        ks[u][0] = bf16_lo(s.x), ks[u][1] = bf16_hi(s.x), ks[u][2 % G] = bf16_lo(s.y), ks[u][3 % G] = bf16_hi(s.y);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(at);
+        kw[u][0] = w.x, kw[u][1] = w.y;
+        const uint32_t s = *reinterpret_cast<const uint32_t *>(st + C::kKs + (key + 8 * u) * 2 * G);
+        ks[u][0] = bf16_lo(s), ks[u][1] = bf16_hi(s);
+      }
+    }
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const uint32_t a = kw[0][i], a8 = a >> 8, d = kw[1][i], d8 = d >> 8;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4] = {start[nt][i][0], start[nt][i][1], start[nt][i][0], start[nt][i][1]};
+        mma_f16(acc, a & 0x000f000fu, d & 0x000f000fu, a & 0x00f000f0u, d & 0x00f000f0u, qf[nt][2 * i][0], qf[nt][2 * i][1], acc);
+        mma_f16(acc, a8 & 0x000f000fu, d8 & 0x000f000fu, a8 & 0x00f000f0u, d8 & 0x00f000f0u, qf[nt][2 * i + 1][0],
+                qf[nt][2 * i + 1][1], acc);
+        s[nt][0] += ks[0][i] * acc[0];
+        s[nt][1] += ks[0][i] * acc[1];
+        s[nt][2] += ks[1][i] * acc[2];
+        s[nt][3] += ks[1][i] * acc[3];
+      }
+    }
+    const bool edge = j0 + kTileKeys > len || (j0 < w0 && j0 + kTileKeys > p.sinks);
+    const bool see0 = !edge || seen(j0 + key), see1 = !edge || seen(j0 + key + 8);
+    bool rise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = (e < 2 ? see0 : see1) ? s[nt][e] * f[nt][e & 1] : -INFINITY;
+      rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, rise)) {  // some head's reference maximum moves: rarely after the first tiles
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[nt][e], s[nt][e + 2]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float m_new = fmaxf(m[nt][e], top), alpha = ex2(m[nt][e] - m_new);
+          m[nt][e] = m_new;
+          l[nt][e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 2 * G; ++i) {
+            o[nt][i][e] *= alpha;
+            o[nt][i][e + 2] *= alpha;
+          }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = ex2(s[nt][e] - m[nt][e & 1]);
+      l[nt][0] += s[nt][0] + s[nt][2];
+      l[nt][1] += s[nt][1] + s[nt][3];
+    }
+    // ---- values ----
+    float vs[2][G];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t *at = st + C::kVs + (key + 8 * u) * 2 * G;
+      if (G == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(at);
+        vs[u][0] = bf16_lo(w.x), vs[u][1] = bf16_hi(w.x), vs[u][2 % G] = bf16_lo(w.y), vs[u][3 % G] = bf16_hi(w.y);
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(at);
+        vs[u][0] = bf16_lo(w), vs[u][1] = bf16_hi(w);
+      }
+    }
+    uint32_t vw[4][G / 2];  // rows c, c + 4, c + 8, c + 12: keys 2c, 2c + 1, 2c + 8, 2c + 9 of the product
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = c + 4 * u;
+      if (G == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(st + C::kV + row * C::kRow + ((r * 8) ^ ((row >> 1 & 1) * 32)));
+        vw[u][0] = w.x, vw[u][G / 2 - 1] = w.y;
+      } else {
+        vw[u][0] = *reinterpret_cast<const uint32_t *>(st + C::kV + row * C::kRow + r * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        pb[nt][0] = turn8x8(pack_bf16(s[nt][0] * vs[0][i], s[nt][1] * vs[0][i]));
+        pb[nt][1] = turn8x8(pack_bf16(s[nt][2] * vs[1][i], s[nt][3] * vs[1][i]));
+      }
+      const uint32_t lo = __byte_perm(vw[0][i >> 1], vw[1][i >> 1], i & 1 ? 0x7632 : 0x5410);
+      const uint32_t hi = __byte_perm(vw[2][i >> 1], vw[3][i >> 1], i & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a0 = bf16_codes(lo >> (8 * h)), a1 = bf16_codes(lo >> (8 * h + 4));
+        const uint32_t a2 = bf16_codes(hi >> (8 * h)), a3 = bf16_codes(hi >> (8 * h + 4));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf(o[nt][2 * i + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+    __syncwarp();  // every lane has read the stage that is filled next
+    fetch(t + (kStages - 1) * kAttnWarps, stage == 0 ? kStages - 1 : stage - 1);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  cp_wait<0>();
+
+  // ---- the warps' sums are joined through shared memory ----
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+      if (r == 0) s_ml[warp][8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
+    }
+  __syncthreads();  // the rings are free
+  float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float *row = sums + (warp * 8 * NT + 8 * nt + 2 * c + e) * C::kJoinRow;
+#pragma unroll
+      for (int i = 0; i < G; ++i)  // values 4r .. 4r + 3 of group i
+        *reinterpret_cast<float4 *>(row + i * kGroup + 4 * r) =
+            make_float4(o[nt][2 * i][e], o[nt][2 * i][e + 2], o[nt][2 * i + 1][e], o[nt][2 * i + 1][e + 2]);
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 8 * NT * (D / 4); i += kAttnThreads4) {
+    const int hl = i / (D / 4), col = i % (D / 4) * 4, g = h0 + hl;
+    if (g >= p.group) break;
+    float top = -FLT_MAX;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_ml[w][hl].x);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      const float2 ml = s_ml[w][hl];
+      const float fw = ex2(ml.x - top);
+      const float4 v = *reinterpret_cast<const float4 *>(sums + (w * 8 * NT + hl) * C::kJoinRow + col);
+      sum += fw * ml.y;
+      acc.x += fw * v.x;
+      acc.y += fw * v.y;
+      acc.z += fw * v.z;
+      acc.w += fw * v.w;
+    }
+    const int head = kv * p.group + g;
+    if (n_splits == 1) {
+      const float inv = 1.f / sum;
+      const int rank = head / p.heads_per_rank;
+      __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
+                           static_cast<long long>(head - rank * p.heads_per_rank) * D + col;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    } else {
+      const long long row = (static_cast<long long>(split) * p.batch + b) * p.heads_q + head;
+      *reinterpret_cast<float4 *>(p.part_o + row * D + col) = acc;
+      if (col == 0) p.part_ml[row] = make_float2(top, sum);
+    }
+  }
+}
+
+// One warp a (sequence, head); those whose keys one CTA had are done already.
+template <int D>
+__global__ void __launch_bounds__(256) k_cache4_join(const __grid_constant__ Attn4Params p) {
+  constexpr int kPer = D / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<long long>(p.batch) * p.heads_q) return;
+  const int b = static_cast<int>(row / p.heads_q), head = static_cast<int>(row - static_cast<long long>(b) * p.heads_q);
+  const Tiles tl = tiles_of(min(max(p.lengths[b], 0), p.cap), p.window, p.sinks);
+  const int n = splits_here(tl, p.chunk);
+  if (n < 2) return;
+  float acc[kPer];
+  const float l = join_splits<D>(p.part_ml, p.part_o, static_cast<long long>(p.batch) * p.heads_q, row, n, lane, acc);
+  const int rank = head / p.heads_per_rank;
+  __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
+                       static_cast<long long>(head - rank * p.heads_per_rank) * D + lane * kPer;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+}
+
+// Tiles a split has at most, and the splits that the longest sequence may have.
+struct Shape4 {
+  int chunk, splits, head_tiles, nt;
+};
+Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long window, long long sinks) {
+  Shape4 s;
+  const int group = d.num_q_heads / d.num_kv_heads;
+  s.nt = group > 8 ? 2 : 1;
+  s.head_tiles = (group + 8 * s.nt - 1) / (8 * s.nt);
+  long long tiles = (cap + kTileKeys - 1) / kTileKeys;
+  if (window < cap) {
+    // the first tokens' tiles and the window's, whose ends may both lie inside one
+    const long long some = (window + kTileKeys - 1) / kTileKeys + 1 + (sinks + kTileKeys - 1) / kTileKeys;
+    if (some < tiles) tiles = some;
+  }
+  const long long units = batch * d.num_kv_heads * s.head_tiles;
+  // 64 tiles (1024 keys) a CTA, halved while the SMs could take twice the CTAs, down to 2 tiles a warp
+  s.chunk = 64;
+  while (s.chunk > 2 * kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 4LL * num_sms()) s.chunk /= 2;
+  // at most 64 splits a sequence
+  while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
+  s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
+  return s;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t sums_bytes(const Shape4 &s, long long rows, long long d) { return s.splits > 1 ? round256(static_cast<size_t>(s.splits) * rows * d * 4) : 0; }
+size_t workspace_bytes_of(const Shape4 &s, long long rows, long long d) {
+  return s.splits > 1 ? sums_bytes(s, rows, d) + round256(static_cast<size_t>(s.splits) * rows * 8) : 0;
+}
+
+// Head sizes that the format's layouts cover, and sizes whose grids and indices are in range.
+bool sizes_ok(const tp_dims &d, long long batch, long long cap) {
+  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kC4Ranks && batch <= 0x7fffffffLL / 256 / d.num_q_heads &&
+         cap <= 0x7fffffffLL - 256 && d.num_q_heads / d.num_kv_heads <= 65535;
+}
+
+// The four tensors of a kv source's cache.
+tp_status check_cache(const tp_tensor *t, int sources, long long rows, long long cols, int32_t dtype) {
+  for (int r = 0; r < sources; ++r) {
+    if (t[r].dtype != dtype) return TP_ERR_DTYPE;
+    if (t[r].rows != rows || t[r].cols != cols || (rows > 1 && t[r].ld != cols)) return TP_ERR_INVALID_ARG;
+    if (rows > 0 && !t[r].ptr) return TP_ERR_INVALID_ARG;
+    // 16-byte pieces of codes; a row's scales at once
+    if (!ptr_aligned(t[r].ptr, dtype == TP_U8 ? 16 : 2 * cols)) return TP_ERR_ALIGNMENT;
+  }
+  return TP_OK;
+}
+
+struct Given {
+  tp_dims dims;
+  int n, sources;
+  long long hd, heads, cap;  // heads of a source, positions of a sequence
+};
+tp_status check_call(const tp_plan *plan, int64_t batch, const tp_tensor *kc, const tp_tensor *ks, const tp_tensor *vc,
+                     const tp_tensor *vs, Given &g, Cache4 &out) {
+  tp_rank_shard sh;
+  if (!plan || tp_plan_dims(plan, &g.dims) != TP_OK || tp_plan_query_rank(plan, 0, &sh) != TP_OK) return TP_ERR_INVALID_ARG;
+  if (!kc || !ks || !vc || !vs || batch < 0 || batch > 0x7fffffffLL) return TP_ERR_INVALID_ARG;
+  g.n = g.dims.tp_size;
+  g.hd = g.dims.head_dim;
+  if ((g.hd != 64 && g.hd != 128) || g.n > kC4Ranks) return TP_ERR_UNSUPPORTED;
+  g.sources = sh.kv_replicated ? 1 : g.n;
+  g.heads = g.dims.num_kv_heads / g.sources;
+  g.cap = batch > 0 ? kc[0].rows / (batch * g.heads) : 0;
+  if (g.cap < 0 || g.cap > 0x7fffffffLL) return TP_ERR_INVALID_ARG;
+  const long long rows = batch * g.heads * g.cap;
+  tp_status st;
+  if ((st = check_cache(kc, g.sources, rows, g.hd / 2, TP_U8)) != TP_OK || (st = check_cache(vc, g.sources, rows, g.hd / 2, TP_U8)) != TP_OK ||
+      (st = check_cache(ks, g.sources, rows, g.hd / kGroup, TP_BF16)) != TP_OK ||
+      (st = check_cache(vs, g.sources, rows, g.hd / kGroup, TP_BF16)) != TP_OK)
+    return st;
+  if (!sizes_ok(g.dims, batch, g.cap)) return TP_ERR_UNSUPPORTED;
+  for (int r = 0; r < g.sources; ++r) {
+    out.k_codes[r] = static_cast<uint8_t *>(kc[r].ptr);
+    out.v_codes[r] = static_cast<uint8_t *>(vc[r].ptr);
+    out.k_scale[r] = static_cast<__nv_bfloat16 *>(ks[r].ptr);
+    out.v_scale[r] = static_cast<__nv_bfloat16 *>(vs[r].ptr);
+  }
+  return TP_OK;
+}
+
+tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t *starts, const tp_tensor *k, const tp_tensor *v,
+                    bool store, cudaStream_t s) {
+  if (!k || !v) return TP_ERR_INVALID_ARG;
+  const long long n = batch > 0 ? k[0].rows / batch : 0;
+  const int32_t dt = k[0].dtype;
+  for (int r = 0; r < g.sources; ++r)
+    for (int w = 0; w < 2; ++w) {
+      const tp_tensor &t = w ? v[r] : k[r];
+      if (!view_ok(t)) return TP_ERR_INVALID_ARG;
+      if (t.dtype != dt || (dt != TP_BF16 && (store || dt != TP_F32))) return TP_ERR_DTYPE;
+      if (t.rows != batch * n || t.cols != g.heads * g.hd) return TP_ERR_INVALID_ARG;
+      if (t.rows > 0 && !vec_aligned(t)) return TP_ERR_ALIGNMENT;
+      p.in[w][r] = t.ptr;
+      p.out[w][r] = t.ptr;
+      p.ld[w][r] = t.ld;
+    }
+  const long long rows = batch * n;
+  if (rows > 0 && !starts) return TP_ERR_INVALID_ARG;
+  if (!ptr_aligned(starts, 4)) return TP_ERR_ALIGNMENT;
+  tp_status st = check_rank_health(g.n);
+  if (st != TP_OK || rows == 0) return st;
+  DevCtx ctx;
+  const cudaError_t e = get_dev_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e);
+  p.starts = starts;
+  p.batch = static_cast<int>(batch);
+  p.n = static_cast<int>(n);
+  p.cap = static_cast<int>(g.cap);
+  p.heads_kv = g.dims.num_kv_heads;
+  p.heads_per_source = static_cast<int>(g.heads);
+  p.status = ctx.status;
+  const long long per = kCopyThreads / (g.hd / 8) * kCopyRows, blocks = (rows * p.heads_kv + per - 1) / per;
+  if (blocks > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), 2);
+  if (store) return launched(launch_kernel(g.hd == 128 ? k_cache4_store<128> : k_cache4_store<64>, grid, dim3(kCopyThreads), 0, s, 1, p));
+  if (dt == TP_F32)
+    return launched(launch_kernel(g.hd == 128 ? k_cache4_load<128, float> : k_cache4_load<64, float>, grid, dim3(kCopyThreads), 0, s, 1, p));
+  return launched(launch_kernel(g.hd == 128 ? k_cache4_load<128, __nv_bfloat16> : k_cache4_load<64, __nv_bfloat16>, grid,
+                                dim3(kCopyThreads), 0, s, 1, p));
+}
+
+}  // namespace
+}  // namespace tpgqa
+
+using namespace tpgqa;
+using namespace tpgqa::op;
+
+extern "C" tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *lengths, const int32_t *counts,
+                                     const tp_tensor *k, const tp_tensor *v, tp_tensor *k_codes, tp_tensor *k_scale,
+                                     tp_tensor *v_codes, tp_tensor *v_scale, tp_stream_t stream) {
+  Given g;
+  CopyParams p = {};
+  const tp_status st = check_call(plan, batch, k_codes, k_scale, v_codes, v_scale, g, p.cache);
+  if (st != TP_OK) return st;
+  if (!ptr_aligned(counts, 4)) return TP_ERR_ALIGNMENT;
+  p.counts = counts;
+  return copy_call(g, p, batch, lengths, k, v, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" tp_status tp_cache4_load(const tp_plan *plan, int64_t batch, const int32_t *first, const tp_tensor *k_codes,
+                                    const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale,
+                                    tp_tensor *k_out, tp_tensor *v_out, tp_stream_t stream) {
+  Given g;
+  CopyParams p = {};
+  const tp_status st = check_call(plan, batch, k_codes, k_scale, v_codes, v_scale, g, p.cache);
+  if (st != TP_OK) return st;
+  return copy_call(g, p, batch, first, k_out, v_out, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t capacity, int32_t window,
+                                                int32_t sinks) {
+  tp_dims d;
+  if (!plan || batch < 1 || capacity < 1 || window < 1 || sinks < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
+  if (!sizes_ok(d, batch, capacity)) return 0;
+  return workspace_bytes_of(shape4_of(d, batch, capacity, window, sinks), batch * d.num_q_heads, d.head_dim);
+}
+
+extern "C" tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_codes,
+                                    const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale,
+                                    const int32_t *lengths, int32_t window, int32_t sinks, tp_tensor *a, void *workspace,
+                                    size_t workspace_bytes, tp_stream_t stream) {
+  Given g;
+  Attn4Params p = {};
+  tp_status st = check_call(plan, batch, k_codes, k_scale, v_codes, v_scale, g, p.cache);
+  if (st != TP_OK) return st;
+  if (!q || !a || window < 1 || sinks < 0) return TP_ERR_INVALID_ARG;
+  const long long qc = g.dims.num_q_heads / g.n * g.hd;
+  for (int r = 0; r < g.n; ++r) {
+    for (const tp_tensor *t : {q + r, static_cast<const tp_tensor *>(a + r)}) {
+      if (!view_ok(*t)) return TP_ERR_INVALID_ARG;
+      if (t->dtype != TP_BF16) return TP_ERR_DTYPE;
+      if (t->rows != batch || t->cols != qc) return TP_ERR_INVALID_ARG;
+      if (batch > 0 && !vec_aligned(*t)) return TP_ERR_ALIGNMENT;
+    }
+    p.q[r] = q[r].ptr;
+    p.q_ld[r] = q[r].ld;
+    p.a[r] = a[r].ptr;
+    p.a_ld[r] = a[r].ld;
+  }
+  if (batch > 0 && !lengths) return TP_ERR_INVALID_ARG;
+  if (!ptr_aligned(lengths, 4)) return TP_ERR_ALIGNMENT;
+  const Shape4 s = shape4_of(g.dims, batch, g.cap, window, sinks);
+  const long long rows = batch * g.dims.num_q_heads;
+  const size_t need = workspace_bytes_of(s, rows, g.hd);
+  if (batch > 0 && need > 0) {
+    if (!workspace || workspace_bytes < need) return TP_ERR_WORKSPACE;
+    if (!ptr_aligned(workspace, 16)) return TP_ERR_ALIGNMENT;
+  }
+  if ((st = check_rank_health(g.n)) != TP_OK) return st;
+  if (batch == 0) return TP_OK;
+  DevCtx ctx;
+  const cudaError_t e = get_dev_ctx(&ctx);
+  if (e != cudaSuccess) return cuda_fail(e);
+  p.batch = static_cast<int>(batch);
+  p.cap = static_cast<int>(g.cap);
+  p.heads_q = g.dims.num_q_heads;
+  p.heads_kv = g.dims.num_kv_heads;
+  p.group = p.heads_q / p.heads_kv;
+  p.heads_per_rank = p.heads_q / g.n;
+  p.heads_per_source = static_cast<int>(g.heads);
+  p.window = window;
+  p.sinks = sinks;
+  p.chunk = s.chunk;
+  p.splits = s.splits > 0 ? s.splits : 1;
+  p.head_tiles = s.head_tiles;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.hd)));
+  p.lengths = lengths;
+  p.part_o = static_cast<float *>(workspace);
+  p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + sums_bytes(s, rows, g.hd));
+  p.status = ctx.status;
+  cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(batch * p.heads_kv), static_cast<unsigned>(p.splits), static_cast<unsigned>(s.head_tiles));
+  auto kernel = g.hd == 128 ? (s.nt == 2 ? k_cache4_attn<128, 2> : k_cache4_attn<128, 1>)
+                            : (s.nt == 2 ? k_cache4_attn<64, 2> : k_cache4_attn<64, 1>);
+  st = launched(launch_kernel(kernel, grid, dim3(kAttnThreads4), 0, str, 1, p));
+  if (st != TP_OK || s.splits < 2) return st;
+  return launched(launch_kernel(g.hd == 128 ? k_cache4_join<128> : k_cache4_join<64>, dim3(static_cast<unsigned>((rows + 7) / 8)),
+                                dim3(256), 0, str, 1, p));
+}

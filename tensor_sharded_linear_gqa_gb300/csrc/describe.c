@@ -12,7 +12,7 @@
 #include "tpgqa.h"
 
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr;
-static PyObject *known[3]; /* by tp_dtype: the type objects, which live as long as torch does */
+static PyObject *known[4]; /* by tp_dtype: the type objects, which live as long as torch does */
 
 /* The long long items of a tuple attribute or result (a reference that this takes). */
 static int items(PyObject *t, long long *out, Py_ssize_t n) {
@@ -28,9 +28,9 @@ static int items(PyObject *t, long long *out, Py_ssize_t n) {
 static int describe(PyObject *t, Py_ssize_t dims, tp_tensor *d) {
   PyObject *v = PyObject_GetAttr(t, s_dtype);
   int type = 0;
-  while (type < 3 && (v == NULL || v != known[type])) ++type;
+  while (type < 4 && (v == NULL || v != known[type])) ++type;
   Py_XDECREF(v);
-  if (type == 3) return 0;
+  if (type == 4) return 0;
   v = PyObject_GetAttr(t, s_is_cuda);
   const int cuda = v == Py_True;
   Py_XDECREF(v);
@@ -100,8 +100,8 @@ static PyObject *py_matrices(PyObject *self, PyObject *const *args, Py_ssize_t n
 
 static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (n != 3) return PyErr_Format(PyExc_TypeError, "dtypes(f32, bf16, e4m3)");
-  for (int i = 0; i < 3; ++i) {
+  if (n != 4) return PyErr_Format(PyExc_TypeError, "dtypes(f32, bf16, e4m3, u8)");
+  for (int i = 0; i < 4; ++i) {
     Py_INCREF(args[i]);
     Py_XSETREF(known[i], args[i]);
   }
@@ -109,7 +109,7 @@ static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) 
 }
 
 static PyMethodDef methods[] = {
-    {"dtypes", (PyCFunction)(void (*)(void))py_dtypes, METH_FASTCALL, "dtypes(f32, bf16, e4m3): the type objects of TP_F32, TP_BF16, TP_E4M3"},
+    {"dtypes", (PyCFunction)(void (*)(void))py_dtypes, METH_FASTCALL, "dtypes(f32, bf16, e4m3, u8): the type objects of TP_F32, TP_BF16, TP_E4M3, TP_U8"},
     {"matrix", (PyCFunction)(void (*)(void))py_matrix, METH_FASTCALL, "matrix(tensor, address) -> whether it was described there"},
     {"row", (PyCFunction)(void (*)(void))py_row, METH_FASTCALL, "row(tensor, address): a 1-D tensor as a matrix of one row"},
     {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address) -> how many of the first were described"},

@@ -73,17 +73,26 @@ __device__ __forceinline__ int k_byte(int group, int piece) { return (piece * G 
 template <int G>
 __device__ __forceinline__ int v_byte(int group, int piece) { return (piece * G + group) * 2; }
 
-// Row index -> (token i of sequence b, kv head); consecutive rows are heads of one token.
+// A CTA has rows [r0, r0 + kRows * kCopyRows) of sequence blockIdx.z's n * heads rows, the heads of a
+// token neighbours.
 struct RowAt {
-  int b, i, kv;
+  int i, src, h;  // token, kv source, head of the source
 };
-__device__ __forceinline__ RowAt row_at(long long row, const CopyParams &p) {
+__device__ __forceinline__ RowAt row_at(int row, const CopyParams &p) {
   RowAt r;
-  const long long token = row / p.heads_kv;
-  r.kv = static_cast<int>(row - token * p.heads_kv);
-  r.b = static_cast<int>(token / p.n);
-  r.i = static_cast<int>(token - static_cast<long long>(r.b) * p.n);
+  r.i = row / p.heads_kv;
+  const int kv = row - r.i * p.heads_kv;
+  r.src = kv / p.heads_per_source;
+  r.h = kv - r.src * p.heads_per_source;
   return r;
+}
+
+// round(x / s) as the quotient rounded to f32 would give it, which the definition asks for and a
+// product with r = 1 / s does not where x / s lies halfway between two codes: one step of
+// Newton's method on the product's remainder gives the rounded quotient.
+__device__ __forceinline__ float rounded_quotient(float x, float s, float r) {
+  const float q = x * r;
+  return rintf(fmaf(fmaf(-q, s, x), r, q));
 }
 
 template <int D>
@@ -92,32 +101,31 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_cons
   constexpr int kRows = kCopyThreads / kPer;   // rows of a CTA at once
   grid_dep_wait();
   grid_dep_launch();
-  const int which = blockIdx.y;  // 0 keys, 1 values
-  const long long rows = static_cast<long long>(p.batch) * p.n * p.heads_kv;
+  const int which = blockIdx.y, b = blockIdx.z;  // keys or values; sequence
+  const int rows = p.n * p.heads_kv;
   const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
-  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int r0 = blockIdx.x * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int start = p.starts[b], given = p.counts ? p.counts[b] : p.n;
+  const bool start_ok = start >= 0 && start <= p.cap;
+  const int count = start_ok ? min(min(max(given, 0), p.n), p.cap - start) : 0;
+  if (count != given && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
   uint4 raw[kCopyRows];
   long long to[kCopyRows];  // row of the cache, -1: not stored
   int src[kCopyRows];
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
-    const long long row = r0 + u * kRows;
+    const int row = r0 + u * kRows;
     to[u] = -1;
     src[u] = 0;
     raw[u] = make_uint4(0, 0, 0, 0);
     if (row >= rows) continue;
     const RowAt r = row_at(row, p);
-    const int start = p.starts[r.b], count = p.counts ? p.counts[r.b] : p.n;
-    const bool start_ok = start >= 0 && start <= p.cap;
-    const bool good = start_ok && count >= 0 && count <= p.n && count <= p.cap - start;
-    if (!good && r.i == 0 && r.kv == 0 && at == 0 && which == 0) atomicCAS(p.status, 0, kDevBadLength);
-    if (!start_ok || r.i >= count || r.i >= p.cap - start) continue;
-    src[u] = r.kv / p.heads_per_source;
-    const int h = r.kv - src[u] * p.heads_per_source;
-    to[u] = (static_cast<long long>(r.b) * p.heads_per_source + h) * p.cap + start + r.i;
-    const long long token = static_cast<long long>(r.b) * p.n + r.i;
-    raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.in[which][src[u]]) +
-                                              token * p.ld[which][src[u]] + h * D + at * 8);
+    if (r.i >= count) continue;
+    src[u] = r.src;
+    to[u] = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
+    const long long token = static_cast<long long>(b) * p.n + r.i;
+    raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.in[which][r.src]) +
+                                              token * p.ld[which][r.src] + r.h * D + at * 8);
   }
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
@@ -133,14 +141,16 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_cons
     if (!finite) top = INFINITY;
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // rounded as the definition says, by true divisions: the codes are the same everywhere
     const __nv_bfloat16 scale = __float2bfloat16_rn(top <= FLT_MAX ? __fdiv_rn(top, 7.f) : NAN);
-    const float s = __bfloat162float(scale);
+    // scales near f32's smallest have no reciprocal: they and the values go up by 2^80
+    const float lift = __bfloat162float(scale) < 0x1p-60f ? 0x1p80f : 1.f;
+    const float s = __bfloat162float(scale) * lift, inv = __frcp_rn(s);
     uint32_t codes = 0;  // 8 codes, the first in the low bits
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -8.f), 7.f) : 0.f;
-      codes |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * i);
+      const float c = s > 0.f ? fminf(fmaxf(rounded_quotient(x[i] * lift, s, inv), -8.f), 7.f) : 0.f;
+      // the integer in the low bits of 1.5 * 2^23 + c
+      codes |= ((__float_as_uint(c + 12582920.f)) & 15u) << (4 * i);
     }
     const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);  // the same part of the neighbour group
     if (to[u] < 0) continue;
@@ -164,30 +174,30 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_const
   constexpr int kRows = kCopyThreads / kPer;
   grid_dep_wait();
   grid_dep_launch();
-  const int which = blockIdx.y;
-  const long long rows = static_cast<long long>(p.batch) * p.n * p.heads_kv;
+  const int which = blockIdx.y, b = blockIdx.z;
+  const int rows = p.n * p.heads_kv;
   const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
-  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int r0 = blockIdx.x * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int start = p.starts[b];
+  if ((start < 0 || start > p.cap) && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
+  const int there = start >= 0 ? p.cap - start : 0;  // positions that exist; the others are zeros
   uint32_t codes[kCopyRows];
   float scale[kCopyRows];
   T *dst[kCopyRows];
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
-    const long long row = r0 + u * kRows;
+    const int row = r0 + u * kRows;
     dst[u] = nullptr;
     codes[u] = 0x88888888u;
     scale[u] = 0.f;
     if (row >= rows) continue;
     const RowAt r = row_at(row, p);
-    const int src = r.kv / p.heads_per_source, h = r.kv - src * p.heads_per_source;
-    const long long token = static_cast<long long>(r.b) * p.n + r.i;
-    dst[u] = static_cast<T *>(p.out[which][src]) + token * p.ld[which][src] + h * D + at * 8;
-    const int start = p.starts[r.b];
-    if ((start < 0 || start > p.cap) && r.i == 0 && r.kv == 0 && at == 0 && which == 0) atomicCAS(p.status, 0, kDevBadLength);
-    if (start < 0 || r.i >= p.cap - start) continue;  // no such position: zeros
-    const long long from = (static_cast<long long>(r.b) * p.heads_per_source + h) * p.cap + start + r.i;
-    scale[u] = __bfloat162float((which ? p.cache.v_scale : p.cache.k_scale)[src][from * G + group]);
-    const uint8_t *bytes = (which ? p.cache.v_codes : p.cache.k_codes)[src] + from * (D / 2);
+    const long long token = static_cast<long long>(b) * p.n + r.i;
+    dst[u] = static_cast<T *>(p.out[which][r.src]) + token * p.ld[which][r.src] + r.h * D + at * 8;
+    if (r.i >= there) continue;
+    const long long from = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
+    scale[u] = __bfloat162float((which ? p.cache.v_scale : p.cache.k_scale)[r.src][from * G + group]);
+    const uint8_t *bytes = (which ? p.cache.v_codes : p.cache.k_codes)[r.src] + from * (D / 2);
     if (which == 0) {
       codes[u] = *reinterpret_cast<const uint32_t *>(bytes + k_byte<G>(group, part));
     } else {
@@ -215,8 +225,8 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_const
 // Attention.
 // ---------------------------------------------------------------------------
 constexpr int kAttnWarps = 4, kAttnThreads4 = 32 * kAttnWarps;
-constexpr int kTileKeys = 16;  // keys of a warp's step
-constexpr int kStages = 4;
+constexpr int kTileKeys = 32;  // keys of a warp's step: two products' rows
+constexpr int kStages = 3;
 
 struct Attn4Params {
   Cache4 cache;
@@ -235,7 +245,7 @@ struct Attn4Params {
   long long a_ld[kC4Ranks];
 };
 
-// The 16-key tiles that a sequence's new token sees: those of the first tokens, then those of the
+// The 32-key tiles that a sequence's new token sees: those of the first tokens, then those of the
 // window. One run from 0 where the two meet.
 struct Tiles {
   int sink_tiles, first, count;
@@ -252,11 +262,18 @@ __device__ __forceinline__ Tiles tiles_of(int len, int window, int sinks) {
 }
 __device__ __forceinline__ int splits_here(const Tiles &t, int chunk) { return (t.count + chunk - 1) / chunk; }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 template <int N>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void *src, bool there) {
+__device__ __forceinline__ void cp_small(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_small_or_zero(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(there ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -304,16 +321,21 @@ struct Attn4Cfg {
   // Where a tile's K row lies in a stage: rows j and j + 4, read by neighbouring rows of a fragment,
   // are no multiple of 128 bytes apart.
   static __device__ __forceinline__ int k_slot(int row) { return row ^ (D == 128 ? row >> 2 & 1 : row >> 1 & 2); }
+  // Where byte `in` of a V row lies: rows 2, 3 mod 4 have their halves exchanged.
+  static __device__ __forceinline__ int v_in(int row, int in) { return D == 128 ? in ^ ((row >> 1 & 1) * 32) : in; }
 };
+template <int D, int NT>
+constexpr int attn4_smem() {
+  const int sums = kAttnWarps * 8 * NT * Attn4Cfg<D>::kJoinRow * 4, ring = kAttnWarps * Attn4Cfg<D>::kWarp;
+  return sums > ring ? sums : ring;
+}
 
 // NT: products of 8 heads a key fragment serves (the CTA has up to 8 NT heads of the group).
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads4) k_cache4_attn(const __grid_constant__ Attn4Params p) {
+__global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(const __grid_constant__ Attn4Params p) {
   using C = Attn4Cfg<D>;
   constexpr int G = C::kG;
-  constexpr int kSums = kAttnWarps * 8 * NT * C::kJoinRow * 4;
-  constexpr int kRing = kAttnWarps * C::kWarp;
-  __shared__ __align__(16) uint8_t smem[kSums > kRing ? kSums : kRing];
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_ml[kAttnWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
@@ -342,32 +364,43 @@ __global__ void __launch_bounds__(kAttnThreads4) k_cache4_attn(const __grid_cons
 
   const int src = kv / p.heads_per_source;
   const long long row0 = (static_cast<long long>(b) * p.heads_per_source + (kv - src * p.heads_per_source)) * p.cap;
-  const uint8_t *k_codes = p.cache.k_codes[src] + row0 * C::kRow, *v_codes = p.cache.v_codes[src] + row0 * C::kRow;
-  const __nv_bfloat16 *k_scale = p.cache.k_scale[src] + row0 * G, *v_scale = p.cache.v_scale[src] + row0 * G;
+  // this lane's first pieces: 16 bytes of codes of row lane / kLanes, the scales of row lane
+  constexpr int kLanes = C::kRow / 16, kRowsAtOnce = 32 / kLanes;
+  const int my_row = lane / kLanes, my_in = lane % kLanes * 16;
+  const uint8_t *k_codes = p.cache.k_codes[src] + row0 * C::kRow + lane * 16, *v_codes = p.cache.v_codes[src] + row0 * C::kRow + lane * 16;
+  const __nv_bfloat16 *k_scale = p.cache.k_scale[src] + (row0 + lane) * G, *v_scale = p.cache.v_scale[src] + (row0 + lane) * G;
   const uint32_t ring = ptx::smem_addr(smem) + warp * C::kWarp;
+  const uint32_t to_k = ring + C::k_slot(my_row) * C::kRow + my_in, to_v = ring + C::kV + my_row * C::kRow + C::v_in(my_row, my_in);
+  const uint32_t to_s = ring + C::kKs + lane * 2 * G;
 
   // A tile's rows into a stage; rows that the token does not see are zeros (their scales too), so
   // that nothing stale is read, however it is encoded.
   auto seen = [&](int j) { return j < len && (j >= w0 || j < p.sinks); };
+  auto whole = [&](int j0) { return j0 + kTileKeys <= len && (j0 >= w0 || j0 + kTileKeys <= p.sinks); };  // all rows are seen
   auto fetch = [&](int t, int stage) {
     if (t < t1) {
       const int j0 = tl.at(t) * kTileKeys;
-      const uint32_t to = ring + stage * C::kStage;
-      constexpr int kPieces = kTileKeys * C::kRow / 16;  // 16-byte pieces of a tile's codes: 64 or 32
+      const uint32_t off = stage * C::kStage;
+      const long long at = static_cast<long long>(j0) * C::kRow, at_s = static_cast<long long>(j0) * G;
+      if (whole(j0)) {
 #pragma unroll
-      for (int i = 0; i < kPieces / 32; ++i) {
-        const int piece = i * 32 + lane, row = piece / (C::kRow / 16);
-        const bool there = seen(j0 + row);
-        const long long at = there ? static_cast<long long>(j0) * C::kRow + piece * 16 : 0;
-        // K rows and pieces of V rows change places so that the fragments' loads hit every bank once
-        const int in = piece % (C::kRow / 16) * 16;
-        cp16(to + C::k_slot(row) * C::kRow + in, k_codes + at, there);
-        cp16(to + C::kV + row * C::kRow + (D == 128 ? in ^ ((row >> 1 & 1) * 32) : in), v_codes + at, there);
+        for (int i = 0; i < kTileKeys / kRowsAtOnce; ++i) {
+          cp16(to_k + off + i * 512, k_codes + at + i * 512);
+          cp16(to_v + off + i * 512, v_codes + at + i * 512);
+        }
+        cp_small<2 * G>(to_s + off, k_scale + at_s);
+        cp_small<2 * G>(to_s + off + C::kVs - C::kKs, v_scale + at_s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTileKeys / kRowsAtOnce; ++i) {
+          const bool there = seen(j0 + my_row + i * kRowsAtOnce);
+          cp16_or_zero(to_k + off + i * 512, there ? k_codes + at + i * 512 : p.cache.k_codes[src], there);
+          cp16_or_zero(to_v + off + i * 512, there ? v_codes + at + i * 512 : p.cache.v_codes[src], there);
+        }
+        const bool there = seen(j0 + lane);
+        cp_small_or_zero<2 * G>(to_s + off, there ? k_scale + at_s : p.cache.k_scale[src], there);
+        cp_small_or_zero<2 * G>(to_s + off + C::kVs - C::kKs, there ? v_scale + at_s : p.cache.v_scale[src], there);
       }
-      const int row = lane & 15;
-      const bool there = seen(j0 + row);
-      const long long at = there ? static_cast<long long>(j0 + row) * G : 0;
-      cp_small<2 * G>(to + (lane < 16 ? C::kKs : C::kVs) + row * 2 * G, (lane < 16 ? k_scale : v_scale) + at, there);
     }
     cp_commit();
   };
@@ -442,73 +475,88 @@ __global__ void __launch_bounds__(kAttnThreads4) k_cache4_attn(const __grid_cons
       for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
   }
 
-  // Row r of a fragment's upper half is the tile's key r/2 + 4 (r & 1), of its lower half that key
+  // Row r of a fragment's upper half is the product's key r/2 + 4 (r & 1), of its lower half that key
   // + 8: the pairs of keys (2c, 2c + 1) of the second product are then the rows c and c + 4, and
   // each of the values' loads takes four neighbouring rows.
   const int key = (r >> 1) + 4 * (r & 1);
   int stage = 0;
   for (int t = t0 + warp; t < t1; t += kAttnWarps) {
     cp_wait<kStages - 2>();
-    __syncwarp();
+    __syncwarp();  // the tile has landed, and every lane has read the one before, whose stage is filled next
+    fetch(t + (kStages - 1) * kAttnWarps, stage == 0 ? kStages - 1 : stage - 1);
     const uint8_t *st = smem + warp * C::kWarp + stage * C::kStage;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     const int j0 = tl.at(t) * kTileKeys;
     // ---- scores ----
-    uint32_t kw[2][G];
-    float ks[2][G];
+    float s[2][NT][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t *at = st + C::k_slot(key + 8 * u) * C::kRow + c * 4 * G;
-      if (G == 4) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(at);
-        kw[u][0] = w.x, kw[u][1] = w.y, kw[u][2 % G] = w.z, kw[u][3 % G] = w.w;
-        const uint2 s = *reinterpret_cast<const uint2 *>(st + C::kKs + (key + 8 * u) * 2 * G);
-        ks[u][0] = bf16_lo(s.x), ks[u][1] = bf16_hi(s.x), ks[u][2 % G] = bf16_lo(s.y), ks[u][3 % G] = bf16_hi(s.y);
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(at);
-        kw[u][0] = w.x, kw[u][1] = w.y;
-        const uint32_t s = *reinterpret_cast<const uint32_t *>(st + C::kKs + (key + 8 * u) * 2 * G);
-        ks[u][0] = bf16_lo(s), ks[u][1] = bf16_hi(s);
+    for (int half = 0; half < 2; ++half) {
+      uint32_t kw[2][G];
+      float ks[2][G];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = key + 8 * u + 16 * half;
+        const uint8_t *at = st + C::k_slot(key) * C::kRow + (8 * u + 16 * half) * C::kRow + c * 4 * G;
+        if (G == 4) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(at);
+          kw[u][0] = w.x, kw[u][1] = w.y, kw[u][2 % G] = w.z, kw[u][3 % G] = w.w;
+          const uint2 v = *reinterpret_cast<const uint2 *>(st + C::kKs + row * 2 * G);
+          ks[u][0] = bf16_lo(v.x), ks[u][1] = bf16_hi(v.x), ks[u][2 % G] = bf16_lo(v.y), ks[u][3 % G] = bf16_hi(v.y);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2 *>(at);
+          kw[u][0] = w.x, kw[u][1] = w.y;
+          const uint32_t v = *reinterpret_cast<const uint32_t *>(st + C::kKs + row * 2 * G);
+          ks[u][0] = bf16_lo(v), ks[u][1] = bf16_hi(v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const uint32_t a = kw[0][i], a8 = a >> 8, d = kw[1][i], d8 = d >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4] = {start[nt][i][0], start[nt][i][1], start[nt][i][0], start[nt][i][1]};
+          mma_f16(acc, a & 0x000f000fu, d & 0x000f000fu, a & 0x00f000f0u, d & 0x00f000f0u, qf[nt][2 * i][0], qf[nt][2 * i][1], acc);
+          mma_f16(acc, a8 & 0x000f000fu, d8 & 0x000f000fu, a8 & 0x00f000f0u, d8 & 0x00f000f0u, qf[nt][2 * i + 1][0],
+                  qf[nt][2 * i + 1][1], acc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[half][nt][e] = i == 0 ? ks[e >> 1][0] * acc[e] : s[half][nt][e] + ks[e >> 1][i] * acc[e];
+        }
       }
     }
-    float s[NT][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[half][nt][e] *= f[nt][e & 1];
+    if (!whole(j0)) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (!seen(j0 + key + 8 * u + 16 * half))
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[half][nt][2 * u] = s[half][nt][2 * u + 1] = -INFINITY;
+    }
+    bool rise = false;
+    float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const uint32_t a = kw[0][i], a8 = a >> 8, d = kw[1][i], d8 = d >> 8;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float acc[4] = {start[nt][i][0], start[nt][i][1], start[nt][i][0], start[nt][i][1]};
-        mma_f16(acc, a & 0x000f000fu, d & 0x000f000fu, a & 0x00f000f0u, d & 0x00f000f0u, qf[nt][2 * i][0], qf[nt][2 * i][1], acc);
-        mma_f16(acc, a8 & 0x000f000fu, d8 & 0x000f000fu, a8 & 0x00f000f0u, d8 & 0x00f000f0u, qf[nt][2 * i + 1][0],
-                qf[nt][2 * i + 1][1], acc);
-        s[nt][0] += ks[0][i] * acc[0];
-        s[nt][1] += ks[0][i] * acc[1];
-        s[nt][2] += ks[1][i] * acc[2];
-        s[nt][3] += ks[1][i] * acc[3];
+      for (int e = 0; e < 2; ++e) {
+        top[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+        rise = rise || top[nt][e] > m[nt][e] + 8.f;
       }
-    }
-    const bool edge = j0 + kTileKeys > len || (j0 < w0 && j0 + kTileKeys > p.sinks);
-    const bool see0 = !edge || seen(j0 + key), see1 = !edge || seen(j0 + key + 8);
-    bool rise = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = (e < 2 ? see0 : see1) ? s[nt][e] * f[nt][e & 1] : -INFINITY;
-      rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
-    }
     if (__any_sync(0xffffffffu, rise)) {  // some head's reference maximum moves: rarely after the first tiles
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(s[nt][e], s[nt][e + 2]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float m_new = fmaxf(m[nt][e], top), alpha = ex2(m[nt][e] - m_new);
+          float mx = top[nt][e];
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float m_new = fmaxf(m[nt][e], mx), alpha = ex2(m[nt][e] - m_new);
           m[nt][e] = m_new;
           l[nt][e] *= alpha;
 #pragma unroll
@@ -519,57 +567,59 @@ __global__ void __launch_bounds__(kAttnThreads4) k_cache4_attn(const __grid_cons
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = ex2(s[nt][e] - m[nt][e & 1]);
-      l[nt][0] += s[nt][0] + s[nt][2];
-      l[nt][1] += s[nt][1] + s[nt][3];
-    }
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[half][nt][e] = ex2(s[half][nt][e] - m[nt][e & 1]);
+        l[nt][0] += s[half][nt][0] + s[half][nt][2];
+        l[nt][1] += s[half][nt][1] + s[half][nt][3];
+      }
     // ---- values ----
-    float vs[2][G];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t *at = st + C::kVs + (key + 8 * u) * 2 * G;
-      if (G == 4) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(at);
-        vs[u][0] = bf16_lo(w.x), vs[u][1] = bf16_hi(w.x), vs[u][2 % G] = bf16_lo(w.y), vs[u][3 % G] = bf16_hi(w.y);
-      } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(at);
-        vs[u][0] = bf16_lo(w), vs[u][1] = bf16_hi(w);
+    for (int half = 0; half < 2; ++half) {
+      float vs[2][G];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t *at = st + C::kVs + (key + 8 * u + 16 * half) * 2 * G;
+        if (G == 4) {
+          const uint2 w = *reinterpret_cast<const uint2 *>(at);
+          vs[u][0] = bf16_lo(w.x), vs[u][1] = bf16_hi(w.x), vs[u][2 % G] = bf16_lo(w.y), vs[u][3 % G] = bf16_hi(w.y);
+        } else {
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(at);
+          vs[u][0] = bf16_lo(w), vs[u][1] = bf16_hi(w);
+        }
+      }
+      uint32_t vw[4][G / 2];  // rows c, c + 4, c + 8, c + 12: keys 2c, 2c + 1, 2c + 8, 2c + 9 of the product
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint8_t *at = st + C::kV + c * C::kRow + (4 * u + 16 * half) * C::kRow + C::v_in(c, r * 2 * G);
+        if (G == 4) {
+          const uint2 w = *reinterpret_cast<const uint2 *>(at);
+          vw[u][0] = w.x, vw[u][G / 2 - 1] = w.y;
+        } else {
+          vw[u][0] = *reinterpret_cast<const uint32_t *>(at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pb[nt][0] = turn8x8(pack_bf16(s[half][nt][0] * vs[0][i], s[half][nt][1] * vs[0][i]));
+          pb[nt][1] = turn8x8(pack_bf16(s[half][nt][2] * vs[1][i], s[half][nt][3] * vs[1][i]));
+        }
+        const uint32_t lo = __byte_perm(vw[0][i >> 1], vw[1][i >> 1], i & 1 ? 0x7632 : 0x5410);
+        const uint32_t hi = __byte_perm(vw[2][i >> 1], vw[3][i >> 1], i & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = bf16_codes(lo >> (8 * h)), a1 = bf16_codes(lo >> (8 * h + 4));
+          const uint32_t a2 = bf16_codes(hi >> (8 * h)), a3 = bf16_codes(hi >> (8 * h + 4));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf(o[nt][2 * i + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
       }
     }
-    uint32_t vw[4][G / 2];  // rows c, c + 4, c + 8, c + 12: keys 2c, 2c + 1, 2c + 8, 2c + 9 of the product
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = c + 4 * u;
-      if (G == 4) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(st + C::kV + row * C::kRow + ((r * 8) ^ ((row >> 1 & 1) * 32)));
-        vw[u][0] = w.x, vw[u][G / 2 - 1] = w.y;
-      } else {
-        vw[u][0] = *reinterpret_cast<const uint32_t *>(st + C::kV + row * C::kRow + r * 4);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        pb[nt][0] = turn8x8(pack_bf16(s[nt][0] * vs[0][i], s[nt][1] * vs[0][i]));
-        pb[nt][1] = turn8x8(pack_bf16(s[nt][2] * vs[1][i], s[nt][3] * vs[1][i]));
-      }
-      const uint32_t lo = __byte_perm(vw[0][i >> 1], vw[1][i >> 1], i & 1 ? 0x7632 : 0x5410);
-      const uint32_t hi = __byte_perm(vw[2][i >> 1], vw[3][i >> 1], i & 1 ? 0x7632 : 0x5410);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t a0 = bf16_codes(lo >> (8 * h)), a1 = bf16_codes(lo >> (8 * h + 4));
-        const uint32_t a2 = bf16_codes(hi >> (8 * h)), a3 = bf16_codes(hi >> (8 * h + 4));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf(o[nt][2 * i + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-      }
-    }
-    __syncwarp();  // every lane has read the stage that is filled next
-    fetch(t + (kStages - 1) * kAttnWarps, stage == 0 ? kStages - 1 : stage - 1);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_wait<0>();
 
@@ -668,13 +718,34 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
     if (some < tiles) tiles = some;
   }
   const long long units = batch * d.num_kv_heads * s.head_tiles;
-  // 64 tiles (1024 keys) a CTA, halved while the SMs could take twice the CTAs, down to 2 tiles a warp
-  s.chunk = 64;
-  while (s.chunk > 2 * kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 4LL * num_sms()) s.chunk /= 2;
+  // 32 tiles (1024 keys) a CTA, halved while the SMs could take twice the CTAs, down to a tile a warp
+  s.chunk = 32;
+  while (s.chunk > kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 4LL * num_sms()) s.chunk /= 2;
   // at most 64 splits a sequence
   while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
   s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
   return s;
+}
+
+template <int D, int NT>
+tp_status launch_attn4(const Attn4Params &p, dim3 grid, cudaStream_t s) {
+  static std::mutex mu;
+  static unsigned mask = 0;
+  constexpr int kSmem = attn4_smem<D, NT>();
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev >= 32 || !(mask & (1u << dev))) {
+      e = cudaFuncSetAttribute(k_cache4_attn<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e == cudaSuccess)  // room for as many CTAs as the registers hold
+        e = cudaFuncSetAttribute(k_cache4_attn<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return cuda_fail(e);
+      if (dev < 32) mask |= 1u << dev;
+    }
+  }
+  return launched(launch_kernel(k_cache4_attn<D, NT>, grid, dim3(kAttnThreads4), kSmem, s, 1, p));
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -751,6 +822,7 @@ tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t 
       p.ld[w][r] = t.ld;
     }
   const long long rows = batch * n;
+  if (n * g.dims.num_kv_heads > 0x7fffffffLL - 1024 || batch > 65535) return TP_ERR_UNSUPPORTED;
   if (rows > 0 && !starts) return TP_ERR_INVALID_ARG;
   if (!ptr_aligned(starts, 4)) return TP_ERR_ALIGNMENT;
   tp_status st = check_rank_health(g.n);
@@ -765,9 +837,8 @@ tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t 
   p.heads_kv = g.dims.num_kv_heads;
   p.heads_per_source = static_cast<int>(g.heads);
   p.status = ctx.status;
-  const long long per = kCopyThreads / (g.hd / 8) * kCopyRows, blocks = (rows * p.heads_kv + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return TP_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks), 2);
+  const long long per = kCopyThreads / (g.hd / 8) * kCopyRows, blocks = (n * p.heads_kv + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(blocks), 2, static_cast<unsigned>(batch));
   if (store) return launched(launch_kernel(g.hd == 128 ? k_cache4_store<128> : k_cache4_store<64>, grid, dim3(kCopyThreads), 0, s, 1, p));
   if (dt == TP_F32)
     return launched(launch_kernel(g.hd == 128 ? k_cache4_load<128, float> : k_cache4_load<64, float>, grid, dim3(kCopyThreads), 0, s, 1, p));
@@ -866,9 +937,8 @@ extern "C" tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp
   p.status = ctx.status;
   cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(batch * p.heads_kv), static_cast<unsigned>(p.splits), static_cast<unsigned>(s.head_tiles));
-  auto kernel = g.hd == 128 ? (s.nt == 2 ? k_cache4_attn<128, 2> : k_cache4_attn<128, 1>)
-                            : (s.nt == 2 ? k_cache4_attn<64, 2> : k_cache4_attn<64, 1>);
-  st = launched(launch_kernel(kernel, grid, dim3(kAttnThreads4), 0, str, 1, p));
+  st = g.hd == 128 ? (s.nt == 2 ? launch_attn4<128, 2>(p, grid, str) : launch_attn4<128, 1>(p, grid, str))
+                   : (s.nt == 2 ? launch_attn4<64, 2>(p, grid, str) : launch_attn4<64, 1>(p, grid, str));
   if (st != TP_OK || s.splits < 2) return st;
   return launched(launch_kernel(g.hd == 128 ? k_cache4_join<128> : k_cache4_join<64>, dim3(static_cast<unsigned>((rows + 7) / 8)),
                                 dim3(256), 0, str, 1, p));

@@ -50,12 +50,35 @@ struct Cache4 {
   __nv_bfloat16 *k_scale[kC4Ranks], *v_scale[kC4Ranks];
 };
 
+// The codes at bits 0-3 and 16-19 of w, less 8, as a bf16 pair: 0x4300 | code is 128 + code, and 136 goes off
+// exactly.
+__device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w));  // (w & a) | b
+  const uint32_t off = 0xc308c308u;  // -136 twice
+  const __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&r), *reinterpret_cast<const __nv_bfloat162 *>(&off));
+  return *reinterpret_cast<const uint32_t *>(&x);
+}
+
 // ---------------------------------------------------------------------------
 // Storing and reading back. A thread has 8 neighbouring values (16 bytes of bf16): four threads a
 // group. Bound by memory.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 4;  // rows (token and head) in flight a thread
+
+// Division by a number that the host knows: x / d = (umulhi(x, mul) + x) >> shift for x < 2^31.
+struct Divider {
+  uint32_t mul, shift;
+  __host__ void set(uint32_t d) {
+    shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int of(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
+  }
+};
 
 struct CopyParams {
   Cache4 cache;
@@ -64,6 +87,7 @@ struct CopyParams {
   long long ld[2][kC4Ranks];
   const int *starts, *counts;
   int batch, n, cap, heads_kv, heads_per_source;
+  Divider by_heads, by_source;
   int *status;
 };
 
@@ -80,19 +104,54 @@ struct RowAt {
 };
 __device__ __forceinline__ RowAt row_at(int row, const CopyParams &p) {
   RowAt r;
-  r.i = row / p.heads_kv;
+  r.i = p.by_heads.of(row);
   const int kv = row - r.i * p.heads_kv;
-  r.src = kv / p.heads_per_source;
+  r.src = p.by_source.of(kv);
   r.h = kv - r.src * p.heads_per_source;
   return r;
 }
 
-// round(x / s) as the quotient rounded to f32 would give it, which the definition asks for and a
-// product with r = 1 / s does not where x / s lies halfway between two codes: one step of
-// Newton's method on the product's remainder gives the rounded quotient.
+// x / s rounded to f32, which the definition asks for and a product with r = 1 / s does not give where
+// x / s lies halfway between two codes: one step of Newton's method on the product's remainder.
 __device__ __forceinline__ float rounded_quotient(float x, float s, float r) {
   const float q = x * r;
-  return rintf(fmaf(fmaf(-q, s, x), r, q));
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The 8 codes of 8 bf16 values and their group's scale (the four threads of a group together).
+__device__ __forceinline__ uint32_t encode(const uint32_t (&w)[4], __nv_bfloat16 *scale_out) {
+  // the largest size as bf16 bits, in whose order infinities and then NaN come last
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t bits = max(m & 0xffffu, m >> 16);
+  const float top = __uint_as_float(bits << 16);
+  // values near f32's smallest have no reciprocal: the group goes up by 2^80
+  const bool tiny = top < 0x1p-60f;
+  const float lift = tiny ? 0x1p80f : 1.f;
+  float q7 = rounded_quotient(top * lift, 7.f, 1.f / 7.f);
+  if (tiny) q7 *= 0x1p-80f;
+  if (bits >= 0x7f80u) q7 = NAN;
+  const __nv_bfloat16 scale = __float2bfloat16_rn(q7);
+  *scale_out = scale;
+  float s = __bfloat162float(scale) * lift, r = rcp_approx(s);
+  if (!(s > 0.f)) s = r = 0.f;  // all codes 8
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float c = rounded_quotient((i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * lift, s, r);
+    if (tiny) c = fminf(fmaxf(c, -8.f), 7.f);  // elsewhere |c| < 7.1: a scale is off by 2^-8 at most
+    // 1.5 * 2^23 + 8 + c rounds c to even and has the code in its low bits; what it has above them
+    // adds up to a constant over the eight
+    codes += __float_as_uint(c + 12582920.f) << (4 * i);
+  }
+  constexpr uint32_t kHigh = 0x4b400000u;  // 1.5 * 2^23
+  return codes - kHigh * 0x11111111u;
 }
 
 template <int D>
@@ -130,28 +189,8 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_cons
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
     const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-    float x[8], top = 0.f;
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-      top = fmaxf(top, fabsf(x[i]));
-      finite = finite && fabsf(x[i]) <= FLT_MAX;
-    }
-    if (!finite) top = INFINITY;
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const __nv_bfloat16 scale = __float2bfloat16_rn(top <= FLT_MAX ? __fdiv_rn(top, 7.f) : NAN);
-    // scales near f32's smallest have no reciprocal: they and the values go up by 2^80
-    const float lift = __bfloat162float(scale) < 0x1p-60f ? 0x1p80f : 1.f;
-    const float s = __bfloat162float(scale) * lift, inv = __frcp_rn(s);
-    uint32_t codes = 0;  // 8 codes, the first in the low bits
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = s > 0.f ? fminf(fmaxf(rounded_quotient(x[i] * lift, s, inv), -8.f), 7.f) : 0.f;
-      // the integer in the low bits of 1.5 * 2^23 + c
-      codes |= ((__float_as_uint(c + 12582920.f)) & 15u) << (4 * i);
-    }
+    __nv_bfloat16 scale;
+    const uint32_t codes = encode(w, &scale);
     const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);  // the same part of the neighbour group
     if (to[u] < 0) continue;
     if (part == 0) (which ? p.cache.v_scale : p.cache.k_scale)[src[u]][to[u] * G + group] = scale;
@@ -182,21 +221,21 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_const
   if ((start < 0 || start > p.cap) && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
   const int there = start >= 0 ? p.cap - start : 0;  // positions that exist; the others are zeros
   uint32_t codes[kCopyRows];
-  float scale[kCopyRows];
+  __nv_bfloat16 scale[kCopyRows];
   T *dst[kCopyRows];
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
     const int row = r0 + u * kRows;
     dst[u] = nullptr;
     codes[u] = 0x88888888u;
-    scale[u] = 0.f;
+    scale[u] = __float2bfloat16_rn(0.f);
     if (row >= rows) continue;
     const RowAt r = row_at(row, p);
     const long long token = static_cast<long long>(b) * p.n + r.i;
     dst[u] = static_cast<T *>(p.out[which][r.src]) + token * p.ld[which][r.src] + r.h * D + at * 8;
     if (r.i >= there) continue;
     const long long from = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
-    scale[u] = __bfloat162float((which ? p.cache.v_scale : p.cache.k_scale)[r.src][from * G + group]);
+    scale[u] = (which ? p.cache.v_scale : p.cache.k_scale)[r.src][from * G + group];
     const uint8_t *bytes = (which ? p.cache.v_codes : p.cache.k_codes)[r.src] + from * (D / 2);
     if (which == 0) {
       codes[u] = *reinterpret_cast<const uint32_t *>(bytes + k_byte<G>(group, part));
@@ -209,14 +248,22 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_const
 #pragma unroll
   for (int u = 0; u < kCopyRows; ++u) {
     if (!dst[u]) continue;
-    float x[8];
+    uint32_t pr[4];  // codes i and i + 4, less 8, as bf16 (exact)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(static_cast<int>(codes[u] >> (4 * i) & 15u) - 8) * scale[u];
+    for (int i = 0; i < 4; ++i) pr[i] = bf16_codes(codes[u] >> (4 * i));
     if (sizeof(T) == 4) {
-      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(x[4], x[5], x[6], x[7]);
+      const float s = __bfloat162float(scale[u]);
+      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(bf16_lo(pr[0]) * s, bf16_lo(pr[1]) * s, bf16_lo(pr[2]) * s, bf16_lo(pr[3]) * s);
+      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(bf16_hi(pr[0]) * s, bf16_hi(pr[1]) * s, bf16_hi(pr[2]) * s, bf16_hi(pr[3]) * s);
     } else {
-      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      const __nv_bfloat162 s = __bfloat162bfloat162(scale[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // one rounding of the product
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pr[i]), s);
+        pr[i] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(__byte_perm(pr[0], pr[1], 0x5410), __byte_perm(pr[2], pr[3], 0x5410),
+                                                      __byte_perm(pr[0], pr[1], 0x7632), __byte_perm(pr[2], pr[3], 0x7632));
     }
   }
 }
@@ -300,15 +347,6 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Four codes in the low nibbles of w's halves (after a shift) as f16 pairs' or bf16 pairs' bits.
-__device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {  // the pair of codes at bits 0-3 and 16-19, less 8
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w));  // (w & a) | b
-  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0xc308), __ushort_as_bfloat16(0xc308));  // -136
-  const __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&r), off);
-  return *reinterpret_cast<const uint32_t *>(&x);
-}
-
 template <int D>
 struct Attn4Cfg {
   static constexpr int kG = D / kGroup;
@@ -332,7 +370,7 @@ constexpr int attn4_smem() {
 
 // NT: products of 8 heads a key fragment serves (the CTA has up to 8 NT heads of the group).
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(const __grid_constant__ Attn4Params p) {
+__global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(const __grid_constant__ Attn4Params p) {
   using C = Attn4Cfg<D>;
   constexpr int G = C::kG;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -467,7 +505,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
   float m[NT][2], l[NT][2], o[NT][2 * G][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -FLT_MAX;
+    m[nt][0] = m[nt][1] = 0.f;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i)
@@ -523,12 +561,13 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
         }
       }
     }
+    // less the reference maximum, in log2 units: p = 2^s
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[half][nt][e] *= f[nt][e & 1];
+        for (int e = 0; e < 4; ++e) s[half][nt][e] = fmaf(s[half][nt][e], f[nt][e & 1], -m[nt][e & 1]);
     if (!whole(j0)) {
 #pragma unroll
       for (int half = 0; half < 2; ++half)
@@ -538,14 +577,16 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[half][nt][2 * u] = s[half][nt][2 * u + 1] = -INFINITY;
     }
-    bool rise = false;
+    // the maximum of the warp's first tile is the first reference; a tile always has a key that is seen
+    const bool first = t == t0 + warp;
+    bool rise = first;
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         top[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
-        rise = rise || top[nt][e] > m[nt][e] + 8.f;
+        rise = rise || top[nt][e] > 8.f;
       }
     if (__any_sync(0xffffffffu, rise)) {  // some head's reference maximum moves: rarely after the first tiles
 #pragma unroll
@@ -556,9 +597,14 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float m_new = fmaxf(m[nt][e], mx), alpha = ex2(m[nt][e] - m_new);
-          m[nt][e] = m_new;
+          const float up = fmaxf(mx, first ? -FLT_MAX : 0.f), alpha = first ? 1.f : ex2(-up);
+          m[nt][e] += up;
           l[nt][e] *= alpha;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            s[half][nt][e] -= up;
+            s[half][nt][e + 2] -= up;
+          }
 #pragma unroll
           for (int i = 0; i < 2 * G; ++i) {
             o[nt][i][e] *= alpha;
@@ -571,7 +617,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[half][nt][e] = ex2(s[half][nt][e] - m[nt][e & 1]);
+        for (int e = 0; e < 4; ++e) s[half][nt][e] = ex2(s[half][nt][e]);
         l[nt][0] += s[half][nt][0] + s[half][nt][2];
         l[nt][1] += s[half][nt][1] + s[half][nt][3];
       }
@@ -630,7 +676,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 4 : 2) k_cache4_attn(
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int x = 4; x < 32; x *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
-      if (r == 0) s_ml[warp][8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
+      if (r == 0) s_ml[warp][8 * nt + 2 * c + e] = make_float2(t0 + warp < t1 ? m[nt][e] : -FLT_MAX, l[nt][e]);
     }
   __syncthreads();  // the rings are free
   float *sums = reinterpret_cast<float *>(smem);
@@ -718,9 +764,9 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
     if (some < tiles) tiles = some;
   }
   const long long units = batch * d.num_kv_heads * s.head_tiles;
-  // 32 tiles (1024 keys) a CTA, halved while the SMs could take twice the CTAs, down to a tile a warp
-  s.chunk = 32;
-  while (s.chunk > kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 4LL * num_sms()) s.chunk /= 2;
+  // 128 tiles (4096 keys) a CTA, halved while there are fewer than three CTAs an SM, down to a tile a warp
+  s.chunk = 128;
+  while (s.chunk > kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 3LL * num_sms()) s.chunk /= 2;
   // at most 64 splits a sequence
   while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
   s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
@@ -836,6 +882,8 @@ tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t 
   p.cap = static_cast<int>(g.cap);
   p.heads_kv = g.dims.num_kv_heads;
   p.heads_per_source = static_cast<int>(g.heads);
+  p.by_heads.set(p.heads_kv);
+  p.by_source.set(p.heads_per_source);
   p.status = ctx.status;
   const long long per = kCopyThreads / (g.hd / 8) * kCopyRows, blocks = (n * p.heads_kv + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(blocks), 2, static_cast<unsigned>(batch));

@@ -5,23 +5,27 @@
 // All query rows of a kv head (T tokens x G heads of its group, token by token) read the same K
 // and V, so they are packed into tiles of 128 rows: 128 / G tokens a tile, which move the
 // window by that little, and every K and V tile serves the whole group. A work item is (kv
-// head, pair of adjacent row tiles, key split); it visits the 128-key blocks that some row
-// of the pair sees, those of the first tokens and then those of the window, and none between. Masks
-// are applied in the blocks where a row's limits lie.
+// head, pair of adjacent row tiles, key split). Its keys are two runs, the pair's window from its first
+// row's first key on and the first tokens before it, each in units of 16 keys; blocks are 8
+// neighbouring units of the two runs together, so that only the last one is short (its products are
+// as narrow as it is) and a few first tokens cost a unit, not a block. Masks are applied
+// in the blocks where a row's limits lie.
 //
 // k_window's roles (one CTA an SM, persistent):
-//   warp 0     TMA: lane 0 the K ring, lane 1 the V ring (two 128-key stages each);
-//   warp 1     MMA issuer (tcgen05): S_A, S_B, P_A V, S_A of the next block, P_B V, ...;
-//   warps 2-5  softmax of tile A, 6-9 of tile B, one thread a row; they also gather their q
-//              rows into the swizzled Q tile (a row is a token's head, which no one tensor
-//              map covers when a group lies on several ranks) and store the output.
+//   warp 0        TMA: lane 0 the K ring, lane 1 the V ring (two 128-key stages each);
+//   warp 1        MMA issuer (tcgen05): S_A, S_B, P_A V, S_A of the next block, P_B V, ..., over
+//                 the items' ends: the next item's first S follows this one's last P V;
+//   warps 4-7     softmax of tile A, 8-11 of tile B, one thread a row; they store the output;
+//   warps 2, 3    gather the q rows of tile A and B of the next item into the swizzled Q tile (a row is
+//                 a token's head, which no one tensor map covers when a group lies on several
+//                 ranks) as soon as this item's last S has read it.
 // TMEM: S of A at columns 0, of B at 128 (P overwrites its first half as bf16 and is read from
 // there), O at 256 and 384. V is used as it lies, [keys x d], as an MN-major operand.
 // The reference maximum m of a row is found on its item's first block and moves later only when
 // a block's sum of p passes 2^64 or is not finite, as when the row's first keys were masked:
 // m is then f32's lowest value, the masked keys weigh 0, and the first key that is seen moves m.
 //
-// Where there are too few items for the SMs (few tokens), the key blocks of an item are
+// Where there are too few items for the SMs (few tokens), the blocks of an item are
 // split, the splits leave f32 sums, and k_window_join joins them.
 #include <cfloat>
 #include <cmath>
@@ -38,7 +42,11 @@ namespace {
 using namespace op;
 
 constexpr int kWinRanks = 32;
-constexpr int kWinThreads = 320;
+constexpr int kWinThreads = 384;
+// Registers a thread: 168 at launch; the softmax's warpgroups take what the first one gives up
+// (128 * (104 + 2 * 200) of 384 * 168).
+constexpr int kRegsOthers = 104, kRegsSoftmax = 200;
+static_assert(kRegsOthers + 2 * kRegsSoftmax <= 3 * 168, "the split fits the launch's registers");
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
 constexpr float kSumLimit = 0x1p64f;
 
@@ -58,25 +66,25 @@ struct WindowParams {
   long long a_ld[kWinRanks];
 };
 struct WindowMaps {
-  CUtensorMap k[kWinRanks], v[kWinRanks];
+  CUtensorMap k[kWinRanks], v[kWinRanks];      // boxes of 128 keys
+  CUtensorMap k16[kWinRanks], v16[kWinRanks];  // of 16, for blocks of both runs
 };
 
-// The key blocks of a pair of row tiles: sink_blocks from block 0 on, then the rest from `first` on.
-struct Blocks {
-  int sink_blocks, first, count;
-  __host__ __device__ int at(int j) const { return j < sink_blocks ? j : j - sink_blocks + first; }
+// The keys of a pair of row tiles in units of 16: the window run (w_units units from key w0 on), then the
+// first tokens (units from key 0 on, keys below `sinks`, which end before w0).
+struct Keys {
+  int w0, w_units, sinks, units, blocks;
 };
-__host__ __device__ inline Blocks blocks_of(int pair, int rows, int group, int tokens, int keys, int window, int sinks) {
+__host__ __device__ inline Keys keys_of(int pair, int rows, int group, int tokens, int keys, int window, int sinks) {
   const int last = 256 * pair + 255 < rows ? 256 * pair + 255 : rows - 1;
   const int p0 = keys - tokens + 256 * pair / group, p1 = keys - tokens + last / group;
-  const int w0 = p0 >= window ? p0 - window + 1 : 0;  // first key of the first row's window
-  Blocks b;
-  b.first = w0 / 128;
-  const int s = sinks < w0 ? sinks : w0;
-  const int sb = (s + 127) / 128;
-  b.sink_blocks = sb < b.first ? sb : b.first;
-  b.count = b.sink_blocks + p1 / 128 - b.first + 1;
-  return b;
+  Keys k;
+  k.w0 = p0 >= window ? p0 - window + 1 : 0;  // first key of the first row's window
+  k.w_units = (p1 - k.w0) / 16 + 1;
+  k.sinks = sinks < k.w0 ? sinks : k.w0;
+  k.units = k.w_units + (k.sinks + 15) / 16;
+  k.blocks = (k.units + 7) / 8;
+  return k;
 }
 
 __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
@@ -111,9 +119,12 @@ template <int D>
 struct WinCfg {
   static constexpr int kCh = D / 64;                 // 64-column sub-tiles of a head
   static constexpr uint32_t kTile = kCh * kSubTile;  // a [128 x D] tile
-  static constexpr uint32_t kK = 2 * kTile, kV = 4 * kTile, kBar = 6 * kTile;
+  static constexpr uint32_t kK = 2 * kTile, kV = 4 * kTile, kOut = 6 * kTile, kBar = kOut + 8 * 4096;
   static constexpr size_t kSmem = kBar + 256 + 1024;
 };
+
+// n low bits, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 template <int D>
 __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant__ WindowParams p, const __grid_constant__ WindowMaps maps) {
@@ -125,38 +136,49 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
   uint8_t *bar_area = smem + C::kBar;
   const uint32_t bar0 = ptx::smem_addr(bar_area);
   const uint32_t q_full0 = bar0, k_full0 = bar0 + 16, k_empty0 = bar0 + 32, v_full0 = bar0 + 48, v_empty0 = bar0 + 64,
-                 s_full0 = bar0 + 80, p_full0 = bar0 + 96, o_full0 = bar0 + 112, o_free0 = bar0 + 128, drain = bar0 + 144;
-  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 152);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 156);
+                 s_full0 = bar0 + 80, p_full0 = bar0 + 96, o_full0 = bar0 + 112, o_free0 = bar0 + 128, q_empty0 = bar0 + 144,
+                 drain = bar0 + 160;
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 168);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 172);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.rows;
   const int items = p.heads_kv * p.pairs * p.split;
-  // This CTA's r-th item in snake order over the CTAs, so that with the longest items first
-  // (an open window's last tokens) every CTA's total stays close to the mean; -1 past the last.
-  auto rank_of = [&](int r) {
-    const int pos = (r & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
-    const long long k = static_cast<long long>(r) * gridDim.x + pos;
-    return k < items ? static_cast<int>(k) : -1;
+  // An item: (kv head, tile pair, split) and its part [j0, j1) of the pair's blocks.
+  struct Item {
+    int kv, pair, split, j0, j1;
+    Keys k;
+    __device__ int units(int j) const { return min(8, k.units - 8 * j); }
   };
-  // item -> (kv head, tile pair, split, its part [j0, j1) of the pair's blocks)
-  auto item = [&](int it, int &kv, int &pair, int &split, Blocks &b, int &j0, int &j1) {
-    split = it % p.split;
-    const int r = it / p.split;
-    kv = r % p.heads_kv;
-    pair = p.pairs - 1 - r / p.heads_kv;
-    b = blocks_of(pair, rows, p.group, p.tokens, p.keys, p.window, p.sinks);
-    const int n = min(p.split, b.count);
-    j0 = j1 = 0;  // more splits than blocks: the last ones have none
-    if (split < n) {
-      j0 = static_cast<int>(static_cast<long long>(b.count) * split / n);
-      j1 = static_cast<int>(static_cast<long long>(b.count) * (split + 1) / n);
+  // This CTA's r-th item in snake order over the CTAs, so that with the longest items first
+  // (an open window's last tokens) every CTA's total stays close to the mean; those without a block
+  // (more splits than blocks) are passed over. False past the last.
+  auto next_item = [&](int &r, Item &it) {
+    for (;; ++r) {
+      const int at = (r & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+      const long long i = static_cast<long long>(r) * gridDim.x + at;
+      if (static_cast<long long>(r) * gridDim.x >= items) return false;
+      if (i >= items) continue;
+      const int first = static_cast<int>(i) / p.split;
+      it.split = static_cast<int>(i) - first * p.split;
+      it.pair = first / p.heads_kv;
+      it.kv = first - it.pair * p.heads_kv;
+      it.pair = p.pairs - 1 - it.pair;
+      it.k = keys_of(it.pair, rows, p.group, p.tokens, p.keys, p.window, p.sinks);
+      const int n = min(p.split, it.k.blocks);
+      if (it.split >= n) continue;
+      it.j0 = static_cast<int>(static_cast<long long>(it.k.blocks) * it.split / n);
+      it.j1 = static_cast<int>(static_cast<long long>(it.k.blocks) * (it.split + 1) / n);
+      ++r;
+      return true;
     }
   };
+  auto tiles_of = [&](const Item &it) { return (2 * it.pair + 1) * 128 < rows ? 2 : 1; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(q_full0 + 8 * s, 128);
+      ptx::mbar_init(q_full0 + 8 * s, 32);
+      ptx::mbar_init(q_empty0 + 8 * s, 1);
       ptx::mbar_init(k_full0 + 8 * s, 1);
       ptx::mbar_init(k_empty0 + 8 * s, 1);
       ptx::mbar_init(v_full0 + 8 * s, 1);
@@ -182,20 +204,21 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
   ptx::griddep_launch_dependents();
 
   int issued[2] = {0, 0};
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
   if (warp == 0) {
     if (lane < 2) {
       const uint32_t full0 = lane == 0 ? k_full0 : v_full0, empty0 = lane == 0 ? k_empty0 : v_empty0;
       const uint32_t dst0 = lane == 0 ? sK0 : sV0;
       bool run = true;
       int g = 0;
-      for (int r = 0, it = rank_of(0); run && it >= 0; it = rank_of(++r)) {
-        int kv, pair, split, j0, j1;
-        Blocks b;
-        item(it, kv, pair, split, b, j0, j1);
-        const int src = p.one_map ? 0 : kv / p.heads_per_source;
-        const int col = (kv - src * p.heads_per_source) * D;
+      Item it;
+      for (int r = 0; run && next_item(r, it);) {
+        const int src = p.one_map ? 0 : it.kv / p.heads_per_source;
+        const int col = (it.kv - src * p.heads_per_source) * D;
         const CUtensorMap *map = lane == 0 ? &maps.k[src] : &maps.v[src];
-        for (int j = j0; j < j1; ++j, ++g) {
+        const CUtensorMap *map16 = lane == 0 ? &maps.k16[src] : &maps.v16[src];
+        for (int j = it.j0; j < it.j1; ++j, ++g) {
           const int s = g & 1;
           if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * s, ((g >> 1) & 1) ^ 1, p.wait_ns)) {
             if (!*abort_flag) record(p.status, kDevTimeoutProducer);
@@ -203,16 +226,29 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
             run = false;
             break;
           }
-          ptx::mbar_arrive_expect_tx(full0 + 8 * s, C::kTile);
-          for (int c = 0; c < C::kCh; ++c)
-            ptx::tma_load_2d(dst0 + s * C::kTile + c * kSubTile, map, col + c * 64, b.at(j) * 128, full0 + 8 * s);
+          const int n = it.units(j), w = min(8, it.k.w_units - 8 * j);  // units of the block; of the window run
+          const uint32_t dst = dst0 + s * C::kTile;
+          if (w > 0 && w < n) {  // of both runs: unit by unit
+            ptx::mbar_arrive_expect_tx(full0 + 8 * s, n * 2048u * C::kCh);
+            for (int u = 0; u < n; ++u) {
+              const int key = u < w ? it.k.w0 + 128 * j + 16 * u : 128 * j - 16 * it.k.w_units + 16 * u;
+              for (int c = 0; c < C::kCh; ++c)
+                ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map16, col + c * 64, key, full0 + 8 * s);
+            }
+          } else {
+            ptx::mbar_arrive_expect_tx(full0 + 8 * s, C::kTile);
+            const int key = w > 0 ? it.k.w0 + 128 * j : 128 * j - 16 * it.k.w_units;
+            for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, full0 + 8 * s);
+          }
           ++issued[s];
         }
       }
     }
   } else if (warp == 1) {  // converged; one lane issues (see elect_one)
-    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_s0 = ptx::idesc_bf16_f32(128, 0);  // + 2 units << 17: 16 columns a unit
     constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+    // descriptors of the tiles' starts; the address field counts 16 bytes
+    const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sK0), vd = desc_mn_sw128(sV0, kSubTile);
     const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -225,66 +261,91 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       if (leader) ptx::mma_commit(bar);
       __syncwarp();
     };
-    auto issue_s = [&](int x, int g) {  // S_X = Q_X K^T
-      const uint32_t qa = sQ + static_cast<uint32_t>(x) * C::kTile, ka = sK0 + static_cast<uint32_t>(g & 1) * C::kTile;
+    auto issue_s = [&](int x, int g, int n) {  // S_X = Q_X K^T, 16 n columns
+      const uint64_t qa = qd + static_cast<uint32_t>(x) * (C::kTile >> 4), ka = kd + static_cast<uint32_t>(g & 1) * (C::kTile >> 4);
       const uint32_t d = tmem + static_cast<uint32_t>(x * 128);
+      const uint32_t idesc = idesc_s0 + (static_cast<uint32_t>(2 * n) << 17);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_bf16(d, ptx::smem_desc_sw128(qa + (kk >> 2) * kSubTile) + 2 * (kk & 3),
-                        ptx::smem_desc_sw128(ka + (kk >> 2) * kSubTile) + 2 * (kk & 3), idesc_s, kk > 0 ? 1u : 0u);
+          ptx::mma_bf16(d, qa + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)), ka + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)),
+                        idesc, kk > 0 ? 1u : 0u);
         ptx::mma_commit(s_full0 + 8 * x);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int x, int g, bool first) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
-      const uint32_t va = sV0 + static_cast<uint32_t>(g & 1) * C::kTile;
+    auto issue_pv = [&](int x, int g, bool first, int n) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
+      const uint64_t va = vd + static_cast<uint32_t>(g & 1) * (C::kTile >> 4);
       const uint32_t d = tmem + 256u + static_cast<uint32_t>(x * 128), a = tmem + static_cast<uint32_t>(x * 128);
       const uint32_t more = first ? 0u : 1u;
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_bf16_ts(d, a + 8u * kk, desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, kk > 0 ? 1u : more);
+          if (kk < n) ptx::mma_bf16_ts(d, a + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
       }
       __syncwarp();
     };
-    int g = 0;
+    int g = 0, r = 0;
     uint32_t np[2] = {0, 0}, nact[2] = {0, 0};
-    for (int r = 0, it = rank_of(0); ok && it >= 0; it = rank_of(++r)) {
-      int kv, pair, split, j0, j1;
-      Blocks b;
-      item(it, kv, pair, split, b, j0, j1);
-      const int nb = j1 - j0;
-      if (nb == 0) continue;
-      const int tiles = (2 * pair + 1) * 128 < rows ? 2 : 1;
-      if (!wait(k_full0 + 8 * (g & 1), (g >> 1) & 1)) break;
-      for (int x = 0; ok && x < tiles; ++x) {
-        if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
-        ptx::tc_fence_after();
-        issue_s(x, g);
-      }
-      if (!ok) break;
-      commit(k_empty0 + 8 * (g & 1));
-      for (int j = 0; ok && j < nb; ++j) {
-        const int gj = g + j;
-        const bool last = j + 1 == nb;
-        if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
-        if (!last && !wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
+    Item it, next;
+    bool have = next_item(r, it);
+    if (have) {  // the first item's first S
+      const int tiles = tiles_of(it);
+      if (wait(k_full0, 0)) {
         for (int x = 0; ok && x < tiles; ++x) {
-          if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
-          ++np[x];
-          if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
+          if (!wait(q_full0 + 8 * x, 0)) break;
           ptx::tc_fence_after();
-          issue_pv(x, gj, j == 0);
-          if (last) commit(o_full0 + 8 * x);
-          else issue_s(x, gj + 1);
+          issue_s(x, 0, it.units(it.j0));
+        }
+        if (ok) {
+          commit(k_empty0);
+          if (it.j1 - it.j0 == 1)
+            for (int x = 0; x < tiles; ++x) commit(q_empty0 + 8 * x);
+        }
+      }
+    }
+    while (ok && have) {
+      const int nb = it.j1 - it.j0, tiles = tiles_of(it);
+      const bool more = next_item(r, next);
+      const int next_tiles = more ? tiles_of(next) : 0;
+      for (int j = 0; ok && j < nb; ++j) {
+        const int gj = g + j, n = it.units(it.j0 + j);
+        const bool last = j + 1 == nb;
+        const int n_next = last ? (more ? next.units(next.j0) : 0) : it.units(it.j0 + j + 1);
+        if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
+        if (n_next > 0 && !wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
+        for (int x = 0; ok && x < 2; ++x) {
+          if (x < tiles) {
+            if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
+            ++np[x];
+            if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
+            ptx::tc_fence_after();
+            issue_pv(x, gj, j == 0, n);
+            if (last) {
+              commit(o_full0 + 8 * x);
+              ++nact[x];
+            } else {
+              issue_s(x, gj + 1, n_next);
+            }
+          }
+          if (last && x < next_tiles) {  // this tile's P has been read by the products before
+            if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
+            ptx::tc_fence_after();
+            issue_s(x, gj + 1, n_next);
+          }
         }
         if (!ok) break;
         commit(v_empty0 + 8 * (gj & 1));
-        if (!last) commit(k_empty0 + 8 * ((gj + 1) & 1));
+        if (n_next > 0) commit(k_empty0 + 8 * ((gj + 1) & 1));
+        // the last S of an item frees its Q
+        if (!last && j + 2 == nb)
+          for (int x = 0; x < tiles; ++x) commit(q_empty0 + 8 * x);
+        if (last && more && next.j1 - next.j0 == 1)
+          for (int x = 0; x < next_tiles; ++x) commit(q_empty0 + 8 * x);
       }
-      for (int x = 0; x < tiles; ++x) ++nact[x];
       g += nb;
+      it = next;
+      have = more;
     }
     if (!ok) *abort_flag = 1;
     if (leader) {
@@ -293,14 +354,58 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     }
     __syncwarp();
   } else {
-    const int x = (warp - 2) >> 2;
+    // ---- q rows, 16-byte pieces of a row by neighbouring lanes ----
+    const int x = warp - 2;
+    constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
+    const int c = lane % kPieces, sub = lane / kPieces;
+    Item it;
+    uint32_t n = 0;
+    for (int r = 0; next_item(r, it);) {
+      if ((2 * it.pair + x) * 128 >= rows) continue;
+      const bool ready = *abort_flag == 0 && ptx::mbar_wait(q_empty0 + 8 * x, (n & 1) ^ 1, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ready)) {
+        if (lane == 0) {
+          if (*abort_flag == 0) record(p.status, kDevTimeoutProducer);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      ++n;
+#pragma unroll 1
+      for (int quarter = 0; quarter < 4; ++quarter) {
+        const int m_row = (2 * it.pair + x) * 128 + quarter * 32 + lane;  // row of the kv head: token * group + head
+        unsigned long long mine = 0;
+        if (m_row < rows) {
+          const int token = m_row / p.group, head = it.kv * p.group + m_row - token * p.group, rank = head / p.heads_per_rank;
+          mine = reinterpret_cast<unsigned long long>(static_cast<const __nv_bfloat16 *>(p.q[rank]) + token * p.q_ld[rank] +
+                                                      static_cast<long long>(head - rank * p.heads_per_rank) * D);
+        }
+        const uint32_t to = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(quarter) * 4096u + (c >> 3) * kSubTile;
+#pragma unroll 4
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = i * kAtOnce + sub;
+          const unsigned long long src = __shfl_sync(0xffffffffu, mine, rr);
+          // rows past the last token are zeros
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + rr * 128 + ((c & 7) ^ (rr & 7)) * 16),
+                       "l"(src ? src + c * 16 : reinterpret_cast<unsigned long long>(p.q[0])), "r"(src ? 16 : 0)
+                       : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(q_full0 + 8 * x);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int x = (warp - 4) >> 2;
     const int qw = warp & 3;
     const int row = qw * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(qw * 32) << 16;
     const uint32_t sb = tmem + lane_off + static_cast<uint32_t>(x * 128);
     const uint32_t ob = tmem + lane_off + 256u + static_cast<uint32_t>(x * 128);
     const uint32_t s_full = s_full0 + 8 * x, p_full = p_full0 + 8 * x;
-    const uint32_t warp_q = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(qw) * 4096u;  // its 32 rows
+    const uint32_t turn = sQ + C::kOut + static_cast<uint32_t>(warp - 4) * 4096u;  // where this warp turns its output
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       const bool ready = ptx::mbar_wait(bar, parity, p.wait_ns);
@@ -312,46 +417,27 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       return false;
     };
     uint32_t gs = 0, nact = 0;
-    for (int r = 0, it = rank_of(0); ok && it >= 0; it = rank_of(++r)) {
-      int kv, pair, split, j0, j1;
-      Blocks blk;
-      item(it, kv, pair, split, blk, j0, j1);
-      if (j0 == j1 || (2 * pair + x) * 128 >= rows) continue;
-      const int m_row = (2 * pair + x) * 128 + row;  // row of the kv head: token * group + head
+    Item it;
+    for (int r = 0; ok && next_item(r, it);) {
+      if ((2 * it.pair + x) * 128 >= rows) continue;
+      const int m_row = (2 * it.pair + x) * 128 + row;  // row of the kv head: token * group + head
       const bool there = m_row < rows;
       const int token = there ? m_row / p.group : 0;
-      const int head = kv * p.group + (there ? m_row - token * p.group : 0);
-      const int rank = head / p.heads_per_rank;
-      const long long head_col = static_cast<long long>(head - rank * p.heads_per_rank) * D;
-      // the warp's q rows into the Q tile, a row's 16-byte pieces by neighbouring lanes; the
-      // previous item's products have read it (its o_full was waited for)
-      {
-        constexpr int kPieces = D / 8;
-        const unsigned long long mine =
-            there ? reinterpret_cast<unsigned long long>(static_cast<const __nv_bfloat16 *>(p.q[rank]) + token * p.q_ld[rank] + head_col) : 0;
-        const int c = lane % kPieces;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int rr = i * (32 / kPieces) + lane / kPieces;
-          const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, mine, rr));
-          const uint4 v = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          st_shared(warp_q + (c >> 3) * kSubTile + rr * 128 + ((c & 7) ^ (rr & 7)) * 16, v);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(q_full0 + 8 * x);
-      }
       // the row sees keys [w0, pos] and [0, sinks)
       const int pos = p.keys - p.tokens + token;
       const int w0 = pos >= p.window ? pos - p.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
-      for (int j = j0; j < j1; ++j, ++gs) {
+      for (int j = it.j0; j < it.j1; ++j, ++gs) {
+        // the block's columns: its window run's up to 16 wu, its first tokens' from there to 16 n
+        const int n = it.units(j), wu = max(0, min(8, it.k.w_units - 8 * j));
+        const int k0 = it.k.w0 + 128 * j;  // key of column 0 of the window run
+        const int hi = min(pos - k0 + 1, 16 * wu), lo = w0 - k0, first = p.sinks - k0;  // seen: i < hi and (i >= lo or i < first)
+        const int hs = it.k.sinks - (128 * j - 16 * it.k.w_units);                     // seen of the first tokens: i < hs
         if (!wait_all(s_full, gs & 1)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const int k0 = blk.at(j) * 128;
-        const int hi = pos - k0 + 1, lo = w0 - k0, first = p.sinks - k0;  // seen: i < hi and (i >= lo or i < first)
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -360,11 +446,19 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         ptx::tmem_regs_ready(v);
         if (__any_sync(0xffffffffu, hi < 128 || (lo > 0 && first < 128))) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= hi || (i < lo && i >= first)) v[i] = __float_as_uint(-INFINITY);
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t win = low_bits(16 * wu - 32 * h);
+            const uint32_t see = (low_bits(hi - 32 * h) & (~low_bits(lo - 32 * h) | low_bits(first - 32 * h))) |
+                                 (low_bits(min(hs, 16 * n) - 32 * h) & ~win);
+            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see & (1u << i))) v[32 * h + i] = __float_as_uint(-INFINITY);
+            }
+          }
         }
         const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
-        bool find_max = j == j0, move = false;
+        bool find_max = j == it.j0, move = false;
         float m_new = m, s0, s1;
 #pragma unroll 1
         for (;;) {
@@ -410,7 +504,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         }
         const float alpha = move ? exp2f(m - m_new) : 1.f;
         m = m_new;
-        if (find_max && j > j0 && __any_sync(0xffffffffu, move)) {
+        if (find_max && j > it.j0 && __any_sync(0xffffffffu, move)) {
           l *= alpha;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -436,10 +530,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       }
       ++nact;
       ptx::tc_fence_after();
-      // out by pieces of 128 bytes, turned in the warp's part of the Q tile, which nothing
-      // reads any more: a lane that stores its own row touches 32 lines an instruction
+      // out by pieces of 128 bytes, turned through shared memory: a lane that stores its own row
+      // touches 32 lines an instruction
       if (p.split > 1) {
-        const long long at = (static_cast<long long>(split) * p.heads_kv + kv) * rows + m_row;
+        const long long at = (static_cast<long long>(it.split) * p.heads_kv + it.kv) * rows + m_row;
         const int left = rows - (m_row - lane);  // of the warp's rows
         if (there) p.part_ml[at] = make_float2(m, l);
 #pragma unroll 1
@@ -450,20 +544,25 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
           ptx::tmem_regs_ready(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            st_shared(warp_q + lane * 128 + (i ^ (lane & 7)) * 16, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            st_shared(turn + lane * 128 + (i ^ (lane & 7)) * 16, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int rr = 4 * i + (lane >> 3), q = lane & 7;
-            const uint4 w = ld_shared(warp_q + rr * 128 + (q ^ (rr & 7)) * 16);
+            const uint4 w = ld_shared(turn + rr * 128 + (q ^ (rr & 7)) * 16);
             if (rr < left) *reinterpret_cast<uint4 *>(p.part_o + (at - lane + rr) * D + c * 32 + q * 4) = w;
           }
           __syncwarp();
         }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(o_free0 + 8 * x);
       } else {
         const float inv = 1.f / l;
+        const int head = it.kv * p.group + (there ? m_row - token * p.group : 0), rank = head / p.heads_per_rank;
         const unsigned long long mine =
-            there ? reinterpret_cast<unsigned long long>(static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] + head_col) : 0;
+            there ? reinterpret_cast<unsigned long long>(static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] +
+                                                         static_cast<long long>(head - rank * p.heads_per_rank) * D)
+                  : 0;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
@@ -478,22 +577,24 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-              st_shared(warp_q + lane * 128 + ((4 * hh + i) ^ (lane & 7)) * 16, make_uint4(w[0], w[1], w[2], w[3]));
+              st_shared(turn + lane * 128 + ((4 * hh + i) ^ (lane & 7)) * 16, make_uint4(w[0], w[1], w[2], w[3]));
             }
+          }
+          if (c == D / 64 - 1) {  // O has been read
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(o_free0 + 8 * x);
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int rr = 4 * i + (lane >> 3), q = lane & 7;
-            const uint4 w = ld_shared(warp_q + rr * 128 + (q ^ (rr & 7)) * 16);
+            const uint4 w = ld_shared(turn + rr * 128 + (q ^ (rr & 7)) * 16);
             __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(__shfl_sync(0xffffffffu, mine, rr));
             if (dst) *reinterpret_cast<uint4 *>(dst + c * 64 + q * 8) = w;
           }
           __syncwarp();
         }
       }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(o_free0 + 8 * x);
     }
   }
 
@@ -523,9 +624,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_const
   const long long all = static_cast<long long>(p.heads_kv) * p.rows;
   if (row >= all) return;
   const int kv = static_cast<int>(row / p.rows), m_row = static_cast<int>(row - static_cast<long long>(kv) * p.rows);
-  const Blocks b = blocks_of(m_row / 256, p.rows, p.group, p.tokens, p.keys, p.window, p.sinks);
+  const int blocks = keys_of(m_row / 256, p.rows, p.group, p.tokens, p.keys, p.window, p.sinks).blocks;
   float acc[kPer];
-  const float l = join_splits<D>(p.part_ml, p.part_o, all, row, min(p.split, b.count), lane, acc);
+  const float l = join_splits<D>(p.part_ml, p.part_o, all, row, min(p.split, blocks), lane, acc);
   const int token = m_row / p.group, head = kv * p.group + (m_row - token * p.group), rank = head / p.heads_per_rank;
   __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] +
                        static_cast<long long>(head - rank * p.heads_per_rank) * D + lane * kPer;
@@ -541,7 +642,7 @@ int splits_of(long long rows, int group, int heads_kv, int tokens, int keys, int
   const long long bases = static_cast<long long>(pairs) * heads_kv;
   const int sms = num_sms();
   if (bases >= sms) return 1;
-  const int most = blocks_of(pairs - 1, static_cast<int>(rows), group, tokens, keys, window, sinks).count;
+  const int most = keys_of(pairs - 1, static_cast<int>(rows), group, tokens, keys, window, sinks).blocks;
   int split = 1;
   long long best = -1;
   for (int c = 1; c <= most && bases * c <= 2LL * sms; ++c) {
@@ -650,7 +751,7 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
   const cudaError_t e = get_dev_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e);
   static thread_local WindowParams p;
-  static thread_local WindowMaps maps;  // 8 KB: kept off the stack
+  static thread_local WindowMaps maps;  // 16 KB: kept off the stack
   std::memset(&p, 0, sizeof(p));
   for (int r = 0; r < n; ++r) {
     p.q[r] = q[r].ptr;
@@ -668,6 +769,7 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
     if (p.one_map) kr.cols = vr.cols = kvc * sources;
     if (S == 1) kr.ld = vr.ld = kvc * sources;  // the pitch of a single row is free
     if (!encode_rows_map(&maps.k[r], kr, 128) || !encode_rows_map(&maps.v[r], vr, 128)) return TP_ERR_INVALID_ARG;
+    if (sinks > 0 && (!encode_rows_map(&maps.k16[r], kr, 16) || !encode_rows_map(&maps.v16[r], vr, 16))) return TP_ERR_INVALID_ARG;
   }
   p.tokens = static_cast<int>(T);
   p.keys = static_cast<int>(S);

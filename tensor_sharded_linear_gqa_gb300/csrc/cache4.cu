@@ -67,19 +67,6 @@ __device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 4;  // rows (token and head) in flight a thread
 
-// Division by a number that the host knows: x / d = (umulhi(x, mul) + x) >> shift for x < 2^31.
-struct Divider {
-  uint32_t mul, shift;
-  __host__ void set(uint32_t d) {
-    shift = 0;
-    while ((1ull << shift) < d) ++shift;
-    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
-  }
-  __device__ __forceinline__ int of(int x) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
-  }
-};
-
 struct CopyParams {
   Cache4 cache;
   const void *in[2][kC4Ranks];   // store: keys and values; load: unused

@@ -2031,6 +2031,17 @@ bool encode_rows_map_3d(CUtensorMap *map, const tp_tensor &t, int box_rows, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_heads_map(CUtensorMap *map, const tp_tensor &t, int d, int box_heads, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || t.cols % d != 0) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(t.cols / d), static_cast<cuuint64_t>(t.rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(t.ld) * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 GemmBuilder::GemmBuilder() { std::memset(&p, 0, sizeof(p)); }
 
 int GemmBuilder::add_map(const void *base, long long rows, long long k, long long ld, int box_rows,

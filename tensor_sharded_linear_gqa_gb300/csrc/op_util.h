@@ -1,5 +1,6 @@
 // Argument checks and small device helpers shared by the operators between the
-// projections (rmsnorm.cu, cache_evict.cu, linear_epilogue.cu, prefix_attention.cu).
+// projections and for long contexts (rmsnorm.cu, cache_evict.cu, linear_epilogue.cu,
+// prefix_attention.cu, rotary.cu, window_attention.cu, cache4.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,6 +36,19 @@ inline tp_status launched(cudaError_t e) {
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? TP_OK : cuda_fail(e);
 }
+
+// Division by a number that the host knows: x / d = (umulhi(x, mul) + x) >> shift for x < 2^31.
+struct Divider {
+  uint32_t mul, shift;
+  __host__ void set(uint32_t d) {
+    shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int of(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
+  }
+};
 
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

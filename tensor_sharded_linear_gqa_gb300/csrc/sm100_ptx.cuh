@@ -67,6 +67,26 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long lo
   }
 }
 
+// The same for waits that are long in the common case: the thread may sleep in each try until the
+// phase completes (for at most about 10 us), so that it takes no issue slots from its SM's other warps.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, long long budget_ns) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(10000u)
+        : "memory");
+    if (ok) return true;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (static_cast<long long>(t - t0) > budget_ns) return false;
+  }
+}
+
 // ---- TMA ----------------------------------------------------------------------
 // 2-D tiled bulk tensor load global -> shared, completion counted in bytes on `bar`.
 // x is the innermost coordinate (elements), y the row.

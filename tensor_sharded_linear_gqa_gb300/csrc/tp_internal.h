@@ -338,6 +338,11 @@ bool encode_rows_map(CUtensorMap *map, const tp_tensor &t, int box_rows);
 // encode_rows_map's box.
 bool encode_rows_map_3d(CUtensorMap *map, const tp_tensor &t, int box_rows, int box_kt);
 
+// A bf16 view of heads of `d` columns as [rows][heads][d]: one copy brings 64 values of box_heads
+// neighbouring heads of box_rows rows, the heads of a row next to one another, 128-byte swizzle,
+// zero fill out of range.
+bool encode_heads_map(CUtensorMap *map, const tp_tensor &t, int d, int box_heads, int box_rows);
+
 // ---------------------------------------------------------------------------
 // Attention core (attention.cu): one CTA per (128-query tile, q head).
 // ---------------------------------------------------------------------------

@@ -2,23 +2,27 @@
 // the query at position i sees key j when j <= i and (j > i - window or j < sinks);
 //   A[t, h] = softmax(q K_g^T / sqrt(d)) V_g over these keys.
 //
-// All query rows of a kv head (T tokens x G heads of its group, token by token) read the same K
-// and V, so they are packed into tiles of 128 rows: 128 / G tokens a tile, which move the
-// window by that little, and every K and V tile serves the whole group. A work item is (kv
-// head, pair of adjacent row tiles, key split). Its keys are two runs, the pair's window from its first
+// The query rows of the heads of a group read the same K and V, so they are packed into tiles of 128
+// rows, token by token: with G heads 128 / G tokens a tile, which move the window by
+// that little, and every K and V tile serves all of them. G is the largest power of two that divides
+// both the plan's group and a rank's heads, so that one copy of a 3-D tensor map (values, heads, tokens) brings
+// a tile in this order. A work item is (such a set of heads, pair of adjacent row tiles,
+// key split). Its keys are two runs, the pair's window from its first
 // row's first key on and the first tokens before it, each in units of 16 keys; blocks are 8
 // neighbouring units of the two runs together, so that only the last one is short (its products are
 // as narrow as it is) and a few first tokens cost a unit, not a block. Masks are applied
 // in the blocks where a row's limits lie.
 //
 // k_window's roles (one CTA an SM, persistent):
-//   warp 0        TMA: lane 0 the K ring, lane 1 the V ring (two 128-key stages each);
-//   warp 1        MMA issuer (tcgen05): S_A, S_B, P_A V, S_A of the next block, P_B V, ..., over
-//                 the items' ends: the next item's first S follows this one's last P V;
-//   warps 4-7     softmax of tile A, 8-11 of tile B, one thread a row; they store the output;
-//   warps 2, 3    gather the q rows of tile A and B of the next item into the swizzled Q tile (a row is
-//                 a token's head, which no one tensor map covers when a group lies on several
-//                 ranks) as soon as this item's last S has read it.
+//   warp 0        TMA: one lane, K and V tiles of 128 keys in turn through one ring of five slots
+//                 (d = 128; eight for d = 64): a tile is asked for one to two steps before it is needed;
+//   warps 1, 2    MMA issuers (tcgen05) of tile A and of tile B: S, P V, S of the next block, ..., over
+//                 the items' ends: the next item's first S follows this one's last P V. One warp
+//                 for both tiles bounds the whole: a product of 128 x 128 x 16 takes the tensor core
+//                 64 cycles and its issue about 80;
+//   warp 3        TMA of the next item's q tiles as soon as this item's last S has read them;
+//   warps 4-7     softmax of tile A, 8-11 of tile B, one thread a row;
+//   warps 12-15   store the outputs, while the softmax is at the next item already.
 // TMEM: S of A at columns 0, of B at 128 (P overwrites its first half as bf16 and is read from
 // there), O at 256 and 384. V is used as it lies, [keys x d], as an MN-major operand.
 // The reference maximum m of a row is found on its item's first block and moves later only when
@@ -42,30 +46,31 @@ namespace {
 using namespace op;
 
 constexpr int kWinRanks = 32;
-constexpr int kWinThreads = 384;
-// Registers a thread: 168 at launch; the softmax's warpgroups take what the first one gives up
-// (128 * (104 + 2 * 200) of 384 * 168).
-constexpr int kRegsOthers = 104, kRegsSoftmax = 200;
-static_assert(kRegsOthers + 2 * kRegsSoftmax <= 3 * 168, "the split fits the launch's registers");
+constexpr int kWinThreads = 512;
+// Registers a thread: 128 at launch; the softmax's two warpgroups take what the other two give up.
+constexpr int kRegsOthers = 80, kRegsSoftmax = 176;
+static_assert(kRegsOthers + kRegsSoftmax <= 2 * 128, "the split fits the launch's registers");
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
 constexpr float kSumLimit = 0x1p64f;
 
 struct WindowParams {
   int tokens, keys, window, sinks;
-  int group, heads_q, heads_kv, heads_per_rank, heads_per_source;
-  int rows, pairs, split;           // rows of a kv head, pairs of row tiles, key splits
+  int group, sets;                  // heads that share a tile; such sets
+  int sets_per_kv, heads_per_rank, heads_per_source;
+  int rows, pairs, split;           // rows of a set, pairs of row tiles, key splits
+  Divider by_sets, by_split;
+  int group_shift;
   int one_map;                      // every source's K (and V) lies in one tensor, in head order
   float scale_log2;
   float *part_o;                    // [split][row][d]
   float2 *part_ml;                  // [split][row]: m (log2 units), l
   int *status;
   long long wait_ns;
-  const void *q[kWinRanks];
-  long long q_ld[kWinRanks];
   void *a[kWinRanks];
   long long a_ld[kWinRanks];
 };
 struct WindowMaps {
+  CUtensorMap q[kWinRanks];                    // boxes of 64 values, the set's heads, 128 / group tokens
   CUtensorMap k[kWinRanks], v[kWinRanks];      // boxes of 128 keys
   CUtensorMap k16[kWinRanks], v16[kWinRanks];  // of 16, for blocks of both runs
 };
@@ -75,9 +80,9 @@ struct WindowMaps {
 struct Keys {
   int w0, w_units, sinks, units, blocks;
 };
-__host__ __device__ inline Keys keys_of(int pair, int rows, int group, int tokens, int keys, int window, int sinks) {
-  const int last = 256 * pair + 255 < rows ? 256 * pair + 255 : rows - 1;
-  const int p0 = keys - tokens + 256 * pair / group, p1 = keys - tokens + last / group;
+// Of tokens t0 .. t1, the pair's first and last.
+__host__ __device__ inline Keys keys_of(int t0, int t1, int tokens, int keys, int window, int sinks) {
+  const int p0 = keys - tokens + t0, p1 = keys - tokens + t1;
   Keys k;
   k.w0 = p0 >= window ? p0 - window + 1 : 0;  // first key of the first row's window
   k.w_units = (p1 - k.w0) / 16 + 1;
@@ -85,6 +90,10 @@ __host__ __device__ inline Keys keys_of(int pair, int rows, int group, int token
   k.units = k.w_units + (k.sinks + 15) / 16;
   k.blocks = (k.units + 7) / 8;
   return k;
+}
+
+__device__ __forceinline__ Keys keys_of_pair(const WindowParams &p, int pair) {
+  return keys_of(256 * pair >> p.group_shift, min(256 * pair + 255, p.rows - 1) >> p.group_shift, p.tokens, p.keys, p.window, p.sinks);
 }
 
 __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
@@ -106,21 +115,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-
 template <int D>
 struct WinCfg {
   static constexpr int kCh = D / 64;                 // 64-column sub-tiles of a head
   static constexpr uint32_t kTile = kCh * kSubTile;  // a [128 x D] tile
-  static constexpr uint32_t kK = 2 * kTile, kV = 4 * kTile, kOut = 6 * kTile, kBar = kOut + 8 * 4096;
-  static constexpr size_t kSmem = kBar + 256 + 1024;
+  static constexpr int kSlots = D == 128 ? 5 : 8;    // of the K and V ring
+  static constexpr uint32_t kRing = 2 * kTile, kL = kRing + kSlots * kTile, kBar = kL + 1024;
+  static constexpr size_t kSmem = kBar + 288 + 1024;
+};
+// A place in the ring: K of block g is tile 2g, V is tile 2g + 1.
+template <int SLOTS>
+struct Slot {
+  int at;
+  uint32_t phase;
+  __device__ __forceinline__ void on(int n) {
+    at += n;
+    if (at >= SLOTS) {
+      at -= SLOTS;
+      phase ^= 1;
+    }
+  }
 };
 
 // n low bits, for any n.
@@ -132,21 +146,22 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const uint32_t sQ = ptx::smem_addr(smem), sK0 = sQ + C::kK, sV0 = sQ + C::kV;
+  const uint32_t sQ = ptx::smem_addr(smem), sR = sQ + C::kRing;
   uint8_t *bar_area = smem + C::kBar;
   const uint32_t bar0 = ptx::smem_addr(bar_area);
-  const uint32_t q_full0 = bar0, k_full0 = bar0 + 16, k_empty0 = bar0 + 32, v_full0 = bar0 + 48, v_empty0 = bar0 + 64,
-                 s_full0 = bar0 + 80, p_full0 = bar0 + 96, o_full0 = bar0 + 112, o_free0 = bar0 + 128, q_empty0 = bar0 + 144,
-                 drain = bar0 + 160;
-  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 168);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 172);
+  const uint32_t q_full0 = bar0, q_empty0 = bar0 + 16, s_full0 = bar0 + 32, p_full0 = bar0 + 48, o_full0 = bar0 + 64,
+                 o_free0 = bar0 + 80, l_full0 = bar0 + 96, drain0 = bar0 + 112, turn0 = bar0 + 128, full0 = bar0 + 144, empty0 = full0 + 8 * C::kSlots;
+  static_assert(144 + 16 * C::kSlots <= 272, "barriers, TMEM slot and abort flag fit");
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bar_area + 272);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bar_area + 276);
+  float *row_l = reinterpret_cast<float *>(smem + C::kL);  // l of the rows of both tiles
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.rows;
-  const int items = p.heads_kv * p.pairs * p.split;
-  // An item: (kv head, tile pair, split) and its part [j0, j1) of the pair's blocks.
+  const int items = p.sets * p.pairs * p.split;
+  // An item: (set of heads, tile pair, split) and its part [j0, j1) of the pair's blocks.
   struct Item {
-    int kv, pair, split, j0, j1;
+    int set, pair, split, j0, j1;
     Keys k;
     __device__ int units(int j) const { return min(8, k.units - 8 * j); }
   };
@@ -159,16 +174,20 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       const long long i = static_cast<long long>(r) * gridDim.x + at;
       if (static_cast<long long>(r) * gridDim.x >= items) return false;
       if (i >= items) continue;
-      const int first = static_cast<int>(i) / p.split;
+      const int first = p.by_split.of(static_cast<int>(i));
       it.split = static_cast<int>(i) - first * p.split;
-      it.pair = first / p.heads_kv;
-      it.kv = first - it.pair * p.heads_kv;
+      it.pair = p.by_sets.of(first);
+      it.set = first - it.pair * p.sets;
       it.pair = p.pairs - 1 - it.pair;
-      it.k = keys_of(it.pair, rows, p.group, p.tokens, p.keys, p.window, p.sinks);
-      const int n = min(p.split, it.k.blocks);
-      if (it.split >= n) continue;
-      it.j0 = static_cast<int>(static_cast<long long>(it.k.blocks) * it.split / n);
-      it.j1 = static_cast<int>(static_cast<long long>(it.k.blocks) * (it.split + 1) / n);
+      it.k = keys_of_pair(p, it.pair);
+      it.j0 = 0;
+      it.j1 = it.k.blocks;
+      if (p.split > 1) {
+        const int n = min(p.split, it.k.blocks);
+        if (it.split >= n) continue;
+        it.j0 = static_cast<int>(static_cast<long long>(it.k.blocks) * it.split / n);
+        it.j1 = static_cast<int>(static_cast<long long>(it.k.blocks) * (it.split + 1) / n);
+      }
       ++r;
       return true;
     }
@@ -177,18 +196,20 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(q_full0 + 8 * s, 32);
+      ptx::mbar_init(q_full0 + 8 * s, 1);
       ptx::mbar_init(q_empty0 + 8 * s, 1);
-      ptx::mbar_init(k_full0 + 8 * s, 1);
-      ptx::mbar_init(k_empty0 + 8 * s, 1);
-      ptx::mbar_init(v_full0 + 8 * s, 1);
-      ptx::mbar_init(v_empty0 + 8 * s, 1);
       ptx::mbar_init(s_full0 + 8 * s, 1);
       ptx::mbar_init(p_full0 + 8 * s, 4);
       ptx::mbar_init(o_full0 + 8 * s, 1);
-      ptx::mbar_init(o_free0 + 8 * s, 128);
+      ptx::mbar_init(o_free0 + 8 * s, 4);
+      ptx::mbar_init(l_full0 + 8 * s, 4);
+      ptx::mbar_init(drain0 + 8 * s, 1);
+      ptx::mbar_init(turn0 + 8 * s, 1);
     }
-    ptx::mbar_init(drain, 1);
+    for (int s = 0; s < C::kSlots; ++s) {
+      ptx::mbar_init(full0 + 8 * s, 1);
+      ptx::mbar_init(empty0 + 8 * s, 2);  // both tiles' products have read it
+    }
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -203,52 +224,55 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  int issued[2] = {0, 0};
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
   if (warp == 0) {
-    if (lane < 2) {
-      const uint32_t full0 = lane == 0 ? k_full0 : v_full0, empty0 = lane == 0 ? k_empty0 : v_empty0;
-      const uint32_t dst0 = lane == 0 ? sK0 : sV0;
+    if (lane == 0) {
       bool run = true;
-      int g = 0;
+      Slot<C::kSlots> at = {0, 0};
+      int filled = 0;
       Item it;
       for (int r = 0; run && next_item(r, it);) {
-        const int src = p.one_map ? 0 : it.kv / p.heads_per_source;
-        const int col = (it.kv - src * p.heads_per_source) * D;
-        const CUtensorMap *map = lane == 0 ? &maps.k[src] : &maps.v[src];
-        const CUtensorMap *map16 = lane == 0 ? &maps.k16[src] : &maps.v16[src];
-        for (int j = it.j0; j < it.j1; ++j, ++g) {
-          const int s = g & 1;
-          if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * s, ((g >> 1) & 1) ^ 1, p.wait_ns)) {
+        const int kv = it.set / p.sets_per_kv, src = p.one_map ? 0 : kv / p.heads_per_source;
+        const int col = (kv - src * p.heads_per_source) * D;
+        for (int t = 2 * it.j0; run && t < 2 * it.j1; ++t) {  // K, V of block t / 2
+          const int j = t >> 1, v = t & 1;
+          if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * at.at, at.phase ^ 1, p.wait_ns)) {
             if (!*abort_flag) record(p.status, kDevTimeoutProducer);
             *abort_flag = 1;
             run = false;
             break;
           }
           const int n = it.units(j), w = min(8, it.k.w_units - 8 * j);  // units of the block; of the window run
-          const uint32_t dst = dst0 + s * C::kTile;
+          const uint32_t dst = sR + at.at * C::kTile, bar = full0 + 8 * at.at;
           if (w > 0 && w < n) {  // of both runs: unit by unit
-            ptx::mbar_arrive_expect_tx(full0 + 8 * s, n * 2048u * C::kCh);
+            const CUtensorMap *map = v ? &maps.v16[src] : &maps.k16[src];
+            ptx::mbar_arrive_expect_tx(bar, n * 2048u * C::kCh);
             for (int u = 0; u < n; ++u) {
               const int key = u < w ? it.k.w0 + 128 * j + 16 * u : 128 * j - 16 * it.k.w_units + 16 * u;
-              for (int c = 0; c < C::kCh; ++c)
-                ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map16, col + c * 64, key, full0 + 8 * s);
+              for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map, col + c * 64, key, bar);
             }
           } else {
-            ptx::mbar_arrive_expect_tx(full0 + 8 * s, C::kTile);
+            const CUtensorMap *map = v ? &maps.v[src] : &maps.k[src];
+            ptx::mbar_arrive_expect_tx(bar, C::kTile);
             const int key = w > 0 ? it.k.w0 + 128 * j : 128 * j - 16 * it.k.w_units;
-            for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, full0 + 8 * s);
+            for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, bar);
           }
-          ++issued[s];
+          at.on(1);
+          ++filled;
         }
       }
+      // every load has landed before the CTA may end: the last fill of each slot
+      Slot<C::kSlots> last = {0, 0};
+      for (int i = 0; i < filled; ++i, last.on(1))
+        if (i + C::kSlots >= filled && !ptx::mbar_wait(full0 + 8 * last.at, last.phase, p.wait_ns)) record(p.status, kDevTimeoutDrain);
     }
-  } else if (warp == 1) {  // converged; one lane issues (see elect_one)
+  } else if (warp < 3) {  // converged; one lane issues (see elect_one)
+    const int x = warp - 1;
     constexpr uint32_t idesc_s0 = ptx::idesc_bf16_f32(128, 0);  // + 2 units << 17: 16 columns a unit
     constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
     // descriptors of the tiles' starts; the address field counts 16 bytes
-    const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sK0), vd = desc_mn_sw128(sV0, kSubTile);
+    const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sR), vd = desc_mn_sw128(sR, kSubTile);
     const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -261,142 +285,152 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       if (leader) ptx::mma_commit(bar);
       __syncwarp();
     };
-    auto issue_s = [&](int x, int g, int n) {  // S_X = Q_X K^T, 16 n columns
-      const uint64_t qa = qd + static_cast<uint32_t>(x) * (C::kTile >> 4), ka = kd + static_cast<uint32_t>(g & 1) * (C::kTile >> 4);
-      const uint32_t d = tmem + static_cast<uint32_t>(x * 128);
+    const uint64_t qa = qd + static_cast<uint32_t>(x) * (C::kTile >> 4);
+    const uint32_t td_s = tmem + static_cast<uint32_t>(x * 128), td_o = tmem + 256u + static_cast<uint32_t>(x * 128);
+    auto issue_s = [&](int slot, int n) {  // S = Q K^T, 16 n columns
+      const uint64_t ka = kd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
       const uint32_t idesc = idesc_s0 + (static_cast<uint32_t>(2 * n) << 17);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_bf16(d, qa + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)), ka + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)),
+          ptx::mma_bf16(td_s, qa + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)), ka + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)),
                         idesc, kk > 0 ? 1u : 0u);
         ptx::mma_commit(s_full0 + 8 * x);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int x, int g, bool first, int n) {  // O_X += P_X V, 16 keys (2048 bytes of V) a step
-      const uint64_t va = vd + static_cast<uint32_t>(g & 1) * (C::kTile >> 4);
-      const uint32_t d = tmem + 256u + static_cast<uint32_t>(x * 128), a = tmem + static_cast<uint32_t>(x * 128);
+    auto issue_pv = [&](int slot, bool first, int n) {  // O += P V, 16 keys (2048 bytes of V) a step
+      const uint64_t va = vd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
       const uint32_t more = first ? 0u : 1u;
-      if (leader) {
+      if (n == 8) {
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (kk < n) ptx::mma_bf16_ts(d, a + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
+          for (int kk = 0; kk < 8; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
+        }
+      } else if (leader) {
+#pragma unroll 1
+        for (int kk = 0; kk < n; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
       }
       __syncwarp();
     };
-    int g = 0, r = 0;
-    uint32_t np[2] = {0, 0}, nact[2] = {0, 0};
-    Item it, next;
-    bool have = next_item(r, it);
-    if (have) {  // the first item's first S
-      const int tiles = tiles_of(it);
-      if (wait(k_full0, 0)) {
-        for (int x = 0; ok && x < tiles; ++x) {
-          if (!wait(q_full0 + 8 * x, 0)) break;
+    // a slot is free of this tile: at once where the tile has no rows, else when its products are done
+    auto release = [&](int slot, bool used) {
+      if (leader) {
+        if (used) ptx::mma_commit(empty0 + 8 * slot);
+        else ptx::mbar_arrive(empty0 + 8 * slot);
+      }
+      __syncwarp();
+    };
+    // what of an item these products need
+    struct Work {
+      int units, nb;  // from its first block on; its blocks, 0: no item
+      bool mine;      // the tile has rows
+    };
+    int r = 0;
+    auto next_work = [&]() {
+      Item it;
+      Work w = {0, 0, false};
+      if (next_item(r, it)) w = {it.k.units - 8 * it.j0, it.j1 - it.j0, x < tiles_of(it)};
+      return w;
+    };
+    // The tiles' products are issued in turn, A's P V and next S, then B's. As they come, both tiles would
+    // fall into step: in their softmax together, then in the tensor core's queue.
+    uint32_t turn = 0;
+    uint32_t np = 0, nact = 0;                     // P tiles consumed; items with rows in the tile
+    Slot<C::kSlots> ks = {0, 0}, vs = {1, 0};      // the next block of each
+    auto first_s = [&](const Work &w) {  // the S of an item's first block
+      if (!wait(full0 + 8 * ks.at, ks.phase)) return;
+      if (w.mine) {
+        if (!wait(q_full0 + 8 * x, nact & 1)) return;
+        ptx::tc_fence_after();
+        issue_s(ks.at, min(8, w.units));
+        if (w.nb == 1) commit(q_empty0 + 8 * x);  // the last S of an item frees its Q
+      }
+      release(ks.at, w.mine);
+      ks.on(2);
+    };
+    Work w = next_work();
+    if (w.nb > 0) first_s(w);
+    while (ok && w.nb > 0) {
+      const Work next = next_work();
+      for (int j = 0; ok && j < w.nb; ++j, vs.on(2)) {
+        const bool last = j + 1 == w.nb;
+        // what is there early is waited for before P, which is there last
+        if (!wait(full0 + 8 * vs.at, vs.phase) || (!last && !wait(full0 + 8 * ks.at, ks.phase))) break;
+        if (!wait(turn0 + 8 * x, turn ^ (x == 0 ? 1 : 0))) break;
+        if (w.mine) {
+          if (j == 0 && !wait(o_free0 + 8 * x, (nact & 1) ^ 1)) break;
+          if (!wait(p_full0 + 8 * x, np & 1)) break;
+          ++np;
           ptx::tc_fence_after();
-          issue_s(x, 0, it.units(it.j0));
-        }
-        if (ok) {
-          commit(k_empty0);
-          if (it.j1 - it.j0 == 1)
-            for (int x = 0; x < tiles; ++x) commit(q_empty0 + 8 * x);
-        }
-      }
-    }
-    while (ok && have) {
-      const int nb = it.j1 - it.j0, tiles = tiles_of(it);
-      const bool more = next_item(r, next);
-      const int next_tiles = more ? tiles_of(next) : 0;
-      for (int j = 0; ok && j < nb; ++j) {
-        const int gj = g + j, n = it.units(it.j0 + j);
-        const bool last = j + 1 == nb;
-        const int n_next = last ? (more ? next.units(next.j0) : 0) : it.units(it.j0 + j + 1);
-        if (!wait(v_full0 + 8 * (gj & 1), (gj >> 1) & 1)) break;
-        if (n_next > 0 && !wait(k_full0 + 8 * ((gj + 1) & 1), ((gj + 1) >> 1) & 1)) break;
-        for (int x = 0; ok && x < 2; ++x) {
-          if (x < tiles) {
-            if (!wait(p_full0 + 8 * x, np[x] & 1)) break;
-            ++np[x];
-            if (j == 0 && !wait(o_free0 + 8 * x, (nact[x] & 1) ^ 1)) break;
-            ptx::tc_fence_after();
-            issue_pv(x, gj, j == 0, n);
-            if (last) {
-              commit(o_full0 + 8 * x);
-              ++nact[x];
-            } else {
-              issue_s(x, gj + 1, n_next);
-            }
-          }
-          if (last && x < next_tiles) {  // this tile's P has been read by the products before
-            if (!wait(q_full0 + 8 * x, nact[x] & 1)) break;
-            ptx::tc_fence_after();
-            issue_s(x, gj + 1, n_next);
+          issue_pv(vs.at, j == 0, min(8, w.units - 8 * j));
+          if (last) {
+            commit(o_full0 + 8 * x);
+            ++nact;
+          } else {
+            issue_s(ks.at, min(8, w.units - 8 * (j + 1)));
           }
         }
-        if (!ok) break;
-        commit(v_empty0 + 8 * (gj & 1));
-        if (n_next > 0) commit(k_empty0 + 8 * ((gj + 1) & 1));
-        // the last S of an item frees its Q
-        if (!last && j + 2 == nb)
-          for (int x = 0; x < tiles; ++x) commit(q_empty0 + 8 * x);
-        if (last && more && next.j1 - next.j0 == 1)
-          for (int x = 0; x < next_tiles; ++x) commit(q_empty0 + 8 * x);
+        if (leader) ptx::mbar_arrive(turn0 + 8 * (x ^ 1));
+        turn ^= 1;
+        release(vs.at, w.mine);
+        if (last) {
+          if (next.nb > 0) first_s(next);  // this tile's P has been read by the products before
+        } else {
+          if (w.mine && j + 2 == w.nb) commit(q_empty0 + 8 * x);
+          release(ks.at, w.mine);
+          ks.on(2);
+        }
       }
-      g += nb;
-      it = next;
-      have = more;
+      w = next;
     }
     if (!ok) *abort_flag = 1;
     if (leader) {
-      ptx::mma_commit(drain);
-      if (!ptx::mbar_wait(drain, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      ptx::mma_commit(drain0 + 8 * x);
+      if (!ptx::mbar_wait(drain0 + 8 * x, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
   } else {
-    // ---- q rows, 16-byte pieces of a row by neighbouring lanes ----
-    const int x = warp - 2;
-    constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
-    const int c = lane % kPieces, sub = lane / kPieces;
-    Item it;
-    uint32_t n = 0;
-    for (int r = 0; next_item(r, it);) {
-      if ((2 * it.pair + x) * 128 >= rows) continue;
-      const bool ready = *abort_flag == 0 && ptx::mbar_wait(q_empty0 + 8 * x, (n & 1) ^ 1, p.wait_ns);
-      if (!__all_sync(0xffffffffu, ready)) {
-        if (lane == 0) {
-          if (*abort_flag == 0) record(p.status, kDevTimeoutProducer);
-          *abort_flag = 1;
+    // ---- the q tiles ----
+    if (lane == 0) {
+      Item it;
+      uint32_t n[2] = {0, 0};
+      int r = 0;
+      bool have = next_item(r, it), ok = true;
+      auto place = [&](const Item &i, int &rank, int &head) {
+        rank = i.set * p.group / p.heads_per_rank;
+        head = i.set * p.group - rank * p.heads_per_rank;
+      };
+      while (have && ok) {
+        int rank, head;
+        place(it, rank, head);
+        for (int x = 0; x < tiles_of(it); ++x) {
+          if (*abort_flag || !ptx::mbar_wait(q_empty0 + 8 * x, (n[x] & 1) ^ 1, p.wait_ns)) {
+            if (!*abort_flag) record(p.status, kDevTimeoutProducer);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          ++n[x];
+          ptx::mbar_arrive_expect_tx(q_full0 + 8 * x, C::kTile);
+          for (int c = 0; c < C::kCh; ++c)
+            ptx::tma_load_3d(sQ + x * C::kTile + c * kSubTile, &maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift,
+                             q_full0 + 8 * x);
         }
-        break;
-      }
-      ++n;
-#pragma unroll 1
-      for (int quarter = 0; quarter < 4; ++quarter) {
-        const int m_row = (2 * it.pair + x) * 128 + quarter * 32 + lane;  // row of the kv head: token * group + head
-        unsigned long long mine = 0;
-        if (m_row < rows) {
-          const int token = m_row / p.group, head = it.kv * p.group + m_row - token * p.group, rank = head / p.heads_per_rank;
-          mine = reinterpret_cast<unsigned long long>(static_cast<const __nv_bfloat16 *>(p.q[rank]) + token * p.q_ld[rank] +
-                                                      static_cast<long long>(head - rank * p.heads_per_rank) * D);
-        }
-        const uint32_t to = sQ + static_cast<uint32_t>(x) * C::kTile + static_cast<uint32_t>(quarter) * 4096u + (c >> 3) * kSubTile;
-#pragma unroll 4
-        for (int i = 0; i < kPieces; ++i) {
-          const int rr = i * kAtOnce + sub;
-          const unsigned long long src = __shfl_sync(0xffffffffu, mine, rr);
-          // rows past the last token are zeros
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + rr * 128 + ((c & 7) ^ (rr & 7)) * 16),
-                       "l"(src ? src + c * 16 : reinterpret_cast<unsigned long long>(p.q[0])), "r"(src ? 16 : 0)
-                       : "memory");
+        have = ok && next_item(r, it);
+        if (have) {  // into L2 meanwhile
+          place(it, rank, head);
+          for (int x = 0; x < tiles_of(it); ++x)
+            for (int c = 0; c < C::kCh; ++c)
+              ptx::tma_prefetch_l2_3d(&maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift);
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(q_full0 + 8 * x);
+      // every load has landed before the CTA may end
+      for (int x = 0; x < 2; ++x)
+        if (n[x] > 0 && !ptx::mbar_wait(q_full0 + 8 * x, (n[x] - 1) & 1, p.wait_ns)) record(p.status, kDevTimeoutDrain);
     }
   }
-  } else {
+  } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = (warp - 4) >> 2;
     const int qw = warp & 3;
@@ -405,7 +439,6 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     const uint32_t sb = tmem + lane_off + static_cast<uint32_t>(x * 128);
     const uint32_t ob = tmem + lane_off + 256u + static_cast<uint32_t>(x * 128);
     const uint32_t s_full = s_full0 + 8 * x, p_full = p_full0 + 8 * x;
-    const uint32_t turn = sQ + C::kOut + static_cast<uint32_t>(warp - 4) * 4096u;  // where this warp turns its output
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       const bool ready = ptx::mbar_wait(bar, parity, p.wait_ns);
@@ -420,9 +453,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     Item it;
     for (int r = 0; ok && next_item(r, it);) {
       if ((2 * it.pair + x) * 128 >= rows) continue;
-      const int m_row = (2 * it.pair + x) * 128 + row;  // row of the kv head: token * group + head
+      const int m_row = (2 * it.pair + x) * 128 + row;  // row of the set: token * group + head
       const bool there = m_row < rows;
-      const int token = there ? m_row / p.group : 0;
+      const int token = there ? m_row >> p.group_shift : 0;
       // the row sees keys [w0, pos] and [0, sinks)
       const int pos = p.keys - p.tokens + token;
       const int w0 = pos >= p.window ? pos - p.window + 1 : 0;
@@ -524,86 +557,81 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         l += s0 + s1;
       }
       if (!ok) break;
-      if (!wait_all(o_full0 + 8 * x, nact & 1)) {
+      // the output of the tile's item before has read its l
+      if (nact > 0 && !wait_all(o_free0 + 8 * x, (nact - 1) & 1)) {
         ok = false;
         break;
       }
       ++nact;
-      ptx::tc_fence_after();
-      // out by pieces of 128 bytes, turned through shared memory: a lane that stores its own row
-      // touches 32 lines an instruction
-      if (p.split > 1) {
-        const long long at = (static_cast<long long>(it.split) * p.heads_kv + it.kv) * rows + m_row;
-        const int left = rows - (m_row - lane);  // of the warp's rows
-        if (there) p.part_ml[at] = make_float2(m, l);
+      row_l[x * 128 + row] = l;
+      if (p.split > 1 && there) p.part_ml[(static_cast<long long>(it.split) * p.sets + it.set) * rows + m_row] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(l_full0 + 8 * x);
+    }
+  } else {
+    // ---- output: warp w has TMEM lanes [32 * (w % 4), +32) of both tiles ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
+    const int qw = warp & 3;
+    const int row = qw * 32 + lane;
+    uint32_t nact[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    for (int r = 0; ok && next_item(r, it);) {
+      for (int x = 0; x < 2; ++x) {
+        if ((2 * it.pair + x) * 128 >= rows) continue;
+        const int m_row = (2 * it.pair + x) * 128 + row;
+        const bool there = m_row < rows;
+        const uint32_t ob = tmem + (static_cast<uint32_t>(qw * 32) << 16) + 256u + static_cast<uint32_t>(x * 128);
+        const int token = there ? m_row >> p.group_shift : 0;
+        const int head = it.set * p.group + (m_row & (p.group - 1)), rank = it.set * p.group / p.heads_per_rank;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] +
+                             static_cast<long long>(head - rank * p.heads_per_rank) * D;
+        const bool ready = ptx::mbar_wait_asleep(l_full0 + 8 * x, nact[x] & 1, p.wait_ns) &&
+                           ptx::mbar_wait(o_full0 + 8 * x, nact[x] & 1, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ready)) {
+          if (lane == 0) {
+            if (*abort_flag == 0) record(p.status, kDevTimeoutEpilogue);
+            *abort_flag = 1;
+          }
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        ++nact[x];
+        const bool split = p.split > 1;
+        const float inv = split ? 1.f : 1.f / row_l[x * 128 + row];
+        float *part = split ? p.part_o + ((static_cast<long long>(it.split) * p.sets + it.set) * rows + m_row) * D : nullptr;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 32; ++c) {  // a lane its row: the lines fill up in L2
           uint32_t v[32];
           ptx::tmem_ld_32cols(ob + c * 32, v);
           ptx::tmem_ld_wait();
           ptx::tmem_regs_ready(v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            st_shared(turn + lane * 128 + (i ^ (lane & 7)) * 16, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), q = lane & 7;
-            const uint4 w = ld_shared(turn + rr * 128 + (q ^ (rr & 7)) * 16);
-            if (rr < left) *reinterpret_cast<uint4 *>(p.part_o + (at - lane + rr) * D + c * 32 + q * 4) = w;
+          if (c == D / 32 - 1) {  // O has been read
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(o_free0 + 8 * x);
           }
-          __syncwarp();
-        }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(o_free0 + 8 * x);
-      } else {
-        const float inv = 1.f / l;
-        const int head = it.kv * p.group + (there ? m_row - token * p.group : 0), rank = head / p.heads_per_rank;
-        const unsigned long long mine =
-            there ? reinterpret_cast<unsigned long long>(static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] +
-                                                         static_cast<long long>(head - rank * p.heads_per_rank) * D)
-                  : 0;
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+          if (!there) continue;
+          if (split) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t v[32];
-            ptx::tmem_ld_32cols(ob + c * 64 + hh * 32, v);
-            ptx::tmem_ld_wait();
-            ptx::tmem_regs_ready(v);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4 *>(part + c * 32 + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
-              st_shared(turn + lane * 128 + ((4 * hh + i) ^ (lane & 7)) * 16, make_uint4(w[0], w[1], w[2], w[3]));
+              *reinterpret_cast<uint4 *>(dst + c * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          if (c == D / 64 - 1) {  // O has been read
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(o_free0 + 8 * x);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), q = lane & 7;
-            const uint4 w = ld_shared(turn + rr * 128 + (q ^ (rr & 7)) * 16);
-            __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(__shfl_sync(0xffffffffu, mine, rr));
-            if (dst) *reinterpret_cast<uint4 *>(dst + c * 64 + q * 8) = w;
-          }
-          __syncwarp();
         }
       }
     }
   }
 
-  __syncthreads();
-  if (warp == 0 && lane < 2) {
-    const uint32_t full0 = lane == 0 ? k_full0 : v_full0;
-    for (int s = 0; s < 2; ++s)
-      if (issued[s] > 0 && !ptx::mbar_wait(full0 + 8 * s, (issued[s] - 1) & 1, p.wait_ns)) record(p.status, kDevTimeoutDrain);
-  }
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
@@ -621,13 +649,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_const
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const long long all = static_cast<long long>(p.heads_kv) * p.rows;
+  const long long all = static_cast<long long>(p.sets) * p.rows;
   if (row >= all) return;
-  const int kv = static_cast<int>(row / p.rows), m_row = static_cast<int>(row - static_cast<long long>(kv) * p.rows);
-  const int blocks = keys_of(m_row / 256, p.rows, p.group, p.tokens, p.keys, p.window, p.sinks).blocks;
+  const int set = static_cast<int>(row / p.rows), m_row = static_cast<int>(row - static_cast<long long>(set) * p.rows);
+  const int blocks = keys_of_pair(p, m_row / 256).blocks;
   float acc[kPer];
   const float l = join_splits<D>(p.part_ml, p.part_o, all, row, min(p.split, blocks), lane, acc);
-  const int token = m_row / p.group, head = kv * p.group + (m_row - token * p.group), rank = head / p.heads_per_rank;
+  const int token = m_row >> p.group_shift, head = set * p.group + (m_row & (p.group - 1)), rank = head / p.heads_per_rank;
   __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + token * p.a_ld[rank] +
                        static_cast<long long>(head - rank * p.heads_per_rank) * D + lane * kPer;
   const float inv = 1.f / l;
@@ -637,12 +665,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_const
 
 // Key splits of an item: the fewest block steps of the busiest CTA, counting about four blocks'
 // time for an item's start and its partial results. One where the items fill the SMs.
-int splits_of(long long rows, int group, int heads_kv, int tokens, int keys, int window, int sinks) {
-  const int pairs = static_cast<int>((rows + 255) / 256);
-  const long long bases = static_cast<long long>(pairs) * heads_kv;
+int splits_of(int group, int sets, int tokens, int keys, int window, int sinks) {
+  const int pairs = static_cast<int>((static_cast<long long>(tokens) * group + 255) / 256);
+  const long long bases = static_cast<long long>(pairs) * sets;
   const int sms = num_sms();
   if (bases >= sms) return 1;
-  const int most = keys_of(pairs - 1, static_cast<int>(rows), group, tokens, keys, window, sinks).blocks;
+  const int most = keys_of(256 * (pairs - 1) / group, tokens - 1, tokens, keys, window, sinks).blocks;
   int split = 1;
   long long best = -1;
   for (int c = 1; c <= most && bases * c <= 2LL * sms; ++c) {
@@ -653,6 +681,14 @@ int splits_of(long long rows, int group, int heads_kv, int tokens, int keys, int
     }
   }
   return split;
+}
+
+// Heads that share a tile.
+int group_of(const tp_dims &d) {
+  const int a = d.num_q_heads / d.num_kv_heads, b = d.num_q_heads / d.tp_size;
+  int g = 1;
+  while (g < 128 && a % (2 * g) == 0 && b % (2 * g) == 0) g *= 2;
+  return g;
 }
 
 // Sizes that the item arithmetic takes in 32 bits.
@@ -679,11 +715,11 @@ tp_status launch_window(const WindowParams &p, const WindowMaps &maps, cudaStrea
   static std::mutex mu;
   const cudaError_t e = allow_smem(k_window<D>, static_cast<int>(WinCfg<D>::kSmem), mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
-  const long long items = static_cast<long long>(p.heads_kv) * p.pairs * p.split;
+  const long long items = static_cast<long long>(p.sets) * p.pairs * p.split;
   const unsigned grid = static_cast<unsigned>(items < num_sms() ? items : num_sms());
   tp_status st = launched(launch_kernel(k_window<D>, dim3(grid), dim3(kWinThreads), WinCfg<D>::kSmem, s, 1, p, maps));
   if (st != TP_OK || p.split == 1) return st;
-  const long long all = static_cast<long long>(p.heads_kv) * p.rows;
+  const long long all = static_cast<long long>(p.sets) * p.rows;
   return launched(launch_kernel(k_window_join<D>, dim3(static_cast<unsigned>((all + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
                                 dim3(kJoinThreads), 0, s, 1, p));
 }
@@ -706,8 +742,8 @@ extern "C" size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tok
   tp_dims d;
   if (!plan || tokens < 1 || keys < tokens || window < 1 || sinks < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
   if (!sizes_ok(d, tokens, keys)) return 0;
-  const int group = d.num_q_heads / d.num_kv_heads;
-  const int split = splits_of(tokens * group, group, d.num_kv_heads, static_cast<int>(tokens), static_cast<int>(keys), window, sinks);
+  const int group = group_of(d);
+  const int split = splits_of(group, d.num_q_heads / group, static_cast<int>(tokens), static_cast<int>(keys), window, sinks);
   return workspace_bytes_of(split, tokens * d.num_q_heads, d.head_dim);
 }
 
@@ -737,9 +773,9 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
     if ((st = check(k[r], S, kvc)) != TP_OK || (st = check(v[r], S, kvc)) != TP_OK) return st;
   if (S < T) return TP_ERR_INVALID_ARG;
   if (!sizes_ok(dims, T, S)) return TP_ERR_UNSUPPORTED;
-  const int group = dims.num_q_heads / dims.num_kv_heads;
+  const int group = group_of(dims), sets = dims.num_q_heads / group;
   const long long rows_all = T * dims.num_q_heads;
-  const int split = T > 0 ? splits_of(T * group, group, dims.num_kv_heads, static_cast<int>(T), static_cast<int>(S), window, sinks) : 1;
+  const int split = T > 0 ? splits_of(group, sets, static_cast<int>(T), static_cast<int>(S), window, sinks) : 1;
   const size_t need = workspace_bytes_of(split, rows_all, hd);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return TP_ERR_WORKSPACE;
@@ -751,11 +787,12 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
   const cudaError_t e = get_dev_ctx(&ctx);
   if (e != cudaSuccess) return cuda_fail(e);
   static thread_local WindowParams p;
-  static thread_local WindowMaps maps;  // 16 KB: kept off the stack
+  static thread_local WindowMaps maps;  // 20 KB: kept off the stack
   std::memset(&p, 0, sizeof(p));
   for (int r = 0; r < n; ++r) {
-    p.q[r] = q[r].ptr;
-    p.q_ld[r] = q[r].ld;
+    tp_tensor qr = q[r];
+    if (T == 1) qr.ld = qc;  // the pitch of a single row is free
+    if (!encode_heads_map(&maps.q[r], qr, static_cast<int>(hd), group, 128 / group)) return TP_ERR_INVALID_ARG;
     p.a[r] = a[r].ptr;
     p.a_ld[r] = a[r].ld;
   }
@@ -776,13 +813,16 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
   p.window = window;
   p.sinks = sinks;
   p.group = group;
-  p.heads_q = dims.num_q_heads;
-  p.heads_kv = dims.num_kv_heads;
+  while ((1 << p.group_shift) < group) ++p.group_shift;
+  p.sets = sets;
+  p.sets_per_kv = sets / dims.num_kv_heads;
   p.heads_per_rank = dims.num_q_heads / n;
   p.heads_per_source = dims.num_kv_heads / sources;
   p.rows = static_cast<int>(T * group);
   p.pairs = (p.rows + 255) / 256;
   p.split = split;
+  p.by_sets.set(sets);
+  p.by_split.set(split);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
   p.part_o = static_cast<float *>(workspace);
   p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + sums_bytes(split, rows_all, hd));

@@ -48,7 +48,7 @@ using namespace op;
 constexpr int kWinRanks = 32;
 constexpr int kWinThreads = 512;
 // Registers a thread: 128 at launch; the softmax's two warpgroups take what the other two give up.
-constexpr int kRegsOthers = 80, kRegsSoftmax = 176;
+constexpr int kRegsOthers = 64, kRegsSoftmax = 192;
 static_assert(kRegsOthers + kRegsSoftmax <= 2 * 128, "the split fits the launch's registers");
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
 constexpr float kSumLimit = 0x1p64f;
@@ -450,9 +450,16 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       return false;
     };
     uint32_t gs = 0, nact = 0;
-    Item it;
-    for (int r = 0; ok && next_item(r, it);) {
-      if ((2 * it.pair + x) * 128 >= rows) continue;
+    // the next item with rows in this tile
+    auto next_rows = [&](int &r, Item &i) {
+      while (next_item(r, i))
+        if ((2 * i.pair + x) * 128 < rows) return true;
+      return false;
+    };
+    Item it, next;
+    int r = 0;
+    bool have = next_rows(r, it), more = false;
+    for (; ok && have; it = next, have = more) {
       const int m_row = (2 * it.pair + x) * 128 + row;  // row of the set: token * group + head
       const bool there = m_row < rows;
       const int token = there ? m_row >> p.group_shift : 0;
@@ -466,6 +473,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         const int k0 = it.k.w0 + 128 * j;  // key of column 0 of the window run
         const int hi = min(pos - k0 + 1, 16 * wu), lo = w0 - k0, first = p.sinks - k0;  // seen: i < hi and (i >= lo or i < first)
         const int hs = it.k.sinks - (128 * j - 16 * it.k.w_units);                     // seen of the first tokens: i < hs
+        if (j + 1 == it.j1) more = next_rows(r, next);  // while S is on its way
         if (!wait_all(s_full, gs & 1)) {
           ok = false;
           break;
@@ -480,14 +488,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         if (__any_sync(0xffffffffu, hi < 128 || (lo > 0 && first < 128))) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
+            if (__all_sync(0xffffffffu, hi >= 32 * h + 32 && lo <= 32 * h)) continue;
             const uint32_t win = low_bits(16 * wu - 32 * h);
             const uint32_t see = (low_bits(hi - 32 * h) & (~low_bits(lo - 32 * h) | low_bits(first - 32 * h))) |
                                  (low_bits(min(hs, 16 * n) - 32 * h) & ~win);
-            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(see & (1u << i))) v[32 * h + i] = __float_as_uint(-INFINITY);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!(see & (1u << i))) v[32 * h + i] = __float_as_uint(-INFINITY);
           }
         }
         const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
@@ -515,20 +522,17 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
           for (int h = 0; h < 4; ++h) {
             uint64_t &sum2 = sumh[h];
             sum2 = pack2(0.f, 0.f);
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {  // P leaves in pieces of 16 keys: v holds most registers
-              uint32_t pk[8];
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const int k = 32 * h + e + i;
-                float y0, y1;
-                unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, nm2), y0, y1);
-                const float a0 = ex2(y0), a1 = ex2(y1);
-                sum2 = add2(sum2, pack2(a0, a1));
-                pk[i >> 1] = pack_bf16(a0, a1);
-              }
-              ptx::tmem_st_8cols(sb + 16 * h + e / 2, pk);
+            for (int i = 0; i < 32; i += 2) {
+              const int k = 32 * h + i;
+              float y0, y1;
+              unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, nm2), y0, y1);
+              const float a0 = ex2(y0), a1 = ex2(y1);
+              sum2 = add2(sum2, pack2(a0, a1));
+              pk[i >> 1] = pack_bf16(a0, a1);
             }
+            ptx::tmem_st_16cols(sb + 16 * h, pk);
           }
           unpack2(add2(add2(sumh[0], sumh[1]), add2(sumh[2], sumh[3])), s0, s1);
           if (find_max || !__any_sync(0xffffffffu, !(s0 + s1 <= kSumLimit))) break;

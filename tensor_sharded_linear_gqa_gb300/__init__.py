@@ -194,14 +194,20 @@ def _load_describe():
     """The same in C, for plain tensors (a small call's issue time is mostly this), loaded by the first
     tensor that is described: importing the package maps no object. None where it is not built (an
     interpreter without its headers): interpreted code does it all."""
-    global _describe, _matrix, _matrices, _row
+    global _describe, _matrix, _matrices, _row, _vector, _bytes
     if "_describe" not in globals():
+        try:
+            import torch  # noqa: F401  the module reads tensors through torch's own libraries
+        except ImportError:
+            pass
         try:
             _describe = importlib.import_module("._describe", __name__)
             _matrix, _matrices, _row = _describe.matrix, _describe.matrices, _describe.row
+            _vector, _bytes = _describe.vector, _describe.bytes
         except ImportError:
             _describe = None
             _matrix = _row = lambda t, to: False  # noqa: E731
+            _vector, _bytes = lambda t, kind, n: None, lambda t: None  # noqa: E731
             _matrices = lambda seq, n, to: 0  # noqa: E731
     return _describe
 
@@ -235,6 +241,16 @@ def _matrices(seq, n, to):
 def _row(t, to):
     _dtypes()
     return _row(t, to)
+
+
+def _vector(t, kind, n):
+    _dtypes()
+    return _vector(t, kind, n)
+
+
+def _bytes(t):
+    _dtypes()
+    return _bytes(t)
 
 
 def _fields(t) -> tuple:
@@ -448,11 +464,15 @@ def tp_moe_workspace_size(dims: TpMoeDims, tokens: int) -> int:
 
 
 _DTYPE_NAMES: dict = {}  # str(dtype) by dtype: formatting it costs more than the rest of the check
+_VECTOR_KINDS = {"torch.float32": TP_F32, "torch.int32": 4}  # the extension module's names of them
 
 
 def _dev_ptr(t, dtype: str, n: int | None = None, what: str = "") -> int:
     """Address of a contiguous CUDA tensor (0 when empty). The library sees no length, so where it
     takes one from elsewhere (n), the tensor's is held against it here."""
+    at = _vector(t, _VECTOR_KINDS[dtype], -1 if n is None else n)
+    if at is not None:
+        return at
     name = _DTYPE_NAMES.get(t.dtype)
     if name is None:
         name = _DTYPE_NAMES[t.dtype] = str(t.dtype)
@@ -675,6 +695,9 @@ def _workspace(t) -> tuple:
     """(address, bytes) of a workspace tensor; None is an empty one."""
     if t is None:
         return None, 0
+    at = _bytes(t)
+    if at is not None:
+        return at
     size = t.numel() * t.element_size()
     if not t.is_contiguous() or not (t.is_cuda or size == 0):
         raise ValueError("workspace must be a contiguous CUDA tensor")

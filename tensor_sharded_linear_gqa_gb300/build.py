@@ -12,6 +12,8 @@ Usage: ``python -m tensor_sharded_linear_gqa_gb300.build [--force] [-v]``.
 from __future__ import annotations
 
 import hashlib
+import importlib.metadata
+import importlib.util
 import json
 import os
 import platform
@@ -33,7 +35,7 @@ DESCRIBE = os.path.join(PKG, "_describe.so")  # the binding's extension module
 SOURCES = ["plan.cpp", "tp_api.cu", "gemm_tcgen05.cu", "gemm_f32.cu", "combine.cu", "mlp_static.cu", "vocab.cu", "moe.cu", "attention.cu",
            "rmsnorm.cu", "cache_evict.cu", "linear_epilogue.cu", "prefix_attention.cu",
            "rotary.cu", "window_attention.cu", "cache4.cu"]
-HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h", "split_join.cuh", "describe.c"]
+HEADERS = ["tp_internal.h", "sm100_ptx.cuh", "op_util.h", "split_join.cuh", "describe.c", "describe_torch.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,8 +61,20 @@ def _python_h() -> str:
     return os.path.join(sysconfig.get_paths()["include"], "Python.h")
 
 
+def _torch() -> tuple:
+    """(version, folder) of the installed torch, without importing it; (None, None) without one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None, None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = None
+    return version, list(spec.submodule_search_locations)[0]
+
+
 def _stamp() -> dict:
-    return {"machine": platform.machine(), "digest": _digest(), "python": sysconfig.get_config_var("SOABI")}
+    return {"machine": platform.machine(), "digest": _digest(), "python": sysconfig.get_config_var("SOABI"), "torch": _torch()[0]}
 
 
 def up_to_date() -> bool:
@@ -91,20 +105,45 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _build_describe(verbose: bool) -> None:
+def _compile_describe_torch(verbose: bool) -> list:
+    """Compiles what reads torch tensors directly; the objects and libraries to link, none without torch's headers."""
+    folder = _torch()[1]
+    if folder is None or not os.path.exists(os.path.join(folder, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return []
+    if not os.path.exists(_python_h()):
+        return []
+    obj = os.path.join(BUILD, "describe_torch.o")
+    cmd = [nvcc(), "-x", "c++", "-std=c++20", "-O2", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", os.path.join(folder, "include"),
+           "-I", os.path.dirname(_python_h()), "-c", os.path.join(CSRC, "describe_torch.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"describe_torch.cpp does not compile against {folder}: tensors are described by way of their attributes\n"
+              + r.stderr[-2000:], file=sys.stderr)
+        return []
+    return [obj, "-L", os.path.join(folder, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+
+
+def _build_describe(torch_parts: list, verbose: bool) -> None:
     """Compiles the extension module that describes tensors; without the interpreter's headers
     there is none, and the binding does without."""
     if not os.path.exists(_python_h()):
         print(f"{_python_h()} is missing: tensors are described by interpreted code", file=sys.stderr)
         return
-    tmp = DESCRIBE + ".tmp"
-    cmd = [nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", "-cudart", "none", "-shared", "-I", INCLUDE,
-           "-I", os.path.dirname(_python_h()), os.path.join(CSRC, "describe.c"), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed on describe.c:\n{r.stdout}\n{r.stderr}")
+    obj, tmp = os.path.join(BUILD, "describe.o"), DESCRIBE + ".tmp"
+    for cmd in ([nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", *(["-DTP_WITH_TORCH"] if torch_parts else []), "-I", INCLUDE,
+                 "-I", os.path.dirname(_python_h()), "-c", os.path.join(CSRC, "describe.c"), "-o", obj],
+                [nvcc(), "-cudart", "none", "-shared", obj, *torch_parts, "-o", tmp]):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0 and torch_parts:
+            print("describe_torch.cpp does not link: tensors are described by way of their attributes\n" + r.stderr[-2000:],
+                  file=sys.stderr)
+            return _build_describe([], verbose)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed on describe.c:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, DESCRIBE)
 
 
@@ -113,7 +152,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        torch_parts = ex.submit(_compile_describe_torch, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
@@ -123,7 +163,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_describe(verbose)
+    _build_describe(torch_parts.result(), verbose)
     with open(STAMP, "w") as fh:
         json.dump(_stamp(), fh)
     return LIB

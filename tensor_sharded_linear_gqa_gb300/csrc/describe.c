@@ -3,6 +3,8 @@
  * A call's descriptors are most of a small call's issue time: 0.9 us a tensor when
  * they are packed by interpreted code, and a one-token projection has eighteen.
  *
+ * Built with describe_torch.cpp, where torch's headers are, plain tensors are read without their attributes.
+ *
  * Only what needs no words is taken here: a CUDA tensor of a type that the library
  * knows, not empty, with unit column stride. Everything else (and every error) is
  * left to the caller, which gets a false result and no exception. */
@@ -10,6 +12,11 @@
 #include <Python.h>
 
 #include "tpgqa.h"
+
+#ifdef TP_WITH_TORCH /* describe_torch.cpp */
+int tp_describe_torch(PyObject *t, long dims, tp_tensor *d);
+unsigned long long tp_address_torch(PyObject *t, int type, long long n, unsigned long long *bytes);
+#endif
 
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr;
 static PyObject *known[4]; /* by tp_dtype: the type objects, which live as long as torch does */
@@ -26,6 +33,10 @@ static int items(PyObject *t, long long *out, Py_ssize_t n) {
 }
 
 static int describe(PyObject *t, Py_ssize_t dims, tp_tensor *d) {
+#ifdef TP_WITH_TORCH
+  const int done = tp_describe_torch(t, (long)dims, d);
+  if (done >= 0) return done;
+#endif
   PyObject *v = PyObject_GetAttr(t, s_dtype);
   int type = 0;
   while (type < 4 && (v == NULL || v != known[type])) ++type;
@@ -98,6 +109,35 @@ static PyObject *py_matrices(PyObject *self, PyObject *const *args, Py_ssize_t n
   return PyLong_FromSsize_t(done);
 }
 
+/* Addresses of contiguous CUDA tensors, or None where the caller has to look for itself. */
+static PyObject *py_vector(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) return PyErr_Format(PyExc_TypeError, "vector(tensor, type, entries)");
+  const long type = PyLong_AsLong(args[1]);
+  const long long entries = PyLong_AsLongLong(args[2]);
+  if (PyErr_Occurred()) return NULL;
+  unsigned long long at = 0, bytes = 0;
+#ifdef TP_WITH_TORCH
+  at = type >= 0 ? tp_address_torch(args[0], (int)type, entries, &bytes) : 0;
+#endif
+  (void)type, (void)entries, (void)bytes;
+  if (at == 0) Py_RETURN_NONE;
+  return PyLong_FromUnsignedLongLong(at);
+}
+
+static PyObject *py_bytes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  (void)self;
+  if (n != 1) return PyErr_Format(PyExc_TypeError, "bytes(tensor)");
+  unsigned long long at = 0, bytes = 0;
+#ifdef TP_WITH_TORCH
+  at = tp_address_torch(args[0], -1, -1, &bytes);
+#else
+  (void)args;
+#endif
+  if (at == 0) Py_RETURN_NONE;
+  return Py_BuildValue("KK", at, bytes);
+}
+
 static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
   if (n != 4) return PyErr_Format(PyExc_TypeError, "dtypes(f32, bf16, e4m3, u8)");
@@ -113,6 +153,8 @@ static PyMethodDef methods[] = {
     {"matrix", (PyCFunction)(void (*)(void))py_matrix, METH_FASTCALL, "matrix(tensor, address) -> whether it was described there"},
     {"row", (PyCFunction)(void (*)(void))py_row, METH_FASTCALL, "row(tensor, address): a 1-D tensor as a matrix of one row"},
     {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address) -> how many of the first were described"},
+    {"vector", (PyCFunction)(void (*)(void))py_vector, METH_FASTCALL, "vector(tensor, type, entries) -> address of a contiguous CUDA tensor of the type (tp_dtype, 4 for int32) with that many entries (-1: any), or None"},
+    {"bytes", (PyCFunction)(void (*)(void))py_bytes, METH_FASTCALL, "bytes(tensor) -> (address, size) of a contiguous CUDA tensor, or None"},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_describe", "Descriptors of torch tensors.", -1, methods, NULL, NULL, NULL, NULL};
 

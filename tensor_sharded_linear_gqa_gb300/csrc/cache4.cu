@@ -61,11 +61,12 @@ __device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {
 }
 
 // ---------------------------------------------------------------------------
-// Storing and reading back. A thread has 8 neighbouring values (16 bytes of bf16): four threads a
-// group. Bound by memory.
+// Storing and reading back. A thread has 32 values of a row, whose codes are 16 neighbouring bytes: 8 of
+// each of four groups (d = 128) or 16 of each of two (d = 64). Bound by memory and, nearly as much, by
+// issue; with 8 neighbouring values a thread, whose addresses and scales cost as much and whose codes
+// are words apart, 16384 tokens of 8 heads took 30 us to store and 21 to read back.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = 4;  // rows (token and head) in flight a thread
 
 struct CopyParams {
   Cache4 cache;
@@ -78,14 +79,31 @@ struct CopyParams {
   int *status;
 };
 
-// Where piece i of a group's lies in a row of codes with G groups, in bytes.
-template <int G>
-__device__ __forceinline__ int k_byte(int group, int piece) { return (piece * G + group) * 4; }
-template <int G>
-__device__ __forceinline__ int v_byte(int group, int piece) { return (piece * G + group) * 2; }
+// A thread's four chunks of 8 values: chunk i of thread c of a row.
+template <int D>
+__device__ __forceinline__ constexpr int chunk_group(int i) { return D == 128 ? i : i >> 1; }
+template <int D>
+__device__ __forceinline__ int chunk_at(int i, int c) { return D == 128 ? i * kGroup + c * 8 : (i >> 1) * kGroup + c * 16 + (i & 1) * 8; }
+// The 16 bytes of a row from the chunks' codes (8 a word), and back. Both are their own inverses: words change
+// places (K, d = 64), or halves of words, the two pieces of 4 values (V).
+template <int D>
+__device__ __forceinline__ uint4 k_order(const uint4 &w) { return D == 128 ? w : make_uint4(w.x, w.z, w.y, w.w); }
+template <int D>
+__device__ __forceinline__ uint4 v_to_row(const uint4 &w) {
+  const uint32_t a = D == 128 ? w.y : w.z, b = D == 128 ? w.z : w.y;  // what lies beside the first and the last chunk's codes
+  const uint32_t p0 = __byte_perm(w.x, a, 0x5410), p1 = __byte_perm(w.x, a, 0x7632);
+  const uint32_t p2 = __byte_perm(b, w.w, 0x5410), p3 = __byte_perm(b, w.w, 0x7632);
+  return D == 128 ? make_uint4(p0, p2, p1, p3) : make_uint4(p0, p1, p2, p3);
+}
+template <int D>
+__device__ __forceinline__ uint4 v_from_row(const uint4 &w) {
+  const uint32_t p0 = w.x, p1 = D == 128 ? w.z : w.y, p2 = D == 128 ? w.y : w.z, p3 = w.w;
+  const uint32_t x = __byte_perm(p0, p1, 0x5410), a = __byte_perm(p0, p1, 0x7632);
+  const uint32_t b = __byte_perm(p2, p3, 0x5410), last = __byte_perm(p2, p3, 0x7632);
+  return D == 128 ? make_uint4(x, a, b, last) : make_uint4(x, b, a, last);
+}
 
-// A CTA has rows [r0, r0 + kRows * kCopyRows) of sequence blockIdx.z's n * heads rows, the heads of a
-// token neighbours.
+// Rows of sequence blockIdx.z: n tokens by heads, the heads of a token neighbours.
 struct RowAt {
   int i, src, h;  // token, kv source, head of the source
 };
@@ -110,147 +128,148 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The 8 codes of 8 bf16 values and their group's scale (the four threads of a group together).
-__device__ __forceinline__ uint32_t encode(const uint32_t (&w)[4], __nv_bfloat16 *scale_out) {
-  // the largest size as bf16 bits, in whose order infinities and then NaN come last
-  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t bits = max(m & 0xffffu, m >> 16);
+// The scale of a group whose largest size has these bf16 bits.
+__device__ __forceinline__ __nv_bfloat16 scale_of(uint32_t bits) {
   const float top = __uint_as_float(bits << 16);
-  // values near f32's smallest have no reciprocal: the group goes up by 2^80
+  // below, f32's smallest values are near: up by 2^80 for the division
   const bool tiny = top < 0x1p-60f;
-  const float lift = tiny ? 0x1p80f : 1.f;
-  float q7 = rounded_quotient(top * lift, 7.f, 1.f / 7.f);
-  if (tiny) q7 *= 0x1p-80f;
-  if (bits >= 0x7f80u) q7 = NAN;
-  const __nv_bfloat16 scale = __float2bfloat16_rn(q7);
-  *scale_out = scale;
-  float s = __bfloat162float(scale) * lift, r = rcp_approx(s);
+  float q = rounded_quotient(tiny ? top * 0x1p80f : top, 7.f, 1.f / 7.f);
+  if (tiny) q *= 0x1p-80f;
+  return __float2bfloat16_rn(bits >= 0x7f80u ? NAN : q);  // infinities and NaN
+}
+// 8 codes of 8 values. TINY: the scale is so small that it has no reciprocal, and the group goes up by 2^80.
+template <bool TINY>
+__device__ __forceinline__ uint32_t codes_of(const uint4 &v, float s) {
+  if (TINY) s *= 0x1p80f;
+  float r = rcp_approx(s);
   if (!(s > 0.f)) s = r = 0.f;  // all codes 8
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float c = rounded_quotient((i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * lift, s, r);
-    if (tiny) c = fminf(fmaxf(c, -8.f), 7.f);  // elsewhere |c| < 7.1: a scale is off by 2^-8 at most
+    const float x = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    float c = rounded_quotient(TINY ? x * 0x1p80f : x, s, r);
+    if (TINY) c = fminf(fmaxf(c, -8.f), 7.f);  // elsewhere |c| < 7.1: a scale is off by 2^-8 at most
     // 1.5 * 2^23 + 8 + c rounds c to even and has the code in its low bits; what it has above them
     // adds up to a constant over the eight
-    codes += __float_as_uint(c + 12582920.f) << (4 * i);
+    codes += __float_as_uint(c + 12582920.f) * (1u << (4 * i));
   }
-  constexpr uint32_t kHigh = 0x4b400000u;  // 1.5 * 2^23
-  return codes - kHigh * 0x11111111u;
+  return codes - 0x4b400000u * 0x11111111u;  // of 1.5 * 2^23
 }
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_constant__ CopyParams p) {
-  constexpr int G = D / kGroup, kPer = D / 8;  // groups, threads a row
-  constexpr int kRows = kCopyThreads / kPer;   // rows of a CTA at once
+  constexpr int G = D / kGroup, kPer = D / 32;  // groups, threads a row
+  constexpr int kRows = kCopyThreads / kPer;    // rows of a CTA
   grid_dep_wait();
   grid_dep_launch();
   const int which = blockIdx.y, b = blockIdx.z;  // keys or values; sequence
-  const int rows = p.n * p.heads_kv;
-  const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
-  const int r0 = blockIdx.x * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int c = threadIdx.x % kPer, row = blockIdx.x * kRows + threadIdx.x / kPer;
   const int start = p.starts[b], given = p.counts ? p.counts[b] : p.n;
   const bool start_ok = start >= 0 && start <= p.cap;
   const int count = start_ok ? min(min(max(given, 0), p.n), p.cap - start) : 0;
   if (count != given && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
-  uint4 raw[kCopyRows];
-  long long to[kCopyRows];  // row of the cache, -1: not stored
-  int src[kCopyRows];
+  const RowAt r = row_at(row, p);
+  const bool there = row < p.n * p.heads_kv && r.i < count;
+  uint4 v[4] = {};
+  if (there) {
+    const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(p.in[which][r.src]) +
+                                (static_cast<long long>(b) * p.n + r.i) * p.ld[which][r.src] + r.h * D;
 #pragma unroll
-  for (int u = 0; u < kCopyRows; ++u) {
-    const int row = r0 + u * kRows;
-    to[u] = -1;
-    src[u] = 0;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (row >= rows) continue;
-    const RowAt r = row_at(row, p);
-    if (r.i >= count) continue;
-    src[u] = r.src;
-    to[u] = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
-    const long long token = static_cast<long long>(b) * p.n + r.i;
-    raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.in[which][r.src]) +
-                                              token * p.ld[which][r.src] + r.h * D + at * 8);
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + chunk_at<D>(i, c));
   }
+  // the groups' largest sizes as bf16 bits, in whose order infinities and then NaN come last; two groups a word
+  uint32_t m[G];
 #pragma unroll
-  for (int u = 0; u < kCopyRows; ++u) {
-    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-    __nv_bfloat16 scale;
-    const uint32_t codes = encode(w, &scale);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);  // the same part of the neighbour group
-    if (to[u] < 0) continue;
-    if (part == 0) (which ? p.cache.v_scale : p.cache.k_scale)[src[u]][to[u] * G + group] = scale;
-    uint8_t *row = (which ? p.cache.v_codes : p.cache.k_codes)[src[u]] + to[u] * (D / 2);
-    if (which == 0) {
-      *reinterpret_cast<uint32_t *>(row + k_byte<G>(group, part)) = codes;
-    } else {
-      // this thread's 8 values are pieces 2 part and 2 part + 1; with the neighbour group's it
-      // writes one of them for both groups, which are neighbours in the row
-      const bool odd = group & 1;
-      const uint32_t word = odd ? __byte_perm(other, codes, 0x7632) : __byte_perm(codes, other, 0x5410);
-      *reinterpret_cast<uint32_t *>(row + v_byte<G>(group & ~1, 2 * part + odd)) = word;
-    }
+  for (int g = 0; g < G; ++g) m[g] = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+    m[chunk_group<D>(i)] = __vmaxu2(m[chunk_group<D>(i)], x);
+  }
+  uint32_t pair[G / 2];
+#pragma unroll
+  for (int g = 0; g < G; g += 2) {
+    uint32_t x = __vmaxu2(__byte_perm(m[g], m[g + 1], 0x5410), __byte_perm(m[g], m[g + 1], 0x7632));
+#pragma unroll
+    for (int o = 1; o < kPer; o *= 2) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, o));
+    pair[g / 2] = x;
+  }
+  if (!there) return;
+  __nv_bfloat162 scale[G / 2];
+#pragma unroll
+  for (int g = 0; g < G / 2; ++g) scale[g] = __halves2bfloat162(scale_of(pair[g] & 0xffffu), scale_of(pair[g] >> 16));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = chunk_group<D>(i);
+    const float one = __bfloat162float(g & 1 ? scale[g / 2].y : scale[g / 2].x);
+    if (one < 0x1p-60f && one > 0.f)
+      w[i] = codes_of<true>(v[i], one);
+    else
+      w[i] = codes_of<false>(v[i], one);
+  }
+  const uint4 codes = make_uint4(w[0], w[1], w[2], w[3]);
+  const long long to = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
+  *reinterpret_cast<uint4 *>((which ? p.cache.v_codes : p.cache.k_codes)[r.src] + to * (D / 2) + c * 16) =
+      which ? v_to_row<D>(codes) : k_order<D>(codes);
+  if (c == 0) {
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>((which ? p.cache.v_scale : p.cache.k_scale)[r.src] + to * G);
+    if (G == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&scale[0]), *reinterpret_cast<const uint32_t *>(&scale[G / 2 - 1]));
+    else
+      dst[0] = scale[0];
   }
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_constant__ CopyParams p) {
-  constexpr int G = D / kGroup, kPer = D / 8;
+  constexpr int G = D / kGroup, kPer = D / 32;
   constexpr int kRows = kCopyThreads / kPer;
   grid_dep_wait();
   grid_dep_launch();
   const int which = blockIdx.y, b = blockIdx.z;
-  const int rows = p.n * p.heads_kv;
-  const int at = threadIdx.x % kPer, group = at / 4, part = at % 4;
-  const int r0 = blockIdx.x * (kRows * kCopyRows) + threadIdx.x / kPer;
+  const int c = threadIdx.x % kPer, row = blockIdx.x * kRows + threadIdx.x / kPer;
   const int start = p.starts[b];
   if ((start < 0 || start > p.cap) && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
-  const int there = start >= 0 ? p.cap - start : 0;  // positions that exist; the others are zeros
-  uint32_t codes[kCopyRows];
-  __nv_bfloat16 scale[kCopyRows];
-  T *dst[kCopyRows];
-#pragma unroll
-  for (int u = 0; u < kCopyRows; ++u) {
-    const int row = r0 + u * kRows;
-    dst[u] = nullptr;
-    codes[u] = 0x88888888u;
-    scale[u] = __float2bfloat16_rn(0.f);
-    if (row >= rows) continue;
-    const RowAt r = row_at(row, p);
-    const long long token = static_cast<long long>(b) * p.n + r.i;
-    dst[u] = static_cast<T *>(p.out[which][r.src]) + token * p.ld[which][r.src] + r.h * D + at * 8;
-    if (r.i >= there) continue;
+  if (row >= p.n * p.heads_kv) return;
+  const RowAt r = row_at(row, p);
+  uint4 codes = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+  uint32_t scale[G / 2] = {};
+  if (start >= 0 && r.i < p.cap - start) {  // positions that do not exist are zeros
     const long long from = (static_cast<long long>(b) * p.heads_per_source + r.h) * p.cap + start + r.i;
-    scale[u] = (which ? p.cache.v_scale : p.cache.k_scale)[r.src][from * G + group];
-    const uint8_t *bytes = (which ? p.cache.v_codes : p.cache.k_codes)[r.src] + from * (D / 2);
-    if (which == 0) {
-      codes[u] = *reinterpret_cast<const uint32_t *>(bytes + k_byte<G>(group, part));
+    codes = *reinterpret_cast<const uint4 *>((which ? p.cache.v_codes : p.cache.k_codes)[r.src] + from * (D / 2) + c * 16);
+    codes = which ? v_from_row<D>(codes) : k_order<D>(codes);
+    const uint32_t *s = reinterpret_cast<const uint32_t *>((which ? p.cache.v_scale : p.cache.k_scale)[r.src] + from * G);
+    if (G == 4) {
+      const uint2 two = *reinterpret_cast<const uint2 *>(s);
+      scale[0] = two.x, scale[G / 2 - 1] = two.y;
     } else {
-      const uint32_t lo = *reinterpret_cast<const uint16_t *>(bytes + v_byte<G>(group, 2 * part));
-      const uint32_t hi = *reinterpret_cast<const uint16_t *>(bytes + v_byte<G>(group, 2 * part + 1));
-      codes[u] = lo | hi << 16;
+      scale[0] = *s;
     }
   }
+  T *dst = static_cast<T *>(p.out[which][r.src]) + (static_cast<long long>(b) * p.n + r.i) * p.ld[which][r.src] + r.h * D;
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int u = 0; u < kCopyRows; ++u) {
-    if (!dst[u]) continue;
-    uint32_t pr[4];  // codes i and i + 4, less 8, as bf16 (exact)
+  for (int i = 0; i < 4; ++i) {
+    const int g = chunk_group<D>(i);
+    uint32_t pr[4];  // codes e and e + 4, less 8, as bf16 (exact)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pr[i] = bf16_codes(codes[u] >> (4 * i));
+    for (int e = 0; e < 4; ++e) pr[e] = bf16_codes(w[i] >> (4 * e));
     if (sizeof(T) == 4) {
-      const float s = __bfloat162float(scale[u]);
-      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(bf16_lo(pr[0]) * s, bf16_lo(pr[1]) * s, bf16_lo(pr[2]) * s, bf16_lo(pr[3]) * s);
-      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(bf16_hi(pr[0]) * s, bf16_hi(pr[1]) * s, bf16_hi(pr[2]) * s, bf16_hi(pr[3]) * s);
+      const float s = g & 1 ? bf16_hi(scale[g / 2]) : bf16_lo(scale[g / 2]);
+      float4 *to = reinterpret_cast<float4 *>(dst + chunk_at<D>(i, c));
+      to[0] = make_float4(bf16_lo(pr[0]) * s, bf16_lo(pr[1]) * s, bf16_lo(pr[2]) * s, bf16_lo(pr[3]) * s);
+      to[1] = make_float4(bf16_hi(pr[0]) * s, bf16_hi(pr[1]) * s, bf16_hi(pr[2]) * s, bf16_hi(pr[3]) * s);
     } else {
-      const __nv_bfloat162 s = __bfloat162bfloat162(scale[u]);
+      const uint32_t twice = __byte_perm(scale[g / 2], 0, g & 1 ? 0x3232 : 0x1010);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // one rounding of the product
-        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pr[i]), s);
-        pr[i] = *reinterpret_cast<const uint32_t *>(&v);
+      for (int e = 0; e < 4; ++e) {  // one rounding of the product
+        const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pr[e]), *reinterpret_cast<const __nv_bfloat162 *>(&twice));
+        pr[e] = *reinterpret_cast<const uint32_t *>(&x);
       }
-      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(__byte_perm(pr[0], pr[1], 0x5410), __byte_perm(pr[2], pr[3], 0x5410),
-                                                      __byte_perm(pr[0], pr[1], 0x7632), __byte_perm(pr[2], pr[3], 0x7632));
+      *reinterpret_cast<uint4 *>(dst + chunk_at<D>(i, c)) = make_uint4(__byte_perm(pr[0], pr[1], 0x5410), __byte_perm(pr[2], pr[3], 0x5410),
+                                                                       __byte_perm(pr[0], pr[1], 0x7632), __byte_perm(pr[2], pr[3], 0x7632));
     }
   }
 }
@@ -872,7 +891,7 @@ tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t 
   p.by_heads.set(p.heads_kv);
   p.by_source.set(p.heads_per_source);
   p.status = ctx.status;
-  const long long per = kCopyThreads / (g.hd / 8) * kCopyRows, blocks = (n * p.heads_kv + per - 1) / per;
+  const long long per = kCopyThreads / (g.hd / 32), blocks = (n * p.heads_kv + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(blocks), 2, static_cast<unsigned>(batch));
   if (store) return launched(launch_kernel(g.hd == 128 ? k_cache4_store<128> : k_cache4_store<64>, grid, dim3(kCopyThreads), 0, s, 1, p));
   if (dt == TP_F32)

@@ -121,7 +121,7 @@ struct WinCfg {
   static constexpr uint32_t kTile = kCh * kSubTile;  // a [128 x D] tile
   static constexpr int kSlots = D == 128 ? 5 : 8;    // of the K and V ring
   static constexpr uint32_t kRing = 2 * kTile, kL = kRing + kSlots * kTile, kBar = kL + 1024;
-  static constexpr size_t kSmem = kBar + 288 + 1024;
+  static constexpr size_t kSmem = kBar + 288 + 64 + 1024;
 };
 // A place in the ring: K of block g is tile 2g, V is tile 2g + 1.
 template <int SLOTS>
@@ -217,6 +217,41 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t *>(tmem_slot)), 512);
     ptx::tmem_relinquish();
   }
+  // Before the wait for the kernel before: the first item, for all roles (from the wait to the first K tile
+  // 1.3 us, 2.6 where each role finds it for itself), and the maps, whose first reads are misses too.
+  struct First {
+    Item it;
+    int r, have;
+  };
+  static_assert(sizeof(First) <= 64, "the first item fits");
+  if (threadIdx.x == 96) {
+    First f;
+    f.r = 0;
+    f.have = next_item(f.r, f.it);
+    int *to = reinterpret_cast<int *>(bar_area + 288);
+    if (!f.have) f.it = Item{};
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(First) / 4); ++i) to[i] = reinterpret_cast<const int *>(&f)[i];
+    if (f.have) {
+      const int kv = f.it.set / p.sets_per_kv, src = p.one_map ? 0 : kv / p.heads_per_source;
+      ptx::prefetch_tensormap(&maps.q[f.it.set * p.group / p.heads_per_rank]);
+      ptx::prefetch_tensormap(&maps.k[src]);
+      ptx::prefetch_tensormap(&maps.v[src]);
+      if (f.it.k.sinks > 0) {
+        ptx::prefetch_tensormap(&maps.k16[src]);
+        ptx::prefetch_tensormap(&maps.v16[src]);
+      }
+    }
+  }
+  auto first_item = [&](int &r, Item &it) {
+    First f;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(First) / 4); ++i)
+      reinterpret_cast<int *>(&f)[i] = reinterpret_cast<const int *>(bar_area + 288)[i];
+    it = f.it;
+    r = f.r;
+    return f.have != 0;
+  };
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -232,7 +267,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       Slot<C::kSlots> at = {0, 0};
       int filled = 0;
       Item it;
-      for (int r = 0; run && next_item(r, it);) {
+      int r;
+      for (bool have = first_item(r, it); run && have; have = next_item(r, it)) {
         const int kv = it.set / p.sets_per_kv, src = p.one_map ? 0 : kv / p.heads_per_source;
         const int col = (kv - src * p.heads_per_source) * D;
         for (int t = 2 * it.j0; run && t < 2 * it.j1; ++t) {  // K, V of block t / 2
@@ -326,11 +362,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       int units, nb;  // from its first block on; its blocks, 0: no item
       bool mine;      // the tile has rows
     };
-    int r = 0;
-    auto next_work = [&]() {
-      Item it;
+    auto work = [&](const Item &it, bool have) {
       Work w = {0, 0, false};
-      if (next_item(r, it)) w = {it.k.units - 8 * it.j0, it.j1 - it.j0, x < tiles_of(it)};
+      if (have) w = {it.k.units - 8 * it.j0, it.j1 - it.j0, x < tiles_of(it)};
       return w;
     };
     // The tiles' products are issued in turn, A's P V and next S, then B's. As they come, both tiles would
@@ -349,10 +383,14 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       release(ks.at, w.mine);
       ks.on(2);
     };
-    Work w = next_work();
+    Item it;
+    int r;
+    const bool any = first_item(r, it);
+    Work w = work(it, any);
     if (w.nb > 0) first_s(w);
     while (ok && w.nb > 0) {
-      const Work next = next_work();
+      const bool more = next_item(r, it);
+      const Work next = work(it, more);
       for (int j = 0; ok && j < w.nb; ++j, vs.on(2)) {
         const bool last = j + 1 == w.nb;
         // what is there early is waited for before P, which is there last
@@ -395,8 +433,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     if (lane == 0) {
       Item it;
       uint32_t n[2] = {0, 0};
-      int r = 0;
-      bool have = next_item(r, it), ok = true;
+      int r;
+      bool have = first_item(r, it), ok = true;
       auto place = [&](const Item &i, int &rank, int &head) {
         rank = i.set * p.group / p.heads_per_rank;
         head = i.set * p.group - rank * p.heads_per_rank;
@@ -457,8 +495,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       return false;
     };
     Item it, next;
-    int r = 0;
-    bool have = next_rows(r, it), more = false;
+    int r;
+    bool have = first_item(r, it), more = false;
+    if (have && (2 * it.pair + x) * 128 >= rows) have = next_rows(r, it);
     for (; ok && have; it = next, have = more) {
       const int m_row = (2 * it.pair + x) * 128 + row;  // row of the set: token * group + head
       const bool there = m_row < rows;
@@ -580,7 +619,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     uint32_t nact[2] = {0, 0};
     bool ok = true;
     Item it;
-    for (int r = 0; ok && next_item(r, it);) {
+    int r;
+    for (bool have = first_item(r, it); ok && have; have = next_item(r, it)) {
       for (int x = 0; x < 2; ++x) {
         if ((2 * it.pair + x) * 128 >= rows) continue;
         const int m_row = (2 * it.pair + x) * 128 + row;

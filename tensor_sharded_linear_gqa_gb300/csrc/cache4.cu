@@ -23,9 +23,10 @@
 //   V  codes of two keys are paired by byte permutes, 0x4300 | code is the bf16 128 + code, and
 //      136 is taken off exactly. The values' scales multiply p before it is rounded to bf16,
 //      once a group; movmatrix turns it from S^T's layout into the B operand's.
-// A warp walks 16 keys at a time by itself, through its own ring of cp.async stages; its m, l
-// and O are joined with the other warps' at the end of the CTA's keys, and k_cache4_join joins
-// the CTAs of a (sequence, kv head).
+// A warp walks 32 keys at a time by itself, through its own ring of cp.async stages; its m, l
+// and O are joined with the other warps' at the end of the CTA's keys. Where they are few, the CTAs
+// of a (sequence, kv head) are a cluster and join their sums through distributed shared memory; else
+// they leave them in memory for k_cache4_join. Either way they share a sequence's keys evenly.
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -285,8 +286,9 @@ struct Attn4Params {
   Cache4 cache;
   int batch, cap, heads_q, heads_kv, group, heads_per_rank, heads_per_source;
   int window, sinks;
-  int chunk;               // tiles a split has at most
-  int splits, head_tiles;  // grid y, grid z
+  int chunk;               // without clusters: tiles a split has at most
+  int splits;              // CTAs of a (sequence, kv head) and head tile
+  int cluster;             // whether they are a cluster
   float scale_log2;
   const int *lengths;
   float *part_o;    // [split][row][d], rows kv head by kv head
@@ -382,15 +384,16 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_ml[kAttnWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int kv = blockIdx.x % p.heads_kv, b = blockIdx.x / p.heads_kv;
-  const int split = blockIdx.y, h0 = blockIdx.z * 8 * NT;  // first head of the group here
+  const int unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
+  const int b = unit / p.heads_kv, kv = unit - b * p.heads_kv;
+  const int h0 = blockIdx.y * 8 * NT;  // first head of the group here
   grid_dep_wait();
   grid_dep_launch();
   const int given = p.lengths[b], len = min(max(given, 0), p.cap);
-  if (given != len && kv == 0 && split == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
+  if (given != len && kv == 0 && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
   const Tiles tl = tiles_of(len, p.window, p.sinks);
-  const int n_splits = splits_here(tl, p.chunk);
-  if (split >= n_splits) {
+  const int n_splits = p.cluster ? (len > 0 ? p.splits : 0) : splits_here(tl, p.chunk);
+  if (split >= n_splits) {  // a whole cluster, or a split that this sequence has not
     if (len > 0 || split > 0) return;
     // no key at all: the heads' outputs are zero
     for (int i = threadIdx.x; i < 8 * NT * (D / 2); i += kAttnThreads4) {
@@ -697,36 +700,85 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
             make_float4(o[nt][2 * i][e], o[nt][2 * i][e + 2], o[nt][2 * i + 1][e], o[nt][2 * i + 1][e + 2]);
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * NT * (D / 4); i += kAttnThreads4) {
-    const int hl = i / (D / 4), col = i % (D / 4) * 4, g = h0 + hl;
-    if (g >= p.group) break;
-    float top = -FLT_MAX;
+  constexpr int kMine = 8 * NT * (D / 4) / kAttnThreads4;  // float4s of the CTA's sums a thread
+  float4 acc[kMine];
+  float2 ml[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
+    float top = -FLT_MAX, sum = 0.f;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_ml[w][hl].x);
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      const float2 ml = s_ml[w][hl];
-      const float fw = ex2(ml.x - top);
+      const float2 one = s_ml[w][hl];
+      const float fw = ex2(one.x - top);
       const float4 v = *reinterpret_cast<const float4 *>(sums + (w * 8 * NT + hl) * C::kJoinRow + col);
-      sum += fw * ml.y;
-      acc.x += fw * v.x;
-      acc.y += fw * v.y;
-      acc.z += fw * v.z;
-      acc.w += fw * v.w;
+      sum += fw * one.y;
+      acc[k].x += fw * v.x;
+      acc[k].y += fw * v.y;
+      acc[k].z += fw * v.z;
+      acc[k].w += fw * v.w;
     }
-    const int head = kv * p.group + g;
+    ml[k] = make_float2(top, sum);
+  }
+  auto store = [&](int hl, int col, const float4 &v, float sum) {
+    const int head = kv * p.group + h0 + hl, rank = head / p.heads_per_rank;
+    const float inv = 1.f / sum;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
+                         static_cast<long long>(head - rank * p.heads_per_rank) * D + col;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  };
+  if (n_splits > 1 && p.cluster) {
+    // the CTA's sums in place of the warps', then every CTA joins a part of them
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
+      *reinterpret_cast<float4 *>(sums + hl * C::kJoinRow + col) = acc[k];
+      if (col == 0) *reinterpret_cast<float4 *>(sums + hl * C::kJoinRow + D) = make_float4(ml[k].x, ml[k].y, 0.f, 0.f);
+    }
+    ptx::cluster_sync();
+    const uint32_t mine = ptx::smem_addr(sums);
+    for (int i = split * kAttnThreads4 + threadIdx.x; i < 8 * NT * (D / 4); i += p.splits * kAttnThreads4) {
+      const int hl = i / (D / 4), col = i % (D / 4) * 4;
+      float4 v[8], m8[8];
+#pragma unroll
+      for (int r8 = 0; r8 < 8; ++r8) {
+        const uint32_t at = ptx::mapa_shared(mine, r8 < p.splits ? r8 : 0) + hl * C::kJoinRow * 4;
+        v[r8] = ptx::ld_shared_cluster_f4(at + col * 4);
+        m8[r8] = ptx::ld_shared_cluster_f4(at + D * 4);
+      }
+      float top = -FLT_MAX, sum = 0.f;
+      float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r8 = 0; r8 < 8; ++r8) top = r8 < p.splits ? fmaxf(top, m8[r8].x) : top;
+#pragma unroll
+      for (int r8 = 0; r8 < 8; ++r8) {
+        if (r8 >= p.splits) continue;
+        const float fw = ex2(m8[r8].x - top);
+        sum += fw * m8[r8].y;
+        all.x += fw * v[r8].x;
+        all.y += fw * v[r8].y;
+        all.z += fw * v[r8].z;
+        all.w += fw * v[r8].w;
+      }
+      if (h0 + hl < p.group) store(hl, col, all, sum);
+    }
+    ptx::cluster_sync();  // nothing is read of a CTA that has ended
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
+    if (h0 + hl >= p.group) break;
     if (n_splits == 1) {
-      const float inv = 1.f / sum;
-      const int rank = head / p.heads_per_rank;
-      __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.a[rank]) + b * p.a_ld[rank] +
-                           static_cast<long long>(head - rank * p.heads_per_rank) * D + col;
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      store(hl, col, acc[k], ml[k].y);
     } else {
-      const long long row = (static_cast<long long>(split) * p.batch + b) * p.heads_q + head;
-      *reinterpret_cast<float4 *>(p.part_o + row * D + col) = acc;
-      if (col == 0) p.part_ml[row] = make_float2(top, sum);
+      const long long row = (static_cast<long long>(split) * p.batch + b) * p.heads_q + kv * p.group + h0 + hl;
+      *reinterpret_cast<float4 *>(p.part_o + row * D + col) = acc[k];
+      if (col == 0) p.part_ml[row] = ml[k];
     }
   }
 }
@@ -754,9 +806,9 @@ __global__ void __launch_bounds__(256) k_cache4_join(const __grid_constant__ Att
   for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
 }
 
-// Tiles a split has at most, and the splits that the longest sequence may have.
+// CTAs a (sequence, kv head), and the tiles that each has at most.
 struct Shape4 {
-  int chunk, splits, head_tiles, nt;
+  int chunk, splits, cluster, head_tiles, nt;
 };
 Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long window, long long sinks) {
   Shape4 s;
@@ -776,6 +828,14 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
   // at most 64 splits a sequence
   while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
   s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
+  if (s.splits < 1) s.splits = 1;
+  // Clusters where all of them are resident at once: one launch in place of two (577 keys of 4 heads 4.5 us
+  // and 5.0). With more they wait for SMs to have room for a whole one (64 sequences of
+  // 5000 to 16384 keys, 8 heads: 159 us and 151).
+  int c = 2;
+  while (c < s.splits) c *= 2;
+  s.cluster = s.splits > 1 && c <= 8 && units * c <= 3LL * num_sms();
+  if (s.cluster) s.splits = c;
   return s;
 }
 
@@ -797,13 +857,13 @@ tp_status launch_attn4(const Attn4Params &p, dim3 grid, cudaStream_t s) {
       if (dev < 32) mask |= 1u << dev;
     }
   }
-  return launched(launch_kernel(k_cache4_attn<D, NT>, grid, dim3(kAttnThreads4), kSmem, s, 1, p));
+  return launched(launch_kernel(k_cache4_attn<D, NT>, grid, dim3(kAttnThreads4), kSmem, s, p.cluster ? p.splits : 1, p));
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t sums_bytes(const Shape4 &s, long long rows, long long d) { return s.splits > 1 ? round256(static_cast<size_t>(s.splits) * rows * d * 4) : 0; }
+size_t sums_bytes(const Shape4 &s, long long rows, long long d) { return s.splits > 1 && !s.cluster ? round256(static_cast<size_t>(s.splits) * rows * d * 4) : 0; }
 size_t workspace_bytes_of(const Shape4 &s, long long rows, long long d) {
-  return s.splits > 1 ? sums_bytes(s, rows, d) + round256(static_cast<size_t>(s.splits) * rows * 8) : 0;
+  return s.splits > 1 && !s.cluster ? sums_bytes(s, rows, d) + round256(static_cast<size_t>(s.splits) * rows * 8) : 0;
 }
 
 // Head sizes that the format's layouts cover, and sizes whose grids and indices are in range.
@@ -982,18 +1042,18 @@ extern "C" tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp
   p.window = window;
   p.sinks = sinks;
   p.chunk = s.chunk;
-  p.splits = s.splits > 0 ? s.splits : 1;
-  p.head_tiles = s.head_tiles;
+  p.splits = s.splits;
+  p.cluster = s.cluster;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.hd)));
   p.lengths = lengths;
   p.part_o = static_cast<float *>(workspace);
   p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + sums_bytes(s, rows, g.hd));
   p.status = ctx.status;
   cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(batch * p.heads_kv), static_cast<unsigned>(p.splits), static_cast<unsigned>(s.head_tiles));
+  const dim3 grid(static_cast<unsigned>(batch * p.heads_kv * p.splits), static_cast<unsigned>(s.head_tiles));
   st = g.hd == 128 ? (s.nt == 2 ? launch_attn4<128, 2>(p, grid, str) : launch_attn4<128, 1>(p, grid, str))
                    : (s.nt == 2 ? launch_attn4<64, 2>(p, grid, str) : launch_attn4<64, 1>(p, grid, str));
-  if (st != TP_OK || s.splits < 2) return st;
+  if (st != TP_OK || s.splits < 2 || s.cluster) return st;
   return launched(launch_kernel(g.hd == 128 ? k_cache4_join<128> : k_cache4_join<64>, dim3(static_cast<unsigned>((rows + 7) / 8)),
                                 dim3(256), 0, str, 1, p));
 }

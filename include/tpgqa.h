@@ -721,9 +721,10 @@ size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tokens, int64_
  *  sinks      : >= 0, first tokens that stay visible.
  *  workspace  : at least tp_window_attn_workspace_size bytes, 16-byte aligned; may be
  *               NULL where that is 0.
- * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16. Keys
- * that no query sees are not read, but for those that share a block of 128 with one that
- * is seen: an infinity or NaN among the latter's values reaches the block's queries.
+ * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16. The
+ * keys of about 256 rows (tokens by heads of a group) are read together, and a weight of 0
+ * times an infinity or NaN among their values is NaN: such a value reaches those of
+ * these rows that do not see its key, too. Scores of keys out of sight may be anything.
  * d must be 64 or 128, tp_size at most 32, S at most 2^31 - 257, T * q heads at
  * most 2^28, else TP_ERR_UNSUPPORTED. Outputs overlap no input.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
@@ -737,14 +738,15 @@ tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, const tp_tenso
  * (round half to even; codes 8 where the scale is 0; a group with an infinity or a NaN
  * has the scale NaN). A cache of `batch` sequences with C positions is four tensors per
  * kv source (one per rank, or one when the plan replicates K/V), all contiguous, the
- * codes on 16-byte boundaries, the scales on those of a row (d/16 bytes); row (b * heads + h) * C + j is position j of sequence b's head h,
- * so a sequence's rows are neighbours and a part of the batch is a part of the rows:
+ * codes on 16-byte boundaries, the scales on those of a row (d/16 bytes); row
+ * (b * heads + h) * C + j is position j of sequence b's head h, so a sequence's rows
+ * are neighbours and a part of the batch is a part of the rows:
  *  k_codes, v_codes : TP_U8 [batch*heads*C x d/2], two codes a byte, the first value's in
  *                     the low half. A group's values are cut into pieces, of 8 values
  *                     for keys and of 4 for values; a row has the first pieces of all
  *                     groups, then the second ones, and so on.
  *  k_scale, v_scale : bf16 [batch*heads*C x d/32].
- * d is 64 or 128 and tp_size at most 32, else TP_ERR_UNSUPPORTED. */
+ * d is 64 or 128, tp_size at most 32 and C at most 2^31 - 257, else TP_ERR_UNSUPPORTED. */
 
 /* Stores n new tokens of every sequence behind what its cache has.
  *  lengths : device int32 [batch], the positions held so far: token i of sequence b
@@ -755,7 +757,7 @@ tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, const tp_tenso
  * A length outside [0, C], a count outside [0, n] and tokens past position C - 1 are
  * reported by tp_device_status (TP_ERR_BAD_LENGTH): a sequence with a bad length stores
  * nothing, one with a bad count as many of its n tokens as the nearer bound allows, and
- * tokens past the end are dropped.
+ * tokens past the end are dropped. A batch above 65535 is TP_ERR_UNSUPPORTED.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_UNSUPPORTED,
  * TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
 tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *lengths, const int32_t *counts,

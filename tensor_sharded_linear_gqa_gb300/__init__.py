@@ -332,6 +332,9 @@ class Plan:
     def __init__(self, handle: int, dims: TpDims):
         self.handle = handle
         self.dims = dims
+        # read on every call: ranks, and copies of K/V (one per rank, or one where they are replicated)
+        self.ranks = int(dims.tp_size)
+        self.sources = 1 if dims.num_kv_heads < dims.tp_size else self.ranks
 
     @property
     def tp_size(self) -> int:
@@ -649,7 +652,7 @@ def tp_prefix_attn_workspace_size(plan: Plan, batch: int, prefix: int, capacity:
 
 
 def _kv_sources(plan: Plan) -> int:
-    return 1 if plan.dims.num_kv_heads < plan.dims.tp_size else plan.dims.tp_size
+    return plan.sources
 
 
 def tp_prefix_attn(plan: Plan, q, k_prefix, v_prefix, k_own, v_own, lengths, a, workspace, weight_in=None, weight_out=None,
@@ -709,7 +712,7 @@ def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout
     """Rotates pairs of values of q's and k's heads by positions[axis] * freq. positions: int32 [T] or
     [axes x T]; freq: f32 [pairs]; axis: per pair (rotary_axes), None: all 0. q, q_out: one entry
     per rank, k, k_out: one per kv source; q or k may be None with its output."""
-    n, src, pairs = plan.dims.tp_size, _kv_sources(plan), freq.numel()
+    n, src, pairs = plan.ranks, plan.sources, freq.numel()
     if positions.dim() not in (1, 2):
         raise ValueError("positions must be [T] or [axes x T]")
     axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
@@ -734,7 +737,7 @@ def tp_window_attn_workspace_size(plan: Plan, tokens: int, keys: int, window: in
 def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=None, stream=None) -> None:
     """The last T of S tokens over a sliding window and the first `sinks` tokens. q, a: one entry per
     rank; k, v: one per kv source; workspace: a CUDA byte tensor."""
-    n, src = plan.dims.tp_size, _kv_sources(plan)
+    n, src = plan.ranks, plan.sources
     ws, size = _workspace(workspace)
     g = _args(2 * n + 2 * src)
     st = _lib.tp_window_attn(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
@@ -746,7 +749,7 @@ def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=No
 def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scale, counts=None, stream=None) -> None:
     """Stores the rows of k and v (batch * n tokens) behind the lengths[b] positions that the 4-bit
     caches hold. All but lengths and counts: one entry per kv source."""
-    batch, src = lengths.numel(), _kv_sources(plan)
+    batch, src = lengths.numel(), plan.sources
     g = _args(6 * src)
     st = _lib.tp_cache4_store(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
                               None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
@@ -759,7 +762,7 @@ def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scal
 def tp_cache4_load(plan: Plan, first, k_codes, k_scale, v_codes, v_scale, k_out, v_out, stream=None) -> None:
     """Positions first[b] .. of every sequence from the 4-bit caches into k_out and v_out (batch * n
     rows). All but first: one entry per kv source."""
-    src = _kv_sources(plan)
+    src = plan.sources
     g = _args(6 * src)
     st = _lib.tp_cache4_load(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
                              g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
@@ -776,7 +779,7 @@ def tp_cache4_attn(plan: Plan, q, k_codes, k_scale, v_codes, v_scale, lengths, w
                    stream=None) -> None:
     """One new token per sequence over the 4-bit caches, a sliding window and the first `sinks` tokens.
     q, a: one entry per rank; caches: one per kv source; workspace: a CUDA byte tensor."""
-    n, src = plan.dims.tp_size, _kv_sources(plan)
+    n, src = plan.ranks, plan.sources
     ws, size = _workspace(workspace)
     g = _args(2 * n + 4 * src)
     st = _lib.tp_cache4_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_store(const __grid_cons
   const int start = p.starts[b], given = p.counts ? p.counts[b] : p.n;
   const bool start_ok = start >= 0 && start <= p.cap;
   const int count = start_ok ? min(min(max(given, 0), p.n), p.cap - start) : 0;
-  if (count != given && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
+  if ((!start_ok || count != given) && blockIdx.x == 0 && which == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
   const RowAt r = row_at(row, p);
   const bool there = row < p.n * p.heads_kv && r.i < count;
   uint4 v[4] = {};
@@ -700,12 +700,13 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
             make_float4(o[nt][2 * i][e], o[nt][2 * i][e + 2], o[nt][2 * i + 1][e], o[nt][2 * i + 1][e + 2]);
     }
   __syncthreads();
-  constexpr int kMine = 8 * NT * (D / 4) / kAttnThreads4;  // float4s of the CTA's sums a thread
+  constexpr int kAll = 8 * NT * (D / 4), kMine = (kAll + kAttnThreads4 - 1) / kAttnThreads4;  // float4s of the CTA's sums; a thread's
   float4 acc[kMine];
   float2 ml[kMine];
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
     const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
+    if (i >= kAll) break;
     float top = -FLT_MAX, sum = 0.f;
     acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -736,12 +737,13 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
       const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
+      if (i >= kAll) break;
       *reinterpret_cast<float4 *>(sums + hl * C::kJoinRow + col) = acc[k];
       if (col == 0) *reinterpret_cast<float4 *>(sums + hl * C::kJoinRow + D) = make_float4(ml[k].x, ml[k].y, 0.f, 0.f);
     }
     ptx::cluster_sync();
     const uint32_t mine = ptx::smem_addr(sums);
-    for (int i = split * kAttnThreads4 + threadIdx.x; i < 8 * NT * (D / 4); i += p.splits * kAttnThreads4) {
+    for (int i = split * kAttnThreads4 + threadIdx.x; i < kAll; i += p.splits * kAttnThreads4) {
       const int hl = i / (D / 4), col = i % (D / 4) * 4;
       float4 v[8], m8[8];
 #pragma unroll
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
     const int i = k * kAttnThreads4 + threadIdx.x, hl = i / (D / 4), col = i % (D / 4) * 4;
-    if (h0 + hl >= p.group) break;
+    if (i >= kAll || h0 + hl >= p.group) break;
     if (n_splits == 1) {
       store(hl, col, acc[k], ml[k].y);
     } else {

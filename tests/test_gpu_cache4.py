@@ -146,7 +146,8 @@ def test_counts_and_lengths_out_of_range():
         assert filled == list(range(start, start + count))
     for lengths, counts, kept in (([-1, 0, 0, 0, 0, 0], None, [0, 4, 4, 4, 4, 4]), ([11, 10, 8, 0, 0, 0], None, [0, 0, 2, 4, 4, 4]),
                                   ([0] * 6, [5, -1, 4, 4, 4, 4], [4, 0, 4, 4, 4, 4]),
-                                  ([2 ** 31 - 1, -2 ** 31, 0, 0, 0, 0], None, [0, 0, 4, 4, 4, 4])):
+                                  ([2 ** 31 - 1, -2 ** 31, 0, 0, 0, 0], None, [0, 0, 4, 4, 4, 4]),
+                                  ([-1, 0, 0, 0, 0, 0], [0, 4, 4, 4, 4, 4], [0, 4, 4, 4, 4, 4])):
         c = Cache(1, 1, 1, 128, B, C, fill=0x88)
         c.scale[0].zero_(), c.scale[1].zero_()
         c.store(k, v, ints(*lengths), counts=None if counts is None else ints(*counts))

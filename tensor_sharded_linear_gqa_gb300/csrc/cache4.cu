@@ -586,23 +586,30 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[half][nt][2 * u] = s[half][nt][2 * u + 1] = -INFINITY;
     }
-    // the maximum of the warp's first tile is the first reference; a tile always has a key that is seen
+    // p, and its sums; the references move when a sum says that some p is large, which is rare after
+    // the first tile, whose maximum is the first reference (a tile always has a key that is seen)
     const bool first = t == t0 + warp;
-    bool rise = first;
-    float top[NT][2];
+    float pr[2][NT][4], sum[NT][2];
+    auto weights = [&]() {
+      bool fine = true;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        top[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
-        rise = rise || top[nt][e] > 8.f;
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[half][nt][e] = ex2(s[half][nt][e]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sum[nt][e] = (pr[0][nt][e] + pr[0][nt][e + 2]) + (pr[1][nt][e] + pr[1][nt][e + 2]);
+        fine = fine && sum[nt][0] + sum[nt][1] <= 1024.f;
       }
-    if (__any_sync(0xffffffffu, rise)) {  // some head's reference maximum moves: rarely after the first tiles
+      return fine;
+    };
+    if (__any_sync(0xffffffffu, !weights() || first)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = top[nt][e];
+          float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -620,16 +627,13 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
             o[nt][i][e + 2] *= alpha;
           }
         }
+      weights();
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[half][nt][e] = ex2(s[half][nt][e]);
-        l[nt][0] += s[half][nt][0] + s[half][nt][2];
-        l[nt][1] += s[half][nt][1] + s[half][nt][3];
-      }
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt][0] += sum[nt][0];
+      l[nt][1] += sum[nt][1];
+    }
     // ---- values ----
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -661,8 +665,8 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = turn8x8(pack_bf16(s[half][nt][0] * vs[0][i], s[half][nt][1] * vs[0][i]));
-          pb[nt][1] = turn8x8(pack_bf16(s[half][nt][2] * vs[1][i], s[half][nt][3] * vs[1][i]));
+          pb[nt][0] = turn8x8(pack_bf16(pr[half][nt][0] * vs[0][i], pr[half][nt][1] * vs[0][i]));
+          pb[nt][1] = turn8x8(pack_bf16(pr[half][nt][2] * vs[1][i], pr[half][nt][3] * vs[1][i]));
         }
         const uint32_t lo = __byte_perm(vw[0][i >> 1], vw[1][i >> 1], i & 1 ? 0x7632 : 0x5410);
         const uint32_t hi = __byte_perm(vw[2][i >> 1], vw[3][i >> 1], i & 1 ? 0x7632 : 0x5410);

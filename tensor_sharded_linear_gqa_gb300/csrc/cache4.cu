@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache4_load(const __grid_const
 constexpr int kAttnWarps = 4, kAttnThreads4 = 32 * kAttnWarps;
 constexpr int kTileKeys = 32;  // keys of a warp's step: two products' rows
 constexpr int kStages = 3;
+constexpr int kOrdered = 256;  // sequences that are put in order at most
 
 struct Attn4Params {
   Cache4 cache;
@@ -289,6 +290,7 @@ struct Attn4Params {
   int chunk;               // without clusters: tiles a split has at most
   int splits;              // CTAs of a (sequence, kv head) and head tile
   int cluster;             // whether they are a cluster
+  int longest_first;       // the order in which the sequences' CTAs start; else as they come
   float scale_log2;
   const int *lengths;
   float *part_o;    // [split][row][d], rows kv head by kv head
@@ -376,19 +378,48 @@ constexpr int attn4_smem() {
   return sums > ring ? sums : ring;
 }
 
+// The sequence whose CTAs have the place-th most tiles (those with the same number in order). All threads of
+// the CTA; s_key has kOrdered entries.
+__device__ __forceinline__ int sequence_at(int place, const Attn4Params &p, int *s_key) {
+  __shared__ int s_found;  // not in the ring, which the first warps fill while others read it
+  for (int i = threadIdx.x; i < kOrdered; i += kAttnThreads4) {
+    int key = -1;
+    if (i < p.batch) {
+      const Tiles t = tiles_of(min(max(p.lengths[i], 0), p.cap), p.window, p.sinks);
+      const int n = splits_here(t, p.chunk);
+      key = (n > 0 ? (t.count + n - 1) / n : 0) * kOrdered + (kOrdered - 1 - i);
+    }
+    s_key[i] = key;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.batch; i += kAttnThreads4) {
+    const int key = s_key[i];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < p.batch; j += 4) {
+      const int4 o = *reinterpret_cast<const int4 *>(s_key + j);
+      before += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+    }
+    if (before == place) s_found = i;
+  }
+  __syncthreads();
+  return s_found;
+}
+
 // NT: products of 8 heads a key fragment serves (the CTA has up to 8 NT heads of the group).
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(const __grid_constant__ Attn4Params p) {
   using C = Attn4Cfg<D>;
   constexpr int G = C::kG;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];  // 16 bytes past a line: 147 us in place of 143
   __shared__ float2 s_ml[kAttnWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
-  const int b = unit / p.heads_kv, kv = unit - b * p.heads_kv;
+  const int place = unit / p.heads_kv, kv = unit - place * p.heads_kv;
   const int h0 = blockIdx.y * 8 * NT;  // first head of the group here
   grid_dep_wait();
   grid_dep_launch();
+  const int b = p.longest_first ? sequence_at(place, p, reinterpret_cast<int *>(smem)) : place;
   const int given = p.lengths[b], len = min(max(given, 0), p.cap);
   if (given != len && kv == 0 && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, kDevBadLength);
   const Tiles tl = tiles_of(len, p.window, p.sinks);
@@ -814,7 +845,7 @@ __global__ void __launch_bounds__(256) k_cache4_join(const __grid_constant__ Att
 
 // CTAs a (sequence, kv head), and the tiles that each has at most.
 struct Shape4 {
-  int chunk, splits, cluster, head_tiles, nt;
+  int chunk, splits, cluster, longest_first, head_tiles, nt;
 };
 Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long window, long long sinks) {
   Shape4 s;
@@ -827,10 +858,15 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
     const long long some = (window + kTileKeys - 1) / kTileKeys + 1 + (sinks + kTileKeys - 1) / kTileKeys;
     if (some < tiles) tiles = some;
   }
-  const long long units = batch * d.num_kv_heads * s.head_tiles;
-  // 128 tiles (4096 keys) a CTA, halved while there are fewer than three CTAs an SM, down to a tile a warp
-  s.chunk = 128;
-  while (s.chunk > kAttnWarps && units * ((tiles + s.chunk - 1) / s.chunk) < 3LL * num_sms()) s.chunk /= 2;
+  const long long units = batch * d.num_kv_heads * s.head_tiles, room = (s.nt == 1 ? 3LL : 2LL) * num_sms();
+  auto ctas = [&]() { return units * ((tiles + s.chunk - 1) / s.chunk); };
+  // Up to 256 tiles (8192 keys) a CTA, halved while there is room on the SMs for more CTAs, down to a tile a
+  // warp. Where CTAs start in the order of their length and there are two of them for each place, else 128:
+  // 64 sequences of 5000 to 16384 keys, 8 heads: 142 us with 256 tiles, 150 with 128, 146 with
+  // 256 as they come; 32 such ones 82 with 128, 91 with 256.
+  s.chunk = batch <= kOrdered ? 256 : 128;
+  while (s.chunk > kAttnWarps && ctas() < room) s.chunk /= 2;
+  if (s.chunk > 128 && ctas() < 2 * room) s.chunk = 128;
   // at most 64 splits a sequence
   while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
   s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
@@ -840,8 +876,10 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
   // 5000 to 16384 keys, 8 heads: 159 us and 151).
   int c = 2;
   while (c < s.splits) c *= 2;
-  s.cluster = s.splits > 1 && c <= 8 && units * c <= 3LL * num_sms();
+  s.cluster = s.splits > 1 && c <= 8 && units * c <= room;
   if (s.cluster) s.splits = c;
+  // 61 sequences with up to 1028 keys in sight: 20.5 us, 21.8 as they come; 128 of 1 to 4096 keys: 64 and 74
+  s.longest_first = !s.cluster && batch <= kOrdered && units * s.splits > room;
   return s;
 }
 
@@ -1050,6 +1088,7 @@ extern "C" tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp
   p.chunk = s.chunk;
   p.splits = s.splits;
   p.cluster = s.cluster;
+  p.longest_first = s.longest_first;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.hd)));
   p.lengths = lengths;
   p.part_o = static_cast<float *>(workspace);

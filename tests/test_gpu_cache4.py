@@ -257,6 +257,25 @@ def test_attention(shape):
     assert tp.tp_device_status()[0] == tp.TP_OK
     assert torch.equal(a, c.run(views=False))  # the same bits every time, whatever the pitch
 
+MANY = [  # more CTAs than the SMs hold: up to 256 sequences start in the order of their length
+    (1, 8, 8, 128, 61, 100, [i * 37 % 101 for i in range(61)], ALL, 0), (2, 16, 8, 64, 64, 50, [50] * 64, 20, 2),
+    (1, 8, 4, 128, 130, 70, [i * 29 % 71 for i in range(130)], 40, 3), (4, 8, 4, 64, 256, 33, [(i * i) % 34 for i in range(256)], ALL, 0),
+    (1, 4, 4, 128, 257, 40, [i * 7 % 41 for i in range(257)], 9, 9), (1, 8, 4, 128, 128, 40, [0] * 127 + [40], ALL, 0),
+    (1, 16, 8, 64, 60, 40, [0] * 60, 5, 1), (1, 36, 2, 64, 129, 64, [64 - i % 65 for i in range(129)], 30, 0),
+    (1, 2, 2, 64, 240, 300, [300 - (i * 17) % 301 for i in range(240)], ALL, 0),
+    (1, 1, 1, 64, 33, 8300, [8300 - 251 * i for i in range(33)], ALL, 0),
+]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "-".join(map(str, s[:6] + s[7:])))
+def test_many_sequences(shape):
+    need_gpu()
+    c = Attention(*shape, seed=3)
+    a = c.run()
+    c.check(a)
+    assert tp.tp_device_status()[0] == tp.TP_OK
+    assert torch.equal(a, c.run(views=False))
+
 
 @pytest.mark.parametrize("q_std, k_std", [(4.0, 1.0), (30.0, 1.0), (1e-3, 1e3), (1e20, 1e-20), (1e-20, 1e20), (2.0 ** 90, 2.0 ** -90)])
 def test_sharp_scores_and_sizes(q_std, k_std):

@@ -704,7 +704,8 @@ tp_status tp_rotary(const tp_plan *plan, int64_t tokens, const int32_t *position
                     const tp_tensor *k, tp_tensor *q_out, tp_tensor *k_out, tp_stream_t stream);
 
 /* Workspace bytes tp_window_attn needs for these sizes on the current device: the key
- * splits' f32 partial results where there are too few tokens to fill it, else 0. 0 too
+ * splits' f32 partial results where there are too few tokens to fill it, else 0. Calls that
+ * may run at the same time need one each. 0 too
  * for a null plan and for sizes that the call refuses. */
 size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tokens, int64_t keys, int32_t window, int32_t sinks);
 
@@ -770,15 +771,16 @@ tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *len
  *  first        : device int32 [batch]. One outside [0, C] is reported by
  *                 tp_device_status (TP_ERR_BAD_LENGTH).
  *  k_out, v_out : per kv source [batch*n x heads*d], all f32 (exact) or all bf16 (rounded
- *                 once). Positions outside the cache give zeros.
+ *                 once). Positions past the cache's end give zeros, a sequence with a
+ *                 bad first nothing else.
  * Errors: as tp_cache4_store. */
 tp_status tp_cache4_load(const tp_plan *plan, int64_t batch, const int32_t *first, const tp_tensor *k_codes,
                          const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale, tp_tensor *k_out,
                          tp_tensor *v_out, tp_stream_t stream);
 
 /* Workspace bytes tp_cache4_attn needs for these sizes on the current device (the key
- * splits' f32 partial results; 0 where one CTA takes a whole sequence). It goes by the
- * capacity, not by the lengths. 0 too for a null plan and for sizes that the call refuses. */
+ * splits' f32 partial results; 0 where one CTA or one cluster takes a whole sequence). It
+ * goes by the capacity, not by the lengths. Calls that may run at the same time need one each. 0 too for a null plan and for sizes that the call refuses. */
 size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t capacity, int32_t window, int32_t sinks);
 
 /* Attention of one new token per sequence over its 4-bit cache: with len = lengths[b],

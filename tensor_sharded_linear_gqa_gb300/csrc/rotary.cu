@@ -206,6 +206,7 @@ extern "C" tp_status tp_rotary(const tp_plan *plan, int64_t tokens, const int32_
         if (!elem_aligned(*t)) return TP_ERR_ALIGNMENT;
         vec = vec && vec_aligned(*t);
       }
+      if (tokens > 1 && in[r].ptr == out[r].ptr && in[r].ld != out[r].ld) return TP_ERR_INVALID_ARG;  // rows would meet others
       in_place = in_place && in[r].ptr == out[r].ptr;
       p.in[slot + r] = in[r].ptr;
       p.out[slot + r] = out[r].ptr;

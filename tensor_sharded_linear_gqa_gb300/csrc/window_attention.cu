@@ -844,7 +844,7 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
     p.a_ld[r] = a[r].ld;
   }
   // Sources that are neighbouring columns of one tensor need one map together.
-  p.one_map = 1;
+  p.one_map = S == 1 || (k[0].ld >= kvc * sources && v[0].ld >= kvc * sources);
   for (int r = 1; r < sources; ++r)
     for (const tp_tensor *t : {k, v})
       if (t[r].ld != t[0].ld || static_cast<const char *>(t[0].ptr) + r * kvc * 2 != t[r].ptr) p.one_map = 0;

@@ -177,3 +177,19 @@ def test_no_tokens():
     plan = tp.tp_plan_create(1, 128, 1, 1, 128, 1)
     e, k = torch.empty(0, 128, device="cuda", dtype=BF16), torch.ones(5, 128, device="cuda", dtype=BF16)
     tp.tp_window_attn(plan, [e], [k], [k], 4, 0, [e])
+
+
+def test_sources_that_overlap():
+    """Two sources' keys in one buffer, the second a row on: each has its own pitch of one source."""
+    need_gpu()
+    c = Case(2, 4, 2, 64, 30, 90, 20, 2)
+    buf = torch.randn(91, 64, device="cuda").to(BF16)
+    plan, q = c.plan, c.parts(c.q, 2)
+    ws = torch.empty(tp.tp_window_attn_workspace_size(plan, 30, 90, 20, 2), dtype=torch.uint8, device="cuda")
+    got, want = ([torch.zeros_like(x) for x in q] for _ in range(2))
+    shared = [buf[:90], buf[1:]]
+    tp.tp_window_attn(plan, q, shared, shared, 20, 2, got, ws)
+    apart = [x.clone() for x in shared]
+    tp.tp_window_attn(plan, q, apart, [x.clone() for x in apart], 20, 2, want, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -55,6 +55,8 @@ def test_rotary_sizes_and_none():
     wide = tp.tp_plan_create(1, 1024, 1, 1, 1024, 1)
     big = T(BF, 4, 1024)
     assert rotary_status(plan=wide, pairs=257, q=big, qo=big, k=big, ko=big) == tp.TP_ERR_UNSUPPORTED
+    # in place with another pitch: a row would meet others
+    assert rotary_status(q=T(BF, 4, 256, ld=512), qo=T(BF, 4, 256)) == tp.TP_ERR_INVALID_ARG
     none = T(BF, 0, 256, ptr=None)
     assert rotary_status(tokens=0, pos=None, freq=None, q=none, qo=none, k=None, ko=None) == tp.TP_OK
 

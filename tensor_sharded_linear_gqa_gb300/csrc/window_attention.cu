@@ -260,214 +260,214 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
   ptx::griddep_launch_dependents();
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
-  if (warp == 0) {
-    if (lane == 0) {
-      bool run = true;
-      Slot<C::kSlots> at = {0, 0};
-      int filled = 0;
-      Item it;
-      int r;
-      for (bool have = first_item(r, it); run && have; have = next_item(r, it)) {
-        const int kv = it.set / p.sets_per_kv, src = p.one_map ? 0 : kv / p.heads_per_source;
-        const int col = (kv - src * p.heads_per_source) * D;
-        for (int t = 2 * it.j0; run && t < 2 * it.j1; ++t) {  // K, V of block t / 2
-          const int j = t >> 1, v = t & 1;
-          if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * at.at, at.phase ^ 1, p.wait_ns)) {
-            if (!*abort_flag) record(p.status, kDevTimeoutProducer);
-            *abort_flag = 1;
-            run = false;
-            break;
-          }
-          const int n = it.units(j), w = min(8, it.k.w_units - 8 * j);  // units of the block; of the window run
-          const uint32_t dst = sR + at.at * C::kTile, bar = full0 + 8 * at.at;
-          if (w > 0 && w < n) {  // of both runs: unit by unit
-            const CUtensorMap *map = v ? &maps.v16[src] : &maps.k16[src];
-            ptx::mbar_arrive_expect_tx(bar, n * 2048u * C::kCh);
-            for (int u = 0; u < n; ++u) {
-              const int key = u < w ? it.k.w0 + 128 * j + 16 * u : 128 * j - 16 * it.k.w_units + 16 * u;
-              for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map, col + c * 64, key, bar);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
+    if (warp == 0) {
+      if (lane == 0) {
+        bool run = true;
+        Slot<C::kSlots> at = {0, 0};
+        int filled = 0;
+        Item it;
+        int r;
+        for (bool have = first_item(r, it); run && have; have = next_item(r, it)) {
+          const int kv = it.set / p.sets_per_kv, src = p.one_map ? 0 : kv / p.heads_per_source;
+          const int col = (kv - src * p.heads_per_source) * D;
+          for (int t = 2 * it.j0; run && t < 2 * it.j1; ++t) {  // K, V of block t / 2
+            const int j = t >> 1, v = t & 1;
+            if (*abort_flag || !ptx::mbar_wait(empty0 + 8 * at.at, at.phase ^ 1, p.wait_ns)) {
+              if (!*abort_flag) record(p.status, kDevTimeoutProducer);
+              *abort_flag = 1;
+              run = false;
+              break;
             }
-          } else {
-            const CUtensorMap *map = v ? &maps.v[src] : &maps.k[src];
-            ptx::mbar_arrive_expect_tx(bar, C::kTile);
-            const int key = w > 0 ? it.k.w0 + 128 * j : 128 * j - 16 * it.k.w_units;
-            for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, bar);
+            const int n = it.units(j), w = min(8, it.k.w_units - 8 * j);  // units of the block; of the window run
+            const uint32_t dst = sR + at.at * C::kTile, bar = full0 + 8 * at.at;
+            if (w > 0 && w < n) {  // of both runs: unit by unit
+              const CUtensorMap *map = v ? &maps.v16[src] : &maps.k16[src];
+              ptx::mbar_arrive_expect_tx(bar, n * 2048u * C::kCh);
+              for (int u = 0; u < n; ++u) {
+                const int key = u < w ? it.k.w0 + 128 * j + 16 * u : 128 * j - 16 * it.k.w_units + 16 * u;
+                for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map, col + c * 64, key, bar);
+              }
+            } else {
+              const CUtensorMap *map = v ? &maps.v[src] : &maps.k[src];
+              ptx::mbar_arrive_expect_tx(bar, C::kTile);
+              const int key = w > 0 ? it.k.w0 + 128 * j : 128 * j - 16 * it.k.w_units;
+              for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, bar);
+            }
+            at.on(1);
+            ++filled;
           }
-          at.on(1);
-          ++filled;
         }
+        // every load has landed before the CTA may end: the last fill of each slot
+        Slot<C::kSlots> last = {0, 0};
+        for (int i = 0; i < filled; ++i, last.on(1))
+          if (i + C::kSlots >= filled && !ptx::mbar_wait(full0 + 8 * last.at, last.phase, p.wait_ns)) record(p.status, kDevTimeoutDrain);
       }
-      // every load has landed before the CTA may end: the last fill of each slot
-      Slot<C::kSlots> last = {0, 0};
-      for (int i = 0; i < filled; ++i, last.on(1))
-        if (i + C::kSlots >= filled && !ptx::mbar_wait(full0 + 8 * last.at, last.phase, p.wait_ns)) record(p.status, kDevTimeoutDrain);
-    }
-  } else if (warp < 3) {  // converged; one lane issues (see elect_one)
-    const int x = warp - 1;
-    constexpr uint32_t idesc_s0 = ptx::idesc_bf16_f32(128, 0);  // + 2 units << 17: 16 columns a unit
-    constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
-    // descriptors of the tiles' starts; the address field counts 16 bytes
-    const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sR), vd = desc_mn_sw128(sR, kSubTile);
-    const bool leader = ptx::elect_one();
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, p.wait_ns))) return true;  // an abort elsewhere ends in a timeout here
-      if (*abort_flag == 0) record(p.status, kDevTimeoutMma);
-      ok = false;
-      return false;
-    };
-    auto commit = [&](uint32_t bar) {
-      if (leader) ptx::mma_commit(bar);
-      __syncwarp();
-    };
-    const uint64_t qa = qd + static_cast<uint32_t>(x) * (C::kTile >> 4);
-    const uint32_t td_s = tmem + static_cast<uint32_t>(x * 128), td_o = tmem + 256u + static_cast<uint32_t>(x * 128);
-    auto issue_s = [&](int slot, int n) {  // S = Q K^T, 16 n columns
-      const uint64_t ka = kd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
-      const uint32_t idesc = idesc_s0 + (static_cast<uint32_t>(2 * n) << 17);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_bf16(td_s, qa + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)), ka + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)),
-                        idesc, kk > 0 ? 1u : 0u);
-        ptx::mma_commit(s_full0 + 8 * x);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int slot, bool first, int n) {  // O += P V, 16 keys (2048 bytes of V) a step
-      const uint64_t va = vd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
-      const uint32_t more = first ? 0u : 1u;
-      if (n == 8) {
+    } else if (warp < 3) {  // converged; one lane issues (see elect_one)
+      const int x = warp - 1;
+      constexpr uint32_t idesc_s0 = ptx::idesc_bf16_f32(128, 0);  // + 2 units << 17: 16 columns a unit
+      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+      // descriptors of the tiles' starts; the address field counts 16 bytes
+      const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sR), vd = desc_mn_sw128(sR, kSubTile);
+      const bool leader = ptx::elect_one();
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, p.wait_ns))) return true;  // an abort elsewhere ends in a timeout here
+        if (*abort_flag == 0) record(p.status, kDevTimeoutMma);
+        ok = false;
+        return false;
+      };
+      auto commit = [&](uint32_t bar) {
+        if (leader) ptx::mma_commit(bar);
+        __syncwarp();
+      };
+      const uint64_t qa = qd + static_cast<uint32_t>(x) * (C::kTile >> 4);
+      const uint32_t td_s = tmem + static_cast<uint32_t>(x * 128), td_o = tmem + 256u + static_cast<uint32_t>(x * 128);
+      auto issue_s = [&](int slot, int n) {  // S = Q K^T, 16 n columns
+        const uint64_t ka = kd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
+        const uint32_t idesc = idesc_s0 + (static_cast<uint32_t>(2 * n) << 17);
         if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
+          for (int kk = 0; kk < D / 16; ++kk)
+            ptx::mma_bf16(td_s, qa + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)), ka + ((kk >> 2) * (kSubTile >> 4) + 2 * (kk & 3)),
+                          idesc, kk > 0 ? 1u : 0u);
+          ptx::mma_commit(s_full0 + 8 * x);
         }
-      } else if (leader) {
-#pragma unroll 1
-        for (int kk = 0; kk < n; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
-      }
-      __syncwarp();
-    };
-    // a slot is free of this tile: at once where the tile has no rows, else when its products are done
-    auto release = [&](int slot, bool used) {
-      if (leader) {
-        if (used) ptx::mma_commit(empty0 + 8 * slot);
-        else ptx::mbar_arrive(empty0 + 8 * slot);
-      }
-      __syncwarp();
-    };
-    // what of an item these products need
-    struct Work {
-      int units, nb;  // from its first block on; its blocks, 0: no item
-      bool mine;      // the tile has rows
-    };
-    auto work = [&](const Item &it, bool have) {
-      Work w = {0, 0, false};
-      if (have) w = {it.k.units - 8 * it.j0, it.j1 - it.j0, x < tiles_of(it)};
-      return w;
-    };
-    // The tiles' products are issued in turn, A's P V and next S, then B's. As they come, both tiles would
-    // fall into step: in their softmax together, then in the tensor core's queue.
-    uint32_t turn = 0;
-    uint32_t np = 0, nact = 0;                     // P tiles consumed; items with rows in the tile
-    Slot<C::kSlots> ks = {0, 0}, vs = {1, 0};      // the next block of each
-    auto first_s = [&](const Work &w) {  // the S of an item's first block
-      if (!wait(full0 + 8 * ks.at, ks.phase)) return;
-      if (w.mine) {
-        if (!wait(q_full0 + 8 * x, nact & 1)) return;
-        ptx::tc_fence_after();
-        issue_s(ks.at, min(8, w.units));
-        if (w.nb == 1) commit(q_empty0 + 8 * x);  // the last S of an item frees its Q
-      }
-      release(ks.at, w.mine);
-      ks.on(2);
-    };
-    Item it;
-    int r;
-    const bool any = first_item(r, it);
-    Work w = work(it, any);
-    if (w.nb > 0) first_s(w);
-    while (ok && w.nb > 0) {
-      const bool more = next_item(r, it);
-      const Work next = work(it, more);
-      for (int j = 0; ok && j < w.nb; ++j, vs.on(2)) {
-        const bool last = j + 1 == w.nb;
-        // what is there early is waited for before P, which is there last
-        if (!wait(full0 + 8 * vs.at, vs.phase) || (!last && !wait(full0 + 8 * ks.at, ks.phase))) break;
-        if (!wait(turn0 + 8 * x, turn ^ (x == 0 ? 1 : 0))) break;
-        if (w.mine) {
-          if (j == 0 && !wait(o_free0 + 8 * x, (nact & 1) ^ 1)) break;
-          if (!wait(p_full0 + 8 * x, np & 1)) break;
-          ++np;
-          ptx::tc_fence_after();
-          issue_pv(vs.at, j == 0, min(8, w.units - 8 * j));
-          if (last) {
-            commit(o_full0 + 8 * x);
-            ++nact;
-          } else {
-            issue_s(ks.at, min(8, w.units - 8 * (j + 1)));
-          }
-        }
-        if (leader) ptx::mbar_arrive(turn0 + 8 * (x ^ 1));
-        turn ^= 1;
-        release(vs.at, w.mine);
-        if (last) {
-          if (next.nb > 0) first_s(next);  // this tile's P has been read by the products before
-        } else {
-          if (w.mine && j + 2 == w.nb) commit(q_empty0 + 8 * x);
-          release(ks.at, w.mine);
-          ks.on(2);
-        }
-      }
-      w = next;
-    }
-    if (!ok) *abort_flag = 1;
-    if (leader) {
-      ptx::mma_commit(drain0 + 8 * x);
-      if (!ptx::mbar_wait(drain0 + 8 * x, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
-    }
-    __syncwarp();
-  } else {
-    // ---- the q tiles ----
-    if (lane == 0) {
-      Item it;
-      uint32_t n[2] = {0, 0};
-      int r;
-      bool have = first_item(r, it), ok = true;
-      auto place = [&](const Item &i, int &rank, int &head) {
-        rank = i.set * p.group / p.heads_per_rank;
-        head = i.set * p.group - rank * p.heads_per_rank;
+        __syncwarp();
       };
-      while (have && ok) {
-        int rank, head;
-        place(it, rank, head);
-        for (int x = 0; x < tiles_of(it); ++x) {
-          if (*abort_flag || !ptx::mbar_wait(q_empty0 + 8 * x, (n[x] & 1) ^ 1, p.wait_ns)) {
-            if (!*abort_flag) record(p.status, kDevTimeoutProducer);
-            *abort_flag = 1;
-            ok = false;
-            break;
+      auto issue_pv = [&](int slot, bool first, int n) {  // O += P V, 16 keys (2048 bytes of V) a step
+        const uint64_t va = vd + static_cast<uint32_t>(slot) * (C::kTile >> 4);
+        const uint32_t more = first ? 0u : 1u;
+        if (n == 8) {
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
           }
-          ++n[x];
-          ptx::mbar_arrive_expect_tx(q_full0 + 8 * x, C::kTile);
-          for (int c = 0; c < C::kCh; ++c)
-            ptx::tma_load_3d(sQ + x * C::kTile + c * kSubTile, &maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift,
-                             q_full0 + 8 * x);
+        } else if (leader) {
+#pragma unroll 1
+          for (int kk = 0; kk < n; ++kk) ptx::mma_bf16_ts(td_o, td_s + 8u * kk, va + kk * (2048u >> 4), idesc_o, kk > 0 ? 1u : more);
         }
-        have = ok && next_item(r, it);
-        if (have) {  // into L2 meanwhile
-          place(it, rank, head);
-          for (int x = 0; x < tiles_of(it); ++x)
-            for (int c = 0; c < C::kCh; ++c)
-              ptx::tma_prefetch_l2_3d(&maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift);
+        __syncwarp();
+      };
+      // a slot is free of this tile: at once where the tile has no rows, else when its products are done
+      auto release = [&](int slot, bool used) {
+        if (leader) {
+          if (used) ptx::mma_commit(empty0 + 8 * slot);
+          else ptx::mbar_arrive(empty0 + 8 * slot);
         }
+        __syncwarp();
+      };
+      // what of an item these products need
+      struct Work {
+        int units, nb;  // from its first block on; its blocks, 0: no item
+        bool mine;      // the tile has rows
+      };
+      auto work = [&](const Item &it, bool have) {
+        Work w = {0, 0, false};
+        if (have) w = {it.k.units - 8 * it.j0, it.j1 - it.j0, x < tiles_of(it)};
+        return w;
+      };
+      // The tiles' products are issued in turn, A's P V and next S, then B's. As they come, both tiles would
+      // fall into step: in their softmax together, then in the tensor core's queue.
+      uint32_t turn = 0;
+      uint32_t np = 0, nact = 0;                     // P tiles consumed; items with rows in the tile
+      Slot<C::kSlots> ks = {0, 0}, vs = {1, 0};      // the next block of each
+      auto first_s = [&](const Work &w) {  // the S of an item's first block
+        if (!wait(full0 + 8 * ks.at, ks.phase)) return;
+        if (w.mine) {
+          if (!wait(q_full0 + 8 * x, nact & 1)) return;
+          ptx::tc_fence_after();
+          issue_s(ks.at, min(8, w.units));
+          if (w.nb == 1) commit(q_empty0 + 8 * x);  // the last S of an item frees its Q
+        }
+        release(ks.at, w.mine);
+        ks.on(2);
+      };
+      Item it;
+      int r;
+      const bool any = first_item(r, it);
+      Work w = work(it, any);
+      if (w.nb > 0) first_s(w);
+      while (ok && w.nb > 0) {
+        const bool more = next_item(r, it);
+        const Work next = work(it, more);
+        for (int j = 0; ok && j < w.nb; ++j, vs.on(2)) {
+          const bool last = j + 1 == w.nb;
+          // what is there early is waited for before P, which is there last
+          if (!wait(full0 + 8 * vs.at, vs.phase) || (!last && !wait(full0 + 8 * ks.at, ks.phase))) break;
+          if (!wait(turn0 + 8 * x, turn ^ (x == 0 ? 1 : 0))) break;
+          if (w.mine) {
+            if (j == 0 && !wait(o_free0 + 8 * x, (nact & 1) ^ 1)) break;
+            if (!wait(p_full0 + 8 * x, np & 1)) break;
+            ++np;
+            ptx::tc_fence_after();
+            issue_pv(vs.at, j == 0, min(8, w.units - 8 * j));
+            if (last) {
+              commit(o_full0 + 8 * x);
+              ++nact;
+            } else {
+              issue_s(ks.at, min(8, w.units - 8 * (j + 1)));
+            }
+          }
+          if (leader) ptx::mbar_arrive(turn0 + 8 * (x ^ 1));
+          turn ^= 1;
+          release(vs.at, w.mine);
+          if (last) {
+            if (next.nb > 0) first_s(next);  // this tile's P has been read by the products before
+          } else {
+            if (w.mine && j + 2 == w.nb) commit(q_empty0 + 8 * x);
+            release(ks.at, w.mine);
+            ks.on(2);
+          }
+        }
+        w = next;
       }
-      // every load has landed before the CTA may end
-      for (int x = 0; x < 2; ++x)
-        if (n[x] > 0 && !ptx::mbar_wait(q_full0 + 8 * x, (n[x] - 1) & 1, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      if (!ok) *abort_flag = 1;
+      if (leader) {
+        ptx::mma_commit(drain0 + 8 * x);
+        if (!ptx::mbar_wait(drain0 + 8 * x, 0, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      }
+      __syncwarp();
+    } else {
+      // ---- the q tiles ----
+      if (lane == 0) {
+        Item it;
+        uint32_t n[2] = {0, 0};
+        int r;
+        bool have = first_item(r, it), ok = true;
+        auto place = [&](const Item &i, int &rank, int &head) {
+          rank = i.set * p.group / p.heads_per_rank;
+          head = i.set * p.group - rank * p.heads_per_rank;
+        };
+        while (have && ok) {
+          int rank, head;
+          place(it, rank, head);
+          for (int x = 0; x < tiles_of(it); ++x) {
+            if (*abort_flag || !ptx::mbar_wait(q_empty0 + 8 * x, (n[x] & 1) ^ 1, p.wait_ns)) {
+              if (!*abort_flag) record(p.status, kDevTimeoutProducer);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            ++n[x];
+            ptx::mbar_arrive_expect_tx(q_full0 + 8 * x, C::kTile);
+            for (int c = 0; c < C::kCh; ++c)
+              ptx::tma_load_3d(sQ + x * C::kTile + c * kSubTile, &maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift,
+                               q_full0 + 8 * x);
+          }
+          have = ok && next_item(r, it);
+          if (have) {  // into L2 meanwhile
+            place(it, rank, head);
+            for (int x = 0; x < tiles_of(it); ++x)
+              for (int c = 0; c < C::kCh; ++c)
+                ptx::tma_prefetch_l2_3d(&maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift);
+          }
+        }
+        // every load has landed before the CTA may end
+        for (int x = 0; x < 2; ++x)
+          if (n[x] > 0 && !ptx::mbar_wait(q_full0 + 8 * x, (n[x] - 1) & 1, p.wait_ns)) record(p.status, kDevTimeoutDrain);
+      }
     }
-  }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = (warp - 4) >> 2;

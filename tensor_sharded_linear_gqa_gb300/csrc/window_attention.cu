@@ -6,9 +6,9 @@
 // rows, token by token: with G heads 128 / G tokens a tile, which move the window by
 // that little, and every K and V tile serves all of them. G is the largest power of two that divides
 // both the plan's group and a rank's heads, so that one copy of a 3-D tensor map (values, heads, tokens) brings
-// a tile in this order. A work item is (such a set of heads, pair of adjacent row tiles,
-// key split). Its keys are two runs, the pair's window from its first
-// row's first key on and the first tokens before it, each in units of 16 keys; blocks are 8
+// a tile in this order. A work item is (such a set of heads, two adjacent row tiles or, where there are few, one,
+// key split). Its keys are two runs, the window of its rows from the first row's first key
+// on and the first tokens before it, each in units of 16 keys; blocks are 8
 // neighbouring units of the two runs together, so that only the last one is short (its products are
 // as narrow as it is) and a few first tokens cost a unit, not a block. Masks are applied
 // in the blocks where a row's limits lie.
@@ -19,7 +19,7 @@
 //   warps 1, 2    MMA issuers (tcgen05) of tile A and of tile B: S, P V, S of the next block, ..., over
 //                 the items' ends: the next item's first S follows this one's last P V. One warp
 //                 for both tiles bounds the whole: a product of 128 x 128 x 16 takes the tensor core
-//                 64 cycles and its issue about 80;
+//                 64 cycles and its issue about 80 (2.1 us a step of both tiles in place of 1.55);
 //   warp 3        TMA of the next item's q tiles as soon as this item's last S has read them;
 //   warps 4-7     softmax of tile A, 8-11 of tile B, one thread a row;
 //   warps 12-15   store the outputs, while the softmax is at the next item already.
@@ -29,7 +29,15 @@
 // a block's sum of p passes 2^64 or is not finite, as when the row's first keys were masked:
 // m is then f32's lowest value, the masked keys weigh 0, and the first key that is seen moves m.
 //
-// Where there are too few items for the SMs (few tokens), the blocks of an item are
+// Bounds. A step (128 keys of both tiles, d = 128) is 32 products of 128 x 128 x 16: 1.0 us at 64 cycles
+// each, 1.35 us at the rate of a large library product (1895 TFLOP/s); and 256 x 128 exponentials, 1.0 us
+// of an SM's 16 a clock. It takes 1.55 us. Every item adds about 4.4 us (its first S, the search for
+// the maximum, masked blocks at both of the window's ends, the output), so a window of 1024 and 4 first
+// tokens over 16384 tokens, 64 heads on 8 (9 blocks an item), takes 455 us, 1.17 PFLOP/s over the keys that are
+// seen. Small calls are bound by one item's latency: 2047 tokens of 16 heads of 64, window 300: 9.8 us; one
+// token, 64 heads, 4100 keys: 9.8.
+//
+// Where there are too few items for the SMs (few tokens), items have one row tile, or their blocks are
 // split, the splits leave f32 sums, and k_window_join joins them.
 #include <cfloat>
 #include <cmath>
@@ -57,7 +65,7 @@ struct WindowParams {
   int tokens, keys, window, sinks;
   int group, sets;                  // heads that share a tile; such sets
   int sets_per_kv, heads_per_rank, heads_per_source;
-  int rows, pairs, split;           // rows of a set, pairs of row tiles, key splits
+  int rows, parts, split;           // rows of a set, parts of one or two row tiles, key splits
   Divider by_sets, by_split;
   int group_shift;
   int one_map;                      // every source's K (and V) lies in one tensor, in head order
@@ -75,12 +83,12 @@ struct WindowMaps {
   CUtensorMap k16[kWinRanks], v16[kWinRanks];  // of 16, for blocks of both runs
 };
 
-// The keys of a pair of row tiles in units of 16: the window run (w_units units from key w0 on), then the
+// The keys of an item's rows in units of 16: the window run (w_units units from key w0 on), then the
 // first tokens (units from key 0 on, keys below `sinks`, which end before w0).
 struct Keys {
   int w0, w_units, sinks, units, blocks;
 };
-// Of tokens t0 .. t1, the pair's first and last.
+// Of tokens t0 .. t1, the item's first and last.
 __host__ __device__ inline Keys keys_of(int t0, int t1, int tokens, int keys, int window, int sinks) {
   const int p0 = keys - tokens + t0, p1 = keys - tokens + t1;
   Keys k;
@@ -92,8 +100,11 @@ __host__ __device__ inline Keys keys_of(int t0, int t1, int tokens, int keys, in
   return k;
 }
 
-__device__ __forceinline__ Keys keys_of_pair(const WindowParams &p, int pair) {
-  return keys_of(256 * pair >> p.group_shift, min(256 * pair + 255, p.rows - 1) >> p.group_shift, p.tokens, p.keys, p.window, p.sinks);
+// Of part `part` of the rows: TILES row tiles.
+template <int TILES>
+__device__ __forceinline__ Keys keys_of_part(const WindowParams &p, int part) {
+  constexpr int kRows = 128 * TILES;
+  return keys_of(kRows * part >> p.group_shift, min(kRows * part + kRows - 1, p.rows - 1) >> p.group_shift, p.tokens, p.keys, p.window, p.sinks);
 }
 
 __device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
@@ -140,7 +151,8 @@ struct Slot {
 // n low bits, for any n.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-template <int D>
+// TILES: row tiles of an item.
+template <int D, int TILES>
 __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant__ WindowParams p, const __grid_constant__ WindowMaps maps) {
   using C = WinCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -158,10 +170,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.rows;
-  const int items = p.sets * p.pairs * p.split;
-  // An item: (set of heads, tile pair, split) and its part [j0, j1) of the pair's blocks.
+  const int items = p.sets * p.parts * p.split;
+  // An item: (set of heads, part of the rows, split) and its own [j0, j1) of the part's blocks.
   struct Item {
-    int set, pair, split, j0, j1;
+    int set, part, split, j0, j1;
     Keys k;
     __device__ int units(int j) const { return min(8, k.units - 8 * j); }
   };
@@ -176,10 +188,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       if (i >= items) continue;
       const int first = p.by_split.of(static_cast<int>(i));
       it.split = static_cast<int>(i) - first * p.split;
-      it.pair = p.by_sets.of(first);
-      it.set = first - it.pair * p.sets;
-      it.pair = p.pairs - 1 - it.pair;
-      it.k = keys_of_pair(p, it.pair);
+      it.part = p.by_sets.of(first);
+      it.set = first - it.part * p.sets;
+      it.part = p.parts - 1 - it.part;
+      it.k = keys_of_part<TILES>(p, it.part);
       it.j0 = 0;
       it.j1 = it.k.blocks;
       if (p.split > 1) {
@@ -192,7 +204,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
       return true;
     }
   };
-  auto tiles_of = [&](const Item &it) { return (2 * it.pair + 1) * 128 < rows ? 2 : 1; };
+  auto row_of = [&](const Item &it, int x) { return (TILES * it.part + x) * 128; };  // first row of a tile
+  auto has = [&](const Item &it, int x) { return x < TILES && row_of(it, x) < rows; };
+  auto tiles_of = [&](const Item &it) { return has(it, 1) ? 2 : 1; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -452,7 +466,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
             ++n[x];
             ptx::mbar_arrive_expect_tx(q_full0 + 8 * x, C::kTile);
             for (int c = 0; c < C::kCh; ++c)
-              ptx::tma_load_3d(sQ + x * C::kTile + c * kSubTile, &maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift,
+              ptx::tma_load_3d(sQ + x * C::kTile + c * kSubTile, &maps.q[rank], c * 64, head, row_of(it, x) >> p.group_shift,
                                q_full0 + 8 * x);
           }
           have = ok && next_item(r, it);
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
             place(it, rank, head);
             for (int x = 0; x < tiles_of(it); ++x)
               for (int c = 0; c < C::kCh; ++c)
-                ptx::tma_prefetch_l2_3d(&maps.q[rank], c * 64, head, (2 * it.pair + x) * 128 >> p.group_shift);
+                ptx::tma_prefetch_l2_3d(&maps.q[rank], c * 64, head, row_of(it, x) >> p.group_shift);
           }
         }
         // every load has landed before the CTA may end
@@ -491,15 +505,15 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     // the next item with rows in this tile
     auto next_rows = [&](int &r, Item &i) {
       while (next_item(r, i))
-        if ((2 * i.pair + x) * 128 < rows) return true;
+        if (has(i, x)) return true;
       return false;
     };
     Item it, next;
     int r;
     bool have = first_item(r, it), more = false;
-    if (have && (2 * it.pair + x) * 128 >= rows) have = next_rows(r, it);
+    if (have && !has(it, x)) have = next_rows(r, it);
     for (; ok && have; it = next, have = more) {
-      const int m_row = (2 * it.pair + x) * 128 + row;  // row of the set: token * group + head
+      const int m_row = row_of(it, x) + row;  // row of the set: token * group + head
       const bool there = m_row < rows;
       const int token = there ? m_row >> p.group_shift : 0;
       // the row sees keys [w0, pos] and [0, sinks)
@@ -622,8 +636,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     int r;
     for (bool have = first_item(r, it); ok && have; have = next_item(r, it)) {
       for (int x = 0; x < 2; ++x) {
-        if ((2 * it.pair + x) * 128 >= rows) continue;
-        const int m_row = (2 * it.pair + x) * 128 + row;
+        if (!has(it, x)) continue;
+        const int m_row = row_of(it, x) + row;
         const bool there = m_row < rows;
         const uint32_t ob = tmem + (static_cast<uint32_t>(qw * 32) << 16) + 256u + static_cast<uint32_t>(x * 128);
         const int token = there ? m_row >> p.group_shift : 0;
@@ -686,7 +700,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
 constexpr int kJoinThreads = 256;
 
 // Joins the splits: one warp a row (token and head).
-template <int D>
+template <int D, int TILES>
 __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_constant__ WindowParams p) {
   constexpr int kPer = D / 32;
   grid_dep_wait();
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_const
   const long long all = static_cast<long long>(p.sets) * p.rows;
   if (row >= all) return;
   const int set = static_cast<int>(row / p.rows), m_row = static_cast<int>(row - static_cast<long long>(set) * p.rows);
-  const int blocks = keys_of_pair(p, m_row / 256).blocks;
+  const int blocks = keys_of_part<TILES>(p, m_row / (128 * TILES)).blocks;
   float acc[kPer];
   const float l = join_splits<D>(p.part_ml, p.part_o, all, row, min(p.split, blocks), lane, acc);
   const int token = m_row >> p.group_shift, head = set * p.group + (m_row & (p.group - 1)), rank = head / p.heads_per_rank;
@@ -707,27 +721,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_window_join(const __grid_const
   for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
 }
 
-// Key splits of an item: the least time of the busiest CTA and the join, with 1.5 us a block step, 5 us for an
-// item's start and end, 3 us for the join and its traffic at 4 TB/s. One where the items fill the
-// SMs. One token, 64 heads, 4100 keys: 17 splits, 9.8 us (one: 50); 515 tokens, 32 heads, 513 keys: one, 14.4
-// (two: 25).
-int splits_of(int group, int sets, int tokens, int keys, int window, int sinks, long long d) {
-  const int pairs = static_cast<int>((static_cast<long long>(tokens) * group + 255) / 256);
-  const long long bases = static_cast<long long>(pairs) * sets;
+// Row tiles and key splits of an item: the least time of the busiest CTA and the join, with 1.5 us a block step
+// of two tiles and 1.35 of one, 5 us for an item's start and end, 3 us for the join and its traffic at 4
+// TB/s. Two tiles and no splits where those items fill the SMs. One token, 64 heads, 4100 keys: 17 splits, 9.8 us (one:
+// 50); 515 tokens, 32 heads, 513 keys in sight: items of one tile 12.8, of two 14.3, in two splits 25.
+struct Shape {
+  int tiles, parts, split;
+};
+Shape shape_of(int group, int sets, int tokens, int keys, int window, int sinks, long long d) {
   const int sms = num_sms();
-  if (bases >= sms) return 1;
-  const int most = keys_of(256 * (pairs - 1) / group, tokens - 1, tokens, keys, window, sinks).blocks;
-  int split = 1;
-  double best = -1;
-  for (int c = 1; c <= most && bases * c <= 2LL * sms; ++c) {
-    double us = (bases * c + sms - 1) / sms * ((most + c - 1) / c * 1.5 + 5);
-    if (c > 1) us += 3 + 8e-6 / 4 * tokens * group * sets * c * d;
-    if (best < 0 || us < best) {
-      best = us;
-      split = c;
+  const long long rows = static_cast<long long>(tokens) * group;
+  Shape best = {2, static_cast<int>((rows + 255) / 256), 1};
+  if (static_cast<long long>(best.parts) * sets >= sms) return best;
+  double least = -1;
+  for (int tiles = 2; tiles >= 1; --tiles) {
+    const int per = 128 * tiles, parts = static_cast<int>((rows + per - 1) / per);
+    const long long bases = static_cast<long long>(parts) * sets;
+    const int most = keys_of(static_cast<int>(static_cast<long long>(per) * (parts - 1) / group), tokens - 1, tokens, keys, window, sinks).blocks;
+    for (int c = 1; c <= most && bases * c <= 2LL * sms; ++c) {
+      double us = (bases * c + sms - 1) / sms * ((most + c - 1) / c * (tiles == 2 ? 1.5 : 1.35) + 5);
+      if (c > 1) us += 3 + 8e-6 / 4 * rows * sets * c * d;
+      if (least < 0 || us < least) {
+        least = us;
+        best = {tiles, parts, c};
+      }
     }
   }
-  return split;
+  return best;
 }
 
 // Heads that share a tile.
@@ -756,18 +776,18 @@ cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
   return e;
 }
 
-template <int D>
+template <int D, int TILES>
 tp_status launch_window(const WindowParams &p, const WindowMaps &maps, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_window<D>, static_cast<int>(WinCfg<D>::kSmem), mask, mu);
+  const cudaError_t e = allow_smem(k_window<D, TILES>, static_cast<int>(WinCfg<D>::kSmem), mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
-  const long long items = static_cast<long long>(p.sets) * p.pairs * p.split;
+  const long long items = static_cast<long long>(p.sets) * p.parts * p.split;
   const unsigned grid = static_cast<unsigned>(items < num_sms() ? items : num_sms());
-  tp_status st = launched(launch_kernel(k_window<D>, dim3(grid), dim3(kWinThreads), WinCfg<D>::kSmem, s, 1, p, maps));
+  tp_status st = launched(launch_kernel(k_window<D, TILES>, dim3(grid), dim3(kWinThreads), WinCfg<D>::kSmem, s, 1, p, maps));
   if (st != TP_OK || p.split == 1) return st;
   const long long all = static_cast<long long>(p.sets) * p.rows;
-  return launched(launch_kernel(k_window_join<D>, dim3(static_cast<unsigned>((all + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
+  return launched(launch_kernel(k_window_join<D, TILES>, dim3(static_cast<unsigned>((all + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
                                 dim3(kJoinThreads), 0, s, 1, p));
 }
 
@@ -790,8 +810,8 @@ extern "C" size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tok
   if (!plan || tokens < 1 || keys < tokens || window < 1 || sinks < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
   if (!sizes_ok(d, tokens, keys)) return 0;
   const int group = group_of(d);
-  const int split = splits_of(group, d.num_q_heads / group, static_cast<int>(tokens), static_cast<int>(keys), window, sinks, d.head_dim);
-  return workspace_bytes_of(split, tokens * d.num_q_heads, d.head_dim);
+  const Shape shape = shape_of(group, d.num_q_heads / group, static_cast<int>(tokens), static_cast<int>(keys), window, sinks, d.head_dim);
+  return workspace_bytes_of(shape.split, tokens * d.num_q_heads, d.head_dim);
 }
 
 extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, const tp_tensor *k, const tp_tensor *v,
@@ -822,8 +842,8 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
   if (!sizes_ok(dims, T, S)) return TP_ERR_UNSUPPORTED;
   const int group = group_of(dims), sets = dims.num_q_heads / group;
   const long long rows_all = T * dims.num_q_heads;
-  const int split = T > 0 ? splits_of(group, sets, static_cast<int>(T), static_cast<int>(S), window, sinks, hd) : 1;
-  const size_t need = workspace_bytes_of(split, rows_all, hd);
+  const Shape shape = T > 0 ? shape_of(group, sets, static_cast<int>(T), static_cast<int>(S), window, sinks, hd) : Shape{2, 0, 1};
+  const size_t need = workspace_bytes_of(shape.split, rows_all, hd);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return TP_ERR_WORKSPACE;
     if (!ptr_aligned(workspace, 16)) return TP_ERR_ALIGNMENT;
@@ -866,15 +886,16 @@ extern "C" tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, con
   p.heads_per_rank = dims.num_q_heads / n;
   p.heads_per_source = dims.num_kv_heads / sources;
   p.rows = static_cast<int>(T * group);
-  p.pairs = (p.rows + 255) / 256;
-  p.split = split;
+  p.parts = shape.parts;
+  p.split = shape.split;
   p.by_sets.set(sets);
-  p.by_split.set(split);
+  p.by_split.set(shape.split);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
   p.part_o = static_cast<float *>(workspace);
-  p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + sums_bytes(split, rows_all, hd));
+  p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + sums_bytes(shape.split, rows_all, hd));
   p.status = ctx.status;
   p.wait_ns = ctx.wait_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return hd == 128 ? launch_window<128>(p, maps, s) : launch_window<64>(p, maps, s);
+  if (shape.tiles == 1) return hd == 128 ? launch_window<128, 1>(p, maps, s) : launch_window<64, 1>(p, maps, s);
+  return hd == 128 ? launch_window<128, 2>(p, maps, s) : launch_window<64, 2>(p, maps, s);
 }

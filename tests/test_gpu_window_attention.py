@@ -193,3 +193,68 @@ def test_sources_that_overlap():
     tp.tp_window_attn(plan, q, apart, [x.clone() for x in apart], 20, 2, want, ws)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# As many items as fill the SMs, of two row tiles each, and items of two row tiles in splits
+FULL = [(1, 64, 32, 64, 560, 700, 130, 20), (8, 64, 8, 128, 2450, 2600, 200, 4), (1, 32, 4, 64, 3000, 3000, 333, 0),
+        (1, 32, 4, 128, 5000, 5000, ALL, 0), (2, 152, 152, 128, 40, 300, 70, 9), (1, 152, 152, 64, 255, 2000, 1500, 300),
+        (1, 32, 8, 128, 512, 5000, 4096, 0), (1, 8, 8, 128, 600, 9000, ALL, 0), (4, 64, 2, 64, 700, 6000, 5000, 33)]
+
+
+@pytest.mark.parametrize("shape", FULL, ids=lambda s: "-".join(map(str, s)))
+def test_many_rows(shape):
+    need_gpu()
+    c = Case(*shape, seed=12)
+    a = c.run()
+    c.check(a)
+    assert tp.tp_device_status()[0] == tp.TP_OK
+    assert torch.equal(a, c.run())
+
+
+@pytest.mark.parametrize("q_std", [4.0, 30.0])
+def test_many_rows_with_sharp_scores(q_std):
+    need_gpu()
+    c = Case(2, 64, 16, 128, 1210, 1300, 150, 3, seed=13, q_std=q_std)
+    c.check(c.run())
+
+
+def test_many_rows_with_maxima_that_jump():
+    need_gpu()
+    c = Case(1, 64, 16, 128, 1200, 1200, 500, 4, seed=14)
+    ramp = torch.arange(1200, device="cuda")[:, None] // 128 * 1.3
+    c.k += (ramp * torch.sign(c.q[0, :128].float()).repeat(16)).to(BF16)
+    c.k[:4] -= (9 * torch.sign(c.q[0, :128].float()).repeat(16)).to(BF16)
+    c.check(c.run())
+
+
+def test_many_rows_out_of_sight_and_nan():
+    need_gpu()
+    c = Case(1, 64, 16, 64, 1300, 3000, 200, 4, seed=15)
+    want = c.run()
+    c.k[128:1400], c.v[128:1400] = float("nan"), float("inf")  # blocks that no query sees
+    c.k[4:128] = float("nan")
+    assert torch.equal(want, c.run())
+    c.q[700, 3] = float("nan")
+    a = c.run()
+    assert a[700, :64].isnan().all()
+    a[700, :64] = want[700, :64]
+    assert torch.equal(a, want)
+
+
+def test_many_rows_in_a_graph():
+    need_gpu()
+    c = Case(2, 64, 16, 128, 900, 900, 300, 4, seed=16)
+    want = c.run()
+    assert torch.equal(want, c.run(stream=torch.cuda.Stream()))
+    q, k, v = c.parts(c.q, 2), c.parts(c.k, 2), c.parts(c.v, 2)
+    a = [torch.zeros_like(x) for x in q]
+    assert tp.tp_window_attn_workspace_size(c.plan, 900, 900, 300, 4) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tp.tp_window_attn(c.plan, q, k, v, 300, 4, a, None)
+    for _ in range(3):
+        for x in a:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(torch.cat(a, 1), want)

@@ -707,12 +707,34 @@ def _workspace(t) -> tuple:
     return t.data_ptr(), size
 
 
+_devices = None  # GPUs that torch sees
+
+
+def _same_device(*given) -> None:
+    """Where there is more than one GPU: the tensors of a call lie on the current one, on which its
+    kernels run (the library sees addresses only, and another GPU's would fault there)."""
+    global _devices
+    if _devices is None:
+        import torch
+        _devices = torch.cuda.device_count()
+    if _devices < 2:
+        return
+    import torch
+    now = torch.cuda.current_device()
+    for one in given:
+        for t in one if isinstance(one, (list, tuple)) else (one,):
+            device = getattr(t, "device", None)
+            if device is not None and device.type == "cuda" and device.index != now:
+                raise ValueError(f"a tensor on {device}, the current device is cuda:{now}")
+
+
 def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout: int = TP_ROTARY_HALVES,
               inverse: bool = False, stream=None) -> None:
     """Rotates pairs of values of q's and k's heads by positions[axis] * freq. positions: int32 [T] or
     [axes x T]; freq: f32 [pairs]; axis: per pair (rotary_axes), None: all 0. q, q_out: one entry
     per rank, k, k_out: one per kv source; q or k may be None with its output."""
     n, src, pairs = plan.ranks, plan.sources, freq.numel()
+    _same_device(positions, freq, q, k, q_out, k_out)
     if positions.dim() not in (1, 2):
         raise ValueError("positions must be [T] or [axes x T]")
     axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
@@ -738,6 +760,7 @@ def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=No
     """The last T of S tokens over a sliding window and the first `sinks` tokens. q, a: one entry per
     rank; k, v: one per kv source; workspace: a CUDA byte tensor."""
     n, src = plan.ranks, plan.sources
+    _same_device(q, k, v, a, workspace)
     ws, size = _workspace(workspace)
     g = _args(2 * n + 2 * src)
     st = _lib.tp_window_attn(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
@@ -750,6 +773,7 @@ def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scal
     """Stores the rows of k and v (batch * n tokens) behind the lengths[b] positions that the 4-bit
     caches hold. All but lengths and counts: one entry per kv source."""
     batch, src = lengths.numel(), plan.sources
+    _same_device(lengths, counts, k, v, k_codes, k_scale, v_codes, v_scale)
     g = _args(6 * src)
     st = _lib.tp_cache4_store(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
                               None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
@@ -763,6 +787,7 @@ def tp_cache4_load(plan: Plan, first, k_codes, k_scale, v_codes, v_scale, k_out,
     """Positions first[b] .. of every sequence from the 4-bit caches into k_out and v_out (batch * n
     rows). All but first: one entry per kv source."""
     src = plan.sources
+    _same_device(first, k_codes, k_scale, v_codes, v_scale, k_out, v_out)
     g = _args(6 * src)
     st = _lib.tp_cache4_load(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
                              g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
@@ -780,6 +805,7 @@ def tp_cache4_attn(plan: Plan, q, k_codes, k_scale, v_codes, v_scale, lengths, w
     """One new token per sequence over the 4-bit caches, a sliding window and the first `sinks` tokens.
     q, a: one entry per rank; caches: one per kv source; workspace: a CUDA byte tensor."""
     n, src = plan.ranks, plan.sources
+    _same_device(q, k_codes, k_scale, v_codes, v_scale, lengths, a, workspace)
     ws, size = _workspace(workspace)
     g = _args(2 * n + 4 * src)
     st = _lib.tp_cache4_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),

@@ -231,3 +231,26 @@ def test_binding_checks_bare_addresses():
         tp.tp_cache4_store(PLAN, FakeTensor(3), q, q, k, k, k, k, counts=FakeTensor(2), stream=1)
     with pytest.raises(TypeError):
         tp.tp_cache4_load(PLAN, FakeTensor(3, dtype=torch.int64), k, k, k, k, q, q, stream=1)
+
+
+def test_binding_refuses_another_device(monkeypatch):
+    """With several GPUs (pretended here) each tensor of a call lies on the current one."""
+    monkeypatch.setattr(tp, "_devices", 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here, there = FakeTensor(3), FakeTensor(3)
+    here.device, there.device = torch.device("cuda", 0), torch.device("cuda", 1)
+    q, k = [T(BF, 3, 256)] * 2, [T(BF, 40, 128)] * 2
+    cache = (k, k, k, k)
+    calls = [lambda x: tp.tp_rotary(PLAN, x, FakeTensor(64, dtype=torch.float32), q, None, q, None, stream=1),
+             lambda x: tp.tp_rotary(PLAN, FakeTensor(3), FakeTensor(64, dtype=torch.float32), [x, x], None, q, None, stream=1),
+             lambda x: tp.tp_window_attn(PLAN, q, k, k, 8, 0, q, x, stream=1),
+             lambda x: tp.tp_cache4_store(PLAN, x, k, k, *cache, stream=1),
+             lambda x: tp.tp_cache4_store(PLAN, here, k, k, *cache, counts=x, stream=1),
+             lambda x: tp.tp_cache4_load(PLAN, x, *cache, k, k, stream=1),
+             lambda x: tp.tp_cache4_attn(PLAN, q, *cache, x, 8, 0, q, None, stream=1)]
+    for call in calls:
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(there)
+    for call in calls[3:]:  # the current device: on to the library's own refusals (k has the wrong type)
+        with pytest.raises(tp.TPError):
+            call(here)

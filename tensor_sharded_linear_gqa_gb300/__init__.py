@@ -15,6 +15,7 @@ None for the current torch stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib
 import os
 import struct
@@ -707,6 +708,20 @@ def _workspace(t) -> tuple:
     return t.data_ptr(), size
 
 
+_entries: dict = {}
+
+
+def _entry(name: str):
+    """The library's call tp_<name>, by way of the extension module where that is built."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = getattr(_lib, "tp_" + name)
+        if _load_describe() is not None:
+            fn = functools.partial(getattr(_describe, name), ctypes.cast(fn, ctypes.c_void_p).value)
+        _entries[name] = fn
+    return fn
+
+
 _devices = None  # GPUs that torch sees
 
 
@@ -744,10 +759,10 @@ def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout
         if axis._type_ is not ctypes.c_int32 or len(axis) != pairs:
             raise ValueError(f"axis must have {pairs} entries, one per pair")
     g = _args(2 * n + 2 * src)
-    st = _lib.tp_rotary(plan.handle, tokens, _dev_ptr(positions, "torch.int32"), axes, _dev_ptr(freq, "torch.float32"), pairs,
-                        axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
-                        None if q_out is None else g.many(q_out, n), None if k_out is None else g.many(k_out, src),
-                        _stream(stream))
+    st = _entry("rotary")(plan.handle, tokens, _dev_ptr(positions, "torch.int32"), axes, _dev_ptr(freq, "torch.float32"), pairs,
+                          axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
+                          None if q_out is None else g.many(q_out, n), None if k_out is None else g.many(k_out, src),
+                          _stream(stream))
     if st:
         raise TPError(st, "tp_rotary")
 
@@ -763,8 +778,8 @@ def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=No
     _same_device(q, k, v, a, workspace)
     ws, size = _workspace(workspace)
     g = _args(2 * n + 2 * src)
-    st = _lib.tp_window_attn(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
-                             _stream(stream))
+    st = _entry("window_attn")(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
+                               _stream(stream))
     if st:
         raise TPError(st, "tp_window_attn")
 
@@ -775,10 +790,10 @@ def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scal
     batch, src = lengths.numel(), plan.sources
     _same_device(lengths, counts, k, v, k_codes, k_scale, v_codes, v_scale)
     g = _args(6 * src)
-    st = _lib.tp_cache4_store(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
-                              None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
-                              g.many(v, src), g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src),
-                              g.many(v_scale, src), _stream(stream))
+    st = _entry("cache4_store")(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
+                                None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
+                                g.many(v, src), g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src),
+                                g.many(v_scale, src), _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_store")
 
@@ -789,9 +804,9 @@ def tp_cache4_load(plan: Plan, first, k_codes, k_scale, v_codes, v_scale, k_out,
     src = plan.sources
     _same_device(first, k_codes, k_scale, v_codes, v_scale, k_out, v_out)
     g = _args(6 * src)
-    st = _lib.tp_cache4_load(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
-                             g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
-                             g.many(v_out, src), _stream(stream))
+    st = _entry("cache4_load")(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
+                               g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
+                               g.many(v_out, src), _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_load")
 
@@ -808,9 +823,9 @@ def tp_cache4_attn(plan: Plan, q, k_codes, k_scale, v_codes, v_scale, lengths, w
     _same_device(q, k_codes, k_scale, v_codes, v_scale, lengths, a, workspace)
     ws, size = _workspace(workspace)
     g = _args(2 * n + 4 * src)
-    st = _lib.tp_cache4_attn(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),
-                             g.many(v_codes, src), g.many(v_scale, src), _dev_ptr(lengths, "torch.int32"), window, sinks,
-                             g.many(a, n), ws, size, _stream(stream))
+    st = _entry("cache4_attn")(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),
+                               g.many(v_codes, src), g.many(v_scale, src), _dev_ptr(lengths, "torch.int32"), window, sinks,
+                               g.many(a, n), ws, size, _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_attn")
 

@@ -138,6 +138,54 @@ static PyObject *py_bytes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   return Py_BuildValue("KK", at, bytes);
 }
 
+/* Calls of the library with many arguments that take a few us: ctypes converts each argument by itself, 1 us a
+ * call. The first argument is the entry point's address (this module does not link the library), then
+ * come its own: integers, and for a pointer also None or an object with a buffer (a ctypes array). */
+static int values(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, unsigned pointers, unsigned long long *v) {
+  if (n != want) return PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", want, n), 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (PyLong_Check(args[i])) {
+      v[i] = PyLong_AsUnsignedLongLongMask(args[i]);
+    } else if (PyIndex_Check(args[i])) {
+      PyObject *x = PyNumber_Index(args[i]);
+      if (x == NULL) return 0;
+      v[i] = PyLong_AsUnsignedLongLongMask(x);
+      Py_DECREF(x);
+    } else if (!(pointers >> i & 1)) {
+      return PyErr_Format(PyExc_TypeError, "argument %zd must be an integer", i), 0;
+    } else if (args[i] == Py_None) {
+      v[i] = 0;
+    } else {
+      Py_buffer b;
+      if (PyObject_GetBuffer(args[i], &b, PyBUF_SIMPLE) != 0) return 0;
+      v[i] = (unsigned long long)(uintptr_t)b.buf;
+      PyBuffer_Release(&b); /* the caller holds the object */
+    }
+  }
+  if (v[0] == 0) return PyErr_Format(PyExc_ValueError, "a null address"), 0;
+  return 1;
+}
+#define AT(i) ((void *)(uintptr_t)v[i])
+#define ENTRY(name, count, pointers, ...)                                                   \
+  static PyObject *py_##name(PyObject *self, PyObject *const *args, Py_ssize_t n) { \
+    (void)self;                                                                   \
+    unsigned long long v[count + 1];                                              \
+    if (!values(args, n, count + 1, pointers, v)) return NULL;                    \
+    tp_status st;                                                                 \
+    Py_BEGIN_ALLOW_THREADS                                                        \
+    st = ((__typeof__(&tp_##name))AT(0))(__VA_ARGS__);                            \
+    Py_END_ALLOW_THREADS                                                          \
+    return PyLong_FromLong((long)st);                                             \
+  }
+/* after the count: which arguments are pointers, a bit each */
+ENTRY(rotary, 14, 0x7caa, AT(1), (int64_t)v[2], AT(3), (int32_t)v[4], AT(5), (int32_t)v[6], AT(7), (int32_t)v[8], (int32_t)v[9], AT(10), AT(11),
+      AT(12), AT(13), AT(14))
+ENTRY(window_attn, 10, 0x59e, AT(1), AT(2), AT(3), AT(4), (int32_t)v[5], (int32_t)v[6], AT(7), AT(8), (size_t)v[9], AT(10))
+ENTRY(cache4_store, 11, 0xffa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10), AT(11))
+ENTRY(cache4_load, 10, 0x7fa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10))
+ENTRY(cache4_attn, 14, 0x59fa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), (int32_t)v[9], (int32_t)v[10], AT(11), AT(12),
+      (size_t)v[13], AT(14))
+
 static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
   if (n != 4) return PyErr_Format(PyExc_TypeError, "dtypes(f32, bf16, e4m3, u8)");
@@ -155,6 +203,8 @@ static PyMethodDef methods[] = {
     {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address) -> how many of the first were described"},
     {"vector", (PyCFunction)(void (*)(void))py_vector, METH_FASTCALL, "vector(tensor, type, entries) -> address of a contiguous CUDA tensor of the type (tp_dtype, 4 for int32) with that many entries (-1: any), or None"},
     {"bytes", (PyCFunction)(void (*)(void))py_bytes, METH_FASTCALL, "bytes(tensor) -> (address, size) of a contiguous CUDA tensor, or None"},
+#define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, #name "(address of tp_" #name ", its arguments) -> status"}
+    METHOD(rotary), METHOD(window_attn), METHOD(cache4_store), METHOD(cache4_load), METHOD(cache4_attn),
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_describe", "Descriptors of torch tensors.", -1, methods, NULL, NULL, NULL, NULL};
 

@@ -30,12 +30,14 @@
 // m is then f32's lowest value, the masked keys weigh 0, and the first key that is seen moves m.
 //
 // Bounds. A step (128 keys of both tiles, d = 128) is 32 products of 128 x 128 x 16: 1.0 us at 64 cycles
-// each, 1.35 us at the rate of a large library product (1895 TFLOP/s); and 256 x 128 exponentials, 1.0 us
-// of an SM's 16 a clock. It takes 1.55 us. Every item adds about 4.4 us (its first S, the search for
-// the maximum, masked blocks at both of the window's ends, the output), so a window of 1024 and 4 first
-// tokens over 16384 tokens, 64 heads on 8 (9 blocks an item), takes 455 us, 1.17 PFLOP/s over the keys that are
-// seen. Small calls are bound by one item's latency: 2047 tokens of 16 heads of 64, window 300: 9.8 us; one
-// token, 64 heads, 4100 keys: 9.8.
+// each, 1.35 us at the rate of a large library product (1895 TFLOP/s); and 256 x 128 exponentials, 0.5 us
+// of their unit (its counter reads 27%). It takes 1.55 us: 0.5 us of a tile's own products, then 1.05 us from S to
+// P, one thread's chain of waits, loads, about 350 instructions and stores, while the other tile's products
+// run. More instructions lengthen it: an eighth of the exponentials as polynomials 1.72 us. Every item adds
+// about 4.4 us (its first S, a short block, masked blocks at both of the window's ends, the output), so a
+// window of 1024 and 4 first tokens over 16384 tokens, 64 heads on 8 (9 blocks an item), takes 455 us,
+// 1.17 PFLOP/s over the keys that are seen. Small calls are bound by one item's latency: 2047 tokens of
+// 16 heads of 64, window 300: 9.8 us; one token, 64 heads, 4100 keys: 9.8.
 //
 // Where there are too few items for the SMs (few tokens), items have one row tile, or their blocks are
 // split, the splits leave f32 sums, and k_window_join joins them.

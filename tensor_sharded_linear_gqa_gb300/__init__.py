@@ -191,26 +191,46 @@ _DESC = struct.Struct("=Qiiqqq")
 _DTYPES: dict = {}
 
 
+_loading = threading.RLock()
+_loaded = False
+
+
 def _load_describe():
     """The same in C, for plain tensors (a small call's issue time is mostly this), loaded by the first
     tensor that is described: importing the package maps no object. None where it is not built (an
     interpreter without its headers): interpreted code does it all."""
-    global _describe, _matrix, _matrices, _row, _vector, _bytes
-    if "_describe" not in globals():
-        try:
-            import torch  # noqa: F401  the module reads tensors through torch's own libraries
-        except ImportError:
-            pass
-        try:
-            _describe = importlib.import_module("._describe", __name__)
-            _matrix, _matrices, _row = _describe.matrix, _describe.matrices, _describe.row
-            _vector, _bytes = _describe.vector, _describe.bytes
-        except ImportError:
-            _describe = None
-            _matrix = _row = lambda t, to: False  # noqa: E731
-            _vector, _bytes = lambda t, kind, n: None, lambda t: None  # noqa: E731
-            _matrices = lambda seq, n, to: 0  # noqa: E731
+    if not _loaded:
+        with _loading:
+            if not _loaded:
+                _first_use()
     return _describe
+
+
+def _first_use() -> None:
+    """Other threads may call meanwhile: they find the functions below, which wait for the lock, until
+    everything that they need is in place. (The import itself already puts _describe into this module.)"""
+    global _describe, _matrix, _matrices, _row, _vector, _bytes, _DTYPES, _loaded
+    types = {}
+    try:
+        import torch  # the module reads tensors through torch's own libraries
+        types = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8}
+    except ImportError:
+        pass
+    try:
+        module = importlib.import_module("._describe", __name__)
+    except ImportError:
+        _describe = None
+        _matrix = _row = lambda t, to: False  # noqa: E731
+        _vector, _bytes = lambda t, kind, n: None, lambda t: None  # noqa: E731
+        _matrices = lambda seq, n, to: 0  # noqa: E731
+    else:
+        if types:
+            module.dtypes(*types)
+        _describe = module
+        _matrix, _matrices, _row = module.matrix, module.matrices, module.row
+        _vector, _bytes = module.vector, module.bytes
+    _DTYPES = types
+    _loaded = True
 
 
 def __getattr__(name):
@@ -220,37 +240,35 @@ def __getattr__(name):
 
 
 def _dtypes() -> dict:
+    _load_describe()
     if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8})
-        if _load_describe() is not None:
-            _describe.dtypes(*_DTYPES)
+        import torch  # noqa: F401  says why there is none
     return _DTYPES
 
 
 def _matrix(t, to):
-    """_describe.matrix; _load_describe puts it in this one's place, as for the next two."""
-    _dtypes()
+    """_describe.matrix; _load_describe puts it in this one's place, as for the next four."""
+    _load_describe()
     return _matrix(t, to)
 
 
 def _matrices(seq, n, to):
-    _dtypes()
+    _load_describe()
     return _matrices(seq, n, to)
 
 
 def _row(t, to):
-    _dtypes()
+    _load_describe()
     return _row(t, to)
 
 
 def _vector(t, kind, n):
-    _dtypes()
+    _load_describe()
     return _vector(t, kind, n)
 
 
 def _bytes(t):
-    _dtypes()
+    _load_describe()
     return _bytes(t)
 
 

@@ -214,11 +214,11 @@ def _first_use() -> None:
     try:
         import torch  # the module reads tensors through torch's own libraries
         types = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8}
-    except ImportError:
+    except Exception:  # none, or one that does not load: descriptors, addresses and streams may be given as they are
         pass
     try:
         module = importlib.import_module("._describe", __name__)
-    except ImportError:
+    except (ImportError, OSError):  # not built, or linked to another torch's libraries
         _describe = None
         _matrix = _row = lambda t, to: False  # noqa: E731
         _vector, _bytes = lambda t, kind, n: None, lambda t: None  # noqa: E731
@@ -226,6 +226,7 @@ def _first_use() -> None:
     else:
         if types:
             module.dtypes(*types)
+            module.reads_torch(f"{torch.version.__version__} {torch.version.git_version}")
         _describe = module
         _matrix, _matrices, _row = module.matrix, module.matrices, module.row
         _vector, _bytes = module.vector, module.bytes
@@ -748,8 +749,11 @@ def _same_device(*given) -> None:
     kernels run (the library sees addresses only, and another GPU's would fault there)."""
     global _devices
     if _devices is None:
-        import torch
-        _devices = torch.cuda.device_count()
+        try:
+            import torch
+            _devices = torch.cuda.device_count()
+        except Exception:  # no torch: no tensors of it
+            _devices = 0
     if _devices < 2:
         return
     import torch

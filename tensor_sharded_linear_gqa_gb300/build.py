@@ -12,11 +12,11 @@ Usage: ``python -m tensor_sharded_linear_gqa_gb300.build [--force] [-v]``.
 from __future__ import annotations
 
 import hashlib
-import importlib.metadata
 import importlib.util
 import json
 import os
 import platform
+import re
 import shutil
 import subprocess
 import sys
@@ -62,15 +62,21 @@ def _python_h() -> str:
 
 
 def _torch() -> tuple:
-    """(version, folder) of the installed torch, without importing it; (None, None) without one."""
+    """(version and revision, folder) of the installed torch, without importing it; (None, None) without
+    one, or with one that does not say which it is."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
         return None, None
+    folder = list(spec.submodule_search_locations)[0]
     try:
-        version = importlib.metadata.version("torch")
-    except importlib.metadata.PackageNotFoundError:
-        version = None
-    return version, list(spec.submodule_search_locations)[0]
+        with open(os.path.join(folder, "version.py")) as fh:
+            text = fh.read()
+    except OSError:
+        return None, None
+    found = [re.search(rf"^{name}\b[^=\n]*= *['\"]([\w.+-]+)['\"]", text, re.M) for name in ("__version__", "git_version")]
+    if None in found:
+        return None, None
+    return " ".join(m[1] for m in found), folder
 
 
 def _stamp() -> dict:
@@ -107,11 +113,13 @@ def _compile(src: str, verbose: bool) -> str:
 
 def _compile_describe_torch(verbose: bool) -> list:
     """Compiles what reads torch tensors directly; the objects and libraries to link, none without torch's headers."""
-    folder = _torch()[1]
+    version, folder = _torch()
     if folder is None or not os.path.exists(os.path.join(folder, "include", "torch", "csrc", "autograd", "python_variable.h")):
         return []
     if not os.path.exists(_python_h()):
         return []
+    with open(os.path.join(BUILD, "torch_version.h"), "w") as fh:
+        fh.write(f'#define TP_TORCH_VERSION "{version}"\n')
     obj = os.path.join(BUILD, "describe_torch.o")
     cmd = [nvcc(), "-x", "c++", "-std=c++20", "-O2", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", os.path.join(folder, "include"),
            "-I", os.path.dirname(_python_h()), "-c", os.path.join(CSRC, "describe_torch.cpp"), "-o", obj]
@@ -132,7 +140,7 @@ def _build_describe(torch_parts: list, verbose: bool) -> None:
         print(f"{_python_h()} is missing: tensors are described by interpreted code", file=sys.stderr)
         return
     obj, tmp = os.path.join(BUILD, "describe.o"), DESCRIBE + ".tmp"
-    for cmd in ([nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", *(["-DTP_WITH_TORCH"] if torch_parts else []), "-I", INCLUDE,
+    for cmd in ([nvcc(), "-x", "c", "-O2", "-Xcompiler", "-fPIC", *(["-DTP_WITH_TORCH", "-I", BUILD] if torch_parts else []), "-I", INCLUDE,
                  "-I", os.path.dirname(_python_h()), "-c", os.path.join(CSRC, "describe.c"), "-o", obj],
                 [nvcc(), "-cudart", "none", "-shared", obj, *torch_parts, "-o", tmp]):
         if verbose:

@@ -3,7 +3,8 @@
  * A call's descriptors are most of a small call's issue time: 0.9 us a tensor when
  * they are packed by interpreted code, and a one-token projection has eighteen.
  *
- * Built with describe_torch.cpp, where torch's headers are, plain tensors are read without their attributes.
+ * Built with describe_torch.cpp, where torch's headers are, plain tensors are read without their attributes. That
+ * holds for the torch of these headers alone: with any other at run time (reads_torch) the attributes are used.
  *
  * Only what needs no words is taken here: a CUDA tensor of a type that the library
  * knows, not empty, with unit column stride. Everything else (and every error) is
@@ -13,7 +14,9 @@
 
 #include "tpgqa.h"
 
+static int with_torch; /* whether the torch that runs is the one of the headers */
 #ifdef TP_WITH_TORCH /* describe_torch.cpp */
+#include "torch_version.h"
 int tp_describe_torch(PyObject *t, long dims, tp_tensor *d);
 unsigned long long tp_address_torch(PyObject *t, int type, long long n, unsigned long long *bytes);
 #endif
@@ -34,7 +37,7 @@ static int items(PyObject *t, long long *out, Py_ssize_t n) {
 
 static int describe(PyObject *t, Py_ssize_t dims, tp_tensor *d) {
 #ifdef TP_WITH_TORCH
-  const int done = tp_describe_torch(t, (long)dims, d);
+  const int done = with_torch ? tp_describe_torch(t, (long)dims, d) : -1;
   if (done >= 0) return done;
 #endif
   PyObject *v = PyObject_GetAttr(t, s_dtype);
@@ -118,7 +121,7 @@ static PyObject *py_vector(PyObject *self, PyObject *const *args, Py_ssize_t n) 
   if (PyErr_Occurred()) return NULL;
   unsigned long long at = 0, bytes = 0;
 #ifdef TP_WITH_TORCH
-  at = type >= 0 ? tp_address_torch(args[0], (int)type, entries, &bytes) : 0;
+  at = with_torch && type >= 0 ? tp_address_torch(args[0], (int)type, entries, &bytes) : 0;
 #endif
   (void)type, (void)entries, (void)bytes;
   if (at == 0) Py_RETURN_NONE;
@@ -130,7 +133,7 @@ static PyObject *py_bytes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (n != 1) return PyErr_Format(PyExc_TypeError, "bytes(tensor)");
   unsigned long long at = 0, bytes = 0;
 #ifdef TP_WITH_TORCH
-  at = tp_address_torch(args[0], -1, -1, &bytes);
+  at = with_torch ? tp_address_torch(args[0], -1, -1, &bytes) : 0;
 #else
   (void)args;
 #endif
@@ -196,8 +199,20 @@ static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) 
   Py_RETURN_NONE;
 }
 
+/* The torch that runs, as its "version revision". */
+static PyObject *py_reads_torch(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  (void)self;
+  const char *version = n == 1 ? PyUnicode_AsUTF8(args[0]) : NULL;
+  if (version == NULL) return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_TypeError, "reads_torch(version)");
+#ifdef TP_WITH_TORCH
+  with_torch = strcmp(version, TP_TORCH_VERSION) == 0;
+#endif
+  return PyBool_FromLong(with_torch);
+}
+
 static PyMethodDef methods[] = {
     {"dtypes", (PyCFunction)(void (*)(void))py_dtypes, METH_FASTCALL, "dtypes(f32, bf16, e4m3, u8): the type objects of TP_F32, TP_BF16, TP_E4M3, TP_U8"},
+    {"reads_torch", (PyCFunction)(void (*)(void))py_reads_torch, METH_FASTCALL, "reads_torch(version and revision of the torch that runs) -> whether tensors are read without their attributes"},
     {"matrix", (PyCFunction)(void (*)(void))py_matrix, METH_FASTCALL, "matrix(tensor, address) -> whether it was described there"},
     {"row", (PyCFunction)(void (*)(void))py_row, METH_FASTCALL, "row(tensor, address): a 1-D tensor as a matrix of one row"},
     {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address) -> how many of the first were described"},

@@ -220,9 +220,9 @@ def _first_use() -> None:
         module = importlib.import_module("._describe", __name__)
     except (ImportError, OSError):  # not built, or linked to another torch's libraries
         _describe = None
-        _matrix = _row = lambda t, to: False  # noqa: E731
-        _vector, _bytes = lambda t, kind, n: None, lambda t: None  # noqa: E731
-        _matrices = lambda seq, n, to: 0  # noqa: E731
+        _matrix = _row = lambda t, to, device=-1: False  # noqa: E731
+        _vector, _bytes = lambda t, kind, n, device=-1: None, lambda t, device=-1: None  # noqa: E731
+        _matrices = lambda seq, n, to, device=-1: 0  # noqa: E731
     else:
         if types:
             module.dtypes(*types)
@@ -247,30 +247,30 @@ def _dtypes() -> dict:
     return _DTYPES
 
 
-def _matrix(t, to):
+def _matrix(*args):
     """_describe.matrix; _load_describe puts it in this one's place, as for the next four."""
     _load_describe()
-    return _matrix(t, to)
+    return _matrix(*args)
 
 
-def _matrices(seq, n, to):
+def _matrices(*args):
     _load_describe()
-    return _matrices(seq, n, to)
+    return _matrices(*args)
 
 
-def _row(t, to):
+def _row(*args):
     _load_describe()
-    return _row(t, to)
+    return _row(*args)
 
 
-def _vector(t, kind, n):
+def _vector(*args):
     _load_describe()
-    return _vector(t, kind, n)
+    return _vector(*args)
 
 
-def _bytes(t):
+def _bytes(*args):
     _load_describe()
-    return _bytes(t)
+    return _bytes(*args)
 
 
 def _fields(t) -> tuple:
@@ -296,11 +296,48 @@ def _fields(t) -> tuple:
     return 0, dt, 0, rows, cols, ld if rows > 1 else max(ld, cols, 1)
 
 
-def tensor(t) -> TpTensor:
-    """TpTensor view of a 2-D CUDA torch tensor with unit column stride (or a TpTensor)."""
+def _tensor(t) -> TpTensor:
     if isinstance(t, TpTensor):
         return t
     return TpTensor(*_fields(t))
+
+
+def tensor(t) -> TpTensor:
+    """TpTensor view of a 2-D CUDA torch tensor with unit column stride (or a TpTensor)."""
+    out = _tensor(t)
+    if out is not t:
+        out.device = _gpu_of(t)
+    return out
+
+
+_devices = None  # GPUs that torch sees
+
+
+def _device() -> int:
+    """The GPU on which the tensors of a call must lie: the current one, on which its kernels run (the
+    library sees addresses only, and another GPU's would fault there). -1 where there is only one."""
+    global _devices
+    if _devices is None:
+        try:
+            import torch
+            _devices = torch.cuda.device_count()
+        except Exception:  # no torch: no tensors of it
+            _devices = 0
+    if _devices < 2:
+        return -1
+    import torch
+    return torch.cuda.current_device()
+
+
+def _gpu_of(t):
+    """The GPU of a tensor or of a descriptor made by tensor(); None: not known."""
+    at = getattr(t, "device", None)
+    return at if at is None or isinstance(at, int) else at.index if at.type == "cuda" else None
+
+
+def _lies_on(device: int, at) -> None:
+    if at is not None and at != device:
+        raise ValueError(f"a tensor on cuda:{at}, the current device is cuda:{device}")
 
 
 _ARRAYS: dict = {}  # array type by length
@@ -405,7 +442,7 @@ def tp_plan_q_to_kv(plan: Plan, rank: int) -> list:
 
 # ---- linear layers and collectives ---------------------------------------------
 def tp_column_linear(tp_size: int, x, w, y, gather: bool, stream=None) -> None:
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_column_linear(tp_size, ctypes.byref(xs), _arr(w), _arr(y), int(gather),
                                  _stream(stream)), "tp_column_linear")
 
@@ -462,7 +499,7 @@ def tp_vocab_embedding(tp_size: int, ids, table, outs, stream=None) -> None:
 
 
 def tp_vocab_lm_head(tp_size: int, x, w, logits, gather: bool, stream=None) -> None:
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_vocab_lm_head(tp_size, ctypes.byref(xs), _arr(w), _arr(logits), int(gather),
                                  _stream(stream)), "tp_vocab_lm_head")
 
@@ -490,12 +527,14 @@ _DTYPE_NAMES: dict = {}  # str(dtype) by dtype: formatting it costs more than th
 _VECTOR_KINDS = {"torch.float32": TP_F32, "torch.int32": 4}  # the extension module's names of them
 
 
-def _dev_ptr(t, dtype: str, n: int | None = None, what: str = "") -> int:
+def _dev_ptr(t, dtype: str, n: int | None = None, what: str = "", device: int = -1) -> int:
     """Address of a contiguous CUDA tensor (0 when empty). The library sees no length, so where it
-    takes one from elsewhere (n), the tensor's is held against it here."""
-    at = _vector(t, _VECTOR_KINDS[dtype], -1 if n is None else n)
+    takes one from elsewhere (n), the tensor's is held against it here. device: as _device gives it."""
+    at = _vector(t, _VECTOR_KINDS[dtype], -1 if n is None else n, device)
     if at is not None:
         return at
+    if device >= 0:
+        _lies_on(device, _gpu_of(t))
     name = _DTYPE_NAMES.get(t.dtype)
     if name is None:
         name = _DTYPE_NAMES[t.dtype] = str(t.dtype)
@@ -515,7 +554,7 @@ def tp_moe_block(dims: TpMoeDims, x, topk_ids, topk_w, w_gate, w_up, w_down, y, 
                  stream=None) -> None:
     """topk_ids: int32 [T x k] CUDA tensor; topk_w: float32 [T x k]; workspace: a
     CUDA byte tensor of at least tp_moe_workspace_size bytes."""
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_moe_block(ctypes.byref(dims), ctypes.byref(xs), _dev_ptr(topk_ids, "torch.int32"),
                              _dev_ptr(topk_w, "torch.float32"), _arr(w_gate), _arr(w_up), _arr(w_down),
                              _arr(y), combine, workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -523,7 +562,7 @@ def tp_moe_block(dims: TpMoeDims, x, topk_ids, topk_w, w_gate, w_up, w_down, y, 
 
 
 def tp_gate_up_swiglu(plan: Plan, x, w_gate, w_up, h, stream=None) -> None:
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_gate_up_swiglu(plan.handle, ctypes.byref(xs), _arr(w_gate), _arr(w_up), _arr(h),
                                   _stream(stream)), "tp_gate_up_swiglu")
 
@@ -540,7 +579,7 @@ def tp_mlp_block(plan: Plan, x, w_gate, w_up, w_down, y, combine: int, workspace
     else:
         wptr = workspace.data_ptr()
         wbytes = workspace.numel() * workspace.element_size()
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_mlp_block(plan.handle, ctypes.byref(xs), _arr(w_gate), _arr(w_up),
                              _arr(w_down), _arr(y), combine, wptr, wbytes, _stream(stream)),
            "tp_mlp_block")
@@ -550,7 +589,7 @@ def tp_mlp_block_static(plan: Plan, x, w_gate, w_up, w_down, y, combine: int, st
     """tp_mlp_block without a workspace argument, for callers that cannot allocate
     device memory: H lives in the library's fixed 16 MiB scratch array. Calls on
     one device share that array, so calls that overlap on the GPU race."""
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_mlp_block_static(plan.handle, ctypes.byref(xs), _arr(w_gate), _arr(w_up),
                                     _arr(w_down), _arr(y), combine, _stream(stream)),
            "tp_mlp_block_static")
@@ -561,14 +600,14 @@ def tp_mlp_block_static_max_bytes() -> int:
 
 
 def tp_qkv_proj(plan: Plan, x, w_q, w_k, w_v, q, k, v, stream=None) -> None:
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_qkv_proj(plan.handle, ctypes.byref(xs), _arr(w_q), _arr(w_k), _arr(w_v), _arr(q),
                             _arr(k), _arr(v), _stream(stream)), "tp_qkv_proj")
 
 
 def tp_attn_proj(plan: Plan, x, w_q, w_k, w_v, q, k, v, a, w_o, y, combine: int,
                  stream=None) -> None:
-    xs = tensor(x)
+    xs = _tensor(x)
     _check(_lib.tp_attn_proj(plan.handle, ctypes.byref(xs), _arr(w_q), _arr(w_k), _arr(w_v),
                              _arr(q), _arr(k), _arr(v), _arr(a), _arr(w_o), _arr(y), combine,
                              _stream(stream)), "tp_attn_proj")
@@ -580,12 +619,13 @@ class _Scratch:
     call only). Each method packs tensors and returns the address: a small call spends less time
     on its kernels than building ctypes objects for its arguments would take."""
 
-    __slots__ = ("buf", "base", "room", "used")
+    __slots__ = ("buf", "base", "room", "used", "device")
 
     def __init__(self, room: int):
         self.buf = bytearray(_DESC.size * room)
         self.base = ctypes.addressof((ctypes.c_char * len(self.buf)).from_buffer(self.buf))
         self.room, self.used = room, 0  # tensors; bytes
+        self.device = -1  # the GPU on which they must lie, -1: not asked
 
     def one(self, t):
         """A single descriptor; None for None."""
@@ -593,7 +633,9 @@ class _Scratch:
             return None
         at = self.used
         self.used = at + _DESC_SIZE
-        if not _matrix(t, self.base + at):
+        if not (_matrix(t, self.base + at) if self.device < 0 else _matrix(t, self.base + at, self.device)):
+            if self.device >= 0:
+                _lies_on(self.device, _gpu_of(t))
             _PACK(self.buf, at, *_fields(t))  # no plain tensor, the first of all, or an error's words
         return self.base + at
 
@@ -602,9 +644,12 @@ class _Scratch:
         if len(seq) < n:
             raise ValueError(f"expected {n} tensors, one per rank or kv source")
         if isinstance(seq, ctypes.Array):
+            if self.device >= 0:
+                for at in getattr(seq, "devices", ()):
+                    _lies_on(self.device, at)
             return seq
         first = self.base + self.used
-        done = _matrices(seq, n, first)
+        done = _matrices(seq, n, first) if self.device < 0 else _matrices(seq, n, first, self.device)
         self.used += done * _DESC_SIZE
         for i in range(done, n):
             self.one(seq[i])
@@ -625,12 +670,12 @@ _DESC_SIZE, _PACK = _DESC.size, _DESC.pack_into
 _local = threading.local()
 
 
-def _args(most: int) -> _Scratch:
+def _args(most: int, device: int = -1) -> _Scratch:
     """The thread's scratch, emptied, with room for `most` tensors."""
     s = getattr(_local, "scratch", None)
     if s is None or s.room < most:
         s = _local.scratch = _Scratch(max(most, 256))
-    s.used = 0
+    s.used, s.device = 0, device
     return s
 
 
@@ -714,13 +759,15 @@ def rotary_axes(sections) -> ctypes.Array:
     return (ctypes.c_int32 * len(axis))(*axis)
 
 
-def _workspace(t) -> tuple:
+def _workspace(t, device: int = -1) -> tuple:
     """(address, bytes) of a workspace tensor; None is an empty one."""
     if t is None:
         return None, 0
-    at = _bytes(t)
+    at = _bytes(t, device)
     if at is not None:
         return at
+    if device >= 0:
+        _lies_on(device, _gpu_of(t))
     size = t.numel() * t.element_size()
     if not t.is_contiguous() or not (t.is_cuda or size == 0):
         raise ValueError("workspace must be a contiguous CUDA tensor")
@@ -741,37 +788,13 @@ def _entry(name: str):
     return fn
 
 
-_devices = None  # GPUs that torch sees
-
-
-def _same_device(*given) -> None:
-    """Where there is more than one GPU: the tensors of a call lie on the current one, on which its
-    kernels run (the library sees addresses only, and another GPU's would fault there)."""
-    global _devices
-    if _devices is None:
-        try:
-            import torch
-            _devices = torch.cuda.device_count()
-        except Exception:  # no torch: no tensors of it
-            _devices = 0
-    if _devices < 2:
-        return
-    import torch
-    now = torch.cuda.current_device()
-    for one in given:
-        for t in one if isinstance(one, (list, tuple)) else (one,):
-            device = getattr(t, "device", None)
-            if device is not None and device.type == "cuda" and device.index != now:
-                raise ValueError(f"a tensor on {device}, the current device is cuda:{now}")
-
-
 def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout: int = TP_ROTARY_HALVES,
               inverse: bool = False, stream=None) -> None:
     """Rotates pairs of values of q's and k's heads by positions[axis] * freq. positions: int32 [T] or
     [axes x T]; freq: f32 [pairs]; axis: per pair (rotary_axes), None: all 0. q, q_out: one entry
     per rank, k, k_out: one per kv source; q or k may be None with its output."""
     n, src, pairs = plan.ranks, plan.sources, freq.numel()
-    _same_device(positions, freq, q, k, q_out, k_out)
+    device = _device()
     if positions.dim() not in (1, 2):
         raise ValueError("positions must be [T] or [axes x T]")
     axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
@@ -780,9 +803,9 @@ def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout
             axis = (ctypes.c_int32 * len(axis))(*axis)
         if axis._type_ is not ctypes.c_int32 or len(axis) != pairs:
             raise ValueError(f"axis must have {pairs} entries, one per pair")
-    g = _args(2 * n + 2 * src)
-    st = _entry("rotary")(plan.handle, tokens, _dev_ptr(positions, "torch.int32"), axes, _dev_ptr(freq, "torch.float32"), pairs,
-                          axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
+    g = _args(2 * n + 2 * src, device)
+    st = _entry("rotary")(plan.handle, tokens, _dev_ptr(positions, "torch.int32", device=device), axes,
+                          _dev_ptr(freq, "torch.float32", device=device), pairs, axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
                           None if q_out is None else g.many(q_out, n), None if k_out is None else g.many(k_out, src),
                           _stream(stream))
     if st:
@@ -797,9 +820,9 @@ def tp_window_attn(plan: Plan, q, k, v, window: int, sinks: int, a, workspace=No
     """The last T of S tokens over a sliding window and the first `sinks` tokens. q, a: one entry per
     rank; k, v: one per kv source; workspace: a CUDA byte tensor."""
     n, src = plan.ranks, plan.sources
-    _same_device(q, k, v, a, workspace)
-    ws, size = _workspace(workspace)
-    g = _args(2 * n + 2 * src)
+    device = _device()
+    ws, size = _workspace(workspace, device)
+    g = _args(2 * n + 2 * src, device)
     st = _entry("window_attn")(plan.handle, g.many(q, n), g.many(k, src), g.many(v, src), window, sinks, g.many(a, n), ws, size,
                                _stream(stream))
     if st:
@@ -810,11 +833,11 @@ def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scal
     """Stores the rows of k and v (batch * n tokens) behind the lengths[b] positions that the 4-bit
     caches hold. All but lengths and counts: one entry per kv source."""
     batch, src = lengths.numel(), plan.sources
-    _same_device(lengths, counts, k, v, k_codes, k_scale, v_codes, v_scale)
-    g = _args(6 * src)
-    st = _entry("cache4_store")(plan.handle, batch, _dev_ptr(lengths, "torch.int32"),
-                                None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts"), g.many(k, src),
-                                g.many(v, src), g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src),
+    device = _device()
+    g = _args(6 * src, device)
+    st = _entry("cache4_store")(plan.handle, batch, _dev_ptr(lengths, "torch.int32", device=device),
+                                None if counts is None else _dev_ptr(counts, "torch.int32", batch, "counts", device),
+                                g.many(k, src), g.many(v, src), g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src),
                                 g.many(v_scale, src), _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_store")
@@ -823,11 +846,10 @@ def tp_cache4_store(plan: Plan, lengths, k, v, k_codes, k_scale, v_codes, v_scal
 def tp_cache4_load(plan: Plan, first, k_codes, k_scale, v_codes, v_scale, k_out, v_out, stream=None) -> None:
     """Positions first[b] .. of every sequence from the 4-bit caches into k_out and v_out (batch * n
     rows). All but first: one entry per kv source."""
-    src = plan.sources
-    _same_device(first, k_codes, k_scale, v_codes, v_scale, k_out, v_out)
-    g = _args(6 * src)
-    st = _entry("cache4_load")(plan.handle, first.numel(), _dev_ptr(first, "torch.int32"), g.many(k_codes, src),
-                               g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
+    src, device = plan.sources, _device()
+    g = _args(6 * src, device)
+    st = _entry("cache4_load")(plan.handle, first.numel(), _dev_ptr(first, "torch.int32", device=device),
+                               g.many(k_codes, src), g.many(k_scale, src), g.many(v_codes, src), g.many(v_scale, src), g.many(k_out, src),
                                g.many(v_out, src), _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_load")
@@ -842,12 +864,12 @@ def tp_cache4_attn(plan: Plan, q, k_codes, k_scale, v_codes, v_scale, lengths, w
     """One new token per sequence over the 4-bit caches, a sliding window and the first `sinks` tokens.
     q, a: one entry per rank; caches: one per kv source; workspace: a CUDA byte tensor."""
     n, src = plan.ranks, plan.sources
-    _same_device(q, k_codes, k_scale, v_codes, v_scale, lengths, a, workspace)
-    ws, size = _workspace(workspace)
-    g = _args(2 * n + 4 * src)
+    device = _device()
+    ws, size = _workspace(workspace, device)
+    g = _args(2 * n + 4 * src, device)
     st = _entry("cache4_attn")(plan.handle, lengths.numel(), g.many(q, n), g.many(k_codes, src), g.many(k_scale, src),
-                               g.many(v_codes, src), g.many(v_scale, src), _dev_ptr(lengths, "torch.int32"), window, sinks,
-                               g.many(a, n), ws, size, _stream(stream))
+                               g.many(v_codes, src), g.many(v_scale, src), _dev_ptr(lengths, "torch.int32", device=device),
+                               window, sinks, g.many(a, n), ws, size, _stream(stream))
     if st:
         raise TPError(st, "tp_cache4_attn")
 
@@ -891,7 +913,12 @@ def tp_version() -> str:
 
 def arr(seq):
     """ctypes array of TpTensor for a per-rank argument (kept alive by the caller)."""
-    return _arr(seq)
+    if isinstance(seq, ctypes.Array):
+        return seq
+    seq = list(seq)
+    out = _arr(seq)
+    out.devices = frozenset(_gpu_of(t) for t in seq) - {None}
+    return out
 
 
 class Prepared:

@@ -17,8 +17,8 @@
 static int with_torch; /* whether the torch that runs is the one of the headers */
 #ifdef TP_WITH_TORCH /* describe_torch.cpp */
 #include "torch_version.h"
-int tp_describe_torch(PyObject *t, long dims, tp_tensor *d);
-unsigned long long tp_address_torch(PyObject *t, int type, long long n, unsigned long long *bytes);
+int tp_describe_torch(PyObject *t, long dims, int device, tp_tensor *d);
+unsigned long long tp_address_torch(PyObject *t, int type, long long n, int device, unsigned long long *bytes);
 #endif
 
 static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr;
@@ -35,11 +35,13 @@ static int items(PyObject *t, long long *out, Py_ssize_t n) {
   return ok;
 }
 
-static int describe(PyObject *t, Py_ssize_t dims, tp_tensor *d) {
+/* device: the GPU on which the tensor must lie (another one's, or one not known, is left to the caller), -1: any. */
+static int describe(PyObject *t, Py_ssize_t dims, int device, tp_tensor *d) {
 #ifdef TP_WITH_TORCH
-  const int done = with_torch ? tp_describe_torch(t, (long)dims, d) : -1;
+  const int done = with_torch ? tp_describe_torch(t, (long)dims, device, d) : -1;
   if (done >= 0) return done;
 #endif
+  if (device >= 0) return 0;
   PyObject *v = PyObject_GetAttr(t, s_dtype);
   int type = 0;
   while (type < 4 && (v == NULL || v != known[type])) ++type;
@@ -72,12 +74,17 @@ static PyObject *truth(int ok) {
 }
 static tp_tensor *address(PyObject *v) { return (tp_tensor *)PyLong_AsVoidPtr(v); }
 
+/* Argument i of n, a device; -1 where it is left out. */
+static int device_of(PyObject *const *args, Py_ssize_t n, Py_ssize_t i) { return i < n ? (int)PyLong_AsLong(args[i]) : -1; }
+
 static PyObject *py_matrix(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (n != 2) return PyErr_Format(PyExc_TypeError, "matrix(tensor, address)");
+  if (n != 2 && n != 3) return PyErr_Format(PyExc_TypeError, "matrix(tensor, address, device)");
   tp_tensor *to = address(args[1]);
   if (to == NULL) return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "a null address");
-  return truth(describe(args[0], 2, to));
+  const int device = device_of(args, n, 2);
+  if (PyErr_Occurred()) return NULL;
+  return truth(describe(args[0], 2, device, to));
 }
 
 static PyObject *py_row(PyObject *self, PyObject *const *args, Py_ssize_t n) {
@@ -85,14 +92,17 @@ static PyObject *py_row(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (n != 2) return PyErr_Format(PyExc_TypeError, "row(tensor, address)");
   tp_tensor *to = address(args[1]);
   if (to == NULL) return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "a null address");
-  return truth(describe(args[0], 1, to));
+  return truth(describe(args[0], 1, -1, to));
 }
 
 static PyObject *py_matrices(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (n != 3) return PyErr_Format(PyExc_TypeError, "matrices(sequence, count, address)");
+  if (n != 3 && n != 4) return PyErr_Format(PyExc_TypeError, "matrices(sequence, count, address, device)");
   const Py_ssize_t count = PyLong_AsSsize_t(args[1]);
+  if (PyErr_Occurred()) return NULL;
   tp_tensor *to = address(args[2]);
+  if (PyErr_Occurred()) return NULL;
+  const int device = device_of(args, n, 3);
   if (PyErr_Occurred()) return NULL;
   Py_ssize_t done = 0;
   if (to != NULL && (PyList_Check(args[0]) || PyTuple_Check(args[0]))) {
@@ -100,7 +110,7 @@ static PyObject *py_matrices(PyObject *self, PyObject *const *args, Py_ssize_t n
     while (done < count && done < PySequence_Fast_GET_SIZE(args[0])) {
       PyObject *t = PySequence_Fast_GET_ITEM(args[0], done);
       Py_INCREF(t);
-      const int ok = describe(t, 2, to + done);
+      const int ok = describe(t, 2, device, to + done);
       Py_DECREF(t);
       if (!ok) {
         PyErr_Clear();
@@ -115,28 +125,32 @@ static PyObject *py_matrices(PyObject *self, PyObject *const *args, Py_ssize_t n
 /* Addresses of contiguous CUDA tensors, or None where the caller has to look for itself. */
 static PyObject *py_vector(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (n != 3) return PyErr_Format(PyExc_TypeError, "vector(tensor, type, entries)");
+  if (n != 3 && n != 4) return PyErr_Format(PyExc_TypeError, "vector(tensor, type, entries, device)");
   const long type = PyLong_AsLong(args[1]);
+  if (PyErr_Occurred()) return NULL;
   const long long entries = PyLong_AsLongLong(args[2]);
+  if (PyErr_Occurred()) return NULL;
+  const int device = device_of(args, n, 3);
   if (PyErr_Occurred()) return NULL;
   unsigned long long at = 0, bytes = 0;
 #ifdef TP_WITH_TORCH
-  at = with_torch && type >= 0 ? tp_address_torch(args[0], (int)type, entries, &bytes) : 0;
+  at = with_torch && type >= 0 ? tp_address_torch(args[0], (int)type, entries, device, &bytes) : 0;
 #endif
-  (void)type, (void)entries, (void)bytes;
+  (void)type, (void)entries, (void)device, (void)bytes;
   if (at == 0) Py_RETURN_NONE;
   return PyLong_FromUnsignedLongLong(at);
 }
 
 static PyObject *py_bytes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (n != 1) return PyErr_Format(PyExc_TypeError, "bytes(tensor)");
+  if (n != 1 && n != 2) return PyErr_Format(PyExc_TypeError, "bytes(tensor, device)");
+  const int device = device_of(args, n, 1);
+  if (PyErr_Occurred()) return NULL;
   unsigned long long at = 0, bytes = 0;
 #ifdef TP_WITH_TORCH
-  at = with_torch ? tp_address_torch(args[0], -1, -1, &bytes) : 0;
-#else
-  (void)args;
+  at = with_torch ? tp_address_torch(args[0], -1, -1, device, &bytes) : 0;
 #endif
+  (void)device;
   if (at == 0) Py_RETURN_NONE;
   return Py_BuildValue("KK", at, bytes);
 }
@@ -213,11 +227,11 @@ static PyObject *py_reads_torch(PyObject *self, PyObject *const *args, Py_ssize_
 static PyMethodDef methods[] = {
     {"dtypes", (PyCFunction)(void (*)(void))py_dtypes, METH_FASTCALL, "dtypes(f32, bf16, e4m3, u8): the type objects of TP_F32, TP_BF16, TP_E4M3, TP_U8"},
     {"reads_torch", (PyCFunction)(void (*)(void))py_reads_torch, METH_FASTCALL, "reads_torch(version and revision of the torch that runs) -> whether tensors are read without their attributes"},
-    {"matrix", (PyCFunction)(void (*)(void))py_matrix, METH_FASTCALL, "matrix(tensor, address) -> whether it was described there"},
+    {"matrix", (PyCFunction)(void (*)(void))py_matrix, METH_FASTCALL, "matrix(tensor, address[, device]) -> whether it was described there (device: the GPU on which it must lie, -1: any)"},
     {"row", (PyCFunction)(void (*)(void))py_row, METH_FASTCALL, "row(tensor, address): a 1-D tensor as a matrix of one row"},
-    {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address) -> how many of the first were described"},
-    {"vector", (PyCFunction)(void (*)(void))py_vector, METH_FASTCALL, "vector(tensor, type, entries) -> address of a contiguous CUDA tensor of the type (tp_dtype, 4 for int32) with that many entries (-1: any), or None"},
-    {"bytes", (PyCFunction)(void (*)(void))py_bytes, METH_FASTCALL, "bytes(tensor) -> (address, size) of a contiguous CUDA tensor, or None"},
+    {"matrices", (PyCFunction)(void (*)(void))py_matrices, METH_FASTCALL, "matrices(sequence, count, address[, device]) -> how many of the first were described"},
+    {"vector", (PyCFunction)(void (*)(void))py_vector, METH_FASTCALL, "vector(tensor, type, entries[, device]) -> address of a contiguous CUDA tensor of the type (tp_dtype, 4 for int32) with that many entries (-1: any), or None"},
+    {"bytes", (PyCFunction)(void (*)(void))py_bytes, METH_FASTCALL, "bytes(tensor[, device]) -> (address, size) of a contiguous CUDA tensor, or None"},
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, #name "(address of tp_" #name ", its arguments) -> status"}
     METHOD(rotary), METHOD(window_attn), METHOD(cache4_store), METHOD(cache4_load), METHOD(cache4_attn),
     {NULL, NULL, 0, NULL}};

@@ -21,13 +21,14 @@ int type_of(const at::Tensor &t) {
 
 }  // namespace
 
-// 1: described; 0: left to the caller; -1: no plain tensor (a subclass, a stand-in).
-extern "C" int tp_describe_torch(PyObject *o, long dims, tp_tensor *d) {
+// 1: described; 0: left to the caller; -1: no plain tensor (a subclass, a stand-in). device: the GPU on which it
+// must lie, -1: any; one comparison here, where the attribute costs the interpreter 0.4 us a tensor.
+extern "C" int tp_describe_torch(PyObject *o, long dims, int device, tp_tensor *d) {
   if (!THPVariable_CheckExact(o)) return -1;
   try {
     const at::Tensor &t = THPVariable_Unpack(o);
     const int type = type_of(t);
-    if (!t.is_cuda() || type < 0 || type > TP_U8 || t.dim() != dims) return 0;
+    if (!t.is_cuda() || type < 0 || type > TP_U8 || t.dim() != dims || (device >= 0 && t.get_device() != device)) return 0;
     const auto size = t.sizes(), stride = t.strides();
     const int64_t rows = dims == 2 ? size[0] : 1, cols = size[dims - 1], ld = dims == 2 ? stride[0] : 1;
     if (rows == 0 || cols == 0 || stride[dims - 1] != 1) return 0;
@@ -43,12 +44,12 @@ extern "C" int tp_describe_torch(PyObject *o, long dims, tp_tensor *d) {
 
 // The address of a contiguous CUDA vector (any shape) of type `type` (as type_of) with n entries (-1: any number),
 // 0 where the caller has to look for itself. *bytes receives its size.
-extern "C" unsigned long long tp_address_torch(PyObject *o, int type, long long n, unsigned long long *bytes) {
+extern "C" unsigned long long tp_address_torch(PyObject *o, int type, long long n, int device, unsigned long long *bytes) {
   if (!THPVariable_CheckExact(o)) return 0;
   try {
     const at::Tensor &t = THPVariable_Unpack(o);
     const int64_t have = t.numel();
-    if (!t.is_cuda() || (type >= 0 && type_of(t) != type) || have == 0 || (n >= 0 && have != n) || !t.is_contiguous()) return 0;
+    if (!t.is_cuda() || (device >= 0 && t.get_device() != device) || (type >= 0 && type_of(t) != type) || have == 0 || (n >= 0 && have != n) || !t.is_contiguous()) return 0;
     *bytes = static_cast<unsigned long long>(have) * t.element_size();
     return reinterpret_cast<unsigned long long>(t.mutable_data_ptr());
   } catch (...) {

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import importlib
+import operator
 import os
 import struct
 import threading
@@ -86,6 +87,21 @@ _P = ctypes.POINTER
 _T = _P(TpTensor)
 _S = ctypes.c_void_p  # cudaStream_t
 _A = ctypes.c_void_p
+
+
+class _I32:
+    """A 32-bit integer argument: ctypes itself would cut a larger one to its low bits."""
+
+    @classmethod
+    def from_param(cls, x):
+        if isinstance(x, ctypes.c_int32):
+            return x
+        x = operator.index(x)
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"out of range: {x}")
+        return ctypes.c_int32(x)
+
+
 _SIGS = {
     "tp_plan_create": ([_P(TpDims), _P(ctypes.c_void_p)], ctypes.c_int),
     "tp_plan_destroy": ([ctypes.c_void_p], ctypes.c_int),
@@ -127,14 +143,14 @@ _SIGS = {
     "tp_prefix_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _A, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
     "tp_cache_evict": ([_A, ctypes.c_int64, _A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _A, _A, _A, _A,
                         _A, _S], ctypes.c_int),
-    "tp_rotary": ([_A, ctypes.c_int64, _A, ctypes.c_int32, _A, ctypes.c_int32, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, _A,
+    "tp_rotary": ([_A, ctypes.c_int64, _A, _I32, _A, _I32, _A, _I32, _I32, _A, _A, _A,
                    _A, _S], ctypes.c_int),
-    "tp_window_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
-    "tp_window_attn": ([_A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
+    "tp_window_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, _I32, _I32], ctypes.c_size_t),
+    "tp_window_attn": ([_A, _A, _A, _A, _I32, _I32, _A, _A, ctypes.c_size_t, _S], ctypes.c_int),
     "tp_cache4_store": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _A, _S], ctypes.c_int),
     "tp_cache4_load": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _A, _S], ctypes.c_int),
-    "tp_cache4_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
-    "tp_cache4_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, ctypes.c_int32, ctypes.c_int32, _A, _A, ctypes.c_size_t,
+    "tp_cache4_attn_workspace_size": ([_A, ctypes.c_int64, ctypes.c_int64, _I32, _I32], ctypes.c_size_t),
+    "tp_cache4_attn": ([_A, ctypes.c_int64, _A, _A, _A, _A, _A, _A, _I32, _I32, _A, _A, ctypes.c_size_t,
                         _S], ctypes.c_int),
     "tp_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "tp_last_cuda_error": ([], ctypes.c_int32),
@@ -800,6 +816,8 @@ def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout
     axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
     if axis is not None:
         if not isinstance(axis, ctypes.Array):
+            if any(not 0 <= x < axes for x in axis):
+                raise ValueError(f"axis must have entries in [0, {axes})")
             axis = (ctypes.c_int32 * len(axis))(*axis)
         if axis._type_ is not ctypes.c_int32 or len(axis) != pairs:
             raise ValueError(f"axis must have {pairs} entries, one per pair")

@@ -157,17 +157,34 @@ static PyObject *py_bytes(PyObject *self, PyObject *const *args, Py_ssize_t n) {
 
 /* Calls of the library with many arguments that take a few us: ctypes converts each argument by itself, 1 us a
  * call. The first argument is the entry point's address (this module does not link the library), then
- * come its own: integers, and for a pointer also None or an object with a buffer (a ctypes array). */
-static int values(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, unsigned pointers, unsigned long long *v) {
+ * come its own: integers, and for a pointer also None or an object with a buffer (a ctypes array). An
+ * integer that its parameter does not hold is an error: cut to 32 bits, a window of 2^32 + 7 would be one of 7. */
+static int integer(PyObject *arg, Py_ssize_t i, int narrow, unsigned long long *v) {
+  int over = 0;
+  const long long x = PyLong_AsLongLongAndOverflow(arg, &over);
+  if (over == 0 && !(x == -1 && PyErr_Occurred()) && (!narrow || (x >= INT32_MIN && x <= INT32_MAX))) {
+    *v = (unsigned long long)x;
+    return 1;
+  }
+  if (over > 0 && !narrow) { /* addresses go up to 2^64 */
+    *v = PyLong_AsUnsignedLongLong(arg);
+    if (!PyErr_Occurred()) return 1;
+    PyErr_Clear();
+  }
+  if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "argument %zd is out of range: %S", i, arg);
+  return 0;
+}
+static int values(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, unsigned pointers, unsigned narrow, unsigned long long *v) {
   if (n != want) return PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", want, n), 0;
   for (Py_ssize_t i = 0; i < n; ++i) {
     if (PyLong_Check(args[i])) {
-      v[i] = PyLong_AsUnsignedLongLongMask(args[i]);
+      if (!integer(args[i], i, narrow >> i & 1, v + i)) return 0;
     } else if (PyIndex_Check(args[i])) {
       PyObject *x = PyNumber_Index(args[i]);
       if (x == NULL) return 0;
-      v[i] = PyLong_AsUnsignedLongLongMask(x);
+      const int ok = integer(x, i, narrow >> i & 1, v + i);
       Py_DECREF(x);
+      if (!ok) return 0;
     } else if (!(pointers >> i & 1)) {
       return PyErr_Format(PyExc_TypeError, "argument %zd must be an integer", i), 0;
     } else if (args[i] == Py_None) {
@@ -183,24 +200,24 @@ static int values(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, unsigned
   return 1;
 }
 #define AT(i) ((void *)(uintptr_t)v[i])
-#define ENTRY(name, count, pointers, ...)                                                   \
+#define ENTRY(name, count, pointers, narrow, ...)                                                 \
   static PyObject *py_##name(PyObject *self, PyObject *const *args, Py_ssize_t n) { \
     (void)self;                                                                   \
     unsigned long long v[count + 1];                                              \
-    if (!values(args, n, count + 1, pointers, v)) return NULL;                    \
+    if (!values(args, n, count + 1, pointers, narrow, v)) return NULL;            \
     tp_status st;                                                                 \
     Py_BEGIN_ALLOW_THREADS                                                        \
     st = ((__typeof__(&tp_##name))AT(0))(__VA_ARGS__);                            \
     Py_END_ALLOW_THREADS                                                          \
     return PyLong_FromLong((long)st);                                             \
   }
-/* after the count: which arguments are pointers, a bit each */
-ENTRY(rotary, 14, 0x7caa, AT(1), (int64_t)v[2], AT(3), (int32_t)v[4], AT(5), (int32_t)v[6], AT(7), (int32_t)v[8], (int32_t)v[9], AT(10), AT(11),
+/* after the count: which arguments are pointers, and which are 32 bits wide, a bit each */
+ENTRY(rotary, 14, 0x7caa, 0x350, AT(1), (int64_t)v[2], AT(3), (int32_t)v[4], AT(5), (int32_t)v[6], AT(7), (int32_t)v[8], (int32_t)v[9], AT(10), AT(11),
       AT(12), AT(13), AT(14))
-ENTRY(window_attn, 10, 0x59e, AT(1), AT(2), AT(3), AT(4), (int32_t)v[5], (int32_t)v[6], AT(7), AT(8), (size_t)v[9], AT(10))
-ENTRY(cache4_store, 11, 0xffa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10), AT(11))
-ENTRY(cache4_load, 10, 0x7fa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10))
-ENTRY(cache4_attn, 14, 0x59fa, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), (int32_t)v[9], (int32_t)v[10], AT(11), AT(12),
+ENTRY(window_attn, 10, 0x59e, 0x60, AT(1), AT(2), AT(3), AT(4), (int32_t)v[5], (int32_t)v[6], AT(7), AT(8), (size_t)v[9], AT(10))
+ENTRY(cache4_store, 11, 0xffa, 0, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10), AT(11))
+ENTRY(cache4_load, 10, 0x7fa, 0, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), AT(9), AT(10))
+ENTRY(cache4_attn, 14, 0x59fa, 0x600, AT(1), (int64_t)v[2], AT(3), AT(4), AT(5), AT(6), AT(7), AT(8), (int32_t)v[9], (int32_t)v[10], AT(11), AT(12),
       (size_t)v[13], AT(14))
 
 static PyObject *py_dtypes(PyObject *self, PyObject *const *args, Py_ssize_t n) {

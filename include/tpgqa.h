@@ -796,7 +796,8 @@ size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t
  *               NULL where that is 0.
  * Scores are products of q's values (at f16's 11 bits or more of the head's largest) with
  * whole codes, in f32; the statistics and sums are f32; p * scale is rounded to bf16 for
- * P V, A to bf16. |q| up to 2^100. Outputs overlap no input.
+ * P V, A to bf16. |q| up to 2^100. A score below f32's range is -infinity and weighs nothing
+ * (a head without any other gives NaN), one above it gives NaN. Outputs overlap no input.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
  * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
 tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_codes,

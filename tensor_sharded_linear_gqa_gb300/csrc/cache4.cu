@@ -566,6 +566,9 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
   // each of the values' loads takes four neighbouring rows.
   const int key = (r >> 1) + 4 * (r & 1);
   int stage = 0;
+  // The heads 2 nt + e that have no reference yet, a bit each: until a tile has a score above -infinity theirs is 0,
+  // and nothing is lost (every p is 0).
+  uint32_t none = (1u << 2 * NT) - 1;
   for (int t = t0 + warp; t < t1; t += kAttnWarps) {
     cp_wait<kStages - 2>();
     __syncwarp();  // the tile has landed, and every lane has read the one before, whose stage is filled next
@@ -626,8 +629,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
             for (int nt = 0; nt < NT; ++nt) s[half][nt][2 * u] = s[half][nt][2 * u + 1] = -INFINITY;
     }
     // p, and its sums; the references move when a sum says that some p is large, which is rare after
-    // the first tile, whose maximum is the first reference (a tile always has a key that is seen)
-    const bool first = t == t0 + warp;
+    // the first tile, whose maximum is the first reference
     float pr[2][NT][4], sum[NT][2];
     auto weights = [&]() {
       bool fine = true;
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
       }
       return fine;
     };
-    if (__any_sync(0xffffffffu, !weights() || first)) {
+    if (__any_sync(0xffffffffu, !weights() || none != 0)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -652,7 +654,10 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float up = fmaxf(mx, first ? -FLT_MAX : 0.f), alpha = first ? 1.f : ex2(-up);
+          const uint32_t bit = 1u << (2 * nt + e);
+          const bool had = !(none & bit), any = mx > -INFINITY;  // NaN are no references
+          const float up = fmaxf(any ? mx : 0.f, had ? 0.f : -FLT_MAX), alpha = had ? ex2(-up) : 1.f;
+          if (any) none &= ~bit;
           m[nt][e] += up;
           l[nt][e] *= alpha;
 #pragma unroll
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(kAttnThreads4, NT == 1 ? 3 : 2) k_cache4_attn(
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int x = 4; x < 32; x *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
-      if (r == 0) s_ml[warp][8 * nt + 2 * c + e] = make_float2(t0 + warp < t1 ? m[nt][e] : -FLT_MAX, l[nt][e]);
+      if (r == 0) s_ml[warp][8 * nt + 2 * c + e] = make_float2(none >> (2 * nt + e) & 1 ? -FLT_MAX : m[nt][e], l[nt][e]);
     }
   __syncthreads();  // the rings are free
   float *sums = reinterpret_cast<float *>(smem);

@@ -758,7 +758,8 @@ tp_status tp_window_attn(const tp_plan *plan, const tp_tensor *q, const tp_tenso
  * A length outside [0, C], a count outside [0, n] and tokens past position C - 1 are
  * reported by tp_device_status (TP_ERR_BAD_LENGTH): a sequence with a bad length stores
  * nothing, one with a bad count as many of its n tokens as the nearer bound allows, and
- * tokens past the end are dropped. A batch above 65535 is TP_ERR_UNSUPPORTED.
+ * tokens past the end are dropped. A batch above 65535 and n * kv heads above 2^31 - 1024 are
+ * TP_ERR_UNSUPPORTED.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_UNSUPPORTED,
  * TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
 tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *lengths, const int32_t *counts,
@@ -773,7 +774,7 @@ tp_status tp_cache4_store(const tp_plan *plan, int64_t batch, const int32_t *len
  *  k_out, v_out : per kv source [batch*n x heads*d], all f32 (exact) or all bf16 (rounded
  *                 once). Positions past the cache's end give zeros, a sequence with a
  *                 bad first nothing else.
- * Errors: as tp_cache4_store. */
+ * Limits and errors: as tp_cache4_store. */
 tp_status tp_cache4_load(const tp_plan *plan, int64_t batch, const int32_t *first, const tp_tensor *k_codes,
                          const tp_tensor *k_scale, const tp_tensor *v_codes, const tp_tensor *v_scale, tp_tensor *k_out,
                          tp_tensor *v_out, tp_stream_t stream);
@@ -797,7 +798,8 @@ size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t batch, int64_t
  * Scores are products of q's values (at f16's 11 bits or more of the head's largest) with
  * whole codes, in f32; the statistics and sums are f32; p * scale is rounded to bf16 for
  * P V, A to bf16. |q| up to 2^100. A score below f32's range is -infinity and weighs nothing
- * (a head without any other gives NaN), one above it gives NaN. Outputs overlap no input.
+ * (a head without any other gives NaN), one above it gives NaN. Outputs overlap no input. batch * q heads above
+ * 2^23 and more than 65535 q heads a kv head are TP_ERR_UNSUPPORTED.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,
  * TP_ERR_UNSUPPORTED, TP_ERR_RANK_FAILED, TP_ERR_CUDA. */
 tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp_tensor *q, const tp_tensor *k_codes,

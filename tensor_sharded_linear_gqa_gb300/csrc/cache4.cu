@@ -923,10 +923,13 @@ size_t workspace_bytes_of(const Shape4 &s, long long rows, long long d) {
   return s.splits > 1 && !s.cluster ? sums_bytes(s, rows, d) + round256(static_cast<size_t>(s.splits) * rows * 8) : 0;
 }
 
-// Head sizes that the format's layouts cover, and sizes whose grids and indices are in range.
-bool sizes_ok(const tp_dims &d, long long batch, long long cap) {
-  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kC4Ranks && batch <= 0x7fffffffLL / 256 / d.num_q_heads &&
-         cap <= 0x7fffffffLL - 256 && d.num_q_heads / d.num_kv_heads <= 65535;
+// Head sizes that the format's layouts cover, and capacities whose positions are in range.
+bool cache_ok(const tp_dims &d, long long cap) {
+  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kC4Ranks && cap <= 0x7fffffffLL - 256;
+}
+// The attention's own: a row is a (sequence, q head), and its grid has up to 64 splits of each.
+bool attn_sizes_ok(const tp_dims &d, long long batch, long long cap) {
+  return cache_ok(d, cap) && batch <= (1LL << 23) / d.num_q_heads && d.num_q_heads / d.num_kv_heads <= 65535;
 }
 
 // The four tensors of a kv source's cache.
@@ -964,7 +967,7 @@ tp_status check_call(const tp_plan *plan, int64_t batch, const tp_tensor *kc, co
       (st = check_cache(ks, g.sources, rows, g.hd / kGroup, TP_BF16)) != TP_OK ||
       (st = check_cache(vs, g.sources, rows, g.hd / kGroup, TP_BF16)) != TP_OK)
     return st;
-  if (!sizes_ok(g.dims, batch, g.cap)) return TP_ERR_UNSUPPORTED;
+  if (!cache_ok(g.dims, g.cap)) return TP_ERR_UNSUPPORTED;
   for (int r = 0; r < g.sources; ++r) {
     out.k_codes[r] = static_cast<uint8_t *>(kc[r].ptr);
     out.v_codes[r] = static_cast<uint8_t *>(vc[r].ptr);
@@ -991,7 +994,7 @@ tp_status copy_call(const Given &g, CopyParams &p, int64_t batch, const int32_t 
       p.ld[w][r] = t.ld;
     }
   const long long rows = batch * n;
-  if (n * g.dims.num_kv_heads > 0x7fffffffLL - 1024 || batch > 65535) return TP_ERR_UNSUPPORTED;
+  if (n * g.dims.num_kv_heads > 0x7fffffffLL - 1023 || batch > 65535) return TP_ERR_UNSUPPORTED;
   if (rows > 0 && !starts) return TP_ERR_INVALID_ARG;
   if (!ptr_aligned(starts, 4)) return TP_ERR_ALIGNMENT;
   tp_status st = check_rank_health(g.n);
@@ -1049,7 +1052,7 @@ extern "C" size_t tp_cache4_attn_workspace_size(const tp_plan *plan, int64_t bat
                                                 int32_t sinks) {
   tp_dims d;
   if (!plan || batch < 1 || capacity < 1 || window < 1 || sinks < 0 || tp_plan_dims(plan, &d) != TP_OK) return 0;
-  if (!sizes_ok(d, batch, capacity)) return 0;
+  if (!attn_sizes_ok(d, batch, capacity)) return 0;
   return workspace_bytes_of(shape4_of(d, batch, capacity, window, sinks), batch * d.num_q_heads, d.head_dim);
 }
 
@@ -1062,6 +1065,7 @@ extern "C" tp_status tp_cache4_attn(const tp_plan *plan, int64_t batch, const tp
   tp_status st = check_call(plan, batch, k_codes, k_scale, v_codes, v_scale, g, p.cache);
   if (st != TP_OK) return st;
   if (!q || !a || window < 1 || sinks < 0) return TP_ERR_INVALID_ARG;
+  if (!attn_sizes_ok(g.dims, batch, g.cap)) return TP_ERR_UNSUPPORTED;
   const long long qc = g.dims.num_q_heads / g.n * g.hd;
   for (int r = 0; r < g.n; ++r) {
     for (const tp_tensor *t : {q + r, static_cast<const tp_tensor *>(a + r)}) {

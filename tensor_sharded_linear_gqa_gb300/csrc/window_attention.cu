@@ -762,7 +762,7 @@ int group_of(const tp_dims &d) {
 
 // Sizes that the item arithmetic takes in 32 bits.
 bool sizes_ok(const tp_dims &d, long long tokens, long long keys) {
-  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kWinRanks && tokens <= 0x7fffffffLL / 8 / d.num_q_heads &&
+  return (d.head_dim == 64 || d.head_dim == 128) && d.tp_size <= kWinRanks && tokens <= (1LL << 28) / d.num_q_heads &&
          keys <= 0x7fffffffLL - 256;
 }
 

@@ -1,8 +1,8 @@
 """A long conversation through one tensor-parallel attention block whose cache is held in 4 bits:
 
   the prompt, a chunk of tokens at a time: norm -> q/k/v product -> rotary positions -> keys and values into
-  the 4-bit cache -> attention over a sliding window and the first tokens (the window's part before
-  the chunk is read back from the cache) -> output product onto the residual;
+  the 4-bit cache -> attention over a sliding window and the first tokens (what the chunk sees of
+  the cache, and no more, is read back) -> output product onto the residual;
   then one token at a time for every sequence: the same with attention over the 4-bit cache itself.
 
 Run it on a GB300 after the library is built:  python examples/long_context.py
@@ -47,6 +47,8 @@ class Block:
         self.cache = [[torch.zeros(rows, cols, dtype=dtype, device="cuda") for _ in range(self.sources)]
                       for cols, dtype in ((head_dim // 2, torch.uint8), (head_dim // 32, BF16)) * 2]
         self.lengths = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        # keys and values of a prompt in bf16, by position; those that no token of a chunk sees are never read back
+        self.kv = [torch.zeros(capacity, self.kv_cols, dtype=BF16, device="cuda") for _ in range(2)]
         size = tp.tp_cache4_attn_workspace_size(self.plan, batch, capacity, window, sinks)
         self.workspace = torch.empty(size, dtype=torch.uint8, device="cuda")
 
@@ -81,10 +83,13 @@ class Block:
             n = part.shape[0]
             q, k, v = self.project(part, positions[:, t0:t0 + n].contiguous())
             tp.tp_cache4_store(self.plan, torch.full((1,), t0, dtype=torch.int32, device="cuda"), k, v, *cache)
-            # every key so far, as its codes say; of those before the window only the first are looked at
-            kv = [torch.empty(t0 + n, self.kv_cols, dtype=BF16, device="cuda") for _ in range(2)]
-            keys, values = (self.shards(t, self.sources) for t in kv)
-            tp.tp_cache4_load(self.plan, torch.zeros(1, dtype=torch.int32, device="cuda"), *cache, keys, values)
+            # the keys that the chunk sees, as their codes say: those from its first token's window on, and the first ones
+            keys, values = (self.shards(t[:t0 + n], self.sources) for t in self.kv)
+            near = max(0, t0 - self.window + 1)
+            for first, end in ((near, t0 + n), (0, min(near, self.sinks))):
+                if first < end:
+                    tp.tp_cache4_load(self.plan, torch.full((1,), first, dtype=torch.int32, device="cuda"), *cache,
+                                      [t[first:end] for t in keys], [t[first:end] for t in values])
             a = torch.empty(n, self.q_cols, dtype=BF16, device="cuda")
             size = tp.tp_window_attn_workspace_size(self.plan, n, t0 + n, self.window, self.sinks)
             tp.tp_window_attn(self.plan, q, keys, values, self.window, self.sinks, self.shards(a, self.ranks),

@@ -725,7 +725,8 @@ size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tokens, int64_
  * S, the statistics and the sums are f32; P is rounded to bf16 for P V, A to bf16. The
  * keys of about 256 rows (tokens by heads of a group) are read together, and a weight of 0
  * times an infinity or NaN among their values is NaN: such a value reaches those of
- * these rows that do not see its key, too. Scores of keys out of sight may be anything.
+ * these rows that do not see its key, too. Scores of keys out of a row's sight may be anything, and so may keys and
+ * values that no query of the call sees: their memory need not have been written.
  * d must be 64 or 128, tp_size at most 32, S at most 2^31 - 257, T * q heads at
  * most 2^28, else TP_ERR_UNSUPPORTED. Outputs overlap no input.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,

@@ -10,8 +10,10 @@
 // key split). Its keys are two runs, the window of its rows from the first row's first key
 // on and the first tokens before it, each in units of 16 keys; blocks are 8
 // neighbouring units of the two runs together, so that only the last one is short (its products are
-// as narrow as it is) and a few first tokens cost a unit, not a block. Masks are applied
-// in the blocks where a row's limits lie.
+// as narrow as it is) and a few first tokens cost a unit, not a block. The units of the first tokens end with the
+// last of these, so that what fills the first one up are rows before key 0, which the copy makes zeros: rows behind
+// them would be keys that maybe no query sees, whose memory holds anything, and 0 * NaN is NaN in P V.
+// Masks are applied in the blocks where a row's limits lie.
 //
 // k_window's roles (one CTA an SM, persistent):
 //   warp 0        TMA: one lane, K and V tiles of 128 keys in turn through one ring of five slots
@@ -86,9 +88,12 @@ struct WindowMaps {
 };
 
 // The keys of an item's rows in units of 16: the window run (w_units units from key w0 on), then the
-// first tokens (units from key 0 on, keys below `sinks`, which end before w0).
+// first tokens (units that end with key sinks - 1, at w0 - 1 or before; the first one's first `pad` keys are below 0).
 struct Keys {
   int w0, w_units, sinks, units, blocks;
+  __host__ __device__ int pad() const { return -sinks & 15; }
+  // the key of column 0 of block j where that lies in the first tokens' run, or would if it went on to the left
+  __host__ __device__ int first(int j) const { return 128 * j - 16 * w_units - pad(); }
 };
 // Of tokens t0 .. t1, the item's first and last.
 __host__ __device__ inline Keys keys_of(int t0, int t1, int tokens, int keys, int window, int sinks) {
@@ -301,13 +306,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
               const CUtensorMap *map = v ? &maps.v16[src] : &maps.k16[src];
               ptx::mbar_arrive_expect_tx(bar, n * 2048u * C::kCh);
               for (int u = 0; u < n; ++u) {
-                const int key = u < w ? it.k.w0 + 128 * j + 16 * u : 128 * j - 16 * it.k.w_units + 16 * u;
+                const int key = (u < w ? it.k.w0 + 128 * j : it.k.first(j)) + 16 * u;
                 for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile + u * 2048u, map, col + c * 64, key, bar);
               }
             } else {
               const CUtensorMap *map = v ? &maps.v[src] : &maps.k[src];
               ptx::mbar_arrive_expect_tx(bar, C::kTile);
-              const int key = w > 0 ? it.k.w0 + 128 * j : 128 * j - 16 * it.k.w_units;
+              const int key = w > 0 ? it.k.w0 + 128 * j : it.k.first(j);
               for (int c = 0; c < C::kCh; ++c) ptx::tma_load_2d(dst + c * kSubTile, map, col + c * 64, key, bar);
             }
             at.on(1);
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
         const int n = it.units(j), wu = max(0, min(8, it.k.w_units - 8 * j));
         const int k0 = it.k.w0 + 128 * j;  // key of column 0 of the window run
         const int hi = min(pos - k0 + 1, 16 * wu), lo = w0 - k0, first = p.sinks - k0;  // seen: i < hi and (i >= lo or i < first)
-        const int hs = it.k.sinks - (128 * j - 16 * it.k.w_units);                     // seen of the first tokens: i < hs
+        const int ls = -it.k.first(j);                                                 // seen of the first tokens: i >= ls
         if (j + 1 == it.j1) more = next_rows(r, next);  // while S is on its way
         if (!wait_all(s_full, gs & 1)) {
           ok = false;
@@ -544,9 +549,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             if (__all_sync(0xffffffffu, hi >= 32 * h + 32 && lo <= 32 * h)) continue;
-            const uint32_t win = low_bits(16 * wu - 32 * h);
             const uint32_t see = (low_bits(hi - 32 * h) & (~low_bits(lo - 32 * h) | low_bits(first - 32 * h))) |
-                                 (low_bits(min(hs, 16 * n) - 32 * h) & ~win);
+                                 (low_bits(16 * n - 32 * h) & ~low_bits(ls - 32 * h));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(see & (1u << i))) v[32 * h + i] = __float_as_uint(-INFINITY);

@@ -681,10 +681,10 @@ typedef enum tp_rotary_layout {
  * pair i of every head of q and k, with the pair's values (a, b):
  *   angle = positions[axis[i]][t] * freq[i],
  *   a' = a cos(angle) - b sin(angle),  b' = a sin(angle) + b cos(angle),
- * computed in f32 from an angle that is reduced without loss, rounded once. The
+ * computed in f32 from an angle that is reduced modulo 2 pi to 2^-29 (whatever the position), rounded once. The
  * values of a head past 2 * pairs are copied.
  *  positions : device int32 [n_axes x tokens], row-major; any value.
- *  freq      : device f32 [pairs], finite, radians a position (scaled frequencies of
+ *  freq      : device f32 [pairs], below 2^56 in size, radians a position (scaled frequencies of
  *              any kind are given here).
  *  axis      : host int32 [pairs] with values in [0, n_axes), or NULL (all 0).
  *  inverse   : 1 turns by the negated angle: the call's own inverse, and the gradient

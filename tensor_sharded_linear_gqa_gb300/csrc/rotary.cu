@@ -8,15 +8,17 @@
 // (those of one 16-byte piece), takes their sines and cosines into registers, and walks the
 // heads of its CTA's share of q and k, two heads' pieces in flight: neither a table nor a
 // barrier stands between the loads and the stores. Values that do not turn have threads of their own.
-// 8192 tokens of 72 heads of 128 (302 MB): 53 us, 5.7 TB/s; with four heads in flight a thread 57,
+// 8192 tokens of 72 heads of 128 (302 MB): 51 us, 6.0 TB/s; with four heads in flight a thread 57,
 // with the values that do not turn copied by the threads of those that do 2047 f32 tokens, half of
 // whose values turn, 7.9 us in place of 5.3.
 //
 // Angles. In f32 the angle of position 10^6 is off by 0.03 already. A turn is therefore a
-// 64-bit fixed-point fraction: F = freq / (2 pi) mod 1 in units of 2^-64, from 64-bit floats once a
-// CTA and pair (they are slow here), and position * F wraps by itself as an integer
-// product, whatever the position's sign. F is off by 2^-53 of freq / (2 pi), so a turn
-// by at most 2^-22 at position 2^31 and by 2^-33 at 10^6; its upper 32 bits go on as f32.
+// 64-bit fixed-point fraction: F = freq / (2 pi) mod 1 in units of 2^-64, once a CTA and pair, and
+// position * F wraps by itself as an integer product, whatever the position's sign. F is the frequency's 24-bit
+// significand times the digits of 1 / (2 pi) from its exponent on (M. Payne and R. Hanek, "Radian reduction for
+// trigonometric functions", 1983), off by little more than a unit, so a turn by 2^-33 at position 2^31; its upper 32 bits go on
+// as f32. A 64-bit float product is off by 2^-52 of the angle (5e-5 at frequency 100 and position 2^31); one of two
+// 64-bit floats is not, but takes longer (2047 f32 tokens 6.1 us, 5.3 here).
 #include <cmath>
 #include <type_traits>
 
@@ -78,6 +80,27 @@ struct Piece<__nv_bfloat16, 8> {
   }
 };
 
+// freq / (2 pi) modulo 1, in units of 2^-64, of a frequency below 2^56.
+__device__ __forceinline__ unsigned long long turn_a_position(float freq) {
+  const uint32_t bits = __float_as_uint(freq), field = bits >> 23 & 255;
+  // freq = m * 2^e; the digits from 2^-(e + 96) up, of which those above 2^-e are whole turns and overflow
+  const uint32_t m = (bits & 0x7fffff) | (field ? 0x800000 : 0);
+  const int e = static_cast<int>(max(field, 1u)) - 150, down = max(32 - e, 0);
+  // 2^128 / (2 pi) in 32-bit words, the lowest first, and its 96 bits from bit `down` up
+  const uint32_t w[4] = {0x7d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
+  const int by = down >> 5;
+  uint32_t x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = 0;
+#pragma unroll
+    for (int k = i; k < 4; ++k)
+      if (k - i == by) x[i] = w[k];
+  }
+  const uint32_t d0 = __funnelshift_r(x[0], x[1], down), d1 = __funnelshift_r(x[1], x[2], down), d2 = __funnelshift_r(x[2], x[3], down);
+  const unsigned long long turn = (static_cast<unsigned long long>(d2) << 32 | d1) * m + (static_cast<unsigned long long>(d0) * m >> 32);
+  return bits >> 31 ? 0 - turn : turn;
+}
 // A turn's sine and cosine, the turn in units of 2^-64.
 __device__ __forceinline__ void turn_sincos(unsigned long long turn, float *s, float *c) {
   const int top = static_cast<int>((turn + 0x80000000ull) >> 32);  // in [-2^31, 2^31): half turns of 2^-31
@@ -89,12 +112,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(const __grid_constant__ 
   __shared__ unsigned long long s_turn[kMaxPairs];
   grid_dep_wait();
   grid_dep_launch();
-  for (int i = threadIdx.x; i < p.pairs; i += kRotThreads) {
-    const double per = static_cast<double>(p.freq[i]) * 0.15915494309189533577;  // turns a position
-    const double part = per - floor(per);
-    // 2^64 is out of the integer's range: the conversion takes 53 bits of the fraction at 2^63
-    s_turn[i] = static_cast<unsigned long long>(part * 0x1p63) << 1;
-  }
+  for (int i = threadIdx.x; i < p.pairs; i += kRotThreads) s_turn[i] = turn_a_position(p.freq[i]);
   __syncthreads();
   // of a head: pieces that turn, E pairs each, then pieces of 2 E values that do not
   const int turning = p.pairs / E, pieces = turning + p.still;

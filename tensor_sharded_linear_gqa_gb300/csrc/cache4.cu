@@ -917,7 +917,6 @@ tp_status launch_attn4(const Attn4Params &p, dim3 grid, cudaStream_t s) {
   return launched(launch_kernel(k_cache4_attn<D, NT>, grid, dim3(kAttnThreads4), kSmem, s, p.cluster ? p.splits : 1, p));
 }
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t sums_bytes(const Shape4 &s, long long rows, long long d) { return s.splits > 1 && !s.cluster ? round256(static_cast<size_t>(s.splits) * rows * d * 4) : 0; }
 size_t workspace_bytes_of(const Shape4 &s, long long rows, long long d) {
   return s.splits > 1 && !s.cluster ? sums_bytes(s, rows, d) + round256(static_cast<size_t>(s.splits) * rows * 8) : 0;

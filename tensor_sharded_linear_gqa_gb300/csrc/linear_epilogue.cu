@@ -75,7 +75,6 @@ struct LinearParams {
   CUtensorMap x[kMaxParts];  // one per K slice
 };
 
-__device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
 
 // Shard of a feature tile (shards are laid out in tile order).
 __device__ __forceinline__ int shard_of(const LinearParams &p, int nt) {
@@ -847,24 +846,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// Dynamic shared memory above 48 KB, granted once per device and kernel.
-template <typename K>
-cudaError_t allow_smem(K kernel, unsigned &mask, std::mutex &mu) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev < 32 && (mask & (1u << dev))) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-  if (e == cudaSuccess && dev < 32) mask |= 1u << dev;
-  return e;
-}
-
 template <bool F8, bool ADD>
 tp_status launch_split(const LinearParams &p, size_t smem, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_linear_split<F8, ADD>, mask, mu);
+  const cudaError_t e = allow_smem(k_linear_split<F8, ADD>, kSmemLimit, mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
   return launched(launch_kernel(k_linear_split<F8, ADD>, dim3(static_cast<unsigned>(p.m_tiles * p.n_tiles * p.split)),
                                 dim3(kThreads), smem, s, static_cast<unsigned>(p.split), p));
@@ -873,7 +859,7 @@ template <bool F8, int BN, bool Y32>
 tp_status launch_pair(const LinearParams &p, cudaStream_t s) {
   static unsigned mask = 0;
   static std::mutex mu;
-  const cudaError_t e = allow_smem(k_linear_pair<F8, BN, Y32>, mask, mu);
+  const cudaError_t e = allow_smem(k_linear_pair<F8, BN, Y32>, kSmemLimit, mask, mu);
   if (e != cudaSuccess) return cuda_fail(e);
   const int tiles = p.m_tiles * p.n_tiles, most = num_sms() / 2;
   return launched(launch_kernel(k_linear_pair<F8, BN, Y32>, dim3(2u * static_cast<unsigned>(tiles < most ? tiles : most)),

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "tp_internal.h"
 
 namespace tpgqa {
@@ -37,6 +39,21 @@ inline tp_status launched(cudaError_t e) {
   return e == cudaSuccess ? TP_OK : cuda_fail(e);
 }
 
+// Dynamic shared memory above 48 KB, granted once per device and kernel.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> g(mu);
+  if (dev < 32 && (mask & (1u << dev))) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 32) mask |= 1u << dev;
+  return e;
+}
+
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }  // regions of a workspace
+
 // Division by a number that the host knows: x / d = (umulhi(x, mul) + x) >> shift for x < 2^31.
 struct Divider {
   uint32_t mul, shift;
@@ -53,6 +70,8 @@ struct Divider {
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+__device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -63,6 +82,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // Two f32 in one register pair.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {

@@ -77,7 +77,6 @@ struct PrefixMaps {
   CUtensorMap k[kMaxRanks32], v[kMaxRanks32];  // prefix K and V of each kv source
 };
 
-__device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
 // q row (or output row) of sequence b, global q head h.
 __device__ __forceinline__ const __nv_bfloat16 *q_row(const PrefixAttnParams &p, int b, int h) {
   const int r = h / p.heads_per_rank;
@@ -118,25 +117,6 @@ constexpr int kPrefThreads = 320;
 constexpr uint32_t kSubTile = 128u * 128u;  // [128 rows x 64 bf16], swizzled
 constexpr float kSumLimit = 0x1p64f;
 
-// Shared-memory descriptor of an MN-major bf16 tile: rows of 64 MN values (128
-// bytes, swizzled) per k index, 8-row groups 1024 bytes apart (stride offset), the
-// next 64 MN values `mn_stride` bytes on (leading offset).
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-constexpr uint32_t kIdescBMn = 1u << 16;  // B operand MN-major
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -238,7 +218,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
     }
   } else if (warp == 1) {  // converged; one lane issues (see elect_one)
     constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
-    constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+    constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | ptx::kIdescBMn;
     const bool leader = ptx::elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -270,7 +250,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1) k_prefix_part(const __grid_co
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_bf16_ts(d, a + 8u * kk, desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, kk > 0 ? 1u : more);
+          ptx::mma_bf16_ts(d, a + 8u * kk, ptx::smem_desc_mn_sw128(va + kk * 2048u, kSubTile), idesc_o, kk > 0 ? 1u : more);
       }
       __syncwarp();
     };
@@ -1184,7 +1164,6 @@ Shape shape_of(long long batch, long long group, long long heads_kv, long long p
   return s;
 }
 long long score_pitch(long long cap) { return (cap + 3) / 4 * 4; }
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Regions {
   size_t o, ml, scores, total;
 };
@@ -1196,18 +1175,6 @@ Regions regions_of(const Shape &s, long long batch, long long heads_q, long long
   r.scores = r.ml + round256(rows * 8);
   r.total = r.scores + (weights ? round256(static_cast<size_t>(batch) * heads_q * score_pitch(cap) * 4) : 0);
   return r;
-}
-
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev < 32 && (mask & (1u << dev))) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 32) mask |= 1u << dev;
-  return e;
 }
 
 template <int D>

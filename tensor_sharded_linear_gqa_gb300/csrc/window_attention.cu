@@ -114,25 +114,6 @@ __device__ __forceinline__ Keys keys_of_part(const WindowParams &p, int part) {
   return keys_of(kRows * part >> p.group_shift, min(kRows * part + kRows - 1, p.rows - 1) >> p.group_shift, p.tokens, p.keys, p.window, p.sinks);
 }
 
-__device__ __forceinline__ void record(int *status, int code) { atomicCAS(status, 0, code); }
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
-  // MN-major bf16 tile: rows of 64 MN values (128 bytes, swizzled) a k index, 8-row groups
-  // 1024 bytes apart, the next 64 MN values mn_stride bytes on
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-constexpr uint32_t kIdescBMn = 1u << 16;  // B operand MN-major
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 template <int D>
 struct WinCfg {
   static constexpr int kCh = D / 64;                 // 64-column sub-tiles of a head
@@ -327,9 +308,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) k_window(const __grid_constant
     } else if (warp < 3) {  // converged; one lane issues (see elect_one)
       const int x = warp - 1;
       constexpr uint32_t idesc_s0 = ptx::idesc_bf16_f32(128, 0);  // + 2 units << 17: 16 columns a unit
-      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | kIdescBMn;
+      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, D) | ptx::kIdescBMn;
       // descriptors of the tiles' starts; the address field counts 16 bytes
-      const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sR), vd = desc_mn_sw128(sR, kSubTile);
+      const uint64_t qd = ptx::smem_desc_sw128(sQ), kd = ptx::smem_desc_sw128(sR), vd = ptx::smem_desc_mn_sw128(sR, kSubTile);
       const bool leader = ptx::elect_one();
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -770,18 +751,6 @@ bool sizes_ok(const tp_dims &d, long long tokens, long long keys) {
          keys <= 0x7fffffffLL - 256;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, unsigned &mask, std::mutex &mu) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev < 32 && (mask & (1u << dev))) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 32) mask |= 1u << dev;
-  return e;
-}
-
 template <int D, int TILES>
 tp_status launch_window(const WindowParams &p, const WindowMaps &maps, cudaStream_t s) {
   static unsigned mask = 0;
@@ -797,7 +766,6 @@ tp_status launch_window(const WindowParams &p, const WindowMaps &maps, cudaStrea
                                 dim3(kJoinThreads), 0, s, 1, p));
 }
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Bytes of the splits' sums before their (m, l), and of both.
 size_t sums_bytes(int split, long long rows_all, long long d) { return split > 1 ? round256(static_cast<size_t>(split) * rows_all * d * 4) : 0; }
 size_t workspace_bytes_of(int split, long long rows_all, long long d) {

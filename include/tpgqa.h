@@ -727,6 +727,8 @@ size_t tp_window_attn_workspace_size(const tp_plan *plan, int64_t tokens, int64_
  * times an infinity or NaN among their values is NaN: such a value reaches those of
  * these rows that do not see its key, too. Scores of keys out of a row's sight may be anything, and so may keys and
  * values that no query of the call sees: their memory need not have been written.
+ * The heads of a group are taken together by the largest power of two that divides the group and a rank's heads: K
+ * and V are read once for 8 heads a kv head, 3 times for 6, 7 times for 7.
  * d must be 64 or 128, tp_size at most 32, S at most 2^31 - 257, T * q heads at
  * most 2^28, else TP_ERR_UNSUPPORTED. Outputs overlap no input.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_DTYPE, TP_ERR_ALIGNMENT, TP_ERR_WORKSPACE,

@@ -823,7 +823,8 @@ def tp_rotary(plan: Plan, positions, freq, q, k, q_out, k_out, axis=None, layout
             raise ValueError(f"axis must have {pairs} entries, one per pair")
     g = _args(2 * n + 2 * src, device)
     st = _entry("rotary")(plan.handle, tokens, _dev_ptr(positions, "torch.int32", device=device), axes,
-                          _dev_ptr(freq, "torch.float32", device=device), pairs, axis, layout, int(inverse), None if q is None else g.many(q, n), None if k is None else g.many(k, src),
+                          _dev_ptr(freq, "torch.float32", device=device), pairs, axis, layout, int(inverse),
+                          None if q is None else g.many(q, n), None if k is None else g.many(k, src),
                           None if q_out is None else g.many(q_out, n), None if k_out is None else g.many(k_out, src),
                           _stream(stream))
     if st:

@@ -29,12 +29,13 @@
 // of a (sequence, kv head) are a cluster and join their sums through distributed shared memory; else
 // they leave them in memory for k_cache4_join. Either way they share a sequence's keys evenly.
 //
-// Measured: 64 sequences of 5000 to 16384 keys, 64 heads on 8 (790 MB): 143 us, 5.5 TB/s, 0.83 of the copy rate;
+// Measured: 64 sequences of 5000 to 16384 keys, 64 heads on 8 (790 MB): 142 us, 5.6 TB/s, 0.83 of the copy rate;
 // issue slots 58% busy, the integer pipe 55%, the tensor cores 25%. Three CTAs of four warps an SM: when
 // that took 153 us, four CTAs (128 registers) took 159 and CTAs of three warps 173. Other ways to the operands: V's
 // -136 as a product of its own 167 for 157 us, shifts as products 167 to 172, K's codes as e4m3 numbers
 // 185 for 151. Short caches are bound by starts and ends (about 7 us a CTA): 61 sequences with up to
-// 1028 keys in sight 20.5 us (floor 9.7), one of 577 4.6 us.
+// 1028 keys in sight 20.4 us (floor 9.7), one of 577 4.6 us. Heads of 64: the long batch 91 us (floor 59), the short
+// caches 14.5 (4.8).
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -72,7 +73,7 @@ __device__ __forceinline__ uint32_t bf16_codes(uint32_t w) {
 // ---------------------------------------------------------------------------
 // Storing and reading back. A thread has 32 values of a row, whose codes are 16 neighbouring bytes: 8 of
 // each of four groups (d = 128) or 16 of each of two (d = 64). Bound by memory and, nearly as much, by
-// issue (slots 66% busy): 16384 tokens of 8 heads take 31.8 us to store and read back (172 MB, 5.4 TB/s), 51
+// issue (slots 66% busy): 16384 tokens of 8 heads take 31.8 us to store and read back (172 MB, 5.4 TB/s; heads of 64 21.9), 51
 // with 8 neighbouring values a thread, whose addresses and scales cost as much and whose codes are words apart.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
@@ -880,7 +881,9 @@ Shape4 shape4_of(const tp_dims &d, long long batch, long long cap, long long win
   s.chunk = batch <= kOrdered ? 256 : 128;
   while (s.chunk > kAttnWarps && ctas() < room) s.chunk /= 2;
   if (s.chunk > 128 && ctas() < 2 * room) s.chunk = 128;
-  // at most 64 splits a sequence
+  // At most 64 splits a sequence: one warp of the join reads all of a row's, eight at a time. One sequence of
+  // 131072 keys: 1 kv head 18.7 us (128 splits 17.8, 256 26, 512 47), 4 kv heads 26.2 (128: 33.8); of 16384, 10.1
+  // (128: 13.4). Only 2^20 keys of 1 or 2 kv heads would gain: 88 and 89 us, with 128 splits 53 and 76.
   while ((tiles + s.chunk - 1) / s.chunk > 64) s.chunk *= 2;
   s.splits = static_cast<int>((tiles + s.chunk - 1) / s.chunk);
   if (s.splits < 1) s.splits = 1;

@@ -38,8 +38,12 @@
 // run. More instructions lengthen it: an eighth of the exponentials as polynomials 1.72 us. Every item adds
 // about 4.4 us (its first S, a short block, masked blocks at both of the window's ends, the output), so a
 // window of 1024 and 4 first tokens over 16384 tokens, 64 heads on 8 (9 blocks an item), takes 455 us,
-// 1.17 PFLOP/s over the keys that are seen. Small calls are bound by one item's latency: 2047 tokens of
-// 16 heads of 64, window 300: 9.8 us; one token, 64 heads, 4100 keys: 9.8.
+// 1.17 PFLOP/s over the keys that are seen (in bursts at 2070 MHz; 467 for seconds on end, when the power cap
+// holds the clock at 2000 to 2025). With heads of 64 it takes 385 us (floor 141): half the products behind the same
+// chain. Small calls are bound by one item's latency: 2047 tokens of 16 heads of 64, window 300: 9.8 us; one token,
+// 64 heads, 4100 keys: 9.8. Groups that are no power of two are taken in parts: one token over 4100 keys of 4 kv
+// heads takes 9.1 us with 8 heads each, 10.8 with 6 (in pairs), 15.8 with 7 (one by one); 4096 tokens, window
+// 1024, take 57, 54 and 73.
 //
 // Where there are too few items for the SMs (few tokens), items have one row tile, or their blocks are
 // split, the splits leave f32 sums, and k_window_join joins them.

@@ -222,6 +222,10 @@ def _load_describe():
     return _describe
 
 
+def _types(torch) -> dict:
+    return {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8}
+
+
 def _first_use() -> None:
     """Other threads may call meanwhile: they find the functions below, which wait for the lock, until
     everything that they need is in place. (The import itself already puts _describe into this module.)"""
@@ -229,7 +233,7 @@ def _first_use() -> None:
     types = {}
     try:
         import torch  # the module reads tensors through torch's own libraries
-        types = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float8_e4m3fn: TP_E4M3, torch.uint8: TP_U8}
+        types = _types(torch)
     except Exception:  # none, or one that does not load: descriptors, addresses and streams may be given as they are
         pass
     try:
@@ -257,9 +261,11 @@ def __getattr__(name):
 
 
 def _dtypes() -> dict:
+    global _DTYPES
     _load_describe()
-    if not _DTYPES:
-        import torch  # noqa: F401  says why there is none
+    if not _DTYPES:  # no torch on the first use: says why, or it is there by now
+        import torch
+        _DTYPES = _types(torch)
     return _DTYPES
 
 

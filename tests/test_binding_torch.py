@@ -56,6 +56,19 @@ def test_descriptors_without_a_torch_that_loads(tmp_path, error):
         PYTHONPATH=os.pathsep.join([str(tmp_path), ROOT]))
 
 
+def test_a_torch_that_comes_after_the_first_use(tmp_path):
+    os.makedirs(tmp_path / "torch")
+    (tmp_path / "torch" / "__init__.py").write_text("raise ImportError('not yet')\n")
+    run("import sys, tensor_sharded_linear_gqa_gb300 as tp\n"
+        "tp._args(2).one(tp.TpTensor(16, tp.TP_F32, 0, 2, 8, 8))\n"
+        "for _ in range(2):\n"
+        "    try:\n        tp._dtypes()\n        raise SystemExit('no torch, and no error')\n    except ImportError as e:\n        assert 'not yet' in str(e)\n"
+        f"sys.path.remove({str(tmp_path)!r})\n"
+        "import torch\n"
+        "assert tp.tensor(torch.empty(0, 4)).dtype == tp.TP_F32 and tp._args(1).one(torch.empty(0, 4))\n",
+        PYTHONPATH=os.pathsep.join([str(tmp_path), ROOT]))
+
+
 @pytest.mark.gpu
 def test_cuda_tensors_by_their_attributes():
     from gpu_util import need_gpu

@@ -77,6 +77,8 @@ class Block:
 
     def prompt(self, sequence, residual, positions, chunk=256):
         """A sequence's prompt [tokens x hidden] f32, updated in place, into its empty cache."""
+        if residual.shape[0] > self.capacity:
+            raise ValueError(f"a prompt of {residual.shape[0]} tokens, the cache has {self.capacity} positions")
         cache = self.of(sequence)
         for t0 in range(0, residual.shape[0], chunk):
             part = residual[t0:t0 + chunk]

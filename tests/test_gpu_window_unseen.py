@@ -75,3 +75,21 @@ def test_the_example_reads_back_what_a_chunk_sees():
     chunks = -(-n // chunk)
     assert sum(rows) <= 2 * chunks * (window + chunk + sinks)  # not of the order of n * chunks / 2
     assert torch.isfinite(results[0]).all() and torch.equal(*results)
+
+
+def test_the_example_refuses_a_prompt_that_its_cache_does_not_hold():
+    need_gpu()
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import long_context
+    b = long_context.Block(batch=1, capacity=100)
+    for n in (100, 101):
+        x = torch.randn(n, b.hidden, device="cuda")
+        positions = torch.arange(n, dtype=torch.int32, device="cuda").expand(3, n)
+        if n <= 100:
+            b.prompt(0, x, positions)
+            continue
+        with pytest.raises(ValueError, match="100 positions"):
+            b.prompt(0, x, positions)
+    assert tp.tp_device_status()[0] == tp.TP_OK
